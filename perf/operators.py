@@ -217,7 +217,7 @@ def _plain_norm_fwd(p):
     amax = torch.where(amax == 0, FP8_MAX, amax)
     y8 = (yg * (FP8_MAX / amax)).clamp(-FP8_MAX, FP8_MAX).to(torch.float8_e4m3fn)
     scale = (amax / FP8_MAX).view(M, groups)
-    return {"y8": y8.view(M, -1)[:, :E].to(torch.bfloat16), "scale": scale[:, 0] if quant == "row" else scale, "s": s}
+    return {"y8": y8.view(M, -1)[:, :E].contiguous(), "scale": scale[:, 0] if quant == "row" else scale, "s": s}
 
 
 def _plain_norm_bwd(p):
