@@ -367,6 +367,26 @@ int *device_status_word(int dev, int *err) {
   return g_status[dev];
 }
 
+int scratch_begin(size_t bytes, cudaStream_t stream, const char *what, char **base) {
+  int dev, rc;
+  cudaMemPool_t pool;
+  if ((rc = current_device(&dev)) != GDR_OK) return rc;
+  if ((rc = scratch_pool(dev, &pool)) != GDR_OK) return rc;
+  cudaError_t e = cudaMallocFromPoolAsync((void **)base, bytes > 0 ? bytes : 256, pool, stream);
+  return e == cudaSuccess ? GDR_OK : cuda_error(e, what);
+}
+
+int scratch_end(char *base, cudaStream_t stream, const char *what, int rc) {
+  cudaError_t e = cudaFreeAsync(base, stream);
+  return rc == GDR_OK && e != cudaSuccess ? cuda_error(e, what) : rc;
+}
+
+int *current_status_word(int *err) {
+  int dev;
+  if ((*err = current_device(&dev)) != GDR_OK) return nullptr;
+  return device_status_word(dev, err);
+}
+
 // Implemented in gdr_fused.cu: returns GDR_ERR_UNSUPPORTED (without setting the
 // message) when the fused form does not cover the request.
 int run_fused(const gdr_desc &d, const void *q, const void *k, const void *v, const float *g, const void *beta,
@@ -523,6 +543,7 @@ int gdr_device_status(void *stream, int clear) {
     if (e != cudaSuccess) return cuda_error(e, "clearing the status word");
   }
   if (host == GDR_ERR_SEQLENS) set_error(host, "cu_seqlens is not non-decreasing from 0 to T");
+  if (host == GDR_ERR_SLOTS) set_error(host, "a state slot is past the end of the pool");
   if (host == GDR_ERR_TIMEOUT) set_error(host, "a bounded device-side wait expired");
   return host;
 }

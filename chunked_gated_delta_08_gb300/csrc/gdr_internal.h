@@ -22,6 +22,22 @@ void count_launch(int n = 1);
 // (bad cu_seqlens, an expired bounded wait).  Zero means OK.
 int *device_status_word(int device, int *err);
 
+// Stream-ordered scratch from the library-owned pool of the current device;
+// scratch_end returns it (and passes `rc` through unless the return fails).
+int scratch_begin(size_t bytes, cudaStream_t stream, const char *what, char **base);
+int scratch_end(char *base, cudaStream_t stream, const char *what, int rc);
+// The status word of the current device (null and *err set on failure).
+int *current_status_word(int *err);
+
+// After a launch: counts it and returns its error, if any.
+inline int launched(const char *what) {
+  count_launch();
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? GDR_OK : cuda_error(e, what);
+}
+inline bool is_aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+constexpr int kSMs = 152;  // multiprocessors of a GB300
+
 // Geometry shared by the launchers: number of chunks in the dense layout,
 // and an upper bound on NT for the varlen layout.
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -91,6 +107,18 @@ struct SplitArgs {
 int launch_split_transitions(const ChunkedArgs &a, const SplitArgs &sp);
 int launch_split_merge(const ChunkedArgs &a, const SplitArgs &sp);
 int launch_split_final(const ChunkedArgs &a, const SplitArgs &sp);
+
+// What a kernel needs to check cu_seqlens (cu null: nothing to check).
+struct SeqCheck {
+  const int64_t *cu;
+  int64_t N, T;
+  int *status;
+};
+// Column sums of part [rows, cols] (rows ld apart) in a fixed order; of each
+// `width` columns the first `keep` are written, none where `seqs` is invalid
+// (gdr_norm.cu).
+int launch_col_sum(const float *part, int64_t rows, int64_t ld, int64_t cols, int64_t width, int64_t keep, float *out,
+                   const SeqCheck &seqs, cudaStream_t stream);
 
 // The per-token form (gdr_recurrent.cu): reads q, k, v, g, beta, h0, cu,
 // chunk_offsets (varlen only, from launch_chunk_index), writes o and ht.

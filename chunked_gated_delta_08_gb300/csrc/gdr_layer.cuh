@@ -1,0 +1,119 @@
+// gdr_layer.cuh -- device helpers of the operators around the recurrence: the
+// norm, the short convolution and the selective state space scan.
+//
+// Rows.  These operators take [tokens, channels] inputs whose rows may lie
+// further apart than their length (a slice of a wider projection output): a row
+// index is multiplied by a 64-bit leading dimension.  Loads go eight elements at
+// a time where every base and leading dimension allows 16-byte accesses
+// (the host decides, per call), else one at a time.
+#pragma once
+
+#include "gdr_device.cuh"
+#include "gdr_internal.h"
+
+namespace gdr {
+
+// Eight consecutive elements as fp32; p is 16-byte aligned (32 for fp32 is not needed: two loads).
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void unpack8(const uint4 &u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
+  unpack8(*reinterpret_cast<const uint4 *>(p), v);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&t);
+}
+__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
+  reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
+  *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                             pack_bf16(v[6], v[7]));
+}
+
+// Four elements; p is aligned to all four.
+__device__ __forceinline__ void load4(const float *p, float (&v)[4]) {
+  const float4 a = *reinterpret_cast<const float4 *>(p);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&v)[4]) {
+  const uint2 u = *reinterpret_cast<const uint2 *>(p);
+  v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
+  v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
+}
+__device__ __forceinline__ void store4(float *p, const float (&v)[4]) {
+  *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&v)[4]) {
+  *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+}
+
+// VEC elements (8, 4 or 1) at p.
+template <int VEC, typename T>
+__device__ __forceinline__ void load_vec(const T *p, float (&v)[VEC]) {
+  if constexpr (VEC == 8) load8(p, v);
+  else if constexpr (VEC == 4) load4(p, v);
+  else v[0] = to_f32(p[0]);
+}
+template <int VEC, typename T>
+__device__ __forceinline__ void store_vec(T *p, const float (&v)[VEC]) {
+  if constexpr (VEC == 8) store8(p, v);
+  else if constexpr (VEC == 4) store4(p, v);
+  else p[0] = from_f32<T>(v[0]);
+}
+
+// An element of a parameter vector that is fp32 or of the input dtype.
+template <typename T>
+__device__ __forceinline__ float param(const void *p, bool f32, int64_t i) {
+  return f32 ? static_cast<const float *>(p)[i] : to_f32(static_cast<const T *>(p)[i]);
+}
+
+// max that keeps NaN: a row or group that holds one must not hide it in its scale.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// 1 / (1 + e^-x), to a few units in the last place; 0 and 1 at the ends, NaN for NaN.
+__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+// Whether cu_seqlens is non-decreasing from 0 to T.  Every thread of the block
+// calls it and gets the same answer; the first violation seen is recorded.
+__device__ __forceinline__ bool seqlens_ok(const int64_t *cu, int64_t N, int64_t T, int *status) {
+  if (!cu) return true;
+  bool bad = threadIdx.x == 0 && (cu[0] != 0 || cu[N] != T);
+  for (int64_t n = threadIdx.x; n < N; n += blockDim.x) bad |= cu[n + 1] < cu[n];
+  if (!__syncthreads_or(bad)) return true;
+  if (threadIdx.x == 0) raise_status(status, GDR_ERR_SEQLENS);
+  return false;
+}
+
+__device__ __forceinline__ bool seqlens_ok(const SeqCheck &s) { return seqlens_ok(s.cu, s.N, s.T, s.status); }
+
+// The sequence of flat token t (the last n with first token <= t: empty ones
+// are passed over).  Dense layout: sequences of T tokens each.
+__device__ __forceinline__ int64_t seq_of_token(const int64_t *cu, int64_t N, int64_t T, int64_t t) {
+  if (!cu) return t / T;
+  int64_t lo = 0, hi = N;  // cu[lo] <= t < cu[hi]
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (cu[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+}  // namespace gdr

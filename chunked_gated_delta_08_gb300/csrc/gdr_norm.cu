@@ -1,0 +1,537 @@
+// gdr_norm.cu -- root-mean-square norm with the residual's addition, an 8-bit
+// output with scales, and the backward.
+//
+//   s = round(x + r);  y = s rho w,  rho = 1 / sqrt(mean(s^2) + eps)
+//   backward, with p = w dy:  dL/ds = ds + rho (p - s rho^2 mean(p s)),  dw = sum over rows of dy s rho
+//
+// One pass over memory: a row is read once, held in fp32 registers while its
+// sum is formed, and written once.  The bound is HBM.
+#include <algorithm>
+
+#include "gdr_layer.cuh"
+
+namespace gdr {
+namespace {
+
+constexpr float kFp8Max = 448.f;
+
+struct NormArgs {
+  gdr_norm_desc d;
+  const void *x, *res, *weight, *ds;  // backward: x is dy, res is s
+  void *y, *s;                        // backward: dx, dres
+  float *scale;                       // backward: dweight partials
+  int64_t ngroups;
+  int rows_per_block;
+};
+
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {  // a in the low byte
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+template <int VEC>
+__device__ __forceinline__ void store_fp8(uint8_t *p, const float (&v)[VEC], float inv) {
+  if constexpr (VEC == 8) {
+    const uint32_t lo = pack_e4m3(v[0] * inv, v[1] * inv) | (pack_e4m3(v[2] * inv, v[3] * inv) << 16);
+    const uint32_t hi = pack_e4m3(v[4] * inv, v[5] * inv) | (pack_e4m3(v[6] * inv, v[7] * inv) << 16);
+    *reinterpret_cast<uint2 *>(p) = make_uint2(lo, hi);
+  } else {
+    p[0] = (uint8_t)(pack_e4m3(v[0] * inv, 0.f) & 0xffu);
+  }
+}
+
+__device__ __forceinline__ float group_inv(float amax) { return amax == 0.f ? 1.f : kFp8Max / amax; }
+__device__ __forceinline__ float group_scale(float amax) { return amax == 0.f ? 1.f : amax / kFp8Max; }
+
+// Sums (or maxima) over the NT threads of a row.  NT == 32: a warp, no barrier.
+template <int NT, bool MAX>
+__device__ __forceinline__ float row_reduce(float v, float *red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float u = __shfl_xor_sync(0xffffffffu, v, o);
+    v = MAX ? max_nan(v, u) : v + u;
+  }
+  if constexpr (NT > 32) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __syncthreads();  // the previous reduction's readers are done
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int i = 1; i < NT / 32; ++i) v = MAX ? max_nan(v, red[i]) : v + red[i];
+  }
+  return v;
+}
+
+// Column of this thread's k-th vector.  VEC == 8: vectors of neighbouring
+// threads follow one another.  VEC == 1: a warp owns NV * 32 columns in a run,
+// so that a scale group of 128 columns is four steps of one warp.
+template <int NT, int VEC, int NV>
+__device__ __forceinline__ int64_t col_of(int tid, int k) {
+  if constexpr (VEC == 8) return ((int64_t)k * NT + tid) * 8;
+  else return (int64_t)(tid >> 5) * (NV * 32) + k * 32 + (tid & 31);
+}
+
+// One row per NT threads; blocks of 256 threads take 256 / NT rows when NT is a warp.
+template <typename T, typename R, int NT, int VEC, int NV, int QUANT, bool RES>
+__global__ void __launch_bounds__(NT == 32 ? 256 : NT) norm_fwd_kernel(NormArgs a) {
+  __shared__ float red[32];
+  const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
+  const int64_t m = NT == 32 ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
+  if (m >= a.d.M) return;  // whole warps, and only where no barrier follows (NT == 32)
+  const int64_t E = a.d.E;
+  const T *x = static_cast<const T *>(a.x) + m * a.d.ld_x;
+  const R *res = static_cast<const R *>(a.res) + (RES ? m * a.d.ld_res : 0);
+  const bool wf32 = a.d.weight_dtype == GDR_F32;
+  float v[NV][VEC];
+  float ss = 0.f;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int64_t c = col_of<NT, VEC, NV>(tid, k);
+    if (c < E) {
+      load_vec<VEC>(x + c, v[k]);
+      if constexpr (RES) {
+        float r[VEC];
+        load_vec<VEC>(res + c, r);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[k][i] = to_f32(from_f32<R>(v[k][i] + r[i]));  // s as stored
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[k][i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) ss = fmaf(v[k][i], v[k][i], ss);
+  }
+  if constexpr (RES) {
+    R *s = static_cast<R *>(a.s) + m * E;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int64_t c = col_of<NT, VEC, NV>(tid, k);
+      if (c < E) store_vec<VEC>(s + c, v[k]);
+    }
+  }
+  float w[NV][VEC];  // the weights' loads overlap the sum's exchange
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int64_t c = col_of<NT, VEC, NV>(tid, k);
+    if (c < E) {
+      if (wf32) load_vec<VEC>(static_cast<const float *>(a.weight) + c, w[k]);
+      else load_vec<VEC>(static_cast<const T *>(a.weight) + c, w[k]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) w[k][i] = 0.f;
+    }
+  }
+  const float rho = rsqrtf(row_reduce<NT, false>(ss, red) / (float)E + a.d.eps);
+  float amax = 0.f;
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      v[k][i] = v[k][i] * rho * w[k][i];
+      if (QUANT == GDR_QUANT_ROW) amax = max_nan(amax, col_of<NT, VEC, NV>(tid, k) < E ? fabsf(v[k][i]) : 0.f);
+    }
+  if constexpr (QUANT == GDR_QUANT_NONE) {
+    T *y = static_cast<T *>(a.y) + m * E;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int64_t c = col_of<NT, VEC, NV>(tid, k);
+      if (c < E) store_vec<VEC>(y + c, v[k]);
+    }
+  } else if constexpr (QUANT == GDR_QUANT_ROW) {
+    amax = row_reduce<NT, true>(amax, red);
+    const float inv = group_inv(amax);
+    uint8_t *y = static_cast<uint8_t *>(a.y) + m * E;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int64_t c = col_of<NT, VEC, NV>(tid, k);
+      if (c < E) store_fp8<VEC>(y + c, v[k], inv);
+    }
+    if (tid == 0) a.scale[m] = group_scale(amax);
+  } else {
+    uint8_t *y = static_cast<uint8_t *>(a.y) + m * E;
+    float *scale = a.scale + m * a.ngroups;
+    if constexpr (VEC == 8) {  // a group is 16 neighbouring lanes
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int64_t c = col_of<NT, VEC, NV>(tid, k);
+        float g = 0.f;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) g = max_nan(g, c < E ? fabsf(v[k][i]) : 0.f);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) g = max_nan(g, __shfl_xor_sync(0xffffffffu, g, o));
+        if (c < E) {
+          store_fp8<VEC>(y + c, v[k], group_inv(g));
+          if ((tid & 15) == 0) scale[c / GDR_QUANT_GROUP_SIZE] = group_scale(g);
+        }
+      }
+    } else {  // a group is four steps of the warp
+      static_assert(NV % 4 == 0, "a warp's run of columns is whole groups");
+#pragma unroll
+      for (int k = 0; k < NV; k += 4) {
+        float g = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          g = max_nan(g, col_of<NT, VEC, NV>(tid, k + q) < E ? fabsf(v[k + q][0]) : 0.f);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) g = max_nan(g, __shfl_xor_sync(0xffffffffu, g, o));
+        const float inv = group_inv(g);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t c = col_of<NT, VEC, NV>(tid, k + q);
+          if (c < E) store_fp8<VEC>(y + c, v[k + q], inv);
+        }
+        const int64_t c0 = col_of<NT, VEC, NV>(tid, k);
+        if ((tid & 31) == 0 && c0 < E) scale[c0 / GDR_QUANT_GROUP_SIZE] = group_scale(g);
+      }
+    }
+  }
+}
+
+// Rows too long for registers: the row is read again (from L2) for the output.
+// One block of 256 threads per row; scale groups are taken a warp at a time.
+template <typename T, typename R, bool RES>
+__global__ void __launch_bounds__(256) norm_fwd_long_kernel(NormArgs a) {
+  __shared__ float red[32];
+  const int64_t m = blockIdx.x, E = a.d.E;
+  const T *x = static_cast<const T *>(a.x) + m * a.d.ld_x;
+  const R *res = static_cast<const R *>(a.res) + (RES ? m * a.d.ld_res : 0);
+  R *s = static_cast<R *>(a.s) + (RES ? m * E : 0);
+  const bool wf32 = a.d.weight_dtype == GDR_F32;
+  auto value = [&](int64_t c) {
+    float v = to_f32(x[c]);
+    if constexpr (RES) v = to_f32(from_f32<R>(v + to_f32(res[c])));
+    return v;
+  };
+  float ss = 0.f;
+  for (int64_t c = threadIdx.x; c < E; c += 256) {
+    const float v = value(c);
+    if constexpr (RES) s[c] = from_f32<R>(v);
+    ss = fmaf(v, v, ss);
+  }
+  const float rho = rsqrtf(row_reduce<256, false>(ss, red) / (float)E + a.d.eps);
+  auto out = [&](int64_t c) { return value(c) * rho * param<T>(a.weight, wf32, c); };
+  if (a.d.quant == GDR_QUANT_NONE) {
+    T *y = static_cast<T *>(a.y) + m * E;
+    for (int64_t c = threadIdx.x; c < E; c += 256) y[c] = from_f32<T>(out(c));
+    return;
+  }
+  uint8_t *y = static_cast<uint8_t *>(a.y) + m * E;
+  if (a.d.quant == GDR_QUANT_ROW) {
+    float amax = 0.f;
+    for (int64_t c = threadIdx.x; c < E; c += 256) amax = max_nan(amax, fabsf(out(c)));
+    amax = row_reduce<256, true>(amax, red);
+    for (int64_t c = threadIdx.x; c < E; c += 256) {
+      const float v[1] = {out(c)};
+      store_fp8<1>(y + c, v, group_inv(amax));
+    }
+    if (threadIdx.x == 0) a.scale[m] = group_scale(amax);
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  for (int64_t g = threadIdx.x >> 5; g < a.ngroups; g += 8) {
+    float v[4], amax = 0.f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t c = g * GDR_QUANT_GROUP_SIZE + q * 32 + lane;
+      v[q] = c < E ? out(c) : 0.f;
+      amax = max_nan(amax, fabsf(v[q]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t c = g * GDR_QUANT_GROUP_SIZE + q * 32 + lane;
+      const float u[1] = {v[q]};
+      if (c < E) store_fp8<1>(y + c, u, group_inv(amax));
+    }
+    if (lane == 0) a.scale[m * a.ngroups + g] = group_scale(amax);
+  }
+}
+
+// Backward, row in registers.  A block takes rows b, b + grid, ...; each thread
+// keeps the weight gradient of its own columns in registers over all of them
+// and leaves it in row b of the partials, which col_sum_kernel adds in order.
+template <typename T, typename R, int NT, int VEC, int NV>
+__global__ void __launch_bounds__(NT) norm_bwd_kernel(NormArgs a) {
+  __shared__ float red[2][32];
+  const int tid = threadIdx.x;
+  const int64_t E = a.d.E;
+  const bool wf32 = a.d.weight_dtype == GDR_F32;
+  float w[NV][VEC], dw[NV][VEC];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int64_t c = col_of<NT, VEC, NV>(tid, k);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) w[k][i] = dw[k][i] = 0.f;
+    if (c < E) {
+      if (wf32) load_vec<VEC>(static_cast<const float *>(a.weight) + c, w[k]);
+      else load_vec<VEC>(static_cast<const T *>(a.weight) + c, w[k]);
+    }
+  }
+  for (int64_t m = blockIdx.x; m < a.d.M; m += gridDim.x) {
+    const T *dy = static_cast<const T *>(a.x) + m * a.d.ld_x;
+    const R *s = static_cast<const R *>(a.res) + m * a.d.ld_res;
+    const R *ds = static_cast<const R *>(a.ds) + (a.ds ? m * a.d.ld_ds : 0);
+    float v[NV][VEC], g[NV][VEC], up[NV][VEC];
+    float ss = 0.f, ps = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int64_t c = col_of<NT, VEC, NV>(tid, k);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[k][i] = g[k][i] = up[k][i] = 0.f;
+      if (c < E) {
+        load_vec<VEC>(s + c, v[k]);
+        load_vec<VEC>(dy + c, g[k]);
+        if (a.ds) load_vec<VEC>(ds + c, up[k]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        ss = fmaf(v[k][i], v[k][i], ss);
+        ps = fmaf(v[k][i] * w[k][i], g[k][i], ps);
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      ps += __shfl_xor_sync(0xffffffffu, ps, o);
+    }
+    if constexpr (NT > 32) {
+      __syncthreads();
+      if ((tid & 31) == 0) {
+        red[0][tid >> 5] = ss;
+        red[1][tid >> 5] = ps;
+      }
+      __syncthreads();
+      ss = red[0][0];
+      ps = red[1][0];
+#pragma unroll
+      for (int i = 1; i < NT / 32; ++i) {
+        ss += red[0][i];
+        ps += red[1][i];
+      }
+    }
+    const float rho = rsqrtf(ss / (float)E + a.d.eps);
+    const float mix = rho * rho * (ps / (float)E);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int64_t c = col_of<NT, VEC, NV>(tid, k);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        dw[k][i] = fmaf(g[k][i] * rho, v[k][i], dw[k][i]);
+        g[k][i] = fmaf(rho, fmaf(w[k][i], g[k][i], -v[k][i] * mix), up[k][i]);
+      }
+      if (c < E) {
+        if (a.y) store_vec<VEC>(static_cast<T *>(a.y) + m * E + c, g[k]);
+        if (a.s) store_vec<VEC>(static_cast<R *>(a.s) + m * E + c, g[k]);
+      }
+    }
+  }
+  if (a.scale) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int64_t c = col_of<NT, VEC, NV>(tid, k);
+      if (c < E) store_vec<VEC>(a.scale + (int64_t)blockIdx.x * E + c, dw[k]);
+    }
+  }
+}
+
+// Backward for rows too long for registers: the weight gradient's partials are
+// kept in this block's own row of global scratch.
+template <typename T, typename R>
+__global__ void __launch_bounds__(256) norm_bwd_long_kernel(NormArgs a) {
+  __shared__ float red[32];
+  const int64_t E = a.d.E;
+  const bool wf32 = a.d.weight_dtype == GDR_F32;
+  float *dw = a.scale ? a.scale + (int64_t)blockIdx.x * E : nullptr;
+  if (dw)
+    for (int64_t c = threadIdx.x; c < E; c += 256) dw[c] = 0.f;
+  for (int64_t m = blockIdx.x; m < a.d.M; m += gridDim.x) {
+    const T *dy = static_cast<const T *>(a.x) + m * a.d.ld_x;
+    const R *s = static_cast<const R *>(a.res) + m * a.d.ld_res;
+    const R *ds = static_cast<const R *>(a.ds) + (a.ds ? m * a.d.ld_ds : 0);
+    float ss = 0.f, ps = 0.f;
+    for (int64_t c = threadIdx.x; c < E; c += 256) {
+      const float v = to_f32(s[c]);
+      ss = fmaf(v, v, ss);
+      ps = fmaf(v * param<T>(a.weight, wf32, c), to_f32(dy[c]), ps);
+    }
+    ss = row_reduce<256, false>(ss, red);
+    ps = row_reduce<256, false>(ps, red);
+    const float rho = rsqrtf(ss / (float)E + a.d.eps), mix = rho * rho * (ps / (float)E);
+    for (int64_t c = threadIdx.x; c < E; c += 256) {
+      const float v = to_f32(s[c]), g = to_f32(dy[c]);
+      if (dw) dw[c] = fmaf(g * rho, v, dw[c]);
+      const float o = fmaf(rho, fmaf(param<T>(a.weight, wf32, c), g, -v * mix), a.ds ? to_f32(ds[c]) : 0.f);
+      if (a.y) static_cast<T *>(a.y)[m * E + c] = from_f32<T>(o);
+      if (a.s) static_cast<R *>(a.s)[m * E + c] = from_f32<R>(o);
+    }
+  }
+}
+
+template <typename T, typename R, int NT, int VEC, int NV, bool RES>
+void launch_fwd_q(const NormArgs &a, cudaStream_t st) {
+  const unsigned grid = (unsigned)(NT == 32 ? cdiv(a.d.M, 8) : a.d.M), block = NT == 32 ? 256 : NT;
+  if (a.d.quant == GDR_QUANT_NONE) norm_fwd_kernel<T, R, NT, VEC, NV, 0, RES><<<grid, block, 0, st>>>(a);
+  else if (a.d.quant == GDR_QUANT_ROW) norm_fwd_kernel<T, R, NT, VEC, NV, 1, RES><<<grid, block, 0, st>>>(a);
+  else norm_fwd_kernel<T, R, NT, VEC, NV, 2, RES><<<grid, block, 0, st>>>(a);
+}
+
+template <typename T, typename R, bool RES>
+int launch_fwd(const NormArgs &a, cudaStream_t st) {
+  const int64_t E = a.d.E;
+  const bool vec = E % 8 == 0 && a.d.ld_x % 8 == 0 && (!RES || a.d.ld_res % 8 == 0) && is_aligned16(a.x) &&
+                   is_aligned16(a.res) && is_aligned16(a.weight) && is_aligned16(a.y) && is_aligned16(a.s);
+  if (vec) {
+    if (E <= 512) launch_fwd_q<T, R, 32, 8, 2, RES>(a, st);
+    else if (E <= 1024) launch_fwd_q<T, R, 128, 8, 1, RES>(a, st);
+    else if (E <= 2048) launch_fwd_q<T, R, 256, 8, 1, RES>(a, st);
+    else if (E <= 4096) launch_fwd_q<T, R, 256, 8, 2, RES>(a, st);
+    else if (E <= 8192) launch_fwd_q<T, R, 512, 8, 2, RES>(a, st);
+    else if (E <= 16384) launch_fwd_q<T, R, 1024, 8, 2, RES>(a, st);
+    else norm_fwd_long_kernel<T, R, RES><<<(unsigned)a.d.M, 256, 0, st>>>(a);
+  } else {
+    if (E <= 256) launch_fwd_q<T, R, 32, 1, 8, RES>(a, st);
+    else if (E <= 2048) launch_fwd_q<T, R, 256, 1, 8, RES>(a, st);
+    else if (E <= 4096) launch_fwd_q<T, R, 256, 1, 16, RES>(a, st);
+    else norm_fwd_long_kernel<T, R, RES><<<(unsigned)a.d.M, 256, 0, st>>>(a);
+  }
+  return launched("norm_fwd_kernel");
+}
+
+template <typename T, typename R>
+int launch_bwd(NormArgs a, float *dweight, cudaStream_t st) {
+  const int64_t E = a.d.E;
+  const bool vec = E % 8 == 0 && a.d.ld_x % 8 == 0 && a.d.ld_res % 8 == 0 && (!a.ds || a.d.ld_ds % 8 == 0) &&
+                   is_aligned16(a.x) && is_aligned16(a.res) && is_aligned16(a.ds) && is_aligned16(a.weight) && is_aligned16(a.y) &&
+                   is_aligned16(a.s);
+  const int64_t most = E <= 256 ? 8 * kSMs : 4 * kSMs;  // blocks, and rows of partials
+  const unsigned grid = (unsigned)std::min<int64_t>(a.d.M, most);
+  char *base = nullptr;
+  int rc;
+  if (dweight) {
+    if ((rc = scratch_begin(sizeof(float) * (size_t)(grid * E), st, "norm backward scratch", &base)) != GDR_OK)
+      return rc;
+    a.scale = (float *)base;
+  }
+  if (vec) {
+    if (E <= 256) norm_bwd_kernel<T, R, 32, 8, 1><<<grid, 32, 0, st>>>(a);
+    else if (E <= 1024) norm_bwd_kernel<T, R, 128, 8, 1><<<grid, 128, 0, st>>>(a);
+    else if (E <= 2048) norm_bwd_kernel<T, R, 256, 8, 1><<<grid, 256, 0, st>>>(a);
+    else if (E <= 4096) norm_bwd_kernel<T, R, 512, 8, 1><<<grid, 512, 0, st>>>(a);
+    else if (E <= 8192) norm_bwd_kernel<T, R, 1024, 8, 1><<<grid, 1024, 0, st>>>(a);
+    else norm_bwd_long_kernel<T, R><<<grid, 256, 0, st>>>(a);
+  } else {
+    if (E <= 256) norm_bwd_kernel<T, R, 32, 1, 8><<<grid, 32, 0, st>>>(a);
+    else if (E <= 2048) norm_bwd_kernel<T, R, 256, 1, 8><<<grid, 256, 0, st>>>(a);
+    else if (E <= 4096) norm_bwd_kernel<T, R, 512, 1, 8><<<grid, 512, 0, st>>>(a);
+    else norm_bwd_long_kernel<T, R><<<grid, 256, 0, st>>>(a);
+  }
+  rc = launched("norm_bwd_kernel");
+  if (dweight) {
+    if (rc == GDR_OK) rc = launch_col_sum((const float *)base, grid, E, E, E, E, dweight, SeqCheck{}, st);
+    rc = scratch_end(base, st, "norm backward scratch", rc);
+  }
+  return rc;
+}
+
+int validate(const gdr_norm_desc *d) {
+  if (!d) return set_error(GDR_ERR_NULLPTR, "desc is NULL");
+  if (d->dtype != GDR_F32 && d->dtype != GDR_BF16) return set_error(GDR_ERR_DTYPE, "dtype must be GDR_F32 or GDR_BF16");
+  if (d->res_dtype != d->dtype && d->res_dtype != GDR_F32)
+    return set_error(GDR_ERR_DTYPE, "the residual must be of the input dtype or fp32");
+  if (d->weight_dtype != d->dtype && d->weight_dtype != GDR_F32)
+    return set_error(GDR_ERR_DTYPE, "weight must be of the input dtype or fp32");
+  if (d->quant < GDR_QUANT_NONE || d->quant > GDR_QUANT_GROUP) return set_error(GDR_ERR_DTYPE, "unknown quant");
+  if (d->flags) return set_error(GDR_ERR_DTYPE, "unknown bits in flags");
+  if (d->M < 0 || d->M > 0x7fffffff) return set_error(GDR_ERR_SHAPE, "M must be in [0, 2^31)");
+  if (d->E < 1 || d->E > (1 << 24)) return set_error(GDR_ERR_SHAPE, "E must be in [1, 2^24]");
+  if (d->ld_x < d->E || d->ld_res < d->E || d->ld_ds < d->E)
+    return set_error(GDR_ERR_SHAPE, "leading dimensions must be at least E");
+  if (!(d->eps >= 0.f)) return set_error(GDR_ERR_SHAPE, "eps must be >= 0");
+  return GDR_OK;
+}
+
+// Column sums of part [rows, cols], rows ld apart: 32 columns a block, eight
+// interleaved runs of rows added in order.  Columns come in groups of `width`,
+// of which the first `keep` go to out, close together.
+__global__ void __launch_bounds__(256) col_sum_kernel(const float *__restrict__ part, int64_t rows, int64_t ld,
+                                                      int64_t cols, int64_t width, int64_t keep,
+                                                      float *__restrict__ out, SeqCheck seqs) {
+  __shared__ float sm[8][32];
+  if (!seqlens_ok(seqs)) return;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  float acc = 0.f;
+  if (c < cols) {
+#pragma unroll 8
+    for (int64_t r = w; r < rows; r += 8) acc += part[r * ld + c];
+  }
+  sm[w][lane] = acc;
+  __syncthreads();
+  if (w == 0 && c < cols && c % width < keep) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) acc += sm[i][lane];
+    out[c / width * keep + c % width] = acc;
+  }
+}
+
+}  // namespace
+
+int launch_col_sum(const float *part, int64_t rows, int64_t ld, int64_t cols, int64_t width, int64_t keep, float *out,
+                   const SeqCheck &seqs, cudaStream_t stream) {
+  col_sum_kernel<<<(unsigned)cdiv(cols, 32), 256, 0, stream>>>(part, rows, ld, cols, width, keep, out, seqs);
+  return launched("col_sum_kernel");
+}
+
+}  // namespace gdr
+
+using namespace gdr;
+
+extern "C" {
+
+int gdr_norm_fwd(const gdr_norm_desc *desc, const void *x, const void *residual, const void *weight, void *y,
+                 float *scale, void *s, void *stream) {
+  int rc = validate(desc);
+  if (rc != GDR_OK) return rc;
+  if (desc->M == 0) return GDR_OK;
+  if (!x || !weight || !y) return set_error(GDR_ERR_NULLPTR, "x, weight and y must be non-NULL");
+  if (residual && !s) return set_error(GDR_ERR_NULLPTR, "with a residual, s must be non-NULL");
+  if (desc->quant != GDR_QUANT_NONE && !scale) return set_error(GDR_ERR_NULLPTR, "an 8-bit output needs scale");
+  NormArgs a{};
+  a.d = *desc;
+  a.x = x; a.res = residual; a.weight = weight; a.y = y; a.s = residual ? s : nullptr; a.scale = scale;
+  a.ngroups = cdiv(desc->E, GDR_QUANT_GROUP_SIZE);
+  cudaStream_t st = (cudaStream_t)stream;
+  if (desc->dtype == GDR_F32)
+    return residual ? launch_fwd<float, float, true>(a, st) : launch_fwd<float, float, false>(a, st);
+  if (!residual) return launch_fwd<__nv_bfloat16, float, false>(a, st);
+  if (desc->res_dtype == GDR_F32) return launch_fwd<__nv_bfloat16, float, true>(a, st);
+  return launch_fwd<__nv_bfloat16, __nv_bfloat16, true>(a, st);
+}
+
+int gdr_norm_bwd(const gdr_norm_desc *desc, const void *dy, const void *s, const void *ds, const void *weight,
+                 void *dx, void *dres, float *dweight, void *stream) {
+  int rc = validate(desc);
+  if (rc != GDR_OK) return rc;
+  if (desc->quant != GDR_QUANT_NONE) return set_error(GDR_ERR_UNSUPPORTED, "the backward has no 8-bit form");
+  cudaStream_t st = (cudaStream_t)stream;
+  if (desc->M == 0) {
+    if (!dweight) return GDR_OK;
+    const cudaError_t e = cudaMemsetAsync(dweight, 0, sizeof(float) * (size_t)desc->E, st);
+    return e == cudaSuccess ? GDR_OK : cuda_error(e, "clearing dweight");
+  }
+  if (!dy || !s || !weight) return set_error(GDR_ERR_NULLPTR, "dy, s and weight must be non-NULL");
+  NormArgs a{};
+  a.d = *desc;
+  a.x = dy; a.res = s; a.ds = ds; a.weight = weight; a.y = dx; a.s = dres;
+  if (desc->dtype == GDR_F32) return launch_bwd<float, float>(a, dweight, st);
+  if (desc->res_dtype == GDR_F32) return launch_bwd<__nv_bfloat16, float>(a, dweight, st);
+  return launch_bwd<__nv_bfloat16, __nv_bfloat16>(a, dweight, st);
+}
+
+}  // extern "C"

@@ -1,0 +1,350 @@
+// gdr_ssm.cu -- the selective state space scan: forward and single-token step.
+// gdr_ssm.cuh has the formulas, the layout and the cut of the time axis.
+//
+// Forward, three launches:
+//   local   per (chunk, channels): the chunk's state from zero, and sum(delta)
+//   carry   per (channel, state): the state that enters each chunk, in order
+//   main    per (chunk, channels): the recurrence again from there, y and ht
+// The recurrence runs twice so that chunks run at once; where one chunk covers
+// a sequence (short ones, or enough sequences to fill the GPU) main runs alone.
+// The bound is arithmetic: per channel, state and token one exponential and
+// four fp32 operations (a third of them more in local), against 8 bytes of HBM
+// traffic per channel and token in bf16.
+#include <algorithm>
+
+#include "gdr_ssm.cuh"
+
+namespace gdr {
+namespace {
+
+template <int SL>
+struct __align__(16) FwdShared {
+  float delta[kTile][Place<SL>::CB], x[kTile][Place<SL>::CB], gate[kTile][Place<SL>::CB];
+  float b[kTile * Place<SL>::SP], c[kTile * Place<SL>::SP];
+  Borders<kTile> bd;
+};
+
+// MAIN: y and ht from the states that enter the chunks (a.hloc, zero where
+// null).  Else: the chunk's own state and sum of delta.
+template <typename T, int SL, int VEC, bool MAIN>
+__global__ void __launch_bounds__(kSsmThreads) ssm_fwd_kernel(SsmArgs a) {
+  using P = Place<SL>;
+  __shared__ FwdShared<SL> sm;
+  if (!seqlens_ok(a.cu, a.d.N, a.M, a.status)) return;
+  const P p(a);
+  if (MAIN && p.chunk == 0) copy_empty_states<SL>(a, p, a.h0, a.ht);
+  f2 A[4][2], h[4][2];
+  load_a<SL>(a, p, A);
+  load_chunk<SL>(a, p, MAIN ? a.hloc : nullptr, p.chunk, h);
+  const int64_t begin = p.chunk * a.L, end = begin + a.L < a.M ? begin + a.L : a.M;
+  const int mine = p.sl & 3;  // of the thread's four channels, the one whose output it finishes
+  const int64_t e_mine = p.e0 + p.col + mine;
+  const bool owner = p.sl < 4 && e_mine < p.e_end;
+  const float skip = MAIN && a.dskip && owner ? a.dskip[e_mine] : 0.f;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  bool started = false;  // a sequence starts in this chunk
+
+  for (int64_t t0 = begin; t0 < end; t0 += kTile) {
+    const int nt = end - t0 < kTile ? (int)(end - t0) : kTile;
+    __syncthreads();  // the previous tile is consumed
+    stage_borders(a, t0, nt, sm.bd);
+    for_tile<kTile, SL, VEC>(p, nt, [&](int t, int c, bool in) {
+      const int64_t e = p.e0 + c;
+      float xv[VEC] = {}, dv[VEC] = {}, zv[VEC] = {};
+      if (in) {
+        load_vec<VEC>(static_cast<const T *>(a.x) + (t0 + t) * a.d.ld_x + e, xv);
+        load_vec<VEC>(static_cast<const T *>(a.dt) + (t0 + t) * a.d.ld_dt + e, dv);
+        if (MAIN && a.z) load_vec<VEC>(static_cast<const T *>(a.z) + (t0 + t) * a.d.ld_z + e, zv);
+      }
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const float raw = dv[i] + (a.dt_bias && in ? a.dt_bias[e + i] : 0.f);
+        sm.delta[t][c + i] = in ? ssm_delta(raw, a.d.flags & GDR_SSM_SOFTPLUS) : 0.f;
+        sm.x[t][c + i] = xv[i];
+        if (MAIN) sm.gate[t][c + i] = a.z ? zv[i] * sigmoid_fast(zv[i]) : 1.f;
+      }
+    });
+    stage_states<T, SL, kTile>(a, p, a.b, a.d.ld_b, t0, nt, sm.b);
+    if (MAIN) stage_states<T, SL, kTile>(a, p, a.c, a.d.ld_c, t0, nt, sm.c);
+    __syncthreads();
+#pragma unroll 2
+    for (int t = 0; t < nt; ++t) {
+      if (sm.bd.first[t] >= 0) {
+        load_h0<SL>(a, p, a.h0, sm.bd.first[t], h);
+        started = true;
+      }
+      const float4 d4 = *reinterpret_cast<const float4 *>(&sm.delta[t][p.col]);
+      const float4 x4 = *reinterpret_cast<const float4 *>(&sm.x[t][p.col]);
+      const ulonglong2 b4 = *reinterpret_cast<const ulonglong2 *>(&sm.b[t * P::SP + p.sl * 4]);
+      ulonglong2 c4;
+      if (MAIN) c4 = *reinterpret_cast<const ulonglong2 *>(&sm.c[t * P::SP + p.sl * 4]);
+      const float dl[4] = {d4.x, d4.y, d4.z, d4.w}, xs[4] = {x4.x, x4.y, x4.z, x4.w};
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f2 dd = f2_pack(dl[j], dl[j]);
+        const float u = dl[j] * xs[j];
+        const f2 uu = f2_pack(u, u);
+        h[j][0] = f2_fma(f2_ex2(f2_mul(A[j][0], dd)), h[j][0], f2_mul(uu, b4.x));
+        h[j][1] = f2_fma(f2_ex2(f2_mul(A[j][1], dd)), h[j][1], f2_mul(uu, b4.y));
+        if (MAIN) {
+          float lo, hi;
+          f2_split(f2_fma(c4.y, h[j][1], f2_mul(c4.x, h[j][0])), lo, hi);
+          v[j] = lo + hi;
+        } else {
+          sum[j] += dl[j];
+        }
+      }
+      if (MAIN) {
+        const float y = sum_over_states<SL>(v, p.sl);
+        if (owner)
+          static_cast<T *>(a.y)[(t0 + t) * a.d.E + e_mine] =
+              from_f32<T>(fmaf(skip, sm.x[t][p.col + mine], y) * sm.gate[t][p.col + mine]);
+        if (a.ht && sm.bd.last[t] >= 0) store_final<SL>(a, p, a.ht, sm.bd.last[t], h);
+      }
+    }
+  }
+  if (!MAIN) {
+    store_chunk<SL>(a, p, a.hloc, p.chunk, h);
+    if (owner) {
+      const float s = mine == 0 ? sum[0] : mine == 1 ? sum[1] : mine == 2 ? sum[2] : sum[3];
+      a.sumd[p.chunk * a.d.E + e_mine] = started ? CUDART_NAN_F : s;  // NaN: nothing passes through
+    }
+  }
+}
+
+// In place, per (channel, state): hloc[c] becomes the state that enters chunk c.
+// A batch of chunks is loaded at once; the additions run in order.
+constexpr int kCarryBatch = 16;
+__global__ void __launch_bounds__(128) ssm_carry_kernel(SsmArgs a, int SP) {
+  const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
+  if (i >= a.d.E * SP) return;
+  const int64_t e = i / SP, row = a.d.E * SP;
+  const int s = (int)(i % SP);
+  const float A = s < a.d.S ? a.a[e * a.d.S + s] * kLog2e : 0.f;
+  float h = 0.f;
+  for (int64_t c0 = 0; c0 < a.chunks; c0 += kCarryBatch) {
+    float loc[kCarryBatch], sum[kCarryBatch];
+#pragma unroll
+    for (int k = 0; k < kCarryBatch; ++k) {
+      const int64_t c = c0 + k;
+      loc[k] = c < a.chunks ? a.hloc[c * row + i] : 0.f;
+      sum[k] = c < a.chunks ? a.sumd[c * a.d.E + e] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < kCarryBatch; ++k) {
+      const int64_t c = c0 + k;
+      if (c < a.chunks) {
+        a.hloc[c * row + i] = h;
+        h = isnan(sum[k]) ? loc[k] : fmaf(ex2(A * sum[k]), h, loc[k]);
+      }
+    }
+  }
+}
+
+// One token per row: states are read and written once, four to a thread, with
+// the lanes of a row on consecutive 16-byte groups.  The bound is HBM.
+template <typename T, int SL>
+__global__ void __launch_bounds__(256) ssm_step_kernel(SsmArgs a, const int32_t *slots, float *state, unsigned tiles) {
+  const int64_t r = blockIdx.x / tiles;
+  const int64_t i = (int64_t)(blockIdx.x % tiles) * 256 + threadIdx.x;
+  const int64_t e = i / SL;
+  const int s0 = (int)(i % SL) * 4, S = (int)a.d.S;
+  int64_t slot = slots ? slots[r] : r;
+  if (slot >= a.d.N) {
+    if (threadIdx.x == 0) raise_status(a.status, GDR_ERR_SLOTS);
+    slot = -1;
+  }
+  const bool in = e < a.d.E;
+  T *y = static_cast<T *>(a.y) + r * a.d.E + e;
+  if (slot < 0) {  // the whole block
+    if (in && s0 == 0) *y = from_f32<T>(0.f);
+    return;
+  }
+  float h[4] = {}, A[4] = {}, b[4] = {}, c[4] = {};
+  float x = 0.f, delta = 0.f, out = 0.f;
+  float *row = state + (slot * a.d.E + e) * S;
+  if (in) {
+    load_states(row, s0, S, a.s4, h);
+    load_states(a.a + e * S, s0, S, a.s4, A);
+    const int64_t g = e / (a.d.E / a.d.G);
+    const T *bp = static_cast<const T *>(a.b) + r * a.d.ld_b + g * S;
+    const T *cp = static_cast<const T *>(a.c) + r * a.d.ld_c + g * S;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (s0 + k < S) {
+        b[k] = to_f32(bp[s0 + k]);
+        c[k] = to_f32(cp[s0 + k]);
+      }
+    x = to_f32(static_cast<const T *>(a.x)[r * a.d.ld_x + e]);
+    delta = ssm_delta(to_f32(static_cast<const T *>(a.dt)[r * a.d.ld_dt + e]) + (a.dt_bias ? a.dt_bias[e] : 0.f),
+                      a.d.flags & GDR_SSM_SOFTPLUS);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      h[k] = fmaf(ex2(delta * (A[k] * kLog2e)), h[k], delta * x * b[k]);
+      out = fmaf(c[k], h[k], out);
+    }
+    store_states(row, s0, S, a.s4, h);
+  }
+#pragma unroll
+  for (int o = SL / 2; o > 0; o >>= 1) out += __shfl_xor_sync(0xffffffffu, out, o);
+  if (in && s0 == 0) {
+    out = fmaf(a.dskip ? a.dskip[e] : 0.f, x, out);
+    if (a.z) {
+      const float z = to_f32(static_cast<const T *>(a.z)[r * a.d.ld_z + e]);
+      out *= z * sigmoid_fast(z);
+    }
+    *y = from_f32<T>(out);
+  }
+}
+
+template <typename T, bool MAIN>
+int launch_fwd(const SsmArgs &a, int sl, bool vec, cudaStream_t st) {
+  const unsigned grid = (unsigned)(a.chunks * a.ctiles);
+  auto go = [&](auto SL) {
+    if (vec) ssm_fwd_kernel<T, decltype(SL)::value, 8, MAIN><<<grid, kSsmThreads, 0, st>>>(a);
+    else ssm_fwd_kernel<T, decltype(SL)::value, 1, MAIN><<<grid, kSsmThreads, 0, st>>>(a);
+    return launched(MAIN ? "ssm_fwd_kernel" : "ssm_local_kernel");
+  };
+  if (sl == 4) return go(std::integral_constant<int, 4>{});
+  if (sl == 8) return go(std::integral_constant<int, 8>{});
+  return go(std::integral_constant<int, 16>{});
+}
+
+template <bool MAIN>
+int launch_fwd(const SsmArgs &a, int sl, bool vec, cudaStream_t st) {
+  return a.d.dtype == GDR_BF16 ? launch_fwd<__nv_bfloat16, MAIN>(a, sl, vec, st)
+                               : launch_fwd<float, MAIN>(a, sl, vec, st);
+}
+
+int lanes_of(int64_t S) { return S <= 16 ? 4 : S <= 32 ? 8 : 16; }
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+template <typename T>
+int launch_step(const SsmArgs &a, const int32_t *slots, float *state, cudaStream_t st) {
+  auto go = [&](auto SL) {
+    const int64_t tiles = cdiv(a.d.E * decltype(SL)::value, 256);
+    if (tiles * a.d.B > 0x7fffffff) return set_error(GDR_ERR_SHAPE, "too many rows for one launch");
+    ssm_step_kernel<T, decltype(SL)::value><<<(unsigned)(tiles * a.d.B), 256, 0, st>>>(a, slots, state, (unsigned)tiles);
+    return launched("ssm_step_kernel");
+  };
+  if (a.d.S <= 4) return go(std::integral_constant<int, 1>{});
+  if (a.d.S <= 8) return go(std::integral_constant<int, 2>{});
+  if (a.d.S <= 16) return go(std::integral_constant<int, 4>{});
+  if (a.d.S <= 32) return go(std::integral_constant<int, 8>{});
+  return go(std::integral_constant<int, 16>{});
+}
+
+int validate(const gdr_ssm_desc *d, const int64_t *cu, bool step) {
+  if (!d) return set_error(GDR_ERR_NULLPTR, "desc is NULL");
+  if (d->dtype != GDR_F32 && d->dtype != GDR_BF16) return set_error(GDR_ERR_DTYPE, "dtype must be GDR_F32 or GDR_BF16");
+  if (d->flags & ~GDR_SSM_SOFTPLUS) return set_error(GDR_ERR_DTYPE, "unknown bits in flags");
+  if (d->B < 0 || d->T < 0 || d->N < 0 || d->N > 0x7fffffff)
+    return set_error(GDR_ERR_SHAPE, "B, T and N must be >= 0 (N below 2^31)");
+  if (d->S < 1 || d->S > 64) return set_error(GDR_ERR_SHAPE, "S must be in [1, 64]");
+  if (d->E < 1 || d->E > (1 << 24)) return set_error(GDR_ERR_SHAPE, "E must be in [1, 2^24]");
+  if (d->G < 1 || d->E % d->G != 0) return set_error(GDR_ERR_SHAPE, "E must be a multiple of G");
+  if (d->ld_x < d->E || d->ld_dt < d->E || d->ld_z < d->E || d->ld_dy < d->E || d->ld_b < d->G * d->S ||
+      d->ld_c < d->G * d->S)
+    return set_error(GDR_ERR_SHAPE, "leading dimensions must be at least E, or G * S");
+  if (step) return d->T == 1 ? GDR_OK : set_error(GDR_ERR_SHAPE, "a step takes one token per row: T must be 1");
+  if (cu) {
+    if (d->B != 1) return set_error(GDR_ERR_SHAPE, "cu_seqlens requires B == 1");
+  } else if (d->N != d->B) {
+    return set_error(GDR_ERR_SHAPE, "N must equal B when cu_seqlens is NULL");
+  }
+  return GDR_OK;
+}
+
+// Chunk length: long chunks cost less carry, short ones fill the GPU.
+int64_t chunk_length(const SsmArgs &a, int64_t lo, int64_t hi) {
+  int64_t L = hi;
+  while (L > lo && cdiv(a.M, L) * a.ctiles < 8 * kSMs) L /= 2;
+  return L;
+}
+
+int run_fwd(SsmArgs a, cudaStream_t st) {
+  int sl, rc;
+  bool vec;
+  if ((rc = ssm_prepare(a, false, &sl, &vec)) != GDR_OK) return rc;
+  // Sequences that are short, or enough of them to fill the GPU: each is one chunk.
+  const bool whole = !a.cu && (a.d.T <= 64 || a.d.B * a.ctiles >= 4 * kSMs);
+  a.L = whole ? std::max<int64_t>(1, a.d.T) : chunk_length(a, 32, 256);
+  a.chunks = std::max<int64_t>(1, cdiv(a.M, a.L));
+  if (a.chunks * a.ctiles > 0x7fffffff) return set_error(GDR_ERR_SHAPE, "too many tokens and channels for one launch");
+  if (whole || a.chunks == 1) return launch_fwd<true>(a, sl, vec, st);
+  const size_t hb = align256(sizeof(float) * (size_t)(a.chunks * a.d.E * 4 * sl));
+  char *base = nullptr;
+  rc = scratch_begin(hb + sizeof(float) * (size_t)(a.chunks * a.d.E), st, "scan scratch", &base);
+  if (rc != GDR_OK) return rc;
+  a.hloc = (float *)base;
+  a.sumd = (float *)(base + hb);
+  rc = launch_fwd<false>(a, sl, vec, st);
+  if (rc == GDR_OK) {
+    ssm_carry_kernel<<<(unsigned)cdiv(a.d.E * 4 * sl, 128), 128, 0, st>>>(a, 4 * sl);
+    rc = launched("ssm_carry_kernel");
+  }
+  if (rc == GDR_OK) rc = launch_fwd<true>(a, sl, vec, st);
+  return scratch_end(base, st, "scan scratch", rc);
+}
+
+}  // namespace
+
+int ssm_validate(const gdr_ssm_desc *d, const int64_t *cu) { return validate(d, cu, false); }
+
+int ssm_prepare(SsmArgs &a, bool backward, int *sl, bool *vec) {
+  int rc;
+  a.M = a.d.B * a.d.T;
+  a.status = current_status_word(&rc);
+  if (!a.status) return rc;
+  *sl = lanes_of(a.d.S);
+  a.tpg = (int)cdiv(a.d.E / a.d.G, 512 / *sl);
+  a.ctiles = (int)(a.d.G * a.tpg);
+  *vec = (a.d.E / a.d.G) % 8 == 0 && a.d.ld_x % 8 == 0 && a.d.ld_dt % 8 == 0 && (!a.z || a.d.ld_z % 8 == 0) &&
+         is_aligned16(a.x) && is_aligned16(a.dt) && is_aligned16(a.z);
+  a.s4 = a.d.S % 4 == 0 && is_aligned16(a.a) && is_aligned16(a.h0) && is_aligned16(a.ht) && is_aligned16(a.dht) && is_aligned16(a.dh0);
+  if (backward) *vec = *vec && a.d.ld_dy % 8 == 0 && is_aligned16(a.dy);
+  return GDR_OK;
+}
+
+}  // namespace gdr
+
+using namespace gdr;
+
+extern "C" {
+
+int gdr_ssm_fwd(const gdr_ssm_desc *desc, const void *x, const void *dt, const float *a, const void *b,
+                const void *c, const float *d, const void *z, const float *dt_bias, const float *h0,
+                const int64_t *cu_seqlens, void *y, float *ht, void *stream) {
+  int rc = validate(desc, cu_seqlens, false);
+  if (rc != GDR_OK) return rc;
+  if (desc->N == 0 && !cu_seqlens) return GDR_OK;
+  if (!a || (desc->B * desc->T > 0 && (!x || !dt || !b || !c || !y)))
+    return set_error(GDR_ERR_NULLPTR, "x, dt, a, b, c and y must be non-NULL");
+  SsmArgs s{};
+  s.d = *desc;
+  s.x = x; s.dt = dt; s.a = a; s.b = b; s.c = c; s.dskip = d; s.z = z; s.dt_bias = dt_bias; s.h0 = h0;
+  s.cu = cu_seqlens; s.y = y; s.ht = ht;
+  return run_fwd(s, (cudaStream_t)stream);
+}
+
+int gdr_ssm_step(const gdr_ssm_desc *desc, const void *x, const void *dt, const float *a, const void *b,
+                 const void *c, const float *d, const void *z, const float *dt_bias, const int32_t *slots,
+                 float *state, void *y, void *stream) {
+  int rc = validate(desc, nullptr, true);
+  if (rc != GDR_OK) return rc;
+  if (desc->B == 0) return GDR_OK;
+  if (!x || !dt || !a || !b || !c || !state || !y)
+    return set_error(GDR_ERR_NULLPTR, "x, dt, a, b, c, state and y must be non-NULL");
+  SsmArgs s{};
+  s.d = *desc;
+  s.x = x; s.dt = dt; s.a = a; s.b = b; s.c = c; s.dskip = d; s.z = z; s.dt_bias = dt_bias; s.y = y;
+  s.s4 = desc->S % 4 == 0 && is_aligned16(a) && is_aligned16(state);
+  s.status = current_status_word(&rc);
+  if (!s.status) return rc;
+  return desc->dtype == GDR_BF16 ? launch_step<__nv_bfloat16>(s, slots, state, (cudaStream_t)stream)
+                                 : launch_step<float>(s, slots, state, (cudaStream_t)stream);
+}
+
+}  // extern "C"

@@ -55,7 +55,8 @@ typedef enum gdr_status {
   GDR_ERR_CUDA = -6,        /* a CUDA runtime call failed (message has the CUDA error string) */
   GDR_ERR_TIMEOUT = -7,     /* a bounded device-side wait expired (reported by gdr_device_status) */
   GDR_ERR_SEQLENS = -8,     /* cu_seqlens not monotone or not spanning [0, T] (gdr_device_status) */
-  GDR_ERR_UNSUPPORTED = -9  /* valid request that the chosen algorithm does not implement */
+  GDR_ERR_UNSUPPORTED = -9, /* valid request that the chosen algorithm does not implement */
+  GDR_ERR_SLOTS = -10       /* a state slot past the end of the pool (gdr_device_status) */
 } gdr_status;
 
 typedef enum gdr_dtype { GDR_F32 = 0, GDR_BF16 = 1 } gdr_dtype;
@@ -220,9 +221,126 @@ int gdr_fwd_noalloc(const gdr_desc *desc, const void *q, const void *k, const vo
                     int use_qk_l2norm, void *o, float *ht, void *stream);
 
 /*
+ * Operators around the recurrence: the norm that feeds a layer, the short
+ * causal convolution on its inputs, and the selective state space scan.  The
+ * conventions above hold, with two differences.  Token-major inputs may have
+ * rows further apart than their length: row m of x starts at x + m * ld_x
+ * elements (ld at least the row's length; a slice of a wider projection output
+ * needs no copy); every output is contiguous.  And a bad state slot is treated
+ * as padding and reported by gdr_device_status as GDR_ERR_SLOTS.
+ * Sums, statistics and states are fp32 throughout.  Results do not depend on
+ * the order in which blocks run: no atomics add anywhere.
+ */
+
+typedef enum gdr_quant { GDR_QUANT_NONE = 0, GDR_QUANT_ROW = 1, GDR_QUANT_GROUP = 2 } gdr_quant;
+#define GDR_QUANT_GROUP_SIZE 128
+
+typedef struct gdr_norm_desc {
+  int64_t M, E;             /* rows, and elements in a row */
+  int64_t ld_x, ld_res, ld_ds; /* forward: x, residual; backward: dy, s, ds */
+  int32_t dtype;            /* of x, y, dy, dx */
+  int32_t res_dtype;        /* of residual, s, ds, dres: dtype or GDR_F32 */
+  int32_t weight_dtype;     /* dtype or GDR_F32 */
+  int32_t quant;            /* gdr_quant; must be GDR_QUANT_NONE in the backward */
+  float eps;
+  int32_t flags;            /* must be 0 */
+} gdr_norm_desc;
+
+/*
+ * gdr_norm_fwd -- root-mean-square norm, with the residual's addition.
+ *   s = round(x + residual)            residual NULL: s is x, and no s is written
+ *   y = s / sqrt(mean(s^2) + eps) * weight
+ * s [M, E] (res_dtype) is the new residual stream; y is of the sum as stored,
+ * so that gdr_norm_bwd differentiates exactly what was computed.
+ *   quant NONE   y [M, E] in dtype, scale NULL.
+ *   quant ROW    y holds e4m3 bytes, scale [M] fp32 with scale = amax(y) / 448:
+ *                byte = e4m3(y * (448 / amax)), round to nearest even.
+ *   quant GROUP  the same over groups of 128 columns (the last one may be
+ *                shorter), scale [M, ceil(E / 128)].
+ * A group of zeros has scale 1; a NaN makes its scale and its bytes NaN.
+ */
+int gdr_norm_fwd(const gdr_norm_desc *desc, const void *x, const void *residual, const void *weight, void *y,
+                 float *scale, void *s, void *stream);
+
+/*
+ * gdr_norm_bwd -- gradients of L = sum(y * dy) + sum(s * ds) (ds NULL: zero).
+ * ld_x, ld_res and ld_ds are those of dy, s and ds.  dx [M, E] in dtype and
+ * dres [M, E] in res_dtype are the one gradient of s in two types; either may
+ * be NULL.  dweight [E] fp32, NULL when not wanted.
+ */
+int gdr_norm_bwd(const gdr_norm_desc *desc, const void *dy, const void *s, const void *ds, const void *weight,
+                 void *dx, void *dres, float *dweight, void *stream);
+
+typedef enum gdr_activation { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1 } gdr_activation;
+
+typedef struct gdr_conv_desc {
+  int64_t B, T, E, N;   /* N: sequences, as in gdr_desc; gdr_conv_step: slots in the pool */
+  int64_t W;            /* taps, 2 to 4 */
+  int64_t ld_x, ld_dy;
+  int32_t dtype;        /* of x, y, states, gradients of activations */
+  int32_t weight_dtype; /* of weight and bias: dtype or GDR_F32 */
+  int32_t activation;   /* gdr_activation */
+  int32_t flags;        /* must be 0 */
+} gdr_conv_desc;
+
+/*
+ * gdr_conv_fwd -- causal convolution per channel over W tokens.
+ *   y_t = act(bias + sum_j weight[:, j] x_{t - W + 1 + j})
+ * x, y [B, T, E]; weight [E, W]; bias [E] or NULL.  s0, st [N, W - 1, E] hold
+ * the W - 1 inputs before the first token and the last W - 1 inputs, earliest
+ * first; s0 NULL means zero, st NULL not wanted.  cu_seqlens as in gdr_fwd.
+ */
+int gdr_conv_fwd(const gdr_conv_desc *desc, const void *x, const void *weight, const void *bias, const void *s0,
+                 const int64_t *cu_seqlens, void *y, void *st, void *stream);
+/* Gradients of L = sum(y * dy) + sum(st * dst).  dx [B,T,E] and ds0 [N,W-1,E] (nullable) in dtype, dweight
+ * [E, W] and dbias [E] (nullable) fp32. */
+int gdr_conv_bwd(const gdr_conv_desc *desc, const void *x, const void *weight, const void *bias, const void *s0,
+                 const int64_t *cu_seqlens, const void *dy, const void *dst, void *dx, float *dweight, float *dbias,
+                 void *ds0, void *stream);
+/*
+ * gdr_conv_step -- one token for each of B rows (T must be 1).  Row r uses and
+ * updates state[slots[r]] of state [N, W - 1, E]; slots NULL means slot r.  A
+ * negative slot is a padding row: its y is zero and no state is touched.  Two
+ * rows of one call must not name the same slot.
+ */
+int gdr_conv_step(const gdr_conv_desc *desc, const void *x, const void *weight, const void *bias,
+                  const int32_t *slots, void *state, void *y, void *stream);
+
+#define GDR_SSM_SOFTPLUS 1 /* delta = softplus(dt + dt_bias), else delta = dt + dt_bias */
+
+typedef struct gdr_ssm_desc {
+  int64_t B, T, E, S, G, N; /* E channels in G groups (E % G == 0), S states each (1 to 64); N as in gdr_conv_desc */
+  int64_t ld_x, ld_dt, ld_z, ld_b, ld_c, ld_dy;
+  int32_t dtype;            /* of x, dt, z, b, c, y and their gradients */
+  int32_t flags;            /* GDR_SSM_SOFTPLUS */
+} gdr_ssm_desc;
+
+/*
+ * gdr_ssm_fwd -- the selective state space scan, per channel e of group g:
+ *   h_t = exp(delta_t a[e, :]) h_{t-1} + delta_t x_t b_t[g, :]
+ *   y_t = (c_t[g, :] . h_t + d[e] x_t) * silu(z_t)
+ * x, dt, z, y [B, T, E]; a [E, S] fp32; b, c [B, T, G, S]; d, dt_bias [E] fp32;
+ * h0, ht [N, E, S] fp32.  d, z, dt_bias, h0 may be NULL (no such term), ht NULL
+ * is not wanted.
+ */
+int gdr_ssm_fwd(const gdr_ssm_desc *desc, const void *x, const void *dt, const float *a, const void *b,
+                const void *c, const float *d, const void *z, const float *dt_bias, const float *h0,
+                const int64_t *cu_seqlens, void *y, float *ht, void *stream);
+/* Gradients of L = sum(y * dy) + sum(ht * dht).  dx, ddt, dz [B,T,E] and db, dc [B,T,G,S] in dtype; da [E,S],
+ * dd, ddt_bias [E] and dh0 [N,E,S] fp32; dd, dz, ddt_bias and dh0 may be NULL.  The forward is recomputed. */
+int gdr_ssm_bwd(const gdr_ssm_desc *desc, const void *x, const void *dt, const float *a, const void *b,
+                const void *c, const float *d, const void *z, const float *dt_bias, const float *h0,
+                const int64_t *cu_seqlens, const void *dy, const float *dht, void *dx, void *ddt, float *da,
+                void *db, void *dc, float *dd, void *dz, float *ddt_bias, float *dh0, void *stream);
+/* One token for each of B rows, states [N, E, S] fp32 updated in place; slots as in gdr_conv_step. */
+int gdr_ssm_step(const gdr_ssm_desc *desc, const void *x, const void *dt, const float *a, const void *b,
+                 const void *c, const float *d, const void *z, const float *dt_bias, const int32_t *slots,
+                 float *state, void *y, void *stream);
+
+/*
  * gdr_device_status -- synchronizes `stream`, then returns (and, if `clear`,
  * resets) the library's device-side status word for the current device:
- * GDR_OK, GDR_ERR_SEQLENS or GDR_ERR_TIMEOUT.  Also returns GDR_ERR_CUDA if
+ * GDR_OK, GDR_ERR_SEQLENS, GDR_ERR_SLOTS or GDR_ERR_TIMEOUT.  Also returns GDR_ERR_CUDA if
  * the stream itself reports an error.
  */
 int gdr_device_status(void *stream, int clear);
