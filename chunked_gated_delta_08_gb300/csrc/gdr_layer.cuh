@@ -103,6 +103,43 @@ __device__ __forceinline__ bool seqlens_ok(const int64_t *cu, int64_t N, int64_t
 
 __device__ __forceinline__ bool seqlens_ok(const SeqCheck &s) { return seqlens_ok(s.cu, s.N, s.T, s.status); }
 
+typedef unsigned long long f2;  // two fp32 values for the packed instructions
+__device__ __forceinline__ f2 f2_pack(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void f2_split(f2 v, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ f2 f2_ex2(f2 v) {
+  float lo, hi;
+  f2_split(v, lo, hi);
+  return f2_pack(ex2(lo), ex2(hi));
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
 // The sequence of flat token t (the last n with first token <= t: empty ones
 // are passed over).  Dense layout: sequences of T tokens each.
 __device__ __forceinline__ int64_t seq_of_token(const int64_t *cu, int64_t N, int64_t T, int64_t t) {

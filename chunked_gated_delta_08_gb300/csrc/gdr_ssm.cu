@@ -20,7 +20,7 @@ namespace {
 template <int SL>
 struct __align__(16) FwdShared {
   float delta[kTile][Place<SL>::CB], x[kTile][Place<SL>::CB], gate[kTile][Place<SL>::CB];
-  float b[kTile * Place<SL>::SP], c[kTile * Place<SL>::SP];
+  float2 b[kTile * Place<SL>::SP], c[kTile * Place<SL>::SP];
   Borders<kTile> bd;
 };
 
@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_fwd_kernel(SsmArgs a) {
   if (!seqlens_ok(a.cu, a.d.N, a.M, a.status)) return;
   const P p(a);
   if (MAIN && p.chunk == 0) copy_empty_states<SL>(a, p, a.h0, a.ht);
-  f2 A[4][2], h[4][2];
+  States A, h;
   load_a<SL>(a, p, A);
   load_chunk<SL>(a, p, MAIN ? a.hloc : nullptr, p.chunk, h);
   const int64_t begin = p.chunk * a.L, end = begin + a.L < a.M ? begin + a.L : a.M;
@@ -41,13 +41,36 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_fwd_kernel(SsmArgs a) {
   const int64_t e_mine = p.e0 + p.col + mine;
   const bool owner = p.sl < 4 && e_mine < p.e_end;
   const float skip = MAIN && a.dskip && owner ? a.dskip[e_mine] : 0.f;
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  T *y = static_cast<T *>(a.y) + e_mine;
+  f2 sum[2] = {0, 0};
   bool started = false;  // a sequence starts in this chunk
+
+  auto token = [&](int64_t t0, int t) {
+    const Pairs delta(&sm.delta[t][p.col]);
+    advance(h, A, delta, Pairs(&sm.x[t][p.col]), Twice(&sm.b[t * P::SP + p.sl * 4]));
+    if (MAIN) {
+      const Twice c(&sm.c[t * P::SP + p.sl * 4]);
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        f2 o = f2_mul(c.v[0], h[i][0]);
+#pragma unroll
+        for (int s = 1; s < 4; ++s) o = f2_fma(c.v[s], h[i][s], o);
+        f2_split(o, v[2 * i], v[2 * i + 1]);
+      }
+      const float o = sum_over_states<SL>(v, p.sl);
+      if (owner)
+        y[(t0 + t) * a.d.E] = from_f32<T>(fmaf(skip, sm.x[t][p.col + mine], o) * sm.gate[t][p.col + mine]);
+    } else {
+      sum[0] = f2_add(sum[0], delta.v[0]);
+      sum[1] = f2_add(sum[1], delta.v[1]);
+    }
+  };
 
   for (int64_t t0 = begin; t0 < end; t0 += kTile) {
     const int nt = end - t0 < kTile ? (int)(end - t0) : kTile;
     __syncthreads();  // the previous tile is consumed
-    stage_borders(a, t0, nt, sm.bd);
+    const bool borders = stage_borders(a, t0, nt, sm.bd);
     for_tile<kTile, SL, VEC>(p, nt, [&](int t, int c, bool in) {
       const int64_t e = p.e0 + c;
       float xv[VEC] = {}, dv[VEC] = {}, zv[VEC] = {};
@@ -59,56 +82,38 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_fwd_kernel(SsmArgs a) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         const float raw = dv[i] + (a.dt_bias && in ? a.dt_bias[e + i] : 0.f);
-        sm.delta[t][c + i] = in ? ssm_delta(raw, a.d.flags & GDR_SSM_SOFTPLUS) : 0.f;
-        sm.x[t][c + i] = xv[i];
-        if (MAIN) sm.gate[t][c + i] = a.z ? zv[i] * sigmoid_fast(zv[i]) : 1.f;
+        dv[i] = in ? ssm_delta(raw, a.d.flags & GDR_SSM_SOFTPLUS) : 0.f;
+        if (MAIN) zv[i] = a.z ? zv[i] * sigmoid_fast(zv[i]) : 1.f;
       }
+      store_vec<VEC>(&sm.delta[t][c], dv);
+      store_vec<VEC>(&sm.x[t][c], xv);
+      if (MAIN) store_vec<VEC>(&sm.gate[t][c], zv);
     });
     stage_states<T, SL, kTile>(a, p, a.b, a.d.ld_b, t0, nt, sm.b);
     if (MAIN) stage_states<T, SL, kTile>(a, p, a.c, a.d.ld_c, t0, nt, sm.c);
-    __syncthreads();
-#pragma unroll 2
-    for (int t = 0; t < nt; ++t) {
-      if (sm.bd.first[t] >= 0) {
-        load_h0<SL>(a, p, a.h0, sm.bd.first[t], h);
-        started = true;
-      }
-      const float4 d4 = *reinterpret_cast<const float4 *>(&sm.delta[t][p.col]);
-      const float4 x4 = *reinterpret_cast<const float4 *>(&sm.x[t][p.col]);
-      const ulonglong2 b4 = *reinterpret_cast<const ulonglong2 *>(&sm.b[t * P::SP + p.sl * 4]);
-      ulonglong2 c4;
-      if (MAIN) c4 = *reinterpret_cast<const ulonglong2 *>(&sm.c[t * P::SP + p.sl * 4]);
-      const float dl[4] = {d4.x, d4.y, d4.z, d4.w}, xs[4] = {x4.x, x4.y, x4.z, x4.w};
-      float v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const f2 dd = f2_pack(dl[j], dl[j]);
-        const float u = dl[j] * xs[j];
-        const f2 uu = f2_pack(u, u);
-        h[j][0] = f2_fma(f2_ex2(f2_mul(A[j][0], dd)), h[j][0], f2_mul(uu, b4.x));
-        h[j][1] = f2_fma(f2_ex2(f2_mul(A[j][1], dd)), h[j][1], f2_mul(uu, b4.y));
-        if (MAIN) {
-          float lo, hi;
-          f2_split(f2_fma(c4.y, h[j][1], f2_mul(c4.x, h[j][0])), lo, hi);
-          v[j] = lo + hi;
-        } else {
-          sum[j] += dl[j];
+    if (!__syncthreads_or(borders) && nt == kTile) {
+#pragma unroll 4
+      for (int t = 0; t < kTile; ++t) token(t0, t);
+    } else {
+#pragma unroll 1
+      for (int t = 0; t < nt; ++t) {
+        if (sm.bd.first[t] >= 0) {
+          load_h0<SL>(a, p, a.h0, sm.bd.first[t], h);
+          started = true;
         }
-      }
-      if (MAIN) {
-        const float y = sum_over_states<SL>(v, p.sl);
-        if (owner)
-          static_cast<T *>(a.y)[(t0 + t) * a.d.E + e_mine] =
-              from_f32<T>(fmaf(skip, sm.x[t][p.col + mine], y) * sm.gate[t][p.col + mine]);
-        if (a.ht && sm.bd.last[t] >= 0) store_final<SL>(a, p, a.ht, sm.bd.last[t], h);
+        token(t0, t);
+        if (MAIN && a.ht && sm.bd.last[t] >= 0) store_final<SL>(a, p, a.ht, sm.bd.last[t], h);
       }
     }
   }
   if (!MAIN) {
     store_chunk<SL>(a, p, a.hloc, p.chunk, h);
     if (owner) {
-      const float s = mine == 0 ? sum[0] : mine == 1 ? sum[1] : mine == 2 ? sum[2] : sum[3];
-      a.sumd[p.chunk * a.d.E + e_mine] = started ? CUDART_NAN_F : s;  // NaN: nothing passes through
+      float s[4];
+      f2_split(sum[0], s[0], s[1]);
+      f2_split(sum[1], s[2], s[3]);
+      const float mine_sum = mine == 0 ? s[0] : mine == 1 ? s[1] : mine == 2 ? s[2] : s[3];
+      a.sumd[p.chunk * a.d.E + e_mine] = started ? CUDART_NAN_F : mine_sum;  // NaN: nothing passes through
     }
   }
 }
@@ -142,59 +147,83 @@ __global__ void __launch_bounds__(128) ssm_carry_kernel(SsmArgs a, int SP) {
   }
 }
 
-// One token per row: states are read and written once, four to a thread, with
-// the lanes of a row on consecutive 16-byte groups.  The bound is HBM.
+// One token per row.  A block takes four rows and 256 / SL channels; SL lanes
+// share a channel, four states each, so that a warp's states are consecutive
+// 16-byte groups, and the four rows' states are in flight together.  Of a
+// channel's first four lanes, lane k works out delta, delta x and the gate of
+// row k for all (they cost more than the four recurrences of a lane), and
+// finishes that row's output.  The bound is HBM: each state is read and written
+// once.
+constexpr int kStepRows = 4;
 template <typename T, int SL>
 __global__ void __launch_bounds__(256) ssm_step_kernel(SsmArgs a, const int32_t *slots, float *state, unsigned tiles) {
-  const int64_t r = blockIdx.x / tiles;
+  const int64_t r0 = (int64_t)(blockIdx.x / tiles) * kStepRows;
   const int64_t i = (int64_t)(blockIdx.x % tiles) * 256 + threadIdx.x;
   const int64_t e = i / SL;
-  const int s0 = (int)(i % SL) * 4, S = (int)a.d.S;
-  int64_t slot = slots ? slots[r] : r;
-  if (slot >= a.d.N) {
-    if (threadIdx.x == 0) raise_status(a.status, GDR_ERR_SLOTS);
-    slot = -1;
-  }
+  const int sl = (int)(i % SL), s0 = sl * 4, S = (int)a.d.S;
   const bool in = e < a.d.E;
-  T *y = static_cast<T *>(a.y) + r * a.d.E + e;
-  if (slot < 0) {  // the whole block
-    if (in && s0 == 0) *y = from_f32<T>(0.f);
-    return;
-  }
-  float h[4] = {}, A[4] = {}, b[4] = {}, c[4] = {};
-  float x = 0.f, delta = 0.f, out = 0.f;
-  float *row = state + (slot * a.d.E + e) * S;
-  if (in) {
-    load_states(row, s0, S, a.s4, h);
-    load_states(a.a + e * S, s0, S, a.s4, A);
-    const int64_t g = e / (a.d.E / a.d.G);
-    const T *bp = static_cast<const T *>(a.b) + r * a.d.ld_b + g * S;
-    const T *cp = static_cast<const T *>(a.c) + r * a.d.ld_c + g * S;
+  float h[kStepRows][4], b[kStepRows][4], c[kStepRows][4], A[4] = {};
+  float *row[kStepRows];
+  const int64_t g = in ? e / (a.d.E / a.d.G) : 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (s0 + k < S) {
-        b[k] = to_f32(bp[s0 + k]);
-        c[k] = to_f32(cp[s0 + k]);
+  for (int k = 0; k < kStepRows; ++k) {
+    const int64_t r = r0 + k;
+    int64_t slot = -1;
+    if (r < a.d.B) {
+      slot = slots ? slots[r] : r;
+      if (slot >= a.d.N) {
+        if (threadIdx.x == 0) raise_status(a.status, GDR_ERR_SLOTS);
+        slot = -1;
       }
+    }
+    row[k] = slot >= 0 && in ? state + (slot * a.d.E + e) * S : nullptr;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) h[k][q] = b[k][q] = c[k][q] = 0.f;
+    if (row[k]) {
+      load_states(row[k], s0, S, a.s4, h[k]);
+      const T *bp = static_cast<const T *>(a.b) + r * a.d.ld_b + g * S;
+      const T *cp = static_cast<const T *>(a.c) + r * a.d.ld_c + g * S;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (s0 + q < S) {
+          b[k][q] = to_f32(bp[s0 + q]);
+          c[k][q] = to_f32(cp[s0 + q]);
+        }
+    }
+  }
+  const int64_t r = r0 + sl;  // the row this lane prepares and finishes
+  const bool owner = sl < kStepRows && in && r < a.d.B;
+  float x = 0.f, delta = 0.f, gate = 1.f, skip = 0.f;
+  if (owner) {
     x = to_f32(static_cast<const T *>(a.x)[r * a.d.ld_x + e]);
     delta = ssm_delta(to_f32(static_cast<const T *>(a.dt)[r * a.d.ld_dt + e]) + (a.dt_bias ? a.dt_bias[e] : 0.f),
                       a.d.flags & GDR_SSM_SOFTPLUS);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      h[k] = fmaf(ex2(delta * (A[k] * kLog2e)), h[k], delta * x * b[k]);
-      out = fmaf(c[k], h[k], out);
-    }
-    store_states(row, s0, S, a.s4, h);
-  }
-#pragma unroll
-  for (int o = SL / 2; o > 0; o >>= 1) out += __shfl_xor_sync(0xffffffffu, out, o);
-  if (in && s0 == 0) {
-    out = fmaf(a.dskip ? a.dskip[e] : 0.f, x, out);
     if (a.z) {
       const float z = to_f32(static_cast<const T *>(a.z)[r * a.d.ld_z + e]);
-      out *= z * sigmoid_fast(z);
+      gate = z * sigmoid_fast(z);
     }
-    *y = from_f32<T>(out);
+    if (a.dskip) skip = a.dskip[e];
+  }
+  if (in) load_states(a.a + e * S, s0, S, a.s4, A);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) A[q] *= kLog2e;
+  const float u = delta * x;
+  float out[kStepRows];
+#pragma unroll
+  for (int k = 0; k < kStepRows; ++k) {
+    const float dk = __shfl_sync(0xffffffffu, delta, k, SL), uk = __shfl_sync(0xffffffffu, u, k, SL);
+    out[k] = 0.f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      h[k][q] = fmaf(ex2(dk * A[q]), h[k][q], uk * b[k][q]);
+      out[k] = fmaf(c[k][q], h[k][q], out[k]);
+    }
+    if (row[k]) store_states(row[k], s0, S, a.s4, h[k]);
+  }
+  const float y = sum_over_states<SL>(out, sl);
+  if (owner) {
+    const float *mine = sl == 0 ? row[0] : sl == 1 ? row[1] : sl == 2 ? row[2] : row[3];
+    static_cast<T *>(a.y)[r * a.d.E + e] = from_f32<T>(mine ? fmaf(skip, x, y) * gate : 0.f);
   }
 }
 
@@ -224,15 +253,14 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 template <typename T>
 int launch_step(const SsmArgs &a, const int32_t *slots, float *state, cudaStream_t st) {
   auto go = [&](auto SL) {
-    const int64_t tiles = cdiv(a.d.E * decltype(SL)::value, 256);
-    if (tiles * a.d.B > 0x7fffffff) return set_error(GDR_ERR_SHAPE, "too many rows for one launch");
-    ssm_step_kernel<T, decltype(SL)::value><<<(unsigned)(tiles * a.d.B), 256, 0, st>>>(a, slots, state, (unsigned)tiles);
+    const int64_t tiles = cdiv(a.d.E * decltype(SL)::value, 256), blocks = tiles * cdiv(a.d.B, kStepRows);
+    if (blocks > 0x7fffffff) return set_error(GDR_ERR_SHAPE, "too many rows for one launch");
+    ssm_step_kernel<T, decltype(SL)::value><<<(unsigned)blocks, 256, 0, st>>>(a, slots, state, (unsigned)tiles);
     return launched("ssm_step_kernel");
   };
-  if (a.d.S <= 4) return go(std::integral_constant<int, 1>{});
-  if (a.d.S <= 8) return go(std::integral_constant<int, 2>{});
-  if (a.d.S <= 16) return go(std::integral_constant<int, 4>{});
-  if (a.d.S <= 32) return go(std::integral_constant<int, 8>{});
+  const int sl = lanes_of(a.d.S);
+  if (sl == 4) return go(std::integral_constant<int, 4>{});
+  if (sl == 8) return go(std::integral_constant<int, 8>{});
   return go(std::integral_constant<int, 16>{});
 }
 

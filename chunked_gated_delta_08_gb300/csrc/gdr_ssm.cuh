@@ -11,7 +11,10 @@
 // inputs, four b and four c from shared memory, 16-byte loads that broadcast,
 // for 16 states; sums over states cross SL lanes, sums over channels cross the
 // others.  One channel per thread would need no exchange over states but eight
-// 16-byte loads of b and c for the same work.
+// 16-byte loads of b and c for the same work.  The packed fp32 instructions take
+// channels two by two: delta, x and the gradients come from shared memory as
+// pairs, and b and c are staged twice over, (b, b), so that no pair is ever
+// assembled in the loop.
 //
 // Time.  The flat token axis is cut into chunks of L tokens.  A sequence's first
 // token replaces the state by h0, wherever in a chunk it falls, so chunks need
@@ -48,47 +51,31 @@ struct SsmArgs {
 constexpr int kSsmThreads = 128;
 constexpr int kTile = 16;  // tokens staged together
 
-typedef unsigned long long f2;  // two fp32 values for the packed instructions
-__device__ __forceinline__ f2 f2_pack(float lo, float hi) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void f2_split(f2 v, float &lo, float &hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ f2 f2_ex2(f2 v) {
-  float lo, hi;
-  f2_split(v, lo, hi);
-  return f2_pack(ex2(lo), ex2(hi));
-}
-
-constexpr float kLog2e = 1.4426950408889634f;
-
-// delta from the raw dt (bias added): softplus, its large arguments returned as they are.
-__device__ __forceinline__ float ssm_delta(float v, int softplus) {
-  if (!softplus) return v;
-  return v > 20.f ? v : log1pf(expf(v));
+// delta from the raw dt (bias added): softplus(v) = max(v, 0) + log1p(u), u = e^-|v|,
+// with log1p(u) = 2 atanh(r), r = u / (2 + u) <= 1/3, by its series in r^2.  Nine
+// terms leave 1e-9 of the value; log(1 + u) would lose a small u against the 1, and
+// small deltas are the ones a state remembers longest.  `slope`: ddelta/dv.
+__device__ __forceinline__ float ssm_delta(float v, int softplus, float *slope = nullptr) {
+  if (!softplus) {
+    if (slope) *slope = 1.f;
+    return v;
+  }
+  const float u = ex2(-fabsf(v) * kLog2e);
+  const float r = __fdividef(u, 2.f + u), q = r * r;
+  float w = 1.f / 17.f;
+  w = fmaf(w, q, 1.f / 15.f);
+  w = fmaf(w, q, 1.f / 13.f);
+  w = fmaf(w, q, 1.f / 11.f);
+  w = fmaf(w, q, 1.f / 9.f);
+  w = fmaf(w, q, 1.f / 7.f);
+  w = fmaf(w, q, 1.f / 5.f);
+  w = fmaf(w, q, 1.f / 3.f);
+  w = fmaf(w, q, 1.f);
+  if (slope) {
+    const float k = __fdividef(1.f, 1.f + u);
+    *slope = v >= 0.f ? k : u * k;
+  }
+  return fmaf(r + r, w, fmaxf(v, 0.f));  // a NaN comes through u
 }
 
 // Four states from s0 of a row of S (zero past its end).
@@ -160,14 +147,18 @@ template <int TT>
 struct Borders {
   int first[TT], last[TT];
 };
+// True in threads whose token is a border.
 template <int TT>
-__device__ __forceinline__ void stage_borders(const SsmArgs &a, int64_t t0, int nt, Borders<TT> &bd) {
+__device__ __forceinline__ bool stage_borders(const SsmArgs &a, int64_t t0, int nt, Borders<TT> &bd) {
+  bool border = false;
   if (threadIdx.x < nt) {
     const int64_t t = t0 + threadIdx.x, n = seq_of_token(a.cu, a.d.N, a.d.T, t);
     const SeqRange r = seq_range(a.cu, n, a.d.T);
     bd.first[threadIdx.x] = t == r.bos ? (int)n : -1;
     bd.last[threadIdx.x] = t + 1 == r.eos ? (int)n : -1;
+    border = t == r.bos || t + 1 == r.eos;
   }
+  return border;
 }
 
 // Runs f(t, column, in range) over a tile of [TT, CB] elements, VEC columns at a time.
@@ -183,80 +174,117 @@ __device__ __forceinline__ void for_tile(const Place<SL> &p, int nt, F &&f) {
   }
 }
 
-// b or c of a tile as fp32 [TT][SP], zero past S and past the tokens.
+// b or c of a tile as fp32 [TT][SP], each twice, zero past S and past the tokens.
 template <typename T, int SL, int TT>
 __device__ __forceinline__ void stage_states(const SsmArgs &a, const Place<SL> &p, const void *src, int64_t ld,
-                                             int64_t t0, int nt, float *dst) {
+                                             int64_t t0, int nt, float2 *dst) {
   constexpr int SP = Place<SL>::SP;
   const T *row = static_cast<const T *>(src) + p.g * a.d.S;
 #pragma unroll
   for (int i0 = 0; i0 < TT * SP; i0 += kSsmThreads) {
     const int i = i0 + threadIdx.x, t = i / SP, s = i % SP;
-    dst[i] = t < nt && s < a.d.S ? to_f32(row[(t0 + t) * ld + s]) : 0.f;
+    const float v = t < nt && s < a.d.S ? to_f32(row[(t0 + t) * ld + s]) : 0.f;
+    dst[i] = make_float2(v, v);
   }
 }
 
-// The state h0 of sequence n (zero where there is none) for a thread's channels.
-template <int SL>
-__device__ __forceinline__ void load_h0(const SsmArgs &a, const Place<SL> &p, const float *h0, int64_t n,
-                                        f2 (&h)[4][2]) {
+// A thread's 16 states: pair i holds channels 2 i and 2 i + 1, for each of the
+// four states.
+typedef f2 States[2][4];
+
+template <int SL, typename F>
+__device__ __forceinline__ void read_states(const Place<SL> &p, States &h, F &&row) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int64_t e = p.e0 + p.col + j;
-    float v[4] = {};
-    if (h0 && e < p.e_end) load_states(h0 + (n * a.d.E + e) * a.d.S, p.sl * 4, (int)a.d.S, a.s4, v);
-    h[j][0] = f2_pack(v[0], v[1]);
-    h[j][1] = f2_pack(v[2], v[3]);
+  for (int i = 0; i < 2; ++i) {
+    float v[4] = {}, w[4] = {};
+    const int64_t e = p.e0 + p.col + 2 * i;
+    if (e < p.e_end) row(e, v);
+    if (e + 1 < p.e_end) row(e + 1, w);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) h[i][s] = f2_pack(v[s], w[s]);
   }
+}
+template <int SL, typename F>
+__device__ __forceinline__ void write_states(const Place<SL> &p, const States &h, F &&row) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float v[4], w[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) f2_split(h[i][s], v[s], w[s]);
+    const int64_t e = p.e0 + p.col + 2 * i;
+    if (e < p.e_end) row(e, v);
+    if (e + 1 < p.e_end) row(e + 1, w);
+  }
+}
+// The state h0 of sequence n (zero where there is none).
+template <int SL>
+__device__ __forceinline__ void load_h0(const SsmArgs &a, const Place<SL> &p, const float *h0, int64_t n, States &h) {
+  read_states(p, h, [&](int64_t e, float (&v)[4]) {
+    if (h0) load_states(h0 + (n * a.d.E + e) * a.d.S, p.sl * 4, (int)a.d.S, a.s4, v);
+  });
 }
 template <int SL>
 __device__ __forceinline__ void store_final(const SsmArgs &a, const Place<SL> &p, float *ht, int64_t n,
-                                            const f2 (&h)[4][2]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int64_t e = p.e0 + p.col + j;
-    float v[4];
-    f2_split(h[j][0], v[0], v[1]);
-    f2_split(h[j][1], v[2], v[3]);
-    if (e < p.e_end) store_states(ht + (n * a.d.E + e) * a.d.S, p.sl * 4, (int)a.d.S, a.s4, v);
-  }
+                                            const States &h) {
+  write_states(p, h, [&](int64_t e, const float (&v)[4]) {
+    store_states(ht + (n * a.d.E + e) * a.d.S, p.sl * 4, (int)a.d.S, a.s4, v);
+  });
 }
 // Chunk states [chunks, E, SP]: always whole 16-byte groups.
 template <int SL>
 __device__ __forceinline__ void load_chunk(const SsmArgs &a, const Place<SL> &p, const float *src, int64_t chunk,
-                                           f2 (&h)[4][2]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int64_t e = p.e0 + p.col + j;
-    float v[4] = {};
-    if (src && e < p.e_end) load4(src + (chunk * a.d.E + e) * Place<SL>::SP + p.sl * 4, v);
-    h[j][0] = f2_pack(v[0], v[1]);
-    h[j][1] = f2_pack(v[2], v[3]);
-  }
+                                           States &h) {
+  read_states(p, h, [&](int64_t e, float (&v)[4]) {
+    if (src) load4(src + (chunk * a.d.E + e) * Place<SL>::SP + p.sl * 4, v);
+  });
 }
 template <int SL>
 __device__ __forceinline__ void store_chunk(const SsmArgs &a, const Place<SL> &p, float *dst, int64_t chunk,
-                                            const f2 (&h)[4][2]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int64_t e = p.e0 + p.col + j;
-    float v[4];
-    f2_split(h[j][0], v[0], v[1]);
-    f2_split(h[j][1], v[2], v[3]);
-    if (e < p.e_end) store4(dst + (chunk * a.d.E + e) * Place<SL>::SP + p.sl * 4, v);
-  }
+                                            const States &h) {
+  write_states(p, h, [&](int64_t e, const float (&v)[4]) {
+    store4(dst + (chunk * a.d.E + e) * Place<SL>::SP + p.sl * 4, v);
+  });
 }
 
 // a[e, s] log2(e) of a thread's channels and states (zero outside: such states stay zero).
 template <int SL>
-__device__ __forceinline__ void load_a(const SsmArgs &a, const Place<SL> &p, f2 (&A)[4][2]) {
+__device__ __forceinline__ void load_a(const SsmArgs &a, const Place<SL> &p, States &A) {
+  read_states(p, A, [&](int64_t e, float (&v)[4]) {
+    load_states(a.a + e * a.d.S, p.sl * 4, (int)a.d.S, a.s4, v);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int64_t e = p.e0 + p.col + j;
-    float v[4] = {};
-    if (e < p.e_end) load_states(a.a + e * a.d.S, p.sl * 4, (int)a.d.S, a.s4, v);
-    A[j][0] = f2_pack(v[0] * kLog2e, v[1] * kLog2e);
-    A[j][1] = f2_pack(v[2] * kLog2e, v[3] * kLog2e);
+    for (int s = 0; s < 4; ++s) v[s] *= kLog2e;
+  });
+}
+
+// Four values of a staged row: the thread's channels, as two pairs.
+struct Pairs {
+  f2 v[2];
+  __device__ __forceinline__ explicit Pairs(const float *row) {
+    const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(row);
+    v[0] = u.x;
+    v[1] = u.y;
+  }
+};
+// Four values of a staged row of b or c: the thread's states, each twice.
+struct Twice {
+  f2 v[4];
+  __device__ __forceinline__ explicit Twice(const float2 *row) {
+    const ulonglong2 *u = reinterpret_cast<const ulonglong2 *>(row);
+    v[0] = u[0].x;
+    v[1] = u[0].y;
+    v[2] = u[1].x;
+    v[3] = u[1].y;
+  }
+};
+
+// One token of the recurrence.
+__device__ __forceinline__ void advance(States &h, const States &A, const Pairs &delta, const Pairs &x,
+                                        const Twice &b) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const f2 u = f2_mul(delta.v[i], x.v[i]);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) h[i][s] = f2_fma(f2_ex2(f2_mul(A[i][s], delta.v[i])), h[i][s], f2_mul(u, b.v[s]));
   }
 }
 
@@ -267,7 +295,7 @@ __device__ __forceinline__ void copy_empty_states(const SsmArgs &a, const Place<
   for (int64_t n = 0; n < a.d.N; ++n) {
     const SeqRange r = seq_range(a.cu, n, a.d.T);
     if (r.eos > r.bos) continue;
-    f2 h[4][2];
+    States h;
     load_h0<SL>(a, p, from, n, h);
     store_final<SL>(a, p, to, n, h);
   }

@@ -31,15 +31,10 @@ constexpr int kMaxL = 64;    // tokens of a chunk
 constexpr int kSubs = kMaxL / kSub;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// raw dt of a tile becomes delta; also its derivative (into dsp, when given).
-__device__ __forceinline__ float delta_grad(float raw, int softplus) {
-  return softplus ? sigmoid_fast(raw) : 1.f;
-}
-
 template <int SL>
 struct __align__(16) LocalShared {
   float delta[kTile][Place<SL>::CB], x[kTile][Place<SL>::CB], up[kTile][Place<SL>::CB];
-  float b[kTile * Place<SL>::SP], c[kTile * Place<SL>::SP];
+  float2 b[kTile * Place<SL>::SP], c[kTile * Place<SL>::SP];
   Borders<kTile> bd;
 };
 
@@ -58,10 +53,12 @@ __device__ __forceinline__ void stage_local(const SsmArgs &a, const Place<SL> &p
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
       const float raw = dv[i] + (a.dt_bias && in ? a.dt_bias[e + i] : 0.f);
-      sm.delta[t][c + i] = in ? ssm_delta(raw, a.d.flags & GDR_SSM_SOFTPLUS) : 0.f;
-      sm.x[t][c + i] = xv[i];
-      sm.up[t][c + i] = gv[i] * (a.z ? zv[i] * sigmoid_fast(zv[i]) : 1.f);
+      dv[i] = in ? ssm_delta(raw, a.d.flags & GDR_SSM_SOFTPLUS) : 0.f;
+      gv[i] *= a.z ? zv[i] * sigmoid_fast(zv[i]) : 1.f;
     }
+    store_vec<VEC>(&sm.delta[t][c], dv);
+    store_vec<VEC>(&sm.x[t][c], xv);
+    store_vec<VEC>(&sm.up[t][c], gv);
   });
 }
 
@@ -71,64 +68,65 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_bwd_local_kernel(SsmArgs a) {
   __shared__ LocalShared<SL> sm;
   if (!seqlens_ok(a.cu, a.d.N, a.M, a.status)) return;
   const P p(a);
-  f2 A[4][2], h[4][2], g[4][2], pass[4][2];
+  States A, h, g, pass;  // pass: product of the decays since the chunk began; zero once a sequence started
   load_a<SL>(a, p, A);
-  const f2 zero = f2_pack(0.f, 0.f), one = f2_pack(1.f, 1.f);
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      h[j][i] = g[j][i] = zero;
-      pass[j][i] = one;  // product of the decays since the chunk began; zero once a sequence started
+    for (int s = 0; s < 4; ++s) {
+      h[i][s] = g[i][s] = 0;
+      pass[i][s] = f2_pack(1.f, 1.f);
     }
   const int64_t begin = p.chunk * a.L, end = begin + a.L < a.M ? begin + a.L : a.M;
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  f2 sum[2] = {0, 0};
   bool started = false;
+  auto token = [&](int t) {
+    const Pairs delta(&sm.delta[t][p.col]), x(&sm.x[t][p.col]), up(&sm.up[t][p.col]);
+    const Twice b(&sm.b[t * P::SP + p.sl * 4]), c(&sm.c[t * P::SP + p.sl * 4]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const f2 u = f2_mul(delta.v[i], x.v[i]);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const f2 at = f2_ex2(f2_mul(A[i][s], delta.v[i]));
+        h[i][s] = f2_fma(at, h[i][s], f2_mul(u, b.v[s]));
+        pass[i][s] = f2_mul(pass[i][s], at);
+        g[i][s] = f2_fma(pass[i][s], f2_mul(up.v[i], c.v[s]), g[i][s]);
+      }
+      sum[i] = f2_add(sum[i], delta.v[i]);
+    }
+  };
   for (int64_t t0 = begin; t0 < end; t0 += kTile) {
     const int nt = end - t0 < kTile ? (int)(end - t0) : kTile;
     __syncthreads();
-    stage_borders(a, t0, nt, sm.bd);
+    const bool borders = stage_borders(a, t0, nt, sm.bd);
     if (a.vec) stage_local<T, SL, 8>(a, p, t0, nt, sm);
     else stage_local<T, SL, 1>(a, p, t0, nt, sm);
     stage_states<T, SL, kTile>(a, p, a.b, a.d.ld_b, t0, nt, sm.b);
     stage_states<T, SL, kTile>(a, p, a.c, a.d.ld_c, t0, nt, sm.c);
-    __syncthreads();
-#pragma unroll 2
-    for (int t = 0; t < nt; ++t) {
-      if (sm.bd.first[t] >= 0) {
-        load_h0<SL>(a, p, a.h0, sm.bd.first[t], h);
-        started = true;
+    if (!__syncthreads_or(borders) && nt == kTile) {
+#pragma unroll 4
+      for (int t = 0; t < kTile; ++t) token(t);
+    } else {
+#pragma unroll 1
+      for (int t = 0; t < nt; ++t) {
+        if (sm.bd.first[t] >= 0) {
+          load_h0<SL>(a, p, a.h0, sm.bd.first[t], h);
+          started = true;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) pass[j][0] = pass[j][1] = zero;
-      }
-      const float4 d4 = *reinterpret_cast<const float4 *>(&sm.delta[t][p.col]);
-      const float4 x4 = *reinterpret_cast<const float4 *>(&sm.x[t][p.col]);
-      const float4 u4 = *reinterpret_cast<const float4 *>(&sm.up[t][p.col]);
-      const ulonglong2 b4 = *reinterpret_cast<const ulonglong2 *>(&sm.b[t * P::SP + p.sl * 4]);
-      const ulonglong2 c4 = *reinterpret_cast<const ulonglong2 *>(&sm.c[t * P::SP + p.sl * 4]);
-      const float dl[4] = {d4.x, d4.y, d4.z, d4.w}, xs[4] = {x4.x, x4.y, x4.z, x4.w},
-                  us[4] = {u4.x, u4.y, u4.z, u4.w};
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const f2 dd = f2_pack(dl[j], dl[j]), up = f2_pack(us[j], us[j]);
-        const float u = dl[j] * xs[j];
-        const f2 uu = f2_pack(u, u);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const f2 at = f2_ex2(f2_mul(A[j][i], dd));
-          h[j][i] = f2_fma(at, h[j][i], f2_mul(uu, i ? b4.y : b4.x));
-          pass[j][i] = f2_mul(pass[j][i], at);
-          g[j][i] = f2_fma(pass[j][i], f2_mul(up, i ? c4.y : c4.x), g[j][i]);
+            for (int s = 0; s < 4; ++s) pass[i][s] = 0;
         }
-        sum[j] += dl[j];
-      }
-      if (a.dht && !started && sm.bd.last[t] >= 0) {
-        f2 dh[4][2];
-        load_h0<SL>(a, p, a.dht, sm.bd.last[t], dh);
+        token(t);
+        if (a.dht && !started && sm.bd.last[t] >= 0) {
+          States dh;
+          load_h0<SL>(a, p, a.dht, sm.bd.last[t], dh);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) g[j][i] = f2_fma(pass[j][i], dh[j][i], g[j][i]);
+            for (int s = 0; s < 4; ++s) g[i][s] = f2_fma(pass[i][s], dh[i][s], g[i][s]);
+        }
       }
     }
   }
@@ -137,8 +135,11 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_bwd_local_kernel(SsmArgs a) {
   const int mine = p.sl & 3;
   const int64_t e_mine = p.e0 + p.col + mine;
   if (p.sl < 4 && e_mine < p.e_end) {
-    const float s = mine == 0 ? sum[0] : mine == 1 ? sum[1] : mine == 2 ? sum[2] : sum[3];
-    a.sumd[p.chunk * a.d.E + e_mine] = started ? CUDART_NAN_F : s;  // NaN: nothing passes through
+    float s[4];
+    f2_split(sum[0], s[0], s[1]);
+    f2_split(sum[1], s[2], s[3]);
+    const float mine_sum = mine == 0 ? s[0] : mine == 1 ? s[1] : mine == 2 ? s[2] : s[3];
+    a.sumd[p.chunk * a.d.E + e_mine] = started ? CUDART_NAN_F : mine_sum;  // NaN: nothing passes through
   }
 }
 
@@ -177,15 +178,15 @@ __global__ void __launch_bounds__(128) ssm_bwd_carry_kernel(SsmArgs a, int SP) {
 template <int SL>
 struct MainShared {
   using P = Place<SL>;
-  float4 ckpt[kSubs][4][kSsmThreads];  // a thread's states before each run of kSub tokens
+  ulonglong2 ckpt[kSubs][4][kSsmThreads];  // a thread's states before each run of kSub tokens
   union {
     struct {
       float delta[kTile][P::CB], x[kTile][P::CB];
-      float b[kTile * P::SP];
+      float2 b[kTile * P::SP];
     } f;
     struct {
-      float delta[kSub][P::CB], x[kSub][P::CB], up[kSub][P::CB], dsp[kSub][P::CB], zf[kSub][P::CB];
-      float b[kSub * P::SP], c[kSub * P::SP];
+      float delta[kSub][P::CB], x[kSub][P::CB], up[kSub][P::CB], slope[kSub][P::CB], zf[kSub][P::CB];
+      float2 b[kSub * P::SP], c[kSub * P::SP];
     } r;
   };
   float red[kSub][4][2 * P::SP];  // db, dc of a token by warp
@@ -205,9 +206,10 @@ __device__ __forceinline__ void stage_forward(const SsmArgs &a, const Place<SL> 
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
       const float raw = dv[i] + (a.dt_bias && in ? a.dt_bias[e + i] : 0.f);
-      sm.f.delta[t][c + i] = in ? ssm_delta(raw, a.d.flags & GDR_SSM_SOFTPLUS) : 0.f;
-      sm.f.x[t][c + i] = xv[i];
+      dv[i] = in ? ssm_delta(raw, a.d.flags & GDR_SSM_SOFTPLUS) : 0.f;
     }
+    store_vec<VEC>(&sm.f.delta[t][c], dv);
+    store_vec<VEC>(&sm.f.x[t][c], xv);
   });
 }
 
@@ -223,16 +225,21 @@ __device__ __forceinline__ void stage_reverse(const SsmArgs &a, const Place<SL> 
       load_vec<VEC>(static_cast<const T *>(a.dy) + (t0 + t) * a.d.ld_dy + e, gv);
       if (a.z) load_vec<VEC>(static_cast<const T *>(a.z) + (t0 + t) * a.d.ld_z + e, zv);
     }
+    float slope[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
       const float raw = dv[i] + (a.dt_bias && in ? a.dt_bias[e + i] : 0.f);
-      const float sg = sigmoid_fast(zv[i]);
-      sm.r.delta[t][c + i] = in ? ssm_delta(raw, a.d.flags & GDR_SSM_SOFTPLUS) : 0.f;
-      sm.r.x[t][c + i] = xv[i];
-      sm.r.up[t][c + i] = gv[i] * (a.z ? zv[i] * sg : 1.f);
-      sm.r.dsp[t][c + i] = delta_grad(raw, a.d.flags & GDR_SSM_SOFTPLUS);
-      sm.r.zf[t][c + i] = gv[i] * sg * fmaf(zv[i], 1.f - sg, 1.f);
+      const float sg = sigmoid_fast(zv[i]), dy = gv[i];
+      dv[i] = ssm_delta(raw, a.d.flags & GDR_SSM_SOFTPLUS, &slope[i]);
+      if (!in) dv[i] = 0.f;
+      gv[i] = dy * (a.z ? zv[i] * sg : 1.f);
+      zv[i] = dy * sg * fmaf(zv[i], 1.f - sg, 1.f);
     }
+    store_vec<VEC>(&sm.r.delta[t][c], dv);
+    store_vec<VEC>(&sm.r.x[t][c], xv);
+    store_vec<VEC>(&sm.r.up[t][c], gv);
+    store_vec<VEC>(&sm.r.slope[t][c], slope);
+    store_vec<VEC>(&sm.r.zf[t][c], zv);
   });
 }
 
@@ -273,12 +280,14 @@ __global__ void __launch_bounds__(kSsmThreads, 2) ssm_bwd_main_kernel(SsmArgs a)
   const P p(a);
   const int tid = threadIdx.x;
   if (p.chunk == 0) copy_empty_states<SL>(a, p, a.dht, a.dh0);
-  f2 A[4][2], h[4][2], g[4][2], dA[4][2];
+  States A, h, g, dA;
   load_a<SL>(a, p, A);
   load_chunk<SL>(a, p, a.hloc, p.chunk, h);
   load_chunk<SL>(a, p, a.gloc, p.chunk, g);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) dA[j][0] = dA[j][1] = f2_pack(0.f, 0.f);
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int s = 0; s < 4; ++s) dA[i][s] = 0;
   const int64_t begin = p.chunk * a.L, end = begin + a.L < a.M ? begin + a.L : a.M;
   const int len = end > begin ? (int)(end - begin) : 0;
   const int subs = (len + kSub - 1) / kSub;
@@ -291,31 +300,14 @@ __global__ void __launch_bounds__(kSsmThreads, 2) ssm_bwd_main_kernel(SsmArgs a)
 
   auto keep = [&](int sub) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float4 v;
-      f2_split(h[j][0], v.x, v.y);
-      f2_split(h[j][1], v.z, v.w);
-      sm.ckpt[sub][j][tid] = v;
-    }
+    for (int i = 0; i < 4; ++i) sm.ckpt[sub][i][tid] = make_ulonglong2(h[i >> 1][2 * (i & 1)], h[i >> 1][2 * (i & 1) + 1]);
   };
-  auto back_to = [&](int sub, f2 (&to)[4][2]) {
+  auto back_to = [&](int sub, States &to) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4 v = sm.ckpt[sub][j][tid];
-      to[j][0] = f2_pack(v.x, v.y);
-      to[j][1] = f2_pack(v.z, v.w);
-    }
-  };
-  // one token of the state's recurrence
-  auto advance = [&](const float4 &d4, const float4 &x4, const ulonglong2 &b4) {
-    const float dl[4] = {d4.x, d4.y, d4.z, d4.w}, xs[4] = {x4.x, x4.y, x4.z, x4.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const f2 dt = f2_pack(dl[j], dl[j]);
-      const float u = dl[j] * xs[j];
-      const f2 uu = f2_pack(u, u);
-      h[j][0] = f2_fma(f2_ex2(f2_mul(A[j][0], dt)), h[j][0], f2_mul(uu, b4.x));
-      h[j][1] = f2_fma(f2_ex2(f2_mul(A[j][1], dt)), h[j][1], f2_mul(uu, b4.y));
+    for (int i = 0; i < 4; ++i) {
+      const ulonglong2 v = sm.ckpt[sub][i][tid];
+      to[i >> 1][2 * (i & 1)] = v.x;
+      to[i >> 1][2 * (i & 1) + 1] = v.y;
     }
   };
 
@@ -329,13 +321,13 @@ __global__ void __launch_bounds__(kSsmThreads, 2) ssm_bwd_main_kernel(SsmArgs a)
     else stage_forward<T, SL, 1>(a, p, begin + f0, nt, sm);
     stage_states<T, SL, kTile>(a, p, a.b, a.d.ld_b, begin + f0, nt, sm.f.b);
     __syncthreads();
-#pragma unroll 2
-    for (int t = 0; t < nt; ++t) {
-      if (sm.bd.first[f0 + t] >= 0) load_h0<SL>(a, p, a.h0, sm.bd.first[f0 + t], h);
-      advance(*reinterpret_cast<const float4 *>(&sm.f.delta[t][p.col]),
-              *reinterpret_cast<const float4 *>(&sm.f.x[t][p.col]),
-              *reinterpret_cast<const ulonglong2 *>(&sm.f.b[t * P::SP + p.sl * 4]));
-      if (((t + 1) & (kSub - 1)) == 0) keep((f0 + t + 1) / kSub);
+    for (int t1 = 0; t1 < nt; t1 += kSub) {
+#pragma unroll 4
+      for (int t = t1; t < t1 + kSub; ++t) {
+        if (sm.bd.first[f0 + t] >= 0) load_h0<SL>(a, p, a.h0, sm.bd.first[f0 + t], h);
+        advance(h, A, Pairs(&sm.f.delta[t][p.col]), Pairs(&sm.f.x[t][p.col]), Twice(&sm.f.b[t * P::SP + p.sl * 4]));
+      }
+      keep((f0 + t1) / kSub + 1);
     }
   }
 
@@ -348,94 +340,81 @@ __global__ void __launch_bounds__(kSsmThreads, 2) ssm_bwd_main_kernel(SsmArgs a)
     stage_states<T, SL, kSub>(a, p, a.b, a.d.ld_b, t0, nt, sm.r.b);
     stage_states<T, SL, kSub>(a, p, a.c, a.d.ld_c, t0, nt, sm.r.c);
     __syncthreads();
-    // after[k]: the state after token k (tokens past the end are never read)
-    f2 after[kSub][4][2];
+    States after[kSub];  // after[k]: the state after token k (past the end: never read)
     back_to(sub, h);
 #pragma unroll
     for (int k = 0; k < kSub; ++k) {
       if (k < nt) {
         if (sm.bd.first[sub * kSub + k] >= 0) load_h0<SL>(a, p, a.h0, sm.bd.first[sub * kSub + k], h);
-        advance(*reinterpret_cast<const float4 *>(&sm.r.delta[k][p.col]),
-                *reinterpret_cast<const float4 *>(&sm.r.x[k][p.col]),
-                *reinterpret_cast<const ulonglong2 *>(&sm.r.b[k * P::SP + p.sl * 4]));
+        advance(h, A, Pairs(&sm.r.delta[k][p.col]), Pairs(&sm.r.x[k][p.col]), Twice(&sm.r.b[k * P::SP + p.sl * 4]));
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        after[k][j][0] = h[j][0];
-        after[k][j][1] = h[j][1];
-      }
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) after[k][i][s] = h[i][s];
     }
 #pragma unroll
     for (int k = kSub - 1; k >= 0; --k) {
       if (k >= nt) continue;
       const int first = sm.bd.first[sub * kSub + k], last = sm.bd.last[sub * kSub + k];
       if (last >= 0) load_h0<SL>(a, p, a.dht, last, g);
-      f2 prev[4][2];
+      States prev;
       if (first >= 0) {
         load_h0<SL>(a, p, a.h0, first, prev);
       } else if (k == 0) {
         back_to(sub, prev);
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          prev[j][0] = after[k > 0 ? k - 1 : 0][j][0];
-          prev[j][1] = after[k > 0 ? k - 1 : 0][j][1];
-        }
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int s = 0; s < 4; ++s) prev[i][s] = after[k > 0 ? k - 1 : 0][i][s];
       }
-      const float4 d4 = *reinterpret_cast<const float4 *>(&sm.r.delta[k][p.col]);
-      const float4 x4 = *reinterpret_cast<const float4 *>(&sm.r.x[k][p.col]);
-      const float4 u4 = *reinterpret_cast<const float4 *>(&sm.r.up[k][p.col]);
-      const ulonglong2 b4 = *reinterpret_cast<const ulonglong2 *>(&sm.r.b[k * P::SP + p.sl * 4]);
-      const ulonglong2 c4 = *reinterpret_cast<const ulonglong2 *>(&sm.r.c[k * P::SP + p.sl * 4]);
-      const float dl[4] = {d4.x, d4.y, d4.z, d4.w}, xs[4] = {x4.x, x4.y, x4.z, x4.w},
-                  us[4] = {u4.x, u4.y, u4.z, u4.w};
-      f2 db[2], dc[2];
+      const Pairs delta(&sm.r.delta[k][p.col]), x(&sm.r.x[k][p.col]), up(&sm.r.up[k][p.col]);
+      const Twice b(&sm.r.b[k * P::SP + p.sl * 4]), c(&sm.r.c[k * P::SP + p.sl * 4]);
+      f2 db[4], dc[4];
       float ys[4], gb[4], qa[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const f2 dt = f2_pack(dl[j], dl[j]), up = f2_pack(us[j], us[j]);
-        const float u = dl[j] * xs[j];
-        const f2 uu = f2_pack(u, u);
-        f2 sy, sb, sq;
+      for (int i = 0; i < 2; ++i) {
+        const f2 u = f2_mul(delta.v[i], x.v[i]);
+        f2 sy = 0, sb = 0, sq = 0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const f2 bb = i ? b4.y : b4.x, cc = i ? c4.y : c4.x;
-          g[j][i] = f2_fma(cc, up, g[j][i]);
-          dc[i] = j ? f2_fma(up, after[k][j][i], dc[i]) : f2_mul(up, after[k][j][i]);
-          sy = i ? f2_fma(cc, after[k][j][i], sy) : f2_mul(cc, after[k][j][i]);
-          db[i] = j ? f2_fma(uu, g[j][i], db[i]) : f2_mul(uu, g[j][i]);
-          sb = i ? f2_fma(bb, g[j][i], sb) : f2_mul(bb, g[j][i]);
-          g[j][i] = f2_mul(g[j][i], f2_ex2(f2_mul(A[j][i], dt)));
-          const f2 q = f2_mul(g[j][i], prev[j][i]);
-          dA[j][i] = f2_fma(q, dt, dA[j][i]);
-          sq = i ? f2_fma(q, A[j][i], sq) : f2_mul(q, A[j][i]);
+        for (int s = 0; s < 4; ++s) {
+          g[i][s] = f2_fma(c.v[s], up.v[i], g[i][s]);
+          dc[s] = i ? f2_fma(up.v[i], after[k][i][s], dc[s]) : f2_mul(up.v[i], after[k][i][s]);
+          sy = s ? f2_fma(c.v[s], after[k][i][s], sy) : f2_mul(c.v[s], after[k][i][s]);
+          db[s] = i ? f2_fma(u, g[i][s], db[s]) : f2_mul(u, g[i][s]);
+          sb = s ? f2_fma(b.v[s], g[i][s], sb) : f2_mul(b.v[s], g[i][s]);
+          g[i][s] = f2_mul(g[i][s], f2_ex2(f2_mul(A[i][s], delta.v[i])));
+          const f2 q = f2_mul(g[i][s], prev[i][s]);
+          dA[i][s] = f2_fma(q, delta.v[i], dA[i][s]);
+          sq = s ? f2_fma(q, A[i][s], sq) : f2_mul(q, A[i][s]);
         }
-        float lo, hi;
-        f2_split(sy, lo, hi);
-        ys[j] = lo + hi;
-        f2_split(sb, lo, hi);
-        gb[j] = lo + hi;
-        f2_split(sq, lo, hi);
-        qa[j] = lo + hi;
+        f2_split(sy, ys[2 * i], ys[2 * i + 1]);
+        f2_split(sb, gb[2 * i], gb[2 * i + 1]);
+        f2_split(sq, qa[2 * i], qa[2 * i + 1]);
       }
       const float ysum = sum_over_states<SL>(ys, p.sl), gsum = sum_over_states<SL>(gb, p.sl),
                   qsum = sum_over_states<SL>(qa, p.sl) * kLn2;  // A carries log2(e)
       if (owner) {
-        const int c = p.col + mine;
-        const float x = sm.r.x[k][c], delta = sm.r.delta[k][c], up = sm.r.up[k][c];
-        const float ddt = fmaf(x, gsum, qsum) * sm.r.dsp[k][c];
+        const int col = p.col + mine;
+        const float xo = sm.r.x[k][col], uo = sm.r.up[k][col];
+        const float ddt = fmaf(xo, gsum, qsum) * sm.r.slope[k][col];
         const int64_t at = (t0 + k) * a.d.E + e_mine;
-        static_cast<T *>(a.dx)[at] = from_f32<T>(fmaf(skip, up, delta * gsum));
+        static_cast<T *>(a.dx)[at] = from_f32<T>(fmaf(skip, uo, sm.r.delta[k][col] * gsum));
         static_cast<T *>(a.ddt)[at] = from_f32<T>(ddt);
-        if (a.dz) static_cast<T *>(a.dz)[at] = from_f32<T>(sm.r.zf[k][c] * fmaf(skip, x, ysum));
-        dd = fmaf(up, x, dd);
+        if (a.dz) static_cast<T *>(a.dz)[at] = from_f32<T>(sm.r.zf[k][col] * fmaf(skip, xo, ysum));
+        dd = fmaf(uo, xo, dd);
         dbias += ddt;
       }
       float v[8];
-      f2_split(db[0], v[0], v[1]);
-      f2_split(db[1], v[2], v[3]);
-      f2_split(dc[0], v[4], v[5]);
-      f2_split(dc[1], v[6], v[7]);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        float lo, hi;
+        f2_split(db[s], lo, hi);
+        v[s] = lo + hi;
+        f2_split(dc[s], lo, hi);
+        v[4 + s] = lo + hi;
+      }
       sum_over_channels<SL>(v, p, sm.red[k][p.warp]);
       if (first >= 0 && a.dh0) store_final<SL>(a, p, a.dh0, first, g);
     }
