@@ -18,12 +18,12 @@ contiguous; outputs are.  Activations are bf16 or fp32.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
 
-from . import (GDR_BF16, GDR_ERR_DTYPE, GDR_ERR_NULLPTR, GDR_ERR_SHAPE, GDR_F32, GdrError, _check, _lib, _ptr,
-               _require, _stream_ptr)
+from . import GDR_BF16, GDR_ERR_DTYPE, GDR_ERR_NULLPTR, GDR_ERR_SHAPE, GDR_F32, GdrError, _check, _lib
 
 _QUANTS = {None: 0, "row": 1, "group": 2}
 _ACTIVATIONS = {None: 0, "silu": 1}
@@ -65,6 +65,12 @@ def _bind():
 _bind()
 
 
+# The smallest calls take less time on the GPU than here, so these checks read
+# each attribute once and hand plain integers to ctypes.
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _dtype_code(t, name):
     code = _DTYPES.get(t.dtype)
     if code is None:
@@ -79,71 +85,91 @@ def _param_code(t, x, name):
     return _DTYPES[t.dtype]
 
 
-def _on(t, ref, name):
-    """t is on the GPU that ref is on."""
+def _device(t, name):
+    """The index of the current device, which must own the inputs."""
     if not t.is_cuda:
         raise GdrError(GDR_ERR_NULLPTR, f"{name} must be a CUDA tensor")
-    if ref is not None and t.device != ref.device:
-        raise GdrError(GDR_ERR_NULLPTR, f"{name} is on {t.device}, expected {ref.device}")
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise GdrError(GDR_ERR_NULLPTR, f"{name} is on {t.device}, but cuda:{torch.cuda.current_device()} is current")
+    return dev
 
 
-def _rows(t, name, ref=None, dtype=None, shape=None, row_dims=1):
-    """Checks a token-major input; returns the distance between its rows in elements."""
-    _on(t, ref, name)
+def _on(t, dev, name):
+    """t is on the GPU that the call runs on."""
+    if not t.is_cuda:
+        raise GdrError(GDR_ERR_NULLPTR, f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise GdrError(GDR_ERR_NULLPTR, f"{name} is on {t.device}, expected cuda:{dev}")
+
+
+def _whole(t, name, dev, dtype, shape):
+    """Checks a contiguous tensor (None: nothing to check)."""
+    if t is None:
+        return
+    _on(t, dev, name)
     if dtype is not None and t.dtype != dtype:
         raise GdrError(GDR_ERR_DTYPE, f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    size, stride = t.shape, t.stride()
-    width = 1
-    for i in range(t.dim() - 1, t.dim() - 1 - row_dims, -1):
-        if size[i] != 1 and stride[i] != width:
+    if not t.is_contiguous():
+        raise GdrError(GDR_ERR_SHAPE, f"{name} must be contiguous")
+
+
+def _rows(t, name, dev, dtype=None, shape=None, row_dims=1):
+    """Checks a token-major input; returns the distance between its rows in elements."""
+    _on(t, dev, name)
+    if dtype is not None and t.dtype != dtype:
+        raise GdrError(GDR_ERR_DTYPE, f"{name} must be {dtype}, got {t.dtype}")
+    size = t.shape
+    if shape is not None and size != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(size)}")
+    width = size[-1] if row_dims == 1 else size[-1] * size[-2]
+    if t.is_contiguous():
+        return width
+    stride = t.stride()
+    inner = 1
+    for i in range(len(size) - 1, len(size) - 1 - row_dims, -1):
+        if size[i] != 1 and stride[i] != inner:
             raise GdrError(GDR_ERR_SHAPE, f"{name}: the elements of a row must be contiguous")
-        width *= size[i]
-    ld = None
-    step = 1
-    for i in range(t.dim() - 1 - row_dims, -1, -1):
+        inner *= size[i]
+    ld, step = None, 1
+    for i in range(len(size) - 1 - row_dims, -1, -1):
         if size[i] != 1:
             if ld is None:
-                if stride[i] < width:
-                    raise GdrError(GDR_ERR_SHAPE, f"{name}: rows overlap")
                 ld = stride[i]
+                if ld < width:
+                    raise GdrError(GDR_ERR_SHAPE, f"{name}: rows overlap")
             elif stride[i] != ld * step:
-                if t.numel():
-                    raise GdrError(GDR_ERR_SHAPE, f"{name}: rows must be evenly spaced; call contiguous()")
+                raise GdrError(GDR_ERR_SHAPE, f"{name}: rows must be evenly spaced; call contiguous()")
             step *= size[i]
-    return width if ld is None else max(ld, width)
+    return width if ld is None else ld
 
 
-def _device_of(t, name):
-    """The call runs on the current device, which must own the inputs."""
-    _on(t, None, name)
-    if t.device.index != torch.cuda.current_device():
-        raise GdrError(GDR_ERR_NULLPTR, f"{name} is on {t.device}, but cuda:{torch.cuda.current_device()} is current")
+_HERE = contextlib.nullcontext()
 
 
-class _outputs_on:
-    """Outputs belong to the launching stream: memory is taken while it is current."""
+def _outputs_on(stream):
+    """Outputs belong to the launching stream: their memory is taken while it is current."""
+    return _HERE if stream is None else torch.cuda.stream(stream)
 
-    def __init__(self, stream):
-        self.ctx = None if stream is None else torch.cuda.stream(stream)
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
+def _stream(stream, dev):
+    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
 
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+
+def _call(fn, desc, *args):
+    rc = fn(desc, *args)
+    if rc:
+        _check(rc)
 
 
 # ------------------------------------------------------------------------------------------------ norm
-def _norm_shape(x, weight, name):
+def _norm_shape(x, weight, dev, name):
     if x.dim() < 1:
         raise ValueError(f"{name} must be [..., E]")
     E = x.shape[-1]
-    _on(weight, x, "weight")
-    _require(weight, "weight", None, (E,))
+    _whole(weight, "weight", dev, None, (E,))
     return x.numel() // E if E else 0, E
 
 
@@ -156,27 +182,26 @@ def norm_fwd(x, weight, residual=None, eps=1e-6, quant=None, stream=None):
     ``(y8, scale, s)`` with y8 in float8_e4m3fn and ``y ~ y8 * scale``.
     """
     code = _dtype_code(x, "x")
-    _device_of(x, "x")
-    M, E = _norm_shape(x, weight, "x")
+    dev = _device(x, "x")
+    M, E = _norm_shape(x, weight, dev, "x")
     if quant not in _QUANTS:
         raise ValueError(f"quant must be None, 'row' or 'group', got {quant!r}")
-    ld_x, ld_r, rcode = _rows(x, "x"), E, code
+    ld_x, ld_r, rcode = _rows(x, "x", dev), E, code
     if residual is not None:
         rcode = _param_code(residual, x, "residual")
-        ld_r = _rows(residual, "residual", x, None, x.shape)
+        ld_r = _rows(residual, "residual", dev, None, x.shape)
     desc = GdrNormDesc(M, E, ld_x, ld_r, E, code, rcode, _param_code(weight, x, "weight"), _QUANTS[quant], eps, 0)
     with _outputs_on(stream):
-        s = None if residual is None else torch.empty(x.shape, dtype=residual.dtype, device=x.device)
+        s = None if residual is None else residual.new_empty(x.shape)
         scale = None
         if quant is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            y = x.new_empty(x.shape)
         else:
-            y = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+            y = x.new_empty(x.shape, dtype=torch.float8_e4m3fn)
             lead = x.shape[:-1]
-            scale = torch.empty(lead if quant == "row" else (*lead, -(-E // GROUP_SIZE)), dtype=torch.float32,
-                                device=x.device)
-    _check(_lib.gdr_norm_fwd(ctypes.byref(desc), _ptr(x), _ptr(residual), _ptr(weight), _ptr(y), _ptr(scale),
-                             _ptr(s), _stream_ptr(stream)))
+            scale = x.new_empty(lead if quant == "row" else (*lead, -(-E // GROUP_SIZE)), dtype=torch.float32)
+    _call(_lib.gdr_norm_fwd, desc, x.data_ptr(), _addr(residual), weight.data_ptr(), y.data_ptr(), _addr(scale),
+          _addr(s), _stream(stream, dev))
     return (y, s) if quant is None else (y, scale, s)
 
 
@@ -187,62 +212,64 @@ def norm_bwd(dy, s, weight, ds=None, eps=1e-6, stream=None):
     tensor where the two agree), dweight fp32.
     """
     code = _dtype_code(dy, "dy")
-    _device_of(dy, "dy")
-    M, E = _norm_shape(dy, weight, "dy")
+    dev = _device(dy, "dy")
+    M, E = _norm_shape(dy, weight, dev, "dy")
     rcode = _param_code(s, dy, "s")
-    ld_s, ld_ds = _rows(s, "s", dy, None, dy.shape), E
+    ld_s, ld_ds = _rows(s, "s", dev, None, dy.shape), E
     if ds is not None:
-        ld_ds = _rows(ds, "ds", dy, s.dtype, dy.shape)
-    desc = GdrNormDesc(M, E, _rows(dy, "dy"), ld_s, ld_ds, code, rcode, _param_code(weight, dy, "weight"), 0, eps, 0)
+        ld_ds = _rows(ds, "ds", dev, s.dtype, dy.shape)
+    desc = GdrNormDesc(M, E, _rows(dy, "dy", dev), ld_s, ld_ds, code, rcode, _param_code(weight, dy, "weight"), 0, eps,
+                       0)
     with _outputs_on(stream):
-        dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
-        dres = dx if s.dtype == dy.dtype else torch.empty(dy.shape, dtype=s.dtype, device=dy.device)
-        dweight = torch.empty(E, dtype=torch.float32, device=dy.device)
-    _check(_lib.gdr_norm_bwd(ctypes.byref(desc), _ptr(dy), _ptr(s), _ptr(ds), _ptr(weight), _ptr(dx),
-                             None if dres is dx else _ptr(dres), _ptr(dweight), _stream_ptr(stream)))
+        dx = dy.new_empty(dy.shape)
+        dres = dx if s.dtype == dy.dtype else s.new_empty(dy.shape)
+        dweight = dy.new_empty(E, dtype=torch.float32)
+    _call(_lib.gdr_norm_bwd, desc, dy.data_ptr(), s.data_ptr(), _addr(ds), weight.data_ptr(), dx.data_ptr(),
+          None if dres is dx else dres.data_ptr(), dweight.data_ptr(), _stream(stream, dev))
     return dx, dres, dweight
 
 
 # ------------------------------------------------------------------------------------------ convolution
-def _conv_desc(x, weight, bias, activation, B, T, N, ld_dy):
+def _conv_desc(x, dev, weight, bias, activation, B, T, N, ld_dy):
     code = _dtype_code(x, "x")
     E = x.shape[-1]
-    _on(weight, x, "weight")
     if weight.dim() != 2 or weight.shape[0] != E:
         raise ValueError(f"weight must be [{E}, W], got {tuple(weight.shape)}")
-    _require(weight, "weight")
+    _whole(weight, "weight", dev, None, weight.shape)
     wcode = _param_code(weight, x, "weight")
-    if bias is not None:
-        _on(bias, x, "bias")
-        _require(bias, "bias", weight.dtype, (E,))
+    _whole(bias, "bias", dev, weight.dtype, (E,))
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation must be None or 'silu', got {activation!r}")
-    return GdrConvDesc(B, T, E, N, weight.shape[1], _rows(x, "x"), ld_dy, code, wcode, _ACTIVATIONS[activation], 0)
+    W = weight.shape[1]
+    if not 2 <= W <= 4:
+        raise ValueError(f"weight must have 2 to 4 taps, got {W}")
+    return GdrConvDesc(B, T, E, N, W, _rows(x, "x", dev), ld_dy, code, wcode, _ACTIVATIONS[activation], 0)
 
 
 def _sequences(x, cu_seqlens):
+    """(device, B, T, N) of a batch."""
     if x.dim() != 3:
         raise ValueError("x must be [B, T, E]")
-    B, T = x.shape[:2]
+    dev = _device(x, "x")
+    B, T, _ = x.shape
     if cu_seqlens is None:
-        return B, T, B
-    _on(cu_seqlens, x, "cu_seqlens")
-    _require(cu_seqlens, "cu_seqlens", torch.int64)
+        return dev, B, T, B
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must be [N + 1]")
-    return B, T, cu_seqlens.numel() - 1
+    _whole(cu_seqlens, "cu_seqlens", dev, torch.int64, cu_seqlens.shape)
+    return dev, B, T, cu_seqlens.numel() - 1
 
 
-def _state(t, name, ref, dtype, shape):
-    if t is not None:
-        _on(t, ref, name)
-        _require(t, name, dtype, shape)
-
-
-def _slots(slots, x, R):
-    if slots is not None:
-        _on(slots, x, "slots")
-        _require(slots, "slots", torch.int32, (R,))
+def _step_rows(x, state, slots):
+    """(device, rows, slots in the pool) of a single-token call."""
+    if x.dim() != 2:
+        raise ValueError("x must be [R, E]")
+    dev = _device(x, "x")
+    R, P = x.shape[0], state.shape[0]
+    _whole(slots, "slots", dev, torch.int32, (R,))
+    if slots is None and P < R:
+        raise ValueError(f"state has {P} slots for {R} rows")
+    return dev, R, P
 
 
 def conv_fwd(x, weight, bias=None, s0=None, cu_seqlens=None, activation="silu", output_final_state=True,
@@ -253,16 +280,15 @@ def conv_fwd(x, weight, bias=None, s0=None, cu_seqlens=None, activation="silu", 
     each sequence (zero when None).  Returns ``(y, st)``, st the last W - 1
     inputs of each sequence (None unless requested).
     """
-    B, T, N = _sequences(x, cu_seqlens)
-    _device_of(x, "x")
-    desc = _conv_desc(x, weight, bias, activation, B, T, N, x.shape[-1])
+    dev, B, T, N = _sequences(x, cu_seqlens)
+    desc = _conv_desc(x, dev, weight, bias, activation, B, T, N, x.shape[-1])
     shape = (N, desc.W - 1, desc.E)
-    _state(s0, "s0", x, x.dtype, shape)
+    _whole(s0, "s0", dev, x.dtype, shape)
     with _outputs_on(stream):
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        st = torch.empty(shape, dtype=x.dtype, device=x.device) if output_final_state and desc.W > 1 else None
-    _check(_lib.gdr_conv_fwd(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(s0), _ptr(cu_seqlens),
-                             _ptr(y), _ptr(st), _stream_ptr(stream)))
+        y = x.new_empty(x.shape)
+        st = x.new_empty(shape) if output_final_state else None
+    _call(_lib.gdr_conv_fwd, desc, x.data_ptr(), weight.data_ptr(), _addr(bias), _addr(s0), _addr(cu_seqlens),
+          y.data_ptr(), _addr(st), _stream(stream, dev))
     return y, st
 
 
@@ -272,20 +298,18 @@ def conv_bwd(x, weight, dy, bias=None, s0=None, dst=None, cu_seqlens=None, activ
     Returns ``(dx, dweight, dbias, ds0)``: dx and ds0 in x's dtype, dweight and
     dbias fp32 (dbias None without a bias).
     """
-    B, T, N = _sequences(x, cu_seqlens)
-    _device_of(x, "x")
-    desc = _conv_desc(x, weight, bias, activation, B, T, N, _rows(dy, "dy", x, x.dtype, x.shape))
+    dev, B, T, N = _sequences(x, cu_seqlens)
+    desc = _conv_desc(x, dev, weight, bias, activation, B, T, N, _rows(dy, "dy", dev, x.dtype, x.shape))
     shape = (N, desc.W - 1, desc.E)
-    _state(s0, "s0", x, x.dtype, shape)
-    _state(dst, "dst", x, x.dtype, shape)
+    _whole(s0, "s0", dev, x.dtype, shape)
+    _whole(dst, "dst", dev, x.dtype, shape)
     with _outputs_on(stream):
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dweight = torch.empty(weight.shape, dtype=torch.float32, device=x.device)
-        dbias = None if bias is None else torch.empty(desc.E, dtype=torch.float32, device=x.device)
-        ds0 = torch.empty((N, max(0, desc.W - 1), desc.E), dtype=x.dtype, device=x.device)
-    _check(_lib.gdr_conv_bwd(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(s0), _ptr(cu_seqlens),
-                             _ptr(dy), _ptr(dst), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(ds0),
-                             _stream_ptr(stream)))
+        dx, ds0 = x.new_empty(x.shape), x.new_empty(shape)
+        dweight = x.new_empty(weight.shape, dtype=torch.float32)
+        dbias = None if bias is None else x.new_empty(desc.E, dtype=torch.float32)
+    _call(_lib.gdr_conv_bwd, desc, x.data_ptr(), weight.data_ptr(), _addr(bias), _addr(s0), _addr(cu_seqlens),
+          dy.data_ptr(), _addr(dst), dx.data_ptr(), dweight.data_ptr(), _addr(dbias), ds0.data_ptr(),
+          _stream(stream, dev))
     return dx, dweight, dbias, ds0
 
 
@@ -295,39 +319,30 @@ def conv_step(x, state, weight, bias=None, activation="silu", slots=None, stream
     Row r uses ``state[slots[r]]`` (slots int32; None: slot r).  A negative slot
     is a padding row with a zero output.  Slots of one call must differ.
     """
-    if x.dim() != 2:
-        raise ValueError("x must be [R, E]")
-    _device_of(x, "x")
-    R = x.shape[0]
-    desc = _conv_desc(x, weight, bias, activation, R, 1, state.shape[0], x.shape[1])
-    _state(state, "state", x, x.dtype, (state.shape[0], desc.W - 1, desc.E))
-    _slots(slots, x, R)
-    if slots is None and state.shape[0] < R:
-        raise ValueError(f"state has {state.shape[0]} slots for {R} rows")
+    dev, R, P = _step_rows(x, state, slots)
+    desc = _conv_desc(x, dev, weight, bias, activation, R, 1, P, x.shape[1])
+    _whole(state, "state", dev, x.dtype, (P, desc.W - 1, desc.E))
     with _outputs_on(stream):
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _check(_lib.gdr_conv_step(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(slots), _ptr(state),
-                              _ptr(y), _stream_ptr(stream)))
+        y = x.new_empty(x.shape)
+    _call(_lib.gdr_conv_step, desc, x.data_ptr(), weight.data_ptr(), _addr(bias), _addr(slots), state.data_ptr(),
+          y.data_ptr(), _stream(stream, dev))
     return y
 
 
 # ------------------------------------------------------------------------------------------------ scan
-def _ssm_desc(x, dt, a, b, c, d, z, dt_bias, B, T, N, softplus, ld_dy):
+def _ssm_desc(x, dev, dt, a, b, c, d, z, dt_bias, B, T, N, softplus, ld_dy):
     code = _dtype_code(x, "x")
-    lead, E = x.shape[:-1], x.shape[-1]
-    if b.dim() != x.dim() + 1 or tuple(b.shape[:-2]) != tuple(lead):
-        raise ValueError(f"b must be {tuple(lead)} + (G, S), got {tuple(b.shape)}")
+    shape, dtype = x.shape, x.dtype
+    E = shape[-1]
+    if b.dim() != x.dim() + 1 or b.shape[:-2] != shape[:-1]:
+        raise ValueError(f"b must be {tuple(shape[:-1])} + (G, S), got {tuple(b.shape)}")
     G, S = b.shape[-2:]
-    _on(a, x, "a")
-    _require(a, "a", torch.float32, (E, S))
-    for t, name in ((d, "d"), (dt_bias, "dt_bias")):
-        if t is not None:
-            _on(t, x, name)
-            _require(t, name, torch.float32, (E,))
-    return GdrSsmDesc(B, T, E, S, G, N, _rows(x, "x"), _rows(dt, "dt", x, x.dtype, x.shape),
-                      E if z is None else _rows(z, "z", x, x.dtype, x.shape),
-                      _rows(b, "b", x, x.dtype, None, 2), _rows(c, "c", x, x.dtype, b.shape, 2), ld_dy, code,
-                      GDR_SSM_SOFTPLUS if softplus else 0)
+    _whole(a, "a", dev, torch.float32, (E, S))
+    _whole(d, "d", dev, torch.float32, (E,))
+    _whole(dt_bias, "dt_bias", dev, torch.float32, (E,))
+    return GdrSsmDesc(B, T, E, S, G, N, _rows(x, "x", dev), _rows(dt, "dt", dev, dtype, shape),
+                      E if z is None else _rows(z, "z", dev, dtype, shape), _rows(b, "b", dev, dtype, None, 2),
+                      _rows(c, "c", dev, dtype, b.shape, 2), ld_dy, code, GDR_SSM_SOFTPLUS if softplus else 0)
 
 
 def ssm_fwd(x, dt, a, b, c, d=None, z=None, dt_bias=None, h0=None, cu_seqlens=None, dt_softplus=True,
@@ -337,19 +352,18 @@ def ssm_fwd(x, dt, a, b, c, d=None, z=None, dt_bias=None, h0=None, cu_seqlens=No
     ``h_t = exp(delta_t a[e]) h_{t-1} + delta_t x_t b_t[g]``,
     ``y_t = (c_t[g] . h_t + d[e] x_t) silu(z_t)``, ``delta = softplus(dt + dt_bias)``.
 
-    x, dt, z [B, T, E]; a [E, S] fp32; b, c [B, T, G, S]; h0 [N, E, S] fp32.
-    Returns ``(y, ht)`` (ht None unless requested).
+    x, dt, z [B, T, E]; a [E, S] fp32, S in 1..64; b, c [B, T, G, S]; h0
+    [N, E, S] fp32.  Returns ``(y, ht)`` (ht None unless requested).
     """
-    B, T, N = _sequences(x, cu_seqlens)
-    _device_of(x, "x")
-    desc = _ssm_desc(x, dt, a, b, c, d, z, dt_bias, B, T, N, dt_softplus, x.shape[-1])
+    dev, B, T, N = _sequences(x, cu_seqlens)
+    desc = _ssm_desc(x, dev, dt, a, b, c, d, z, dt_bias, B, T, N, dt_softplus, x.shape[-1])
     shape = (N, desc.E, desc.S)
-    _state(h0, "h0", x, torch.float32, shape)
+    _whole(h0, "h0", dev, torch.float32, shape)
     with _outputs_on(stream):
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        ht = torch.empty(shape, dtype=torch.float32, device=x.device) if output_final_state else None
-    _check(_lib.gdr_ssm_fwd(ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(a), _ptr(b), _ptr(c), _ptr(d), _ptr(z),
-                            _ptr(dt_bias), _ptr(h0), _ptr(cu_seqlens), _ptr(y), _ptr(ht), _stream_ptr(stream)))
+        y = x.new_empty(x.shape)
+        ht = a.new_empty(shape) if output_final_state else None
+    _call(_lib.gdr_ssm_fwd, desc, x.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(), _addr(d),
+          _addr(z), _addr(dt_bias), _addr(h0), _addr(cu_seqlens), y.data_ptr(), _addr(ht), _stream(stream, dev))
     return y, ht
 
 
@@ -361,26 +375,22 @@ def ssm_bwd(x, dt, a, b, c, dy, d=None, z=None, dt_bias=None, h0=None, dht=None,
     dz in x's dtype, the others fp32; dd, dz and ddt_bias are None where d, z
     and dt_bias are.  The forward is recomputed inside the call.
     """
-    B, T, N = _sequences(x, cu_seqlens)
-    _device_of(x, "x")
-    desc = _ssm_desc(x, dt, a, b, c, d, z, dt_bias, B, T, N, dt_softplus, _rows(dy, "dy", x, x.dtype, x.shape))
+    dev, B, T, N = _sequences(x, cu_seqlens)
+    desc = _ssm_desc(x, dev, dt, a, b, c, d, z, dt_bias, B, T, N, dt_softplus, _rows(dy, "dy", dev, x.dtype, x.shape))
     shape = (N, desc.E, desc.S)
-    _state(h0, "h0", x, torch.float32, shape)
-    _state(dht, "dht", x, torch.float32, shape)
-    like = dict(dtype=x.dtype, device=x.device)
-    f32 = dict(dtype=torch.float32, device=x.device)
+    _whole(h0, "h0", dev, torch.float32, shape)
+    _whole(dht, "dht", dev, torch.float32, shape)
     with _outputs_on(stream):
-        dx, ddt = torch.empty(x.shape, **like), torch.empty(x.shape, **like)
-        db, dc = torch.empty(b.shape, **like), torch.empty(b.shape, **like)
-        dz = None if z is None else torch.empty(x.shape, **like)
-        da = torch.empty(a.shape, **f32)
-        dd = None if d is None else torch.empty(desc.E, **f32)
-        ddt_bias = None if dt_bias is None else torch.empty(desc.E, **f32)
-        dh0 = torch.empty(shape, **f32)
-    _check(_lib.gdr_ssm_bwd(ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(a), _ptr(b), _ptr(c), _ptr(d), _ptr(z),
-                            _ptr(dt_bias), _ptr(h0), _ptr(cu_seqlens), _ptr(dy), _ptr(dht), _ptr(dx), _ptr(ddt),
-                            _ptr(da), _ptr(db), _ptr(dc), _ptr(dd), _ptr(dz), _ptr(ddt_bias), _ptr(dh0),
-                            _stream_ptr(stream)))
+        dx, ddt = x.new_empty(x.shape), x.new_empty(x.shape)
+        db, dc = x.new_empty(b.shape), x.new_empty(b.shape)
+        dz = None if z is None else x.new_empty(x.shape)
+        da, dh0 = a.new_empty(a.shape), a.new_empty(shape)
+        dd = None if d is None else a.new_empty(desc.E)
+        ddt_bias = None if dt_bias is None else a.new_empty(desc.E)
+    _call(_lib.gdr_ssm_bwd, desc, x.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(), _addr(d),
+          _addr(z), _addr(dt_bias), _addr(h0), _addr(cu_seqlens), dy.data_ptr(), _addr(dht), dx.data_ptr(),
+          ddt.data_ptr(), da.data_ptr(), db.data_ptr(), dc.data_ptr(), _addr(dd), _addr(dz), _addr(ddt_bias),
+          dh0.data_ptr(), _stream(stream, dev))
     return dx, ddt, da, db, dc, dd, dz, ddt_bias, dh0
 
 
@@ -389,17 +399,11 @@ def ssm_step(x, dt, a, b, c, state, d=None, z=None, dt_bias=None, slots=None, dt
 
     ``slots`` as in ``conv_step``.
     """
-    if x.dim() != 2:
-        raise ValueError("x must be [R, E]")
-    _device_of(x, "x")
-    R = x.shape[0]
-    desc = _ssm_desc(x, dt, a, b, c, d, z, dt_bias, R, 1, state.shape[0], dt_softplus, x.shape[1])
-    _state(state, "state", x, torch.float32, (state.shape[0], desc.E, desc.S))
-    _slots(slots, x, R)
-    if slots is None and state.shape[0] < R:
-        raise ValueError(f"state has {state.shape[0]} slots for {R} rows")
+    dev, R, P = _step_rows(x, state, slots)
+    desc = _ssm_desc(x, dev, dt, a, b, c, d, z, dt_bias, R, 1, P, dt_softplus, x.shape[1])
+    _whole(state, "state", dev, torch.float32, (P, desc.E, desc.S))
     with _outputs_on(stream):
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _check(_lib.gdr_ssm_step(ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(a), _ptr(b), _ptr(c), _ptr(d), _ptr(z),
-                             _ptr(dt_bias), _ptr(slots), _ptr(state), _ptr(y), _stream_ptr(stream)))
+        y = x.new_empty(x.shape)
+    _call(_lib.gdr_ssm_step, desc, x.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(), _addr(d),
+          _addr(z), _addr(dt_bias), _addr(slots), state.data_ptr(), y.data_ptr(), _stream(stream, dev))
     return y
