@@ -6,11 +6,12 @@
 // with x_{-1}, .. x_{-W+1} taken from the sequence's state, and the last W - 1
 // inputs of each sequence left as its new state.
 //
-// A thread owns VEC neighbouring channels and walks a run of tokens with the
-// W - 1 inputs before in registers, so every input is read from HBM once (the
-// W - 1 tokens around a run come from L2 again).  Runs are cut from the flat
-// token axis; a sequence's border inside one reloads the window.  The bound is
-// HBM.
+// A thread owns two or four neighbouring channels, in pairs for the packed fp32
+// instructions, and walks a run of tokens with the W - 1 inputs before in
+// registers, so every input is read from HBM once (the W - 1 tokens around a run
+// come from L2 again).  The next batch of tokens is loaded while one is computed.
+// Runs are cut from the flat token axis; a sequence's border inside one reloads
+// the window.  The bound is HBM.
 #include <algorithm>
 
 #include "gdr_layer.cuh"
@@ -44,110 +45,227 @@ __device__ __forceinline__ Seq seq_at(const ConvArgs &a, int64_t t) {
   return {n, r.bos, r.eos};
 }
 
-template <typename T, int VEC, int W>
+// A thread's NP pairs of channels in memory.  AL: one aligned access holds them
+// all (the host checks); else element by element, the first `n` of them.
+template <typename T, int NP, bool AL>
+struct Io {
+  struct Raw {
+    f2 v[NP];
+  };
+  static __device__ __forceinline__ Raw load(const T *p, int n) {
+    Raw r;
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+      r.v[i] = f2_pack(2 * i < n ? to_f32(p[2 * i]) : 0.f, 2 * i + 1 < n ? to_f32(p[2 * i + 1]) : 0.f);
+    return r;
+  }
+  static __device__ __forceinline__ void expand(const Raw &r, f2 (&v)[NP]) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) v[i] = r.v[i];
+  }
+  static __device__ __forceinline__ void store(T *p, int n, const f2 (&v)[NP]) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      float lo, hi;
+      f2_split(v[i], lo, hi);
+      if (2 * i < n) p[2 * i] = from_f32<T>(lo);
+      if (2 * i + 1 < n) p[2 * i + 1] = from_f32<T>(hi);
+    }
+  }
+};
+template <int NP>
+struct Io<__nv_bfloat16, NP, true> {
+  struct __align__(4 * NP) Raw {
+    uint32_t u[NP];
+  };
+  static __device__ __forceinline__ Raw load(const __nv_bfloat16 *p, int) { return *reinterpret_cast<const Raw *>(p); }
+  static __device__ __forceinline__ void expand(const Raw &r, f2 (&v)[NP]) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) v[i] = f2_pack(__uint_as_float(r.u[i] << 16), __uint_as_float(r.u[i] & 0xffff0000u));
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16 *p, int, const f2 (&v)[NP]) {
+    Raw r;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      float lo, hi;
+      f2_split(v[i], lo, hi);
+      r.u[i] = pack_bf16(lo, hi);
+    }
+    *reinterpret_cast<Raw *>(p) = r;
+  }
+};
+template <int NP>
+struct Io<float, NP, true> {
+  struct __align__(8 * NP) Raw {
+    f2 v[NP];
+  };
+  static __device__ __forceinline__ Raw load(const float *p, int) { return *reinterpret_cast<const Raw *>(p); }
+  static __device__ __forceinline__ void expand(const Raw &r, f2 (&v)[NP]) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) v[i] = r.v[i];
+  }
+  static __device__ __forceinline__ void store(float *p, int, const f2 (&v)[NP]) {
+    Raw r;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) r.v[i] = v[i];
+    *reinterpret_cast<Raw *>(p) = r;
+  }
+};
+
+template <typename T, int NP, int W>
 struct Taps {
-  float w[W][VEC], bias[VEC];
-  __device__ __forceinline__ void load(const ConvArgs &a, int64_t e) {
+  f2 w[W][NP], bias[NP];
+  __device__ __forceinline__ void load(const ConvArgs &a, int64_t e, int n) {
     const bool f32 = a.d.weight_dtype == GDR_F32;
-    float v[W][VEC];  // the VEC * W weights are one run of memory
 #pragma unroll
-    for (int k = 0; k < W; ++k) {
-      if (f32) load_vec<VEC>(static_cast<const float *>(a.weight) + e * W + k * VEC, v[k]);
-      else load_vec<VEC>(static_cast<const T *>(a.weight) + e * W + k * VEC, v[k]);
+    for (int i = 0; i < NP; ++i) {
+      const int64_t e0 = e + 2 * i;
+      const bool in0 = 2 * i < n, in1 = 2 * i + 1 < n;
+#pragma unroll
+      for (int j = 0; j < W; ++j)
+        w[j][i] = f2_pack(in0 ? param<T>(a.weight, f32, e0 * W + j) : 0.f,
+                          in1 ? param<T>(a.weight, f32, (e0 + 1) * W + j) : 0.f);
+      bias[i] = f2_pack(in0 && a.bias ? param<T>(a.bias, f32, e0) : 0.f,
+                        in1 && a.bias ? param<T>(a.bias, f32, e0 + 1) : 0.f);
     }
+  }
+  // The filter at the window's last token.
+  __device__ __forceinline__ f2 at(const f2 (&win)[W][NP], int i) const {
+    f2 v = bias[i];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-#pragma unroll
-      for (int j = 0; j < W; ++j) w[j][i] = v[(i * W + j) / VEC][(i * W + j) % VEC];
-      bias[i] = a.bias ? param<T>(a.bias, f32, e + i) : 0.f;
-    }
+    for (int j = 0; j < W; ++j) v = f2_fma(w[j][i], win[j][i], v);
+    return v;
   }
 };
 
 // The W - 1 inputs before token t of sequence s (x rows, or rows of the state).
-template <typename T, int VEC, int W>
-__device__ __forceinline__ void load_window(const ConvArgs &a, const Seq &s, int64_t t, int64_t e,
-                                            float (&win)[W][VEC]) {
+template <typename T, int NP, bool AL, int W>
+__device__ __forceinline__ void load_window(const ConvArgs &a, const Seq &s, int64_t t, int64_t e, int n,
+                                            f2 (&win)[W][NP]) {
+  using I = Io<T, NP, AL>;
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) {
     const int64_t u = t - (W - 1) + j;
     if (u >= s.bos) {
-      load_vec<VEC>(static_cast<const T *>(a.x) + u * a.d.ld_x + e, win[j]);
+      I::expand(I::load(static_cast<const T *>(a.x) + u * a.d.ld_x + e, n), win[j]);
     } else if (a.s0) {
-      load_vec<VEC>(static_cast<const T *>(a.s0) + (s.n * (W - 1) + (u - s.bos + W - 1)) * a.d.E + e, win[j]);
+      I::expand(I::load(static_cast<const T *>(a.s0) + (s.n * (W - 1) + (u - s.bos + W - 1)) * a.d.E + e, n), win[j]);
     } else {
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) win[j][i] = 0.f;
+      for (int i = 0; i < NP; ++i) win[j][i] = 0;
     }
   }
 }
 
 // States of sequences without tokens: `to` = `from` (zero where null).
-template <typename T, int VEC, int W>
-__device__ __forceinline__ void copy_empty(const ConvArgs &a, int64_t e, const void *from, void *to) {
+template <typename T, int NP, bool AL, int W>
+__device__ __forceinline__ void copy_empty(const ConvArgs &a, int64_t e, int n, const void *from, void *to) {
+  using I = Io<T, NP, AL>;
   if (!to) return;
-  for (int64_t n = 0; n < a.d.N; ++n) {
-    const SeqRange r = seq_range(a.cu, n, a.d.T);
+  for (int64_t q = 0; q < a.d.N; ++q) {
+    const SeqRange r = seq_range(a.cu, q, a.d.T);
     if (r.eos > r.bos) continue;
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
-      float v[VEC] = {};
-      const int64_t at = (n * (W - 1) + j) * a.d.E + e;
-      if (from) load_vec<VEC>(static_cast<const T *>(from) + at, v);
-      store_vec<VEC>(static_cast<T *>(to) + at, v);
+      f2 v[NP] = {};
+      const int64_t at = (q * (W - 1) + j) * a.d.E + e;
+      if (from) I::expand(I::load(static_cast<const T *>(from) + at, n), v);
+      I::store(static_cast<T *>(to) + at, n, v);
     }
   }
 }
 
-template <typename T, int VEC, int W>
+template <int NP, int W>
+__device__ __forceinline__ void shift(f2 (&win)[W][NP]) {
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+    for (int i = 0; i < NP; ++i) win[j][i] = win[j + 1][i];
+}
+
+__device__ __forceinline__ f2 f2_silu(f2 v) {
+  float lo, hi;
+  f2_split(v, lo, hi);
+  return f2_pack(lo * sigmoid_fast(lo), hi * sigmoid_fast(hi));
+}
+
+// Where a thread stands: its first channel, how many it has, its run (or row).
+struct Place {
+  int64_t e, run;
+  int n;
+  __device__ __forceinline__ Place(const ConvArgs &a, int vec) {
+    e = (int64_t)((blockIdx.x % a.tiles) * a.cx + threadIdx.x % a.cx) * vec;
+    run = (int64_t)(blockIdx.x / a.tiles) * (kThreads / a.cx) + threadIdx.x / a.cx;
+    n = a.d.E - e < vec ? (int)(a.d.E - e) : vec;
+  }
+};
+
+template <typename T, int NP, bool AL, int W>
 __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvArgs a) {
+  using I = Io<T, NP, AL>;
   if (!seqlens_ok(a.cu, a.d.N, a.M, a.status)) return;
-  const int64_t e = (int64_t)((blockIdx.x % a.tiles) * a.cx + threadIdx.x % a.cx) * VEC;
-  const int64_t run = (int64_t)(blockIdx.x / a.tiles) * (kThreads / a.cx) + threadIdx.x / a.cx;
-  if (e >= a.d.E) return;
-  if (run == 0) copy_empty<T, VEC, W>(a, e, a.s0, a.st);
-  int64_t t = run * a.L;
+  const Place p(a, 2 * NP);
+  if (p.n <= 0) return;
+  if (p.run == 0) copy_empty<T, NP, AL, W>(a, p.e, p.n, a.s0, a.st);
+  int64_t t = p.run * a.L;
   const int64_t end = t + a.L < a.M ? t + a.L : a.M;
   if (t >= end) return;
   const bool silu = a.d.activation == GDR_ACT_SILU;
-  Taps<T, VEC, W> p;
-  p.load(a, e);
-  Seq s = seq_at(a, t);
-  float win[W][VEC];
-  load_window<T, VEC, W>(a, s, t, e, win);
-  const T *x = static_cast<const T *>(a.x) + e;
-  T *y = static_cast<T *>(a.y) + e;
-  constexpr int U = 4;  // tokens whose loads are in flight together
-  for (; t < end; t += U) {
-    float in[U][VEC];
+  constexpr int U = 8;  // tokens of a batch
+  // counted from the run's first token, in 32 bits; pointers move along
+  const int len = (int)(end - t);
+  const T *x = static_cast<const T *>(a.x) + t * a.d.ld_x + p.e;
+  T *y = static_cast<T *>(a.y) + t * a.d.E + p.e;
+  typename I::Raw next[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (t + u < end) load_vec<VEC>(x + (t + u) * a.d.ld_x, in[u]);
+  for (int u = 0; u < U; ++u) {
+    if (u < len) next[u] = I::load(x, p.n);
+    x += a.d.ld_x;
+  }
+  Taps<T, NP, W> taps;
+  taps.load(a, p.e, p.n);
+  Seq s = seq_at(a, t);
+  int border = s.eos - t <= len ? (int)(s.eos - t) : len + 1;  // where the sequence ends, if it does here
+  f2 win[W][NP];
+  load_window<T, NP, AL, W>(a, s, t, p.e, p.n, win);
+  auto token = [&](const typename I::Raw &in) {
+    I::expand(in, win[W - 1]);
+    f2 o[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      o[i] = taps.at(win, i);
+      if (silu) o[i] = f2_silu(o[i]);
+    }
+    I::store(y, p.n, o);
+    y += a.d.E;
+    shift<NP, W>(win);
+  };
+  for (int q = 0; q < len; q += U) {
+    typename I::Raw in[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (t + u < end) {
-        if (t + u == s.eos) {  // the next sequence that has tokens starts here
-          s = seq_at(a, t + u);
-          load_window<T, VEC, W>(a, s, t + u, e, win);
-        }
-        float o[VEC];
+      in[u] = next[u];
+      if (q + U + u < len) next[u] = I::load(x, p.n);
+      x += a.d.ld_x;
+    }
+    if (q + U <= len && q + U < border) {  // a whole batch inside one sequence
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          win[W - 1][i] = in[u][i];
-          o[i] = p.bias[i];
+      for (int u = 0; u < U; ++u) token(in[u]);
+    } else {
 #pragma unroll
-          for (int j = 0; j < W; ++j) o[i] = fmaf(p.w[j][i], win[j][i], o[i]);
-          if (silu) o[i] *= sigmoid_fast(o[i]);
-        }
-        store_vec<VEC>(y + (t + u) * a.d.E, o);
+      for (int u = 0; u < U; ++u) {
+        if (q + u < len) {
+          if (q + u == border) {  // the next sequence that has tokens starts here
+            s = seq_at(a, t + q + u);
+            border = s.eos - t <= len ? (int)(s.eos - t) : len + 1;
+            load_window<T, NP, AL, W>(a, s, t + q + u, p.e, p.n, win);
+          }
+          token(in[u]);
+          if (a.st && q + u + 1 == border) {
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) win[j][i] = win[j + 1][i];
-        if (a.st && t + u + 1 == s.eos) {
-#pragma unroll
-          for (int j = 0; j < W - 1; ++j)
-            store_vec<VEC>(static_cast<T *>(a.st) + (s.n * (W - 1) + j) * a.d.E + e, win[j]);
+            for (int j = 0; j < W - 1; ++j)
+              I::store(static_cast<T *>(a.st) + (s.n * (W - 1) + j) * a.d.E + p.e, p.n, win[j]);
+          }
         }
       }
     }
@@ -158,108 +276,142 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvArgs a) {
 // walk goes W - 1 further, because dx_t needs g up to token t + W - 1 (zero past
 // the sequence).  At step u the gradient of token u - W + 1 is complete; where
 // that is before the sequence it is the gradient of a row of the state.
-template <typename T, int VEC, int W>
+template <typename T, int NP, bool AL, int W>
 __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvArgs a) {
+  using I = Io<T, NP, AL>;
   if (!seqlens_ok(a.cu, a.d.N, a.M, a.status)) return;
-  const int64_t e = (int64_t)((blockIdx.x % a.tiles) * a.cx + threadIdx.x % a.cx) * VEC;
-  const int64_t run = (int64_t)(blockIdx.x / a.tiles) * (kThreads / a.cx) + threadIdx.x / a.cx;
-  if (e >= a.d.E || run >= a.runs) return;
-  if (run == 0) copy_empty<T, VEC, W>(a, e, a.dst, a.st);
-  const int64_t t0 = run * a.L, end = t0 + a.L < a.M ? t0 + a.L : a.M;
+  const Place p(a, 2 * NP);
+  if (p.n <= 0 || p.run >= a.runs) return;
+  if (p.run == 0) copy_empty<T, NP, AL, W>(a, p.e, p.n, a.dst, a.st);
+  const int64_t t0 = p.run * a.L, end = t0 + a.L < a.M ? t0 + a.L : a.M;
   const bool silu = a.d.activation == GDR_ACT_SILU;
-  Taps<T, VEC, W> p;
-  p.load(a, e);
-  float dw[W][VEC], db[VEC];
+  Taps<T, NP, W> taps;
+  taps.load(a, p.e, p.n);
+  f2 dw[W][NP], db[NP];
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    db[i] = 0.f;
+  for (int i = 0; i < NP; ++i) {
+    db[i] = 0;
 #pragma unroll
-    for (int j = 0; j < W; ++j) dw[j][i] = 0.f;
+    for (int j = 0; j < W; ++j) dw[j][i] = 0;
   }
-  const T *x = static_cast<const T *>(a.x) + e, *dy = static_cast<const T *>(a.dy) + e;
-  const T *dst = a.dst ? static_cast<const T *>(a.dst) + e : nullptr;
-  T *dx = static_cast<T *>(a.y) + e, *ds0 = a.st ? static_cast<T *>(a.st) + e : nullptr;
+  const T *dst = a.dst ? static_cast<const T *>(a.dst) + p.e : nullptr;
+  T *ds0 = a.st ? static_cast<T *>(a.st) + p.e : nullptr;
+  constexpr int U = 4;
   for (int64_t ta = t0; ta < end;) {
     const Seq s = seq_at(a, ta);
     const int64_t tb = s.eos < end ? s.eos : end;
-    float win[W][VEC], g[W][VEC];
-    load_window<T, VEC, W>(a, s, ta, e, win);
+    // counted from ta, in 32 bits; pointers move along
+    const int own = (int)(tb - ta), last = own + W - 1;       // the run's own tokens; one past the last step
+    const int eos = s.eos - ta < last ? (int)(s.eos - ta) : last;  // one past the last token read
+    const int tail = s.eos - ta - (W - 1) < last ? (int)(s.eos - ta) - (W - 1) : last;  // tokens from here are in st
+    const bool begins = ta == s.bos && ds0;
+    const T *x = static_cast<const T *>(a.x) + ta * a.d.ld_x + p.e;
+    const T *dy = static_cast<const T *>(a.dy) + ta * a.d.ld_dy + p.e;
+    T *dx = static_cast<T *>(a.y) + (ta - (W - 1)) * a.d.E + p.e;  // row of the token that step 0 completes
+    f2 win[W][NP], g[W][NP];
+    typename I::Raw nx[U], ny[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (u < eos) {
+        nx[u] = I::load(x, p.n);
+        ny[u] = I::load(dy, p.n);
+      }
+      x += a.d.ld_x;
+      dy += a.d.ld_dy;
+    }
+    load_window<T, NP, AL, W>(a, s, ta, p.e, p.n, win);
 #pragma unroll
     for (int j = 0; j < W; ++j)
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) g[j][i] = 0.f;
-    constexpr int U = 4;
-    const int64_t last = tb + W - 1;  // one past the last step
-    for (int64_t t = ta; t < last; t += U) {
-      float in[U][VEC], up[U][VEC];
+      for (int i = 0; i < NP; ++i) g[j][i] = 0;
+    // g at a token, from its input and upstream gradient; dw and db where it is one of the run's own
+    auto grad = [&](const typename I::Raw &rx, const typename I::Raw &ry, bool mine) {
+      I::expand(rx, win[W - 1]);
+      I::expand(ry, g[W - 1]);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        if (silu) {
+          float lo, hi;
+          f2_split(taps.at(win, i), lo, hi);
+          const float sl = sigmoid_fast(lo), sh = sigmoid_fast(hi);
+          g[W - 1][i] = f2_mul(g[W - 1][i], f2_pack(sl * fmaf(lo, 1.f - sl, 1.f), sh * fmaf(hi, 1.f - sh, 1.f)));
+        }
+        if (mine) {
+          db[i] = f2_add(db[i], g[W - 1][i]);
+#pragma unroll
+          for (int j = 0; j < W; ++j) dw[j][i] = f2_fma(g[W - 1][i], win[j][i], dw[j][i]);
+        }
+      }
+    };
+    auto complete = [&](f2 (&o)[NP]) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        o[i] = f2_mul(taps.w[W - 1][i], g[0][i]);
+#pragma unroll
+        for (int j = 1; j < W; ++j) o[i] = f2_fma(taps.w[W - 1 - j][i], g[j][i], o[i]);
+      }
+    };
+    for (int q0 = 0; q0 < last; q0 += U) {
+      typename I::Raw cx[U], cy[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (t + u < last && t + u < s.eos) {
-          load_vec<VEC>(x + (t + u) * a.d.ld_x, in[u]);
-          load_vec<VEC>(dy + (t + u) * a.d.ld_dy, up[u]);
+        cx[u] = nx[u];
+        cy[u] = ny[u];
+        if (q0 + U + u < eos) {
+          nx[u] = I::load(x, p.n);
+          ny[u] = I::load(dy, p.n);
         }
+        x += a.d.ld_x;
+        dy += a.d.ld_dy;
+      }
+      // a whole batch of the run's own tokens that completes none before ta and none of st's
+      if (q0 >= W - 1 && q0 + U <= own && q0 + U - (W - 1) <= tail) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          grad(cx[u], cy[u], true);
+          f2 o[NP];
+          complete(o);
+          I::store(dx, p.n, o);
+          dx += a.d.E;
+          shift<NP, W>(win);
+          shift<NP, W>(g);
+        }
+        continue;
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t q = t + u;
+        const int q = q0 + u, to = q - (W - 1);  // `to` is complete now
         if (q >= last) continue;
-        if (q < s.eos) {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            win[W - 1][i] = in[u][i];
-            float v = p.bias[i];
-#pragma unroll
-            for (int j = 0; j < W; ++j) v = fmaf(p.w[j][i], win[j][i], v);
-            float gr = up[u][i];
-            if (silu) {
-              const float sg = sigmoid_fast(v);
-              gr *= sg * fmaf(v, 1.f - sg, 1.f);
-            }
-            g[W - 1][i] = gr;
-            if (q < tb) {
-              db[i] += gr;
-#pragma unroll
-              for (int j = 0; j < W; ++j) dw[j][i] = fmaf(gr, win[j][i], dw[j][i]);
-            }
-          }
+        if (q < eos) {
+          grad(cx[u], cy[u], q < own);
         } else {
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) g[W - 1][i] = 0.f;
+          for (int i = 0; i < NP; ++i) g[W - 1][i] = 0;
         }
-        const int64_t to = q - (W - 1);  // complete now
-        if (to >= ta || (ta == s.bos && ds0)) {
-          float o[VEC];
+        if (to >= 0 || begins) {
+          f2 o[NP];
+          complete(o);
+          if (dst && to >= tail) {
+            f2 v[NP];
+            I::expand(I::load(dst + (s.n * (W - 1) + (to - tail)) * a.d.E, p.n), v);
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            o[i] = 0.f;
-#pragma unroll
-            for (int j = 0; j < W; ++j) o[i] = fmaf(p.w[W - 1 - j][i], g[j][i], o[i]);
+            for (int i = 0; i < NP; ++i) o[i] = f2_add(o[i], v[i]);
           }
-          const int64_t row = to - s.eos + (W - 1);  // its row in the new state, if it is there
-          if (dst && row >= 0) {
-            float v[VEC];
-            load_vec<VEC>(dst + (s.n * (W - 1) + row) * a.d.E, v);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) o[i] += v[i];
-          }
-          if (to >= ta) store_vec<VEC>(dx + to * a.d.E, o);
-          else store_vec<VEC>(ds0 + (s.n * (W - 1) + (to - s.bos + W - 1)) * a.d.E, o);
+          if (to >= 0) I::store(dx, p.n, o);
+          else I::store(ds0 + (s.n * (W - 1) + (to + W - 1)) * a.d.E, p.n, o);
         }
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            win[j][i] = win[j + 1][i];
-            g[j][i] = g[j + 1][i];
-          }
+        dx += a.d.E;
+        shift<NP, W>(win);
+        shift<NP, W>(g);
       }
     }
     ta = tb;
   }
-  float *part = a.part + run * (W + 1) * a.d.E + e;
+  using O = Io<float, NP, AL>;
+  float *part = a.part + p.run * (W + 1) * a.d.E + p.e;
 #pragma unroll
-  for (int j = 0; j < W; ++j) store_vec<VEC>(part + j * a.d.E, dw[j]);
-  store_vec<VEC>(part + W * a.d.E, db);
+  for (int j = 0; j < W; ++j) O::store(part + j * a.d.E, p.n, dw[j]);
+  O::store(part + W * a.d.E, p.n, db);
 }
 
 // dweight [E, W] and dbias [E] from the runs' partials, added in run order.
@@ -286,41 +438,37 @@ __global__ void __launch_bounds__(256) conv_sum_kernel(const float *__restrict__
 }
 
 // One token per row: window from the slot, shifted back with the new input.
-template <typename T, int VEC, int W>
+template <typename T, int NP, bool AL, int W>
 __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvArgs a) {
-  const int64_t e = (int64_t)((blockIdx.x % a.tiles) * a.cx + threadIdx.x % a.cx) * VEC;
-  const int64_t r = (int64_t)(blockIdx.x / a.tiles) * (kThreads / a.cx) + threadIdx.x / a.cx;
-  if (e >= a.d.E || r >= a.d.B) return;
-  int64_t slot = a.slots ? a.slots[r] : r;
+  using I = Io<T, NP, AL>;
+  const Place p(a, 2 * NP);
+  if (p.n <= 0 || p.run >= a.d.B) return;
+  int64_t slot = a.slots ? a.slots[p.run] : p.run;
   if (slot >= a.d.N) {
     raise_status(a.status, GDR_ERR_SLOTS);
     slot = -1;
   }
-  T *y = static_cast<T *>(a.y) + r * a.d.E + e;
-  float o[VEC];
+  T *y = static_cast<T *>(a.y) + p.run * a.d.E + p.e;
+  f2 o[NP] = {};
   if (slot < 0) {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) o[i] = 0.f;
-    store_vec<VEC>(y, o);
+    I::store(y, p.n, o);
     return;
   }
-  T *st = static_cast<T *>(a.st) + slot * (W - 1) * a.d.E + e;
-  float win[W][VEC];
+  T *st = static_cast<T *>(a.st) + slot * (W - 1) * a.d.E + p.e;
+  f2 win[W][NP];
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) load_vec<VEC>(st + j * a.d.E, win[j]);
-  load_vec<VEC>(static_cast<const T *>(a.x) + r * a.d.ld_x + e, win[W - 1]);
-  Taps<T, VEC, W> p;
-  p.load(a, e);
+  for (int j = 0; j < W - 1; ++j) I::expand(I::load(st + j * a.d.E, p.n), win[j]);
+  I::expand(I::load(static_cast<const T *>(a.x) + p.run * a.d.ld_x + p.e, p.n), win[W - 1]);
+  Taps<T, NP, W> taps;
+  taps.load(a, p.e, p.n);
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) store_vec<VEC>(st + j * a.d.E, win[j + 1]);
+  for (int j = 0; j < W - 1; ++j) I::store(st + j * a.d.E, p.n, win[j + 1]);
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    o[i] = p.bias[i];
-#pragma unroll
-    for (int j = 0; j < W; ++j) o[i] = fmaf(p.w[j][i], win[j][i], o[i]);
-    if (a.d.activation == GDR_ACT_SILU) o[i] *= sigmoid_fast(o[i]);
+  for (int i = 0; i < NP; ++i) {
+    o[i] = taps.at(win, i);
+    if (a.d.activation == GDR_ACT_SILU) o[i] = f2_silu(o[i]);
   }
-  store_vec<VEC>(y, o);
+  I::store(y, p.n, o);
 }
 
 // Threads across channels: a power of two that covers E, a block at most.
@@ -349,29 +497,30 @@ int run_length(int64_t M, int64_t E, int vec, int lo, int hi) {
   return L;
 }
 
-// Channels of a thread: VF in the forward and the step, VB in the backward.
-template <typename T, int VF, int VB>
+// Four channels of a thread in the forward and the step.  The backward keeps
+// taps, windows, gradients and their sums of its channels: two of them.
+template <typename T, bool AL>
 int launch(ConvArgs a, Dir dir, float *dweight, float *dbias, cudaStream_t st) {
   const gdr_conv_desc &d = a.d;
-  const int VEC = dir == kBwd ? VB : VF;
-  a.cx = channel_threads(d.E, VEC);
-  const int64_t tiles = cdiv(d.E, (int64_t)VEC * a.cx), per = kThreads / a.cx;
+  const int vec = dir == kBwd ? 2 : 4;
+  a.cx = channel_threads(d.E, vec);
+  const int64_t tiles = cdiv(d.E, (int64_t)vec * a.cx), per = kThreads / a.cx;
   a.tiles = (unsigned)tiles;
   if (dir == kStep) {
     const int64_t blocks = tiles * cdiv(d.B, per);
     if (blocks > 0x7fffffff) return set_error(GDR_ERR_SHAPE, "too many rows for one launch");
     return with_taps(d.W, [&](auto w) {
-      conv_step_kernel<T, VF, decltype(w)::value><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+      conv_step_kernel<T, 2, AL, decltype(w)::value><<<(unsigned)blocks, kThreads, 0, st>>>(a);
       return launched("conv_step_kernel");
     });
   }
-  a.L = dir == kFwd ? run_length(a.M, d.E, VEC, 8, 32) : run_length(a.M, d.E, VEC, 16, 128);
+  a.L = dir == kFwd ? run_length(a.M, d.E, vec, 8, 64) : run_length(a.M, d.E, vec, 16, 128);
   a.runs = std::max<int64_t>(1, cdiv(a.M, a.L));
   const int64_t blocks = tiles * cdiv(a.runs, per);
   if (blocks > 0x7fffffff) return set_error(GDR_ERR_SHAPE, "too many tokens for one launch");
   if (dir == kFwd) {
     return with_taps(d.W, [&](auto w) {
-      conv_fwd_kernel<T, VF, decltype(w)::value><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+      conv_fwd_kernel<T, 2, AL, decltype(w)::value><<<(unsigned)blocks, kThreads, 0, st>>>(a);
       return launched("conv_fwd_kernel");
     });
   }
@@ -380,7 +529,7 @@ int launch(ConvArgs a, Dir dir, float *dweight, float *dbias, cudaStream_t st) {
   if (rc != GDR_OK) return rc;
   a.part = (float *)base;
   rc = with_taps(d.W, [&](auto w) {
-    conv_bwd_kernel<T, VB, decltype(w)::value><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+    conv_bwd_kernel<T, 1, AL, decltype(w)::value><<<(unsigned)blocks, kThreads, 0, st>>>(a);
     return launched("conv_bwd_kernel");
   });
   if (rc == GDR_OK) {
@@ -417,16 +566,14 @@ int run(ConvArgs a, Dir dir, float *dweight, float *dbias, void *stream) {
   a.M = a.d.B * a.d.T;
   a.status = current_status_word(&rc);
   if (!a.status) return rc;
-  const int64_t E = a.d.E;
-  const bool vec = E % 8 == 0 && a.d.ld_x % 8 == 0 && a.d.ld_dy % 8 == 0 && is_aligned16(a.x) && is_aligned16(a.s0) &&
-                   is_aligned16(a.dy) && is_aligned16(a.dst) && is_aligned16(a.y) && is_aligned16(a.st) && is_aligned16(a.weight);
+  const bool al = a.d.E % 4 == 0 && a.d.ld_x % 4 == 0 && a.d.ld_dy % 4 == 0 && is_aligned16(a.x) &&
+                  is_aligned16(a.s0) && is_aligned16(a.dy) && is_aligned16(a.dst) && is_aligned16(a.y) &&
+                  is_aligned16(a.st);
   cudaStream_t st = (cudaStream_t)stream;
-  if (a.d.dtype == GDR_BF16) {
-    if (!vec) return launch<__nv_bfloat16, 1, 1>(a, dir, dweight, dbias, st);
-    // the backward keeps taps, windows and sums of its channels in registers: four channels fit, eight do not
-    return launch<__nv_bfloat16, 8, 4>(a, dir, dweight, dbias, st);
-  }
-  return vec ? launch<float, 4, 4>(a, dir, dweight, dbias, st) : launch<float, 1, 1>(a, dir, dweight, dbias, st);
+  if (a.d.dtype == GDR_BF16)
+    return al ? launch<__nv_bfloat16, true>(a, dir, dweight, dbias, st)
+              : launch<__nv_bfloat16, false>(a, dir, dweight, dbias, st);
+  return al ? launch<float, true>(a, dir, dweight, dbias, st) : launch<float, false>(a, dir, dweight, dbias, st);
 }
 
 }  // namespace

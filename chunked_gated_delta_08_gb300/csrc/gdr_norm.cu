@@ -251,91 +251,193 @@ __global__ void __launch_bounds__(256) norm_fwd_long_kernel(NormArgs a) {
   }
 }
 
-// Backward, row in registers.  A block takes rows b, b + grid, ...; each thread
-// keeps the weight gradient of its own columns in registers over all of them
-// and leaves it in row b of the partials, which col_sum_kernel adds in order.
-template <typename T, typename R, int NT, int VEC, int NV>
-__global__ void __launch_bounds__(NT) norm_bwd_kernel(NormArgs a) {
-  __shared__ float red[2][32];
-  const int tid = threadIdx.x;
-  const int64_t E = a.d.E;
-  const bool wf32 = a.d.weight_dtype == GDR_F32;
-  float w[NV][VEC], dw[NV][VEC];
+// Backward.  A block takes rows b, b + grid, ...  Each thread owns eight columns
+// and copies its own part of the next row into its own shared memory while it
+// works on this one: 16-byte asynchronous copies that cost no registers and, as
+// no other thread reads them, no barrier.  Held in registers instead, the next
+// row took the kernel from two blocks of 512 threads per multiprocessor to one,
+// or spilled.  The weight gradient of the thread's columns stays in registers
+// over all its rows and ends in row b of the partials, which col_sum_kernel adds
+// in order.
+__device__ __forceinline__ void copy_async(void *smem, const void *global) {
+  const uint32_t to = (uint32_t)__cvta_generic_to_shared(smem);
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(global) : "memory");
+}
+
+// A thread's eight elements of a row in shared memory: 16-byte pieces, NT apart.
+template <typename T, int NT>
+struct Slot {
+  static constexpr int kPieces = sizeof(T) / 2;
+  uint4 v[kPieces][NT];
+  __device__ __forceinline__ void fetch(const T *p, int tid) {
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int64_t c = col_of<NT, VEC, NV>(tid, k);
+    for (int i = 0; i < kPieces; ++i) copy_async(&v[i][tid], reinterpret_cast<const uint4 *>(p) + i);
+  }
+  __device__ __forceinline__ void get(int tid, float (&o)[8]) const {
+    if constexpr (kPieces == 1) {
+      unpack8(v[0][tid], o);
+    } else {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) w[k][i] = dw[k][i] = 0.f;
-    if (c < E) {
-      if (wf32) load_vec<VEC>(static_cast<const float *>(a.weight) + c, w[k]);
-      else load_vec<VEC>(static_cast<const T *>(a.weight) + c, w[k]);
+      for (int i = 0; i < 2; ++i) {
+        const uint4 u = v[i][tid];
+        o[4 * i] = __uint_as_float(u.x);
+        o[4 * i + 1] = __uint_as_float(u.y);
+        o[4 * i + 2] = __uint_as_float(u.z);
+        o[4 * i + 3] = __uint_as_float(u.w);
+      }
     }
   }
+  __device__ __forceinline__ void put(int tid, const float (&o)[8]) {  // T float only
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      v[i][tid] = make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]), __float_as_uint(o[4 * i + 2]),
+                             __float_as_uint(o[4 * i + 3]));
+  }
+};
+template <typename T, typename R, int NT>
+struct BwdShared {
+  Slot<float, NT> w;
+  struct Row {
+    Slot<T, NT> dy;
+    Slot<R, NT> s, ds;
+  } row[2];
+  float red[2][2][32];
+};
+
+template <typename T, typename R, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) norm_bwd_kernel(NormArgs a) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  BwdShared<T, R, NT> &sm = *reinterpret_cast<BwdShared<T, R, NT> *>(smem_raw);
+  const int tid = threadIdx.x;
+  const int64_t E = a.d.E;
+  const int c = tid * 8;
+  const bool in = c < E;
+  float dw[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) dw[i] = 0.f;
+  auto fetch = [&](int64_t m, int buf) {
+    if (!in) return;
+    auto &row = sm.row[buf];
+    row.dy.fetch(static_cast<const T *>(a.x) + m * a.d.ld_x + c, tid);
+    row.s.fetch(static_cast<const R *>(a.res) + m * a.d.ld_res + c, tid);
+    if (a.ds) row.ds.fetch(static_cast<const R *>(a.ds) + m * a.d.ld_ds + c, tid);
+  };
+  if (blockIdx.x < a.d.M) fetch(blockIdx.x, 0);
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  if (in) {
+    float w[8];
+    if (a.d.weight_dtype == GDR_F32) load8(static_cast<const float *>(a.weight) + c, w);
+    else load8(static_cast<const T *>(a.weight) + c, w);
+    sm.w.put(tid, w);
+  }
+  int buf = 0;
   for (int64_t m = blockIdx.x; m < a.d.M; m += gridDim.x) {
-    const T *dy = static_cast<const T *>(a.x) + m * a.d.ld_x;
-    const R *s = static_cast<const R *>(a.res) + m * a.d.ld_res;
-    const R *ds = static_cast<const R *>(a.ds) + (a.ds ? m * a.d.ld_ds : 0);
-    float v[NV][VEC], g[NV][VEC], up[NV][VEC];
+    if (m + gridDim.x < a.d.M) fetch(m + gridDim.x, buf ^ 1);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group 1;" ::: "memory");  // this row is here, the next one on its way
+    const auto &row = sm.row[buf];
     float ss = 0.f, ps = 0.f;
+    if (in) {
+      float v[8], g[8], w[8];
+      row.s.get(tid, v);
+      row.dy.get(tid, g);
+      sm.w.get(tid, w);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int64_t c = col_of<NT, VEC, NV>(tid, k);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) v[k][i] = g[k][i] = up[k][i] = 0.f;
-      if (c < E) {
-        load_vec<VEC>(s + c, v[k]);
-        load_vec<VEC>(dy + c, g[k]);
-        if (a.ds) load_vec<VEC>(ds + c, up[k]);
+      for (int i = 0; i < 8; ++i) {
+        ss = fmaf(v[i], v[i], ss);
+        ps = fmaf(v[i] * w[i], g[i], ps);
       }
     }
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        ss = fmaf(v[k][i], v[k][i], ss);
-        ps = fmaf(v[k][i] * w[k][i], g[k][i], ps);
-      }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       ss += __shfl_xor_sync(0xffffffffu, ss, o);
       ps += __shfl_xor_sync(0xffffffffu, ps, o);
     }
-    if constexpr (NT > 32) {
-      __syncthreads();
+    if constexpr (NT > 32) {  // two buffers: one barrier a row
       if ((tid & 31) == 0) {
-        red[0][tid >> 5] = ss;
-        red[1][tid >> 5] = ps;
+        sm.red[buf][0][tid >> 5] = ss;
+        sm.red[buf][1][tid >> 5] = ps;
       }
       __syncthreads();
-      ss = red[0][0];
-      ps = red[1][0];
-#pragma unroll
+      ss = sm.red[buf][0][0];
+      ps = sm.red[buf][1][0];
+#pragma unroll 4
       for (int i = 1; i < NT / 32; ++i) {
-        ss += red[0][i];
-        ps += red[1][i];
+        ss += sm.red[buf][0][i];
+        ps += sm.red[buf][1][i];
       }
     }
     const float rho = rsqrtf(ss / (float)E + a.d.eps);
     const float mix = rho * rho * (ps / (float)E);
+    if (in) {
+      float v[8], g[8], w[8], o[8];
+      row.s.get(tid, v);
+      row.dy.get(tid, g);
+      sm.w.get(tid, w);
+      if (a.ds) {
+        row.ds.get(tid, o);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        dw[i] = fmaf(g[i] * rho, v[i], dw[i]);
+        o[i] = fmaf(rho, fmaf(w[i], g[i], -v[i] * mix), o[i]);
+      }
+      if (a.y) store8(static_cast<T *>(a.y) + m * E + c, o);
+      if (a.s) store8(static_cast<R *>(a.s) + m * E + c, o);
+    }
+    buf ^= 1;
+  }
+  if (a.scale && in) store8(a.scale + (int64_t)blockIdx.x * E + c, dw);
+}
+
+// The same for rows that allow no 16-byte accesses: NV single columns of a thread.
+template <typename T, typename R, int NT, int NV>
+__global__ void __launch_bounds__(NT) norm_bwd_scalar_kernel(NormArgs a) {
+  __shared__ float red[2][32];
+  const int tid = threadIdx.x;
+  const int64_t E = a.d.E;
+  float w[NV], dw[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int64_t c = k * NT + tid;
+    dw[k] = 0.f;
+    w[k] = c < E ? param<T>(a.weight, a.d.weight_dtype == GDR_F32, c) : 0.f;
+  }
+  for (int64_t m = blockIdx.x; m < a.d.M; m += gridDim.x) {
+    const T *dy = static_cast<const T *>(a.x) + m * a.d.ld_x;
+    const R *s = static_cast<const R *>(a.res) + m * a.d.ld_res;
+    const R *ds = static_cast<const R *>(a.ds) + (a.ds ? m * a.d.ld_ds : 0);
+    float v[NV], g[NV], up[NV];
+    float ss = 0.f, ps = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int64_t c = col_of<NT, VEC, NV>(tid, k);
+      const int64_t c = k * NT + tid;
+      v[k] = c < E ? to_f32(s[c]) : 0.f;
+      g[k] = c < E ? to_f32(dy[c]) : 0.f;
+      up[k] = c < E && a.ds ? to_f32(ds[c]) : 0.f;
+      ss = fmaf(v[k], v[k], ss);
+      ps = fmaf(v[k] * w[k], g[k], ps);
+    }
+    ss = row_reduce<NT, false>(ss, red[0]);
+    ps = row_reduce<NT, false>(ps, red[1]);
+    const float rho = rsqrtf(ss / (float)E + a.d.eps), mix = rho * rho * (ps / (float)E);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        dw[k][i] = fmaf(g[k][i] * rho, v[k][i], dw[k][i]);
-        g[k][i] = fmaf(rho, fmaf(w[k][i], g[k][i], -v[k][i] * mix), up[k][i]);
-      }
-      if (c < E) {
-        if (a.y) store_vec<VEC>(static_cast<T *>(a.y) + m * E + c, g[k]);
-        if (a.s) store_vec<VEC>(static_cast<R *>(a.s) + m * E + c, g[k]);
-      }
+    for (int k = 0; k < NV; ++k) {
+      const int64_t c = k * NT + tid;
+      dw[k] = fmaf(g[k] * rho, v[k], dw[k]);
+      const float o = fmaf(rho, fmaf(w[k], g[k], -v[k] * mix), up[k]);
+      if (c < E && a.y) static_cast<T *>(a.y)[m * E + c] = from_f32<T>(o);
+      if (c < E && a.s) static_cast<R *>(a.s)[m * E + c] = from_f32<R>(o);
     }
   }
   if (a.scale) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int64_t c = col_of<NT, VEC, NV>(tid, k);
-      if (c < E) store_vec<VEC>(a.scale + (int64_t)blockIdx.x * E + c, dw[k]);
+      const int64_t c = k * NT + tid;
+      if (c < E) a.scale[(int64_t)blockIdx.x * E + c] = dw[k];
     }
   }
 }
@@ -409,7 +511,8 @@ int launch_bwd(NormArgs a, float *dweight, cudaStream_t st) {
   const bool vec = E % 8 == 0 && a.d.ld_x % 8 == 0 && a.d.ld_res % 8 == 0 && (!a.ds || a.d.ld_ds % 8 == 0) &&
                    is_aligned16(a.x) && is_aligned16(a.res) && is_aligned16(a.ds) && is_aligned16(a.weight) && is_aligned16(a.y) &&
                    is_aligned16(a.s);
-  const int64_t most = E <= 256 ? 8 * kSMs : 4 * kSMs;  // blocks, and rows of partials
+  // blocks, and rows of partials: 1024 threads of them on each multiprocessor
+  const int64_t most = kSMs * (E <= 256 ? 16 : E <= 1024 ? 8 : E <= 2048 ? 4 : E <= 4096 ? 2 : vec && E <= 8192 ? 1 : 4);
   const unsigned grid = (unsigned)std::min<int64_t>(a.d.M, most);
   char *base = nullptr;
   int rc;
@@ -418,17 +521,22 @@ int launch_bwd(NormArgs a, float *dweight, cudaStream_t st) {
       return rc;
     a.scale = (float *)base;
   }
-  if (vec) {
-    if (E <= 256) norm_bwd_kernel<T, R, 32, 8, 1><<<grid, 32, 0, st>>>(a);
-    else if (E <= 1024) norm_bwd_kernel<T, R, 128, 8, 1><<<grid, 128, 0, st>>>(a);
-    else if (E <= 2048) norm_bwd_kernel<T, R, 256, 8, 1><<<grid, 256, 0, st>>>(a);
-    else if (E <= 4096) norm_bwd_kernel<T, R, 512, 8, 1><<<grid, 512, 0, st>>>(a);
-    else if (E <= 8192) norm_bwd_kernel<T, R, 1024, 8, 1><<<grid, 1024, 0, st>>>(a);
-    else norm_bwd_long_kernel<T, R><<<grid, 256, 0, st>>>(a);
+  if (vec && E <= 8192) {
+    auto go = [&](auto nt) {
+      constexpr int NT = decltype(nt)::value, smem = sizeof(BwdShared<T, R, NT>);
+      const cudaError_t e =
+          cudaFuncSetAttribute(norm_bwd_kernel<T, R, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e == cudaSuccess) norm_bwd_kernel<T, R, NT><<<grid, NT, smem, st>>>(a);
+    };
+    if (E <= 256) go(std::integral_constant<int, 32>{});
+    else if (E <= 1024) go(std::integral_constant<int, 128>{});
+    else if (E <= 2048) go(std::integral_constant<int, 256>{});
+    else if (E <= 4096) go(std::integral_constant<int, 512>{});
+    else go(std::integral_constant<int, 1024>{});
   } else {
-    if (E <= 256) norm_bwd_kernel<T, R, 32, 1, 8><<<grid, 32, 0, st>>>(a);
-    else if (E <= 2048) norm_bwd_kernel<T, R, 256, 1, 8><<<grid, 256, 0, st>>>(a);
-    else if (E <= 4096) norm_bwd_kernel<T, R, 512, 1, 8><<<grid, 512, 0, st>>>(a);
+    if (E <= 256) norm_bwd_scalar_kernel<T, R, 32, 8><<<grid, 32, 0, st>>>(a);
+    else if (E <= 2048) norm_bwd_scalar_kernel<T, R, 256, 8><<<grid, 256, 0, st>>>(a);
+    else if (E <= 4096) norm_bwd_scalar_kernel<T, R, 512, 8><<<grid, 512, 0, st>>>(a);
     else norm_bwd_long_kernel<T, R><<<grid, 256, 0, st>>>(a);
   }
   rc = launched("norm_bwd_kernel");
