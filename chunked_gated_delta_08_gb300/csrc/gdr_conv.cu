@@ -183,12 +183,6 @@ __device__ __forceinline__ void shift(f2 (&win)[W][NP]) {
     for (int i = 0; i < NP; ++i) win[j][i] = win[j + 1][i];
 }
 
-__device__ __forceinline__ f2 f2_silu(f2 v) {
-  float lo, hi;
-  f2_split(v, lo, hi);
-  return f2_pack(lo * sigmoid_fast(lo), hi * sigmoid_fast(hi));
-}
-
 // Where a thread stands: its first channel, how many it has, its run (or row).
 struct Place {
   int64_t e, run;
@@ -330,12 +324,7 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvArgs a) {
       I::expand(ry, g[W - 1]);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        if (silu) {
-          float lo, hi;
-          f2_split(taps.at(win, i), lo, hi);
-          const float sl = sigmoid_fast(lo), sh = sigmoid_fast(hi);
-          g[W - 1][i] = f2_mul(g[W - 1][i], f2_pack(sl * fmaf(lo, 1.f - sl, 1.f), sh * fmaf(hi, 1.f - sh, 1.f)));
-        }
+        if (silu) g[W - 1][i] = f2_mul(g[W - 1][i], f2_silu_grad(taps.at(win, i)));
         if (mine) {
           db[i] = f2_add(db[i], g[W - 1][i]);
 #pragma unroll
@@ -414,24 +403,25 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvArgs a) {
   O::store(part + W * a.d.E, p.n, db);
 }
 
-// dweight [E, W] and dbias [E] from the runs' partials, added in run order.
-__global__ void __launch_bounds__(256) conv_sum_kernel(const float *__restrict__ part, int64_t runs, int64_t E, int W,
-                                                       float *__restrict__ dweight, float *__restrict__ dbias,
-                                                       SeqCheck seqs) {
-  __shared__ float sm[8][32];
+// dweight [E, W] and dbias [E] from the runs' partials: 32 columns a block, 32
+// interleaved sets of runs, each added in order, then the sets in order.
+__global__ void __launch_bounds__(1024) conv_sum_kernel(const float *__restrict__ part, int64_t runs, int64_t E, int W,
+                                                        float *__restrict__ dweight, float *__restrict__ dbias,
+                                                        SeqCheck seqs) {
+  __shared__ float sm[32][33];
   if (!seqlens_ok(seqs)) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, j = blockIdx.y;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float acc = 0.f;
   if (c < E) {
-#pragma unroll 8
-    for (int64_t r = w; r < runs; r += 8) acc += part[(r * (W + 1) + j) * E + c];
+#pragma unroll 4
+    for (int64_t r = w; r < runs; r += 32) acc += part[(r * (W + 1) + j) * E + c];
   }
   sm[w][lane] = acc;
   __syncthreads();
   if (w == 0 && c < E) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) acc += sm[i][lane];
+    for (int i = 1; i < 32; ++i) acc += sm[i][lane];
     if (j < W) dweight[c * W + j] = acc;
     else if (dbias) dbias[c] = acc;
   }
@@ -533,7 +523,7 @@ int launch(ConvArgs a, Dir dir, float *dweight, float *dbias, cudaStream_t st) {
     return launched("conv_bwd_kernel");
   });
   if (rc == GDR_OK) {
-    conv_sum_kernel<<<dim3((unsigned)cdiv(d.E, 32), (unsigned)(d.W + (dbias ? 1 : 0))), 256, 0, st>>>(
+    conv_sum_kernel<<<dim3((unsigned)cdiv(d.E, 32), (unsigned)(d.W + (dbias ? 1 : 0))), 1024, 0, st>>>(
         a.part, a.runs, d.E, (int)d.W, dweight, dbias, SeqCheck{a.cu, d.N, a.M, a.status});
     rc = launched("conv_sum_kernel");
   }

@@ -13,6 +13,65 @@
 
 namespace gdr {
 
+typedef unsigned long long f2;  // two fp32 values for the packed instructions
+__device__ __forceinline__ f2 f2_pack(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void f2_split(f2 v, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ f2 f2_ex2(f2 v) {
+  float lo, hi;
+  f2_split(v, lo, hi);
+  return f2_pack(ex2(lo), ex2(hi));
+}
+__device__ __forceinline__ f2 f2_rcp(f2 v) {
+  float lo, hi;
+  f2_split(v, lo, hi);
+  return f2_pack(rcp(lo), rcp(hi));
+}
+__device__ __forceinline__ f2 f2_both(float x) { return f2_pack(x, x); }
+
+// 1 / (1 + e^-x), to a few units in the last place; 0 and 1 at the ends, NaN for NaN.
+__device__ __forceinline__ float sigmoid_fast(float x) { return rcp(1.f + ex2(x * -kLog2e)); }
+__device__ __forceinline__ f2 f2_sigmoid(f2 v) {
+  return f2_rcp(f2_add(f2_both(1.f), f2_ex2(f2_mul(v, f2_both(-kLog2e)))));
+}
+// x sigmoid(x) and its derivative s + x s (1 - s).
+__device__ __forceinline__ f2 f2_silu(f2 v) { return f2_mul(v, f2_sigmoid(v)); }
+__device__ __forceinline__ f2 f2_silu_grad(f2 v) {
+  const f2 s = f2_sigmoid(v);
+  return f2_fma(f2_mul(v, s), f2_fma(s, f2_both(-1.f), f2_both(1.f)), s);
+}
+
 // Eight consecutive elements as fp32; p is 16-byte aligned (32 for fp32 is not needed: two loads).
 __device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
   const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
@@ -87,9 +146,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// 1 / (1 + e^-x), to a few units in the last place; 0 and 1 at the ends, NaN for NaN.
-__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-
 // Whether cu_seqlens is non-decreasing from 0 to T.  Every thread of the block
 // calls it and gets the same answer; the first violation seen is recorded.
 __device__ __forceinline__ bool seqlens_ok(const int64_t *cu, int64_t N, int64_t T, int *status) {
@@ -102,43 +158,6 @@ __device__ __forceinline__ bool seqlens_ok(const int64_t *cu, int64_t N, int64_t
 }
 
 __device__ __forceinline__ bool seqlens_ok(const SeqCheck &s) { return seqlens_ok(s.cu, s.N, s.T, s.status); }
-
-typedef unsigned long long f2;  // two fp32 values for the packed instructions
-__device__ __forceinline__ f2 f2_pack(float lo, float hi) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void f2_split(f2 v, float &lo, float &hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ f2 f2_ex2(f2 v) {
-  float lo, hi;
-  f2_split(v, lo, hi);
-  return f2_pack(ex2(lo), ex2(hi));
-}
-
-constexpr float kLog2e = 1.4426950408889634f;
 
 // The sequence of flat token t (the last n with first token <= t: empty ones
 // are passed over).  Dense layout: sequences of T tokens each.

@@ -57,9 +57,12 @@ __device__ __forceinline__ float row_reduce(float v, float *red) {
     __syncthreads();  // the previous reduction's readers are done
     if (lane == 0) red[warp] = v;
     __syncthreads();
-    v = red[0];
+    v = 0.f;  // below every absolute value
 #pragma unroll
-    for (int i = 1; i < NT / 32; ++i) v = MAX ? max_nan(v, red[i]) : v + red[i];
+    for (int i = 0; i < NT / 128; ++i) {  // four warps in each 16-byte load
+      const float4 q = reinterpret_cast<const float4 *>(red)[i];
+      v = MAX ? max_nan(max_nan(v, max_nan(q.x, q.y)), max_nan(q.z, q.w)) : v + ((q.x + q.y) + (q.z + q.w));
+    }
   }
   return v;
 }
@@ -76,7 +79,7 @@ __device__ __forceinline__ int64_t col_of(int tid, int k) {
 // One row per NT threads; blocks of 256 threads take 256 / NT rows when NT is a warp.
 template <typename T, typename R, int NT, int VEC, int NV, int QUANT, bool RES>
 __global__ void __launch_bounds__(NT == 32 ? 256 : NT) norm_fwd_kernel(NormArgs a) {
-  __shared__ float red[32];
+  __shared__ __align__(16) float red[32];
   const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
   const int64_t m = NT == 32 ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
   if (m >= a.d.M) return;  // whole warps, and only where no barrier follows (NT == 32)
@@ -194,7 +197,7 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) norm_fwd_kernel(NormArgs 
 // One block of 256 threads per row; scale groups are taken a warp at a time.
 template <typename T, typename R, bool RES>
 __global__ void __launch_bounds__(256) norm_fwd_long_kernel(NormArgs a) {
-  __shared__ float red[32];
+  __shared__ __align__(16) float red[32];
   const int64_t m = blockIdx.x, E = a.d.E;
   const T *x = static_cast<const T *>(a.x) + m * a.d.ld_x;
   const R *res = static_cast<const R *>(a.res) + (RES ? m * a.d.ld_res : 0);
@@ -301,7 +304,7 @@ struct BwdShared {
     Slot<T, NT> dy;
     Slot<R, NT> s, ds;
   } row[2];
-  float red[2][2][32];
+  float2 red[2][32];
 };
 
 template <typename T, typename R, int NT>
@@ -354,17 +357,16 @@ __global__ void __launch_bounds__(NT, 1024 / NT) norm_bwd_kernel(NormArgs a) {
       ps += __shfl_xor_sync(0xffffffffu, ps, o);
     }
     if constexpr (NT > 32) {  // two buffers: one barrier a row
-      if ((tid & 31) == 0) {
-        sm.red[buf][0][tid >> 5] = ss;
-        sm.red[buf][1][tid >> 5] = ps;
-      }
+      constexpr int NW = NT / 32;
+      if ((tid & 31) == 0) sm.red[buf][tid >> 5] = make_float2(ss, ps);
       __syncthreads();
-      ss = sm.red[buf][0][0];
-      ps = sm.red[buf][1][0];
-#pragma unroll 4
-      for (int i = 1; i < NT / 32; ++i) {
-        ss += sm.red[buf][0][i];
-        ps += sm.red[buf][1][i];
+      const float2 q = sm.red[buf][tid & (NW - 1)];
+      ss = q.x;
+      ps = q.y;
+#pragma unroll
+      for (int o = NW / 2; o > 0; o >>= 1) {
+        ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        ps += __shfl_xor_sync(0xffffffffu, ps, o);
       }
     }
     const float rho = rsqrtf(ss / (float)E + a.d.eps);
@@ -396,7 +398,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) norm_bwd_kernel(NormArgs a) {
 // The same for rows that allow no 16-byte accesses: NV single columns of a thread.
 template <typename T, typename R, int NT, int NV>
 __global__ void __launch_bounds__(NT) norm_bwd_scalar_kernel(NormArgs a) {
-  __shared__ float red[2][32];
+  __shared__ __align__(16) float red[2][32];
   const int tid = threadIdx.x;
   const int64_t E = a.d.E;
   float w[NV], dw[NV];
@@ -446,7 +448,7 @@ __global__ void __launch_bounds__(NT) norm_bwd_scalar_kernel(NormArgs a) {
 // kept in this block's own row of global scratch.
 template <typename T, typename R>
 __global__ void __launch_bounds__(256) norm_bwd_long_kernel(NormArgs a) {
-  __shared__ float red[32];
+  __shared__ __align__(16) float red[32];
   const int64_t E = a.d.E;
   const bool wf32 = a.d.weight_dtype == GDR_F32;
   float *dw = a.scale ? a.scale + (int64_t)blockIdx.x * E : nullptr;
@@ -564,26 +566,27 @@ int validate(const gdr_norm_desc *d) {
   return GDR_OK;
 }
 
-// Column sums of part [rows, cols], rows ld apart: 32 columns a block, eight
-// interleaved runs of rows added in order.  Columns come in groups of `width`,
-// of which the first `keep` go to out, close together.
-__global__ void __launch_bounds__(256) col_sum_kernel(const float *__restrict__ part, int64_t rows, int64_t ld,
-                                                      int64_t cols, int64_t width, int64_t keep,
-                                                      float *__restrict__ out, SeqCheck seqs) {
-  __shared__ float sm[8][32];
+// Column sums of part [rows, cols], rows ld apart: 32 columns a block, 32
+// interleaved sets of rows, each added in order, then the sets in order.
+// Columns come in groups of `width`, of which the first `keep` go to out, close
+// together.
+__global__ void __launch_bounds__(1024) col_sum_kernel(const float *__restrict__ part, int64_t rows, int64_t ld,
+                                                       int64_t cols, int64_t width, int64_t keep,
+                                                       float *__restrict__ out, SeqCheck seqs) {
+  __shared__ float sm[32][33];
   if (!seqlens_ok(seqs)) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float acc = 0.f;
   if (c < cols) {
-#pragma unroll 8
-    for (int64_t r = w; r < rows; r += 8) acc += part[r * ld + c];
+#pragma unroll 4
+    for (int64_t r = w; r < rows; r += 32) acc += part[r * ld + c];
   }
   sm[w][lane] = acc;
   __syncthreads();
   if (w == 0 && c < cols && c % width < keep) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) acc += sm[i][lane];
+    for (int i = 1; i < 32; ++i) acc += sm[i][lane];
     out[c / width * keep + c % width] = acc;
   }
 }
@@ -592,7 +595,7 @@ __global__ void __launch_bounds__(256) col_sum_kernel(const float *__restrict__ 
 
 int launch_col_sum(const float *part, int64_t rows, int64_t ld, int64_t cols, int64_t width, int64_t keep, float *out,
                    const SeqCheck &seqs, cudaStream_t stream) {
-  col_sum_kernel<<<(unsigned)cdiv(cols, 32), 256, 0, stream>>>(part, rows, ld, cols, width, keep, out, seqs);
+  col_sum_kernel<<<(unsigned)cdiv(cols, 32), 1024, 0, stream>>>(part, rows, ld, cols, width, keep, out, seqs);
   return launched("col_sum_kernel");
 }
 

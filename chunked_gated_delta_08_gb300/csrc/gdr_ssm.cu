@@ -17,37 +17,72 @@
 namespace gdr {
 namespace {
 
-template <int SL>
+template <typename P>
 struct __align__(16) FwdShared {
-  float delta[kTile][Place<SL>::CB], x[kTile][Place<SL>::CB], gate[kTile][Place<SL>::CB];
-  float2 b[kTile * Place<SL>::SP], c[kTile * Place<SL>::SP];
+  float delta[kTile][P::CB], x[kTile][P::CB], gate[kTile][P::CB];
+  float bias[P::CB];
+  float2 b[kTile * P::SP], c[kTile * P::SP];
   Borders<kTile> bd;
+};
+
+// What a thread stages of a tile, as loaded.
+template <typename T, bool VEC, bool MAIN, int COUNT, int NB>
+struct FwdTile {
+  Raw8<T, VEC> x[COUNT], dt[COUNT], z[MAIN ? COUNT : 1];
+  T b[NB], c[MAIN ? NB : 1];
 };
 
 // MAIN: y and ht from the states that enter the chunks (a.hloc, zero where
 // null).  Else: the chunk's own state and sum of delta.
-template <typename T, int SL, int VEC, bool MAIN>
-__global__ void __launch_bounds__(kSsmThreads) ssm_fwd_kernel(SsmArgs a) {
+template <typename T, int SL, bool VEC, bool MAIN>
+__global__ void __launch_bounds__(kSsmThreads, 4) ssm_fwd_kernel(SsmArgs a) {
   using P = Place<SL>;
-  __shared__ FwdShared<SL> sm;
+  constexpr int NB = kTile * P::SP / kSsmThreads;
+  // bf16 tiles are loaded while the one before is computed; fp32 ones would take twice the registers
+  constexpr bool kAhead = VEC && sizeof(T) == 2;
+  __shared__ FwdShared<P> sm;
   if (!seqlens_ok(a.cu, a.d.N, a.M, a.status)) return;
   const P p(a);
-  if (MAIN && p.chunk == 0) copy_empty_states<SL>(a, p, a.h0, a.ht);
+  if (MAIN && p.chunk == 0) copy_empty_states(a, p, a.h0, a.ht);
+  const Stager<kTile, P::CB, kSsmThreads> st(p);
+  FwdTile<T, VEC, MAIN, st.kCount, NB> tile;
   States A, h;
-  load_a<SL>(a, p, A);
-  load_chunk<SL>(a, p, MAIN ? a.hloc : nullptr, p.chunk, h);
   const int64_t begin = p.chunk * a.L, end = begin + a.L < a.M ? begin + a.L : a.M;
+  auto fetch = [&](int64_t t0) {
+    const int nt = end - t0 < kTile ? (int)(end - t0) : kTile;
+    const int64_t e = p.e0 + st.col;
+#pragma unroll
+    for (int k = 0; k < st.kCount; ++k) {
+      const int n = st.has(k) && st.token(k) < nt ? st.n : 0;
+      const int64_t t = t0 + st.token(k);
+      tile.x[k].load(static_cast<const T *>(a.x) + t * a.d.ld_x + e, n);
+      tile.dt[k].load(static_cast<const T *>(a.dt) + t * a.d.ld_dt + e, n);
+      if (MAIN && a.z) tile.z[k].load(static_cast<const T *>(a.z) + t * a.d.ld_z + e, n);
+    }
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int i = k * kSsmThreads + threadIdx.x, t = i / P::SP, s = i % P::SP;
+      const bool in = t < nt && s < a.d.S;
+      const int64_t at = p.g * a.d.S + s;
+      tile.b[k] = in ? static_cast<const T *>(a.b)[(t0 + t) * a.d.ld_b + at] : from_f32<T>(0.f);
+      if (MAIN) tile.c[k] = in ? static_cast<const T *>(a.c)[(t0 + t) * a.d.ld_c + at] : from_f32<T>(0.f);
+    }
+  };
+  if (kAhead && begin < end) fetch(begin);
+  stage_bias<P::CB, kSsmThreads>(a, p, sm.bias);
+  load_a(a, p, A);
+  load_chunk(a, p, MAIN ? a.hloc : nullptr, p.chunk, h);
   const int mine = p.sl & 3;  // of the thread's four channels, the one whose output it finishes
   const int64_t e_mine = p.e0 + p.col + mine;
   const bool owner = p.sl < 4 && e_mine < p.e_end;
   const float skip = MAIN && a.dskip && owner ? a.dskip[e_mine] : 0.f;
-  T *y = static_cast<T *>(a.y) + e_mine;
+  T *y = static_cast<T *>(a.y) + begin * a.d.E + e_mine;
   f2 sum[2] = {0, 0};
   bool started = false;  // a sequence starts in this chunk
 
-  auto token = [&](int64_t t0, int t) {
-    const Pairs delta(&sm.delta[t][p.col]);
-    advance(h, A, delta, Pairs(&sm.x[t][p.col]), Twice(&sm.b[t * P::SP + p.sl * 4]));
+  auto token = [&](int t) {
+    const Pairs<2> delta(&sm.delta[t][p.col]);
+    advance(h, A, delta, Pairs<2>(&sm.x[t][p.col]), Twice(&sm.b[t * P::SP + p.sl * 4]));
     if (MAIN) {
       const Twice c(&sm.c[t * P::SP + p.sl * 4]);
       float v[4];
@@ -59,55 +94,74 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_fwd_kernel(SsmArgs a) {
         f2_split(o, v[2 * i], v[2 * i + 1]);
       }
       const float o = sum_over_states<SL>(v, p.sl);
-      if (owner)
-        y[(t0 + t) * a.d.E] = from_f32<T>(fmaf(skip, sm.x[t][p.col + mine], o) * sm.gate[t][p.col + mine]);
+      if (owner) *y = from_f32<T>(fmaf(skip, sm.x[t][p.col + mine], o) * sm.gate[t][p.col + mine]);
+      y += a.d.E;
     } else {
       sum[0] = f2_add(sum[0], delta.v[0]);
       sum[1] = f2_add(sum[1], delta.v[1]);
     }
   };
 
+  int64_t bos = -1, eos = -1;  // of the sequence that the tile begins in
   for (int64_t t0 = begin; t0 < end; t0 += kTile) {
     const int nt = end - t0 < kTile ? (int)(end - t0) : kTile;
-    __syncthreads();  // the previous tile is consumed
-    const bool borders = stage_borders(a, t0, nt, sm.bd);
-    for_tile<kTile, SL, VEC>(p, nt, [&](int t, int c, bool in) {
-      const int64_t e = p.e0 + c;
-      float xv[VEC] = {}, dv[VEC] = {}, zv[VEC] = {};
-      if (in) {
-        load_vec<VEC>(static_cast<const T *>(a.x) + (t0 + t) * a.d.ld_x + e, xv);
-        load_vec<VEC>(static_cast<const T *>(a.dt) + (t0 + t) * a.d.ld_dt + e, dv);
-        if (MAIN && a.z) load_vec<VEC>(static_cast<const T *>(a.z) + (t0 + t) * a.d.ld_z + e, zv);
-      }
+    if (!kAhead) fetch(t0);
+    if (t0 >= eos) {
+      const SeqRange r = seq_range(a.cu, seq_of_token(a.cu, a.d.N, a.d.T, t0), a.d.T);
+      bos = r.bos;
+      eos = r.eos;
+    }
+    const bool borders = bos >= t0 || eos <= t0 + nt;  // a sequence starts or ends in the tile
+    __syncthreads();                                   // the previous tile is consumed
+    if (borders) stage_borders(a, t0, nt, sm.bd);
+    Eight bias;
+    get8(&sm.bias[st.col], bias);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float raw = dv[i] + (a.dt_bias && in ? a.dt_bias[e + i] : 0.f);
-        dv[i] = in ? ssm_delta(raw, a.d.flags & GDR_SSM_SOFTPLUS) : 0.f;
-        if (MAIN) zv[i] = a.z ? zv[i] * sigmoid_fast(zv[i]) : 1.f;
+    for (int k = 0; k < st.kCount; ++k) {
+      if (!st.has(k)) continue;
+      const int t = st.token(k);
+      Eight v;
+      tile.x[k].expand(v);
+      put8(&sm.x[t][st.col], v);
+      tile.dt[k].expand(v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = f2_delta(f2_add(v[i], bias[i]), a.d.flags & GDR_SSM_SOFTPLUS);
+      put8(&sm.delta[t][st.col], v);
+      if (MAIN) {
+        if (a.z) tile.z[k].expand(v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = a.z ? f2_silu(v[i]) : f2_both(1.f);
+        put8(&sm.gate[t][st.col], v);
       }
-      store_vec<VEC>(&sm.delta[t][c], dv);
-      store_vec<VEC>(&sm.x[t][c], xv);
-      if (MAIN) store_vec<VEC>(&sm.gate[t][c], zv);
-    });
-    stage_states<T, SL, kTile>(a, p, a.b, a.d.ld_b, t0, nt, sm.b);
-    if (MAIN) stage_states<T, SL, kTile>(a, p, a.c, a.d.ld_c, t0, nt, sm.c);
-    if (!__syncthreads_or(borders) && nt == kTile) {
+    }
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const float bv = to_f32(tile.b[k]);
+      sm.b[k * kSsmThreads + threadIdx.x] = make_float2(bv, bv);
+      if (MAIN) {
+        const float cv = to_f32(tile.c[k]);
+        sm.c[k * kSsmThreads + threadIdx.x] = make_float2(cv, cv);
+      }
+    }
+    if (kAhead && t0 + kTile < end) fetch(t0 + kTile);
+    __syncthreads();
+    if (!borders && nt == kTile) {
 #pragma unroll 4
-      for (int t = 0; t < kTile; ++t) token(t0, t);
+      for (int t = 0; t < kTile; ++t) token(t);
     } else {
 #pragma unroll 1
       for (int t = 0; t < nt; ++t) {
-        if (sm.bd.first[t] >= 0) {
-          load_h0<SL>(a, p, a.h0, sm.bd.first[t], h);
+        if (borders && sm.bd.first[t] >= 0) {
+          load_h0(a, p, a.h0, sm.bd.first[t], h);
           started = true;
         }
-        token(t0, t);
-        if (MAIN && a.ht && sm.bd.last[t] >= 0) store_final<SL>(a, p, a.ht, sm.bd.last[t], h);
+        token(t);
+        if (MAIN && a.ht && borders && sm.bd.last[t] >= 0) store_final(a, p, a.ht, sm.bd.last[t], h);
       }
     }
   }
   if (!MAIN) {
-    store_chunk<SL>(a, p, a.hloc, p.chunk, h);
+    store_chunk(a, p, a.hloc, p.chunk, h);
     if (owner) {
       float s[4];
       f2_split(sum[0], s[0], s[1]);
@@ -164,7 +218,7 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(SsmArgs a, const int32_t 
   const bool in = e < a.d.E;
   float h[kStepRows][4], b[kStepRows][4], c[kStepRows][4], A[4] = {};
   float *row[kStepRows];
-  const int64_t g = in ? e / (a.d.E / a.d.G) : 0;
+  const unsigned g = in ? (unsigned)e / (unsigned)(a.d.E / a.d.G) : 0;
 #pragma unroll
   for (int k = 0; k < kStepRows; ++k) {
     const int64_t r = r0 + k;
@@ -181,14 +235,21 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(SsmArgs a, const int32_t 
     for (int q = 0; q < 4; ++q) h[k][q] = b[k][q] = c[k][q] = 0.f;
     if (row[k]) {
       load_states(row[k], s0, S, a.s4, h[k]);
-      const T *bp = static_cast<const T *>(a.b) + r * a.d.ld_b + g * S;
-      const T *cp = static_cast<const T *>(a.c) + r * a.d.ld_c + g * S;
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (s0 + q < S) {
-          b[k][q] = to_f32(bp[s0 + q]);
-          c[k][q] = to_f32(cp[s0 + q]);
+      const T *bp = static_cast<const T *>(a.b) + r * a.d.ld_b + (int64_t)g * S;
+      const T *cp = static_cast<const T *>(a.c) + r * a.d.ld_c + (int64_t)g * S;
+      if (a.bc4) {
+        if (s0 < S) {
+          load4(bp + s0, b[k]);
+          load4(cp + s0, c[k]);
         }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (s0 + q < S) {
+            b[k][q] = to_f32(bp[s0 + q]);
+            c[k][q] = to_f32(cp[s0 + q]);
+          }
+      }
     }
   }
   const int64_t r = r0 + sl;  // the row this lane prepares and finishes
@@ -231,8 +292,8 @@ template <typename T, bool MAIN>
 int launch_fwd(const SsmArgs &a, int sl, bool vec, cudaStream_t st) {
   const unsigned grid = (unsigned)(a.chunks * a.ctiles);
   auto go = [&](auto SL) {
-    if (vec) ssm_fwd_kernel<T, decltype(SL)::value, 8, MAIN><<<grid, kSsmThreads, 0, st>>>(a);
-    else ssm_fwd_kernel<T, decltype(SL)::value, 1, MAIN><<<grid, kSsmThreads, 0, st>>>(a);
+    if (vec) ssm_fwd_kernel<T, decltype(SL)::value, true, MAIN><<<grid, kSsmThreads, 0, st>>>(a);
+    else ssm_fwd_kernel<T, decltype(SL)::value, false, MAIN><<<grid, kSsmThreads, 0, st>>>(a);
     return launched(MAIN ? "ssm_fwd_kernel" : "ssm_local_kernel");
   };
   if (sl == 4) return go(std::integral_constant<int, 4>{});
@@ -369,6 +430,7 @@ int gdr_ssm_step(const gdr_ssm_desc *desc, const void *x, const void *dt, const 
   s.d = *desc;
   s.x = x; s.dt = dt; s.a = a; s.b = b; s.c = c; s.dskip = d; s.z = z; s.dt_bias = dt_bias; s.y = y;
   s.s4 = desc->S % 4 == 0 && is_aligned16(a) && is_aligned16(state);
+  s.bc4 = desc->S % 4 == 0 && desc->ld_b % 4 == 0 && desc->ld_c % 4 == 0 && is_aligned16(b) && is_aligned16(c);
   s.status = current_status_word(&rc);
   if (!s.status) return rc;
   return desc->dtype == GDR_BF16 ? launch_step<__nv_bfloat16>(s, slots, state, (cudaStream_t)stream)

@@ -5,8 +5,8 @@
 //   h_t = exp(delta_t a) h_{t-1} + (delta_t x_t) b_t      per channel e and state s
 //   y_t = (sum_s c_t h_t + d x_t) silu(z_t)
 //
-// Layout.  A thread owns four neighbouring channels and four neighbouring
-// states, 16 recurrences in registers; SL lanes (4, 8 or 16: up to 16, 32 or 64
+// Layout.  A thread owns four neighbouring channels (the backward's last kernel:
+// two) and four neighbouring states, 16 recurrences in registers; SL lanes (4, 8 or 16: up to 16, 32 or 64
 // states) cover a channel's states.  Per token it reads four deltas, four
 // inputs, four b and four c from shared memory, 16-byte loads that broadcast,
 // for 16 states; sums over states cross SL lanes, sums over channels cross the
@@ -44,6 +44,7 @@ struct SsmArgs {
   int64_t L;
   int tpg;       // blocks across the channels of a group
   int ctiles;    // blocks across all channels: G * tpg
+  int bc4;       // step: four elements of b and c at a time
   int s4;        // state rows may be read and written 16 bytes at a time
   int *status;
 };
@@ -55,27 +56,38 @@ constexpr int kTile = 16;  // tokens staged together
 // with log1p(u) = 2 atanh(r), r = u / (2 + u) <= 1/3, by its series in r^2.  Nine
 // terms leave 1e-9 of the value; log(1 + u) would lose a small u against the 1, and
 // small deltas are the ones a state remembers longest.  `slope`: ddelta/dv.
-__device__ __forceinline__ float ssm_delta(float v, int softplus, float *slope = nullptr) {
+template <bool SLOPE = false>
+__device__ __forceinline__ f2 f2_delta(f2 v, int softplus, f2 *slope = nullptr) {
   if (!softplus) {
-    if (slope) *slope = 1.f;
+    if (SLOPE) *slope = f2_both(1.f);
     return v;
   }
-  const float u = ex2(-fabsf(v) * kLog2e);
-  const float r = __fdividef(u, 2.f + u), q = r * r;
-  float w = 1.f / 17.f;
-  w = fmaf(w, q, 1.f / 15.f);
-  w = fmaf(w, q, 1.f / 13.f);
-  w = fmaf(w, q, 1.f / 11.f);
-  w = fmaf(w, q, 1.f / 9.f);
-  w = fmaf(w, q, 1.f / 7.f);
-  w = fmaf(w, q, 1.f / 5.f);
-  w = fmaf(w, q, 1.f / 3.f);
-  w = fmaf(w, q, 1.f);
-  if (slope) {
-    const float k = __fdividef(1.f, 1.f + u);
-    *slope = v >= 0.f ? k : u * k;
+  float lo, hi;
+  f2_split(v, lo, hi);
+  const f2 u = f2_ex2(f2_pack(-fabsf(lo) * kLog2e, -fabsf(hi) * kLog2e));
+  const f2 r = f2_mul(u, f2_rcp(f2_add(u, f2_both(2.f)))), q = f2_mul(r, r);
+  f2 w = f2_both(1.f / 17.f);
+  w = f2_fma(w, q, f2_both(1.f / 15.f));
+  w = f2_fma(w, q, f2_both(1.f / 13.f));
+  w = f2_fma(w, q, f2_both(1.f / 11.f));
+  w = f2_fma(w, q, f2_both(1.f / 9.f));
+  w = f2_fma(w, q, f2_both(1.f / 7.f));
+  w = f2_fma(w, q, f2_both(1.f / 5.f));
+  w = f2_fma(w, q, f2_both(1.f / 3.f));
+  w = f2_fma(w, q, f2_both(1.f));
+  if (SLOPE) {  // 1 / (1 + u), or u / (1 + u) where v < 0
+    const f2 k = f2_rcp(f2_add(u, f2_both(1.f)));
+    float k0, k1, m0, m1;
+    f2_split(k, k0, k1);
+    f2_split(f2_mul(u, k), m0, m1);
+    *slope = f2_pack(lo >= 0.f ? k0 : m0, hi >= 0.f ? k1 : m1);
   }
-  return fmaf(r + r, w, fmaxf(v, 0.f));  // a NaN comes through u
+  return f2_fma(f2_add(r, r), w, f2_pack(fmaxf(lo, 0.f), fmaxf(hi, 0.f)));  // a NaN comes through u
+}
+__device__ __forceinline__ float ssm_delta(float v, int softplus) {
+  float lo, hi;
+  f2_split(f2_delta(f2_both(v), softplus), lo, hi);
+  return lo;
 }
 
 // Four states from s0 of a row of S (zero past its end).
@@ -98,30 +110,35 @@ __device__ __forceinline__ void store_states(float *row, int s0, int S, int s4, 
     if (s0 + i < S) row[s0 + i] = v[i];
 }
 
-// Sums of v[0..3] over the SL lanes of a channel group; lane sl returns that of
-// channel sl & 3.  Halves of the values are exchanged, so that three shuffles
-// serve four channels; lanes past the first four first fold onto them.
-template <int SL>
-__device__ __forceinline__ float sum_over_states(float (&v)[4], int sl) {
+// Sums of v[0..NV) over the SL lanes of a channel group, NV 4 or 2; lane sl
+// returns that of v[sl & (NV - 1)].  Halves of the values are exchanged, so that
+// three shuffles serve four values; lanes past the first NV first fold onto them.
+template <int SL, int NV>
+__device__ __forceinline__ float sum_over_states(float (&v)[NV], int sl) {
 #pragma unroll
-  for (int o = SL / 2; o >= 4; o >>= 1)
+  for (int o = SL / 2; o >= NV; o >>= 1)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
-  const bool b1 = sl & 2, b0 = sl & 1;
-  float k0 = b1 ? v[2] : v[0], k1 = b1 ? v[3] : v[1];
-  const float g0 = b1 ? v[0] : v[2], g1 = b1 ? v[1] : v[3];
-  k0 += __shfl_xor_sync(0xffffffffu, g0, 2);
-  k1 += __shfl_xor_sync(0xffffffffu, g1, 2);
-  const float k = b0 ? k1 : k0, g = b0 ? k0 : k1;
-  return k + __shfl_xor_sync(0xffffffffu, g, 1);
+    for (int j = 0; j < NV; ++j) v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
+  const bool b0 = sl & 1;
+  float k0 = v[0], k1 = v[1];
+  if constexpr (NV == 4) {
+    const bool b1 = sl & 2;
+    k0 = b1 ? v[2] : v[0];
+    k1 = b1 ? v[3] : v[1];
+    k0 += __shfl_xor_sync(0xffffffffu, b1 ? v[0] : v[2], 2);
+    k1 += __shfl_xor_sync(0xffffffffu, b1 ? v[1] : v[3], 2);
+  }
+  return (b0 ? k1 : k0) + __shfl_xor_sync(0xffffffffu, b0 ? k0 : k1, 1);
 }
 
 // Where a block and its threads stand.
-template <int SL>
+template <int SL_, int NP_ = 2, int WARPS = 4>
 struct Place {
-  static constexpr int CPW = 128 / SL;  // channels of a warp
-  static constexpr int CB = 4 * CPW;    // of a block
-  static constexpr int SP = 4 * SL;     // states, padded
+  static constexpr int SL = SL_, NP = NP_;
+  static constexpr int CPW = 32 / SL * 2 * NP;  // channels of a warp
+  static constexpr int CB = WARPS * CPW;        // of a block
+  static constexpr int SP = 4 * SL;             // states, padded
+  static constexpr int kThreads = 32 * WARPS;
   int lane, warp, sl, cl;
   int64_t chunk, e0, e_end;  // first channel of the block; end of its group
   int64_t g;
@@ -137,7 +154,7 @@ struct Place {
     g = ct / a.tpg;
     e0 = g * eg + (int64_t)(ct % a.tpg) * CB;
     e_end = (g + 1) * eg;
-    col = warp * CPW + cl * 4;
+    col = warp * CPW + cl * 2 * NP;
   }
 };
 
@@ -161,41 +178,116 @@ __device__ __forceinline__ bool stage_borders(const SsmArgs &a, int64_t t0, int 
   return border;
 }
 
-// Runs f(t, column, in range) over a tile of [TT, CB] elements, VEC columns at a time.
-template <int TT, int SL, int VEC, typename F>
-__device__ __forceinline__ void for_tile(const Place<SL> &p, int nt, F &&f) {
-  constexpr int CB = Place<SL>::CB, N = TT * CB / VEC;
-#pragma unroll
-  for (int i0 = 0; i0 < N; i0 += kSsmThreads) {
-    const int i = i0 + threadIdx.x;
-    if (N % kSsmThreads != 0 && i >= N) break;
-    const int t = i / (CB / VEC), c = (i % (CB / VEC)) * VEC;
-    f(t, c, t < nt && p.e0 + c < p.e_end);
+// Eight neighbouring columns of one token, in pairs: how a thread stages a tile.
+typedef f2 Eight[4];
+__device__ __forceinline__ void put8(float *p, const Eight &v) {
+  reinterpret_cast<ulonglong2 *>(p)[0] = make_ulonglong2(v[0], v[1]);
+  reinterpret_cast<ulonglong2 *>(p)[1] = make_ulonglong2(v[2], v[3]);
+}
+__device__ __forceinline__ void get8(const float *p, Eight &v) {
+  const ulonglong2 a = reinterpret_cast<const ulonglong2 *>(p)[0], b = reinterpret_cast<const ulonglong2 *>(p)[1];
+  v[0] = a.x;
+  v[1] = a.y;
+  v[2] = b.x;
+  v[3] = b.y;
+}
+// Eight elements as they lie in memory.  VEC: by 16-byte accesses; else one by
+// one, those of the first n columns (zero past them).
+template <typename T, bool VEC>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16, true> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p, int n) {
+    u = n > 0 ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0);
   }
+  __device__ __forceinline__ void expand(Eight &v) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+};
+template <>
+struct Raw8<float, true> {
+  Eight u;
+  __device__ __forceinline__ void load(const float *p, int n) {
+    if (n > 0) {
+      get8(p, u);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = 0;
+    }
+  }
+  __device__ __forceinline__ void expand(Eight &v) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = u[i];
+  }
+};
+template <typename T>
+struct Raw8<T, false> {
+  T u[8];
+  __device__ __forceinline__ void load(const T *p, int n) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = i < n ? p[i] : from_f32<T>(0.f);
+  }
+  __device__ __forceinline__ void expand(Eight &v) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f2_pack(to_f32(u[2 * i]), to_f32(u[2 * i + 1]));
+  }
+};
+
+// A block's threads over a tile of [TT, CB] elements, eight columns each: the
+// k-th of a thread's kCount is token `token(k)`, columns `col` and on, the same
+// columns for every k.
+template <int TT, int CB, int THREADS>
+struct Stager {
+  static constexpr int kRow = CB / 8, kCount = (TT * kRow + THREADS - 1) / THREADS;
+  static_assert(THREADS % kRow == 0, "a thread keeps its columns");
+  int row, col, n;  // n: columns inside the group
+  template <typename P>
+  __device__ __forceinline__ explicit Stager(const P &p) {
+    row = threadIdx.x / kRow;
+    col = (threadIdx.x % kRow) * 8;
+    const int64_t left = p.e_end - p.e0 - col;
+    n = left < 0 ? 0 : left < 8 ? (int)left : 8;
+  }
+  __device__ __forceinline__ int token(int k) const { return row + k * (THREADS / kRow); }
+  // Whether token(k) is in the tile at all: not where the block has more threads than the tile.
+  __device__ __forceinline__ bool has(int k) const { return TT * kRow >= THREADS * (k + 1) || token(k) < TT; }
+};
+
+// The block's row of dt_bias as fp32, zero past the group.
+template <int CB, int THREADS, typename P>
+__device__ __forceinline__ void stage_bias(const SsmArgs &a, const P &p, float *bias) {
+  for (int i = threadIdx.x; i < CB; i += THREADS)
+    bias[i] = a.dt_bias && p.e0 + i < p.e_end ? a.dt_bias[p.e0 + i] : 0.f;
 }
 
 // b or c of a tile as fp32 [TT][SP], each twice, zero past S and past the tokens.
-template <typename T, int SL, int TT>
-__device__ __forceinline__ void stage_states(const SsmArgs &a, const Place<SL> &p, const void *src, int64_t ld,
-                                             int64_t t0, int nt, float2 *dst) {
-  constexpr int SP = Place<SL>::SP;
+template <typename T, int TT, int THREADS, typename P>
+__device__ __forceinline__ void stage_states(const SsmArgs &a, const P &p, const void *src, int64_t ld, int64_t t0,
+                                             int nt, float2 *dst) {
+  constexpr int SP = P::SP;
   const T *row = static_cast<const T *>(src) + p.g * a.d.S;
 #pragma unroll
-  for (int i0 = 0; i0 < TT * SP; i0 += kSsmThreads) {
+  for (int i0 = 0; i0 < TT * SP; i0 += THREADS) {
     const int i = i0 + threadIdx.x, t = i / SP, s = i % SP;
+    if (TT * SP % THREADS != 0 && i >= TT * SP) break;
     const float v = t < nt && s < a.d.S ? to_f32(row[(t0 + t) * ld + s]) : 0.f;
     dst[i] = make_float2(v, v);
   }
 }
 
-// A thread's 16 states: pair i holds channels 2 i and 2 i + 1, for each of the
-// four states.
-typedef f2 States[2][4];
+// A thread's states: pair i holds channels 2 i and 2 i + 1, for each of the four
+// states.
+template <int NP>
+using StatesOf = f2[NP][4];
+typedef StatesOf<2> States;
 
-template <int SL, typename F>
-__device__ __forceinline__ void read_states(const Place<SL> &p, States &h, F &&row) {
+template <typename P, int NP, typename F>
+__device__ __forceinline__ void read_states(const P &p, f2 (&h)[NP][4], F &&row) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < NP; ++i) {
     float v[4] = {}, w[4] = {};
     const int64_t e = p.e0 + p.col + 2 * i;
     if (e < p.e_end) row(e, v);
@@ -204,10 +296,10 @@ __device__ __forceinline__ void read_states(const Place<SL> &p, States &h, F &&r
     for (int s = 0; s < 4; ++s) h[i][s] = f2_pack(v[s], w[s]);
   }
 }
-template <int SL, typename F>
-__device__ __forceinline__ void write_states(const Place<SL> &p, const States &h, F &&row) {
+template <typename P, int NP, typename F>
+__device__ __forceinline__ void write_states(const P &p, const f2 (&h)[NP][4], F &&row) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < NP; ++i) {
     float v[4], w[4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) f2_split(h[i][s], v[s], w[s]);
@@ -217,38 +309,38 @@ __device__ __forceinline__ void write_states(const Place<SL> &p, const States &h
   }
 }
 // The state h0 of sequence n (zero where there is none).
-template <int SL>
-__device__ __forceinline__ void load_h0(const SsmArgs &a, const Place<SL> &p, const float *h0, int64_t n, States &h) {
+template <typename P, int NP>
+__device__ __forceinline__ void load_h0(const SsmArgs &a, const P &p, const float *h0, int64_t n, f2 (&h)[NP][4]) {
   read_states(p, h, [&](int64_t e, float (&v)[4]) {
     if (h0) load_states(h0 + (n * a.d.E + e) * a.d.S, p.sl * 4, (int)a.d.S, a.s4, v);
   });
 }
-template <int SL>
-__device__ __forceinline__ void store_final(const SsmArgs &a, const Place<SL> &p, float *ht, int64_t n,
-                                            const States &h) {
+template <typename P, int NP>
+__device__ __forceinline__ void store_final(const SsmArgs &a, const P &p, float *ht, int64_t n,
+                                            const f2 (&h)[NP][4]) {
   write_states(p, h, [&](int64_t e, const float (&v)[4]) {
     store_states(ht + (n * a.d.E + e) * a.d.S, p.sl * 4, (int)a.d.S, a.s4, v);
   });
 }
 // Chunk states [chunks, E, SP]: always whole 16-byte groups.
-template <int SL>
-__device__ __forceinline__ void load_chunk(const SsmArgs &a, const Place<SL> &p, const float *src, int64_t chunk,
-                                           States &h) {
+template <typename P, int NP>
+__device__ __forceinline__ void load_chunk(const SsmArgs &a, const P &p, const float *src, int64_t chunk,
+                                           f2 (&h)[NP][4]) {
   read_states(p, h, [&](int64_t e, float (&v)[4]) {
-    if (src) load4(src + (chunk * a.d.E + e) * Place<SL>::SP + p.sl * 4, v);
+    if (src) load4(src + (chunk * a.d.E + e) * P::SP + p.sl * 4, v);
   });
 }
-template <int SL>
-__device__ __forceinline__ void store_chunk(const SsmArgs &a, const Place<SL> &p, float *dst, int64_t chunk,
-                                            const States &h) {
+template <typename P, int NP>
+__device__ __forceinline__ void store_chunk(const SsmArgs &a, const P &p, float *dst, int64_t chunk,
+                                            const f2 (&h)[NP][4]) {
   write_states(p, h, [&](int64_t e, const float (&v)[4]) {
-    store4(dst + (chunk * a.d.E + e) * Place<SL>::SP + p.sl * 4, v);
+    store4(dst + (chunk * a.d.E + e) * P::SP + p.sl * 4, v);
   });
 }
 
 // a[e, s] log2(e) of a thread's channels and states (zero outside: such states stay zero).
-template <int SL>
-__device__ __forceinline__ void load_a(const SsmArgs &a, const Place<SL> &p, States &A) {
+template <typename P, int NP>
+__device__ __forceinline__ void load_a(const SsmArgs &a, const P &p, f2 (&A)[NP][4]) {
   read_states(p, A, [&](int64_t e, float (&v)[4]) {
     load_states(a.a + e * a.d.S, p.sl * 4, (int)a.d.S, a.s4, v);
 #pragma unroll
@@ -256,13 +348,18 @@ __device__ __forceinline__ void load_a(const SsmArgs &a, const Place<SL> &p, Sta
   });
 }
 
-// Four values of a staged row: the thread's channels, as two pairs.
+// A staged row's values of the thread's channels, in pairs.
+template <int NP>
 struct Pairs {
-  f2 v[2];
+  f2 v[NP];
   __device__ __forceinline__ explicit Pairs(const float *row) {
-    const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(row);
-    v[0] = u.x;
-    v[1] = u.y;
+    if constexpr (NP == 2) {
+      const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(row);
+      v[0] = u.x;
+      v[1] = u.y;
+    } else {
+      v[0] = *reinterpret_cast<const f2 *>(row);
+    }
   }
 };
 // Four values of a staged row of b or c: the thread's states, each twice.
@@ -278,10 +375,11 @@ struct Twice {
 };
 
 // One token of the recurrence.
-__device__ __forceinline__ void advance(States &h, const States &A, const Pairs &delta, const Pairs &x,
-                                        const Twice &b) {
+template <int NP>
+__device__ __forceinline__ void advance(f2 (&h)[NP][4], const f2 (&A)[NP][4], const Pairs<NP> &delta,
+                                        const Pairs<NP> &x, const Twice &b) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < NP; ++i) {
     const f2 u = f2_mul(delta.v[i], x.v[i]);
 #pragma unroll
     for (int s = 0; s < 4; ++s) h[i][s] = f2_fma(f2_ex2(f2_mul(A[i][s], delta.v[i])), h[i][s], f2_mul(u, b.v[s]));
@@ -289,15 +387,15 @@ __device__ __forceinline__ void advance(States &h, const States &A, const Pairs 
 }
 
 // States of sequences without tokens: `to` = `from` (zero where null).
-template <int SL>
-__device__ __forceinline__ void copy_empty_states(const SsmArgs &a, const Place<SL> &p, const float *from, float *to) {
+template <typename P>
+__device__ __forceinline__ void copy_empty_states(const SsmArgs &a, const P &p, const float *from, float *to) {
   if (!to) return;
   for (int64_t n = 0; n < a.d.N; ++n) {
     const SeqRange r = seq_range(a.cu, n, a.d.T);
     if (r.eos > r.bos) continue;
-    States h;
-    load_h0<SL>(a, p, from, n, h);
-    store_final<SL>(a, p, to, n, h);
+    StatesOf<P::NP> h;
+    load_h0(a, p, from, n, h);
+    store_final(a, p, to, n, h);
   }
 }
 

@@ -31,45 +31,67 @@ constexpr int kMaxL = 64;    // tokens of a chunk
 constexpr int kSubs = kMaxL / kSub;
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <int SL>
+template <typename P>
 struct __align__(16) LocalShared {
-  float delta[kTile][Place<SL>::CB], x[kTile][Place<SL>::CB], up[kTile][Place<SL>::CB];
-  float2 b[kTile * Place<SL>::SP], c[kTile * Place<SL>::SP];
+  float delta[kTile][P::CB], x[kTile][P::CB], up[kTile][P::CB];
+  float bias[P::CB];
+  float2 b[kTile * P::SP], c[kTile * P::SP];
   Borders<kTile> bd;
 };
 
-template <typename T, int SL, int VEC>
-__device__ __forceinline__ void stage_local(const SsmArgs &a, const Place<SL> &p, int64_t t0, int nt,
-                                            LocalShared<SL> &sm) {
-  for_tile<kTile, SL, VEC>(p, nt, [&](int t, int c, bool in) {
-    const int64_t e = p.e0 + c;
-    float xv[VEC] = {}, dv[VEC] = {}, zv[VEC] = {}, gv[VEC] = {};
-    if (in) {
-      load_vec<VEC>(static_cast<const T *>(a.x) + (t0 + t) * a.d.ld_x + e, xv);
-      load_vec<VEC>(static_cast<const T *>(a.dt) + (t0 + t) * a.d.ld_dt + e, dv);
-      load_vec<VEC>(static_cast<const T *>(a.dy) + (t0 + t) * a.d.ld_dy + e, gv);
-      if (a.z) load_vec<VEC>(static_cast<const T *>(a.z) + (t0 + t) * a.d.ld_z + e, zv);
-    }
+// Eight columns of token t, n of them inside the group.
+template <typename T, bool VEC>
+__device__ __forceinline__ void fetch8(const void *src, int64_t ld, int64_t t, int64_t e, int n, Eight &v) {
+  Raw8<T, VEC> r;
+  r.load(static_cast<const T *>(src) + t * ld + e, n);
+  r.expand(v);
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void fetch_delta(const SsmArgs &a, int64_t t, int64_t e, int n, const float *bias,
+                                            Eight &v) {
+  Eight w;
+  fetch8<T, VEC>(a.dt, a.d.ld_dt, t, e, n, v);
+  get8(bias, w);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const float raw = dv[i] + (a.dt_bias && in ? a.dt_bias[e + i] : 0.f);
-      dv[i] = in ? ssm_delta(raw, a.d.flags & GDR_SSM_SOFTPLUS) : 0.f;
-      gv[i] *= a.z ? zv[i] * sigmoid_fast(zv[i]) : 1.f;
+  for (int i = 0; i < 4; ++i) v[i] = f2_add(v[i], w[i]);
+}
+
+template <typename T, typename P, bool VEC>
+__device__ __forceinline__ void stage_local(const SsmArgs &a, const P &p, const Stager<kTile, P::CB, P::kThreads> &st,
+                                            int64_t t0, int nt, LocalShared<P> &sm) {
+  const int64_t e = p.e0 + st.col;
+#pragma unroll
+  for (int k = 0; k < st.kCount; ++k) {
+    if (!st.has(k)) continue;
+    const int t = st.token(k), n = t < nt ? st.n : 0;
+    Eight v, w;
+    fetch8<T, VEC>(a.x, a.d.ld_x, t0 + t, e, n, v);
+    put8(&sm.x[t][st.col], v);
+    fetch_delta<T, VEC>(a, t0 + t, e, n, &sm.bias[st.col], v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f2_delta(v[i], a.d.flags & GDR_SSM_SOFTPLUS);
+    put8(&sm.delta[t][st.col], v);
+    fetch8<T, VEC>(a.dy, a.d.ld_dy, t0 + t, e, n, v);
+    if (a.z) {
+      fetch8<T, VEC>(a.z, a.d.ld_z, t0 + t, e, n, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = f2_mul(v[i], f2_silu(w[i]));
     }
-    store_vec<VEC>(&sm.delta[t][c], dv);
-    store_vec<VEC>(&sm.x[t][c], xv);
-    store_vec<VEC>(&sm.up[t][c], gv);
-  });
+    put8(&sm.up[t][st.col], v);
+  }
 }
 
 template <typename T, int SL>
 __global__ void __launch_bounds__(kSsmThreads) ssm_bwd_local_kernel(SsmArgs a) {
   using P = Place<SL>;
-  __shared__ LocalShared<SL> sm;
+  __shared__ LocalShared<P> sm;
   if (!seqlens_ok(a.cu, a.d.N, a.M, a.status)) return;
   const P p(a);
+  const Stager<kTile, P::CB, P::kThreads> st(p);
+  stage_bias<P::CB, P::kThreads>(a, p, sm.bias);
+  __syncthreads();
   States A, h, g, pass;  // pass: product of the decays since the chunk began; zero once a sequence started
-  load_a<SL>(a, p, A);
+  load_a(a, p, A);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -81,7 +103,7 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_bwd_local_kernel(SsmArgs a) {
   f2 sum[2] = {0, 0};
   bool started = false;
   auto token = [&](int t) {
-    const Pairs delta(&sm.delta[t][p.col]), x(&sm.x[t][p.col]), up(&sm.up[t][p.col]);
+    const Pairs<2> delta(&sm.delta[t][p.col]), x(&sm.x[t][p.col]), up(&sm.up[t][p.col]);
     const Twice b(&sm.b[t * P::SP + p.sl * 4]), c(&sm.c[t * P::SP + p.sl * 4]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -96,22 +118,30 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_bwd_local_kernel(SsmArgs a) {
       sum[i] = f2_add(sum[i], delta.v[i]);
     }
   };
+  int64_t bos = -1, eos = -1;  // of the sequence that the tile begins in
   for (int64_t t0 = begin; t0 < end; t0 += kTile) {
     const int nt = end - t0 < kTile ? (int)(end - t0) : kTile;
+    if (t0 >= eos) {
+      const SeqRange r = seq_range(a.cu, seq_of_token(a.cu, a.d.N, a.d.T, t0), a.d.T);
+      bos = r.bos;
+      eos = r.eos;
+    }
+    const bool borders = bos >= t0 || eos <= t0 + nt;  // a sequence starts or ends in the tile
+    __syncthreads();                                   // the previous tile is consumed
+    if (borders) stage_borders(a, t0, nt, sm.bd);
+    if (a.vec) stage_local<T, P, true>(a, p, st, t0, nt, sm);
+    else stage_local<T, P, false>(a, p, st, t0, nt, sm);
+    stage_states<T, kTile, P::kThreads>(a, p, a.b, a.d.ld_b, t0, nt, sm.b);
+    stage_states<T, kTile, P::kThreads>(a, p, a.c, a.d.ld_c, t0, nt, sm.c);
     __syncthreads();
-    const bool borders = stage_borders(a, t0, nt, sm.bd);
-    if (a.vec) stage_local<T, SL, 8>(a, p, t0, nt, sm);
-    else stage_local<T, SL, 1>(a, p, t0, nt, sm);
-    stage_states<T, SL, kTile>(a, p, a.b, a.d.ld_b, t0, nt, sm.b);
-    stage_states<T, SL, kTile>(a, p, a.c, a.d.ld_c, t0, nt, sm.c);
-    if (!__syncthreads_or(borders) && nt == kTile) {
+    if (!borders && nt == kTile) {
 #pragma unroll 4
       for (int t = 0; t < kTile; ++t) token(t);
     } else {
 #pragma unroll 1
       for (int t = 0; t < nt; ++t) {
-        if (sm.bd.first[t] >= 0) {
-          load_h0<SL>(a, p, a.h0, sm.bd.first[t], h);
+        if (borders && sm.bd.first[t] >= 0) {
+          load_h0(a, p, a.h0, sm.bd.first[t], h);
           started = true;
 #pragma unroll
           for (int i = 0; i < 2; ++i)
@@ -119,9 +149,9 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_bwd_local_kernel(SsmArgs a) {
             for (int s = 0; s < 4; ++s) pass[i][s] = 0;
         }
         token(t);
-        if (a.dht && !started && sm.bd.last[t] >= 0) {
+        if (a.dht && !started && borders && sm.bd.last[t] >= 0) {
           States dh;
-          load_h0<SL>(a, p, a.dht, sm.bd.last[t], dh);
+          load_h0(a, p, a.dht, sm.bd.last[t], dh);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -130,8 +160,8 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_bwd_local_kernel(SsmArgs a) {
       }
     }
   }
-  store_chunk<SL>(a, p, a.hloc, p.chunk, h);
-  store_chunk<SL>(a, p, a.gloc, p.chunk, g);
+  store_chunk(a, p, a.hloc, p.chunk, h);
+  store_chunk(a, p, a.gloc, p.chunk, g);
   const int mine = p.sl & 3;
   const int64_t e_mine = p.e0 + p.col + mine;
   if (p.sl < 4 && e_mine < p.e_end) {
@@ -175,10 +205,16 @@ __global__ void __launch_bounds__(128) ssm_bwd_carry_kernel(SsmArgs a, int SP) {
   }
 }
 
+// Main: two channels to a thread and eight warps to a block, against four and
+// four before: half the registers for the eight states held back, so that two
+// blocks of 256 threads fit a multiprocessor where two of 128 did, and half the
+// unrolled code.
 template <int SL>
+using MainPlace = Place<SL, 1, 8>;
+
+template <typename P>
 struct MainShared {
-  using P = Place<SL>;
-  ulonglong2 ckpt[kSubs][4][kSsmThreads];  // a thread's states before each run of kSub tokens
+  ulonglong2 ckpt[kSubs][2][P::kThreads];  // a thread's states before each run of kSub tokens
   union {
     struct {
       float delta[kTile][P::CB], x[kTile][P::CB];
@@ -189,66 +225,67 @@ struct MainShared {
       float2 b[kSub * P::SP], c[kSub * P::SP];
     } r;
   };
-  float red[kSub][4][2 * P::SP];  // db, dc of a token by warp
+  float bias[P::CB];
+  float red[kSub][8][2 * P::SP];  // db, dc of a token by warp
   Borders<kMaxL> bd;
 };
 
-template <typename T, int SL, int VEC>
-__device__ __forceinline__ void stage_forward(const SsmArgs &a, const Place<SL> &p, int64_t t0, int nt,
-                                              MainShared<SL> &sm) {
-  for_tile<kTile, SL, VEC>(p, nt, [&](int t, int c, bool in) {
-    const int64_t e = p.e0 + c;
-    float xv[VEC] = {}, dv[VEC] = {};
-    if (in) {
-      load_vec<VEC>(static_cast<const T *>(a.x) + (t0 + t) * a.d.ld_x + e, xv);
-      load_vec<VEC>(static_cast<const T *>(a.dt) + (t0 + t) * a.d.ld_dt + e, dv);
-    }
+template <typename T, typename P, bool VEC>
+__device__ __forceinline__ void stage_forward(const SsmArgs &a, const P &p,
+                                              const Stager<kTile, P::CB, P::kThreads> &st, int64_t t0, int nt,
+                                              MainShared<P> &sm) {
+  const int64_t e = p.e0 + st.col;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const float raw = dv[i] + (a.dt_bias && in ? a.dt_bias[e + i] : 0.f);
-      dv[i] = in ? ssm_delta(raw, a.d.flags & GDR_SSM_SOFTPLUS) : 0.f;
-    }
-    store_vec<VEC>(&sm.f.delta[t][c], dv);
-    store_vec<VEC>(&sm.f.x[t][c], xv);
-  });
+  for (int k = 0; k < st.kCount; ++k) {
+    if (!st.has(k)) continue;
+    const int t = st.token(k), n = t < nt ? st.n : 0;
+    Eight v;
+    fetch8<T, VEC>(a.x, a.d.ld_x, t0 + t, e, n, v);
+    put8(&sm.f.x[t][st.col], v);
+    fetch_delta<T, VEC>(a, t0 + t, e, n, &sm.bias[st.col], v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f2_delta(v[i], a.d.flags & GDR_SSM_SOFTPLUS);
+    put8(&sm.f.delta[t][st.col], v);
+  }
 }
 
-template <typename T, int SL, int VEC>
-__device__ __forceinline__ void stage_reverse(const SsmArgs &a, const Place<SL> &p, int64_t t0, int nt,
-                                              MainShared<SL> &sm) {
-  for_tile<kSub, SL, VEC>(p, nt, [&](int t, int c, bool in) {
-    const int64_t e = p.e0 + c;
-    float xv[VEC] = {}, dv[VEC] = {}, zv[VEC] = {}, gv[VEC] = {};
-    if (in) {
-      load_vec<VEC>(static_cast<const T *>(a.x) + (t0 + t) * a.d.ld_x + e, xv);
-      load_vec<VEC>(static_cast<const T *>(a.dt) + (t0 + t) * a.d.ld_dt + e, dv);
-      load_vec<VEC>(static_cast<const T *>(a.dy) + (t0 + t) * a.d.ld_dy + e, gv);
-      if (a.z) load_vec<VEC>(static_cast<const T *>(a.z) + (t0 + t) * a.d.ld_z + e, zv);
-    }
-    float slope[VEC];
+// The first half of the block stages x and dt, the second dy and z.
+template <typename T, typename P, bool VEC>
+__device__ __forceinline__ void stage_reverse(const SsmArgs &a, const P &p, int64_t t0, int nt, MainShared<P> &sm) {
+  constexpr int kHalf = P::kThreads / 2, kRow = P::CB / 8;
+  const int half = threadIdx.x / kHalf, i0 = threadIdx.x % kHalf, t = i0 / kRow, col = i0 % kRow * 8;
+  if (t >= kSub) return;
+  const int64_t e = p.e0 + col, left = p.e_end - e;
+  const int n = t >= nt || left < 0 ? 0 : left < 8 ? (int)left : 8;
+  Eight v, w, o;
+  if (half == 0) {
+    fetch8<T, VEC>(a.x, a.d.ld_x, t0 + t, e, n, v);
+    put8(&sm.r.x[t][col], v);
+    fetch_delta<T, VEC>(a, t0 + t, e, n, &sm.bias[col], v);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const float raw = dv[i] + (a.dt_bias && in ? a.dt_bias[e + i] : 0.f);
-      const float sg = sigmoid_fast(zv[i]), dy = gv[i];
-      dv[i] = ssm_delta(raw, a.d.flags & GDR_SSM_SOFTPLUS, &slope[i]);
-      if (!in) dv[i] = 0.f;
-      gv[i] = dy * (a.z ? zv[i] * sg : 1.f);
-      zv[i] = dy * sg * fmaf(zv[i], 1.f - sg, 1.f);
+    for (int i = 0; i < 4; ++i) o[i] = f2_delta<true>(v[i], a.d.flags & GDR_SSM_SOFTPLUS, &w[i]);
+    put8(&sm.r.delta[t][col], o);
+    put8(&sm.r.slope[t][col], w);
+  } else {
+    fetch8<T, VEC>(a.dy, a.d.ld_dy, t0 + t, e, n, v);
+    if (a.z) {
+      fetch8<T, VEC>(a.z, a.d.ld_z, t0 + t, e, n, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = f2_mul(v[i], f2_silu_grad(w[i]));
+      put8(&sm.r.zf[t][col], o);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = f2_mul(v[i], f2_silu(w[i]));
     }
-    store_vec<VEC>(&sm.r.delta[t][c], dv);
-    store_vec<VEC>(&sm.r.x[t][c], xv);
-    store_vec<VEC>(&sm.r.up[t][c], gv);
-    store_vec<VEC>(&sm.r.slope[t][c], slope);
-    store_vec<VEC>(&sm.r.zf[t][c], zv);
-  });
+    put8(&sm.r.up[t][col], v);
+  }
 }
 
 // Sums v[0..7] (db of the thread's four states, then dc) over the channel lanes
 // of a warp, halving the values a lane holds at each step, and leaves them in
 // out[2 * SP] (db, then dc).
-template <int SL>
-__device__ __forceinline__ void sum_over_channels(float (&v)[8], const Place<SL> &p, float *out) {
-  constexpr int SP = Place<SL>::SP, CL = 32 / SL;
+template <typename P>
+__device__ __forceinline__ void sum_over_channels(float (&v)[8], const P &p, float *out) {
+  constexpr int SP = P::SP, CL = 32 / P::SL;
   int base = 0;  // which of the eight the lane holds first
   int n = 8;
 #pragma unroll
@@ -259,7 +296,7 @@ __device__ __forceinline__ void sum_over_channels(float (&v)[8], const Place<SL>
     for (int i = 0; i < 4; ++i) {
       if (i < n) {
         const float keep = up ? v[n + i] : v[i], give = up ? v[i] : v[n + i];
-        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o * SL);
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o * P::SL);
       }
     }
     base += up ? n : 0;
@@ -272,162 +309,158 @@ __device__ __forceinline__ void sum_over_channels(float (&v)[8], const Place<SL>
 }
 
 template <typename T, int SL>
-__global__ void __launch_bounds__(kSsmThreads, 2) ssm_bwd_main_kernel(SsmArgs a) {
-  using P = Place<SL>;
+__global__ void __launch_bounds__(256, 2) ssm_bwd_main_kernel(SsmArgs a) {
+  using P = MainPlace<SL>;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  MainShared<SL> &sm = *reinterpret_cast<MainShared<SL> *>(smem_raw);
+  MainShared<P> &sm = *reinterpret_cast<MainShared<P> *>(smem_raw);
   if (!seqlens_ok(a.cu, a.d.N, a.M, a.status)) return;
   const P p(a);
   const int tid = threadIdx.x;
-  if (p.chunk == 0) copy_empty_states<SL>(a, p, a.dht, a.dh0);
-  States A, h, g, dA;
-  load_a<SL>(a, p, A);
-  load_chunk<SL>(a, p, a.hloc, p.chunk, h);
-  load_chunk<SL>(a, p, a.gloc, p.chunk, g);
+  if (p.chunk == 0) copy_empty_states(a, p, a.dht, a.dh0);
+  StatesOf<1> A, h, g, dA;
+  load_a(a, p, A);
+  load_chunk(a, p, a.hloc, p.chunk, h);
+  load_chunk(a, p, a.gloc, p.chunk, g);
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int s = 0; s < 4; ++s) dA[i][s] = 0;
+  for (int s = 0; s < 4; ++s) dA[0][s] = 0;
   const int64_t begin = p.chunk * a.L, end = begin + a.L < a.M ? begin + a.L : a.M;
   const int len = end > begin ? (int)(end - begin) : 0;
   const int subs = (len + kSub - 1) / kSub;
-  const int mine = p.sl & 3;
-  const int64_t e_mine = p.e0 + p.col + mine;
-  const bool owner = p.sl < 4 && e_mine < p.e_end;
+  // Of a channel pair's first four lanes, two finish dz and two dx and ddt, a channel each.
+  const int col = p.col + (p.sl & 1);
+  const int64_t e_mine = p.e0 + col;
+  const bool owner = p.sl < 4 && e_mine < p.e_end, owns_z = owner && p.sl < 2, owns_x = owner && p.sl >= 2;
   const float skip = a.dskip && owner ? a.dskip[e_mine] : 0.f;
   float dd = 0.f, dbias = 0.f;
+  stage_bias<P::CB, P::kThreads>(a, p, sm.bias);
   stage_borders(a, begin, len, sm.bd);
 
   auto keep = [&](int sub) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sm.ckpt[sub][i][tid] = make_ulonglong2(h[i >> 1][2 * (i & 1)], h[i >> 1][2 * (i & 1) + 1]);
+    sm.ckpt[sub][0][tid] = make_ulonglong2(h[0][0], h[0][1]);
+    sm.ckpt[sub][1][tid] = make_ulonglong2(h[0][2], h[0][3]);
   };
-  auto back_to = [&](int sub, States &to) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const ulonglong2 v = sm.ckpt[sub][i][tid];
-      to[i >> 1][2 * (i & 1)] = v.x;
-      to[i >> 1][2 * (i & 1) + 1] = v.y;
-    }
+  auto back_to = [&](int sub, StatesOf<1> &to) {
+    const ulonglong2 u = sm.ckpt[sub][0][tid], v = sm.ckpt[sub][1][tid];
+    to[0][0] = u.x;
+    to[0][1] = u.y;
+    to[0][2] = v.x;
+    to[0][3] = v.y;
   };
 
   // States at the start of every run of kSub tokens; the last run needs only its start.
   keep(0);
   const int flen = subs > 0 ? (subs - 1) * kSub : 0;
-  for (int f0 = 0; f0 < flen; f0 += kTile) {
-    const int nt = flen - f0 < kTile ? flen - f0 : kTile;
-    __syncthreads();
-    if (a.vec) stage_forward<T, SL, 8>(a, p, begin + f0, nt, sm);
-    else stage_forward<T, SL, 1>(a, p, begin + f0, nt, sm);
-    stage_states<T, SL, kTile>(a, p, a.b, a.d.ld_b, begin + f0, nt, sm.f.b);
-    __syncthreads();
-    for (int t1 = 0; t1 < nt; t1 += kSub) {
+  {
+    const Stager<kTile, P::CB, P::kThreads> st(p);
+    for (int f0 = 0; f0 < flen; f0 += kTile) {
+      const int nt = flen - f0 < kTile ? flen - f0 : kTile;
+      __syncthreads();
+      if (a.vec) stage_forward<T, P, true>(a, p, st, begin + f0, nt, sm);
+      else stage_forward<T, P, false>(a, p, st, begin + f0, nt, sm);
+      stage_states<T, kTile, P::kThreads>(a, p, a.b, a.d.ld_b, begin + f0, nt, sm.f.b);
+      __syncthreads();
+#pragma unroll 1
+      for (int t1 = 0; t1 < nt; t1 += kSub) {
 #pragma unroll 4
-      for (int t = t1; t < t1 + kSub; ++t) {
-        if (sm.bd.first[f0 + t] >= 0) load_h0<SL>(a, p, a.h0, sm.bd.first[f0 + t], h);
-        advance(h, A, Pairs(&sm.f.delta[t][p.col]), Pairs(&sm.f.x[t][p.col]), Twice(&sm.f.b[t * P::SP + p.sl * 4]));
+        for (int t = t1; t < t1 + kSub; ++t) {
+          if (sm.bd.first[f0 + t] >= 0) load_h0(a, p, a.h0, sm.bd.first[f0 + t], h);
+          advance(h, A, Pairs<1>(&sm.f.delta[t][p.col]), Pairs<1>(&sm.f.x[t][p.col]),
+                  Twice(&sm.f.b[t * P::SP + p.sl * 4]));
+        }
+        keep((f0 + t1) / kSub + 1);
       }
-      keep((f0 + t1) / kSub + 1);
     }
   }
 
+#pragma unroll 1
   for (int sub = subs - 1; sub >= 0; --sub) {
     const int64_t t0 = begin + sub * kSub;
     const int nt = len - sub * kSub < kSub ? len - sub * kSub : kSub;
     __syncthreads();  // the previous run's staging and partials are consumed
-    if (a.vec) stage_reverse<T, SL, 8>(a, p, t0, nt, sm);
-    else stage_reverse<T, SL, 1>(a, p, t0, nt, sm);
-    stage_states<T, SL, kSub>(a, p, a.b, a.d.ld_b, t0, nt, sm.r.b);
-    stage_states<T, SL, kSub>(a, p, a.c, a.d.ld_c, t0, nt, sm.r.c);
+    if (a.vec) stage_reverse<T, P, true>(a, p, t0, nt, sm);
+    else stage_reverse<T, P, false>(a, p, t0, nt, sm);
+    stage_states<T, kSub, P::kThreads>(a, p, a.b, a.d.ld_b, t0, nt, sm.r.b);
+    stage_states<T, kSub, P::kThreads>(a, p, a.c, a.d.ld_c, t0, nt, sm.r.c);
     __syncthreads();
-    States after[kSub];  // after[k]: the state after token k (past the end: never read)
+    StatesOf<1> after[kSub];  // after[k]: the state after token k (past the end: never read)
     back_to(sub, h);
 #pragma unroll
     for (int k = 0; k < kSub; ++k) {
       if (k < nt) {
-        if (sm.bd.first[sub * kSub + k] >= 0) load_h0<SL>(a, p, a.h0, sm.bd.first[sub * kSub + k], h);
-        advance(h, A, Pairs(&sm.r.delta[k][p.col]), Pairs(&sm.r.x[k][p.col]), Twice(&sm.r.b[k * P::SP + p.sl * 4]));
+        if (sm.bd.first[sub * kSub + k] >= 0) load_h0(a, p, a.h0, sm.bd.first[sub * kSub + k], h);
+        advance(h, A, Pairs<1>(&sm.r.delta[k][p.col]), Pairs<1>(&sm.r.x[k][p.col]),
+                Twice(&sm.r.b[k * P::SP + p.sl * 4]));
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int s = 0; s < 4; ++s) after[k][i][s] = h[i][s];
+      for (int s = 0; s < 4; ++s) after[k][0][s] = h[0][s];
     }
 #pragma unroll
     for (int k = kSub - 1; k >= 0; --k) {
       if (k >= nt) continue;
       const int first = sm.bd.first[sub * kSub + k], last = sm.bd.last[sub * kSub + k];
-      if (last >= 0) load_h0<SL>(a, p, a.dht, last, g);
-      States prev;
+      if (last >= 0) load_h0(a, p, a.dht, last, g);
+      StatesOf<1> prev;
       if (first >= 0) {
-        load_h0<SL>(a, p, a.h0, first, prev);
+        load_h0(a, p, a.h0, first, prev);
       } else if (k == 0) {
         back_to(sub, prev);
       } else {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int s = 0; s < 4; ++s) prev[i][s] = after[k > 0 ? k - 1 : 0][i][s];
+        for (int s = 0; s < 4; ++s) prev[0][s] = after[k > 0 ? k - 1 : 0][0][s];
       }
-      const Pairs delta(&sm.r.delta[k][p.col]), x(&sm.r.x[k][p.col]), up(&sm.r.up[k][p.col]);
+      const f2 delta = Pairs<1>(&sm.r.delta[k][p.col]).v[0], up = Pairs<1>(&sm.r.up[k][p.col]).v[0];
+      const f2 u = f2_mul(delta, Pairs<1>(&sm.r.x[k][p.col]).v[0]);
       const Twice b(&sm.r.b[k * P::SP + p.sl * 4]), c(&sm.r.c[k * P::SP + p.sl * 4]);
-      f2 db[4], dc[4];
-      float ys[4], gb[4], qa[4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const f2 u = f2_mul(delta.v[i], x.v[i]);
-        f2 sy = 0, sb = 0, sq = 0;
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          g[i][s] = f2_fma(c.v[s], up.v[i], g[i][s]);
-          dc[s] = i ? f2_fma(up.v[i], after[k][i][s], dc[s]) : f2_mul(up.v[i], after[k][i][s]);
-          sy = s ? f2_fma(c.v[s], after[k][i][s], sy) : f2_mul(c.v[s], after[k][i][s]);
-          db[s] = i ? f2_fma(u, g[i][s], db[s]) : f2_mul(u, g[i][s]);
-          sb = s ? f2_fma(b.v[s], g[i][s], sb) : f2_mul(b.v[s], g[i][s]);
-          g[i][s] = f2_mul(g[i][s], f2_ex2(f2_mul(A[i][s], delta.v[i])));
-          const f2 q = f2_mul(g[i][s], prev[i][s]);
-          dA[i][s] = f2_fma(q, delta.v[i], dA[i][s]);
-          sq = s ? f2_fma(q, A[i][s], sq) : f2_mul(q, A[i][s]);
-        }
-        f2_split(sy, ys[2 * i], ys[2 * i + 1]);
-        f2_split(sb, gb[2 * i], gb[2 * i + 1]);
-        f2_split(sq, qa[2 * i], qa[2 * i + 1]);
-      }
-      const float ysum = sum_over_states<SL>(ys, p.sl), gsum = sum_over_states<SL>(gb, p.sl),
-                  qsum = sum_over_states<SL>(qa, p.sl) * kLn2;  // A carries log2(e)
-      if (owner) {
-        const int col = p.col + mine;
-        const float xo = sm.r.x[k][col], uo = sm.r.up[k][col];
-        const float ddt = fmaf(xo, gsum, qsum) * sm.r.slope[k][col];
-        const int64_t at = (t0 + k) * a.d.E + e_mine;
-        static_cast<T *>(a.dx)[at] = from_f32<T>(fmaf(skip, uo, sm.r.delta[k][col] * gsum));
-        static_cast<T *>(a.ddt)[at] = from_f32<T>(ddt);
-        if (a.dz) static_cast<T *>(a.dz)[at] = from_f32<T>(sm.r.zf[k][col] * fmaf(skip, xo, ysum));
-        dd = fmaf(uo, xo, dd);
-        dbias += ddt;
-      }
+      f2 sy = 0, sb = 0, sq = 0;
       float v[8];
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         float lo, hi;
-        f2_split(db[s], lo, hi);
-        v[s] = lo + hi;
-        f2_split(dc[s], lo, hi);
-        v[4 + s] = lo + hi;
+        g[0][s] = f2_fma(c.v[s], up, g[0][s]);
+        f2_split(f2_mul(u, g[0][s]), lo, hi);
+        v[s] = lo + hi;  // db
+        f2_split(f2_mul(up, after[k][0][s]), lo, hi);
+        v[4 + s] = lo + hi;  // dc
+        sy = s ? f2_fma(c.v[s], after[k][0][s], sy) : f2_mul(c.v[s], after[k][0][s]);
+        sb = s ? f2_fma(b.v[s], g[0][s], sb) : f2_mul(b.v[s], g[0][s]);
+        g[0][s] = f2_mul(g[0][s], f2_ex2(f2_mul(A[0][s], delta)));
+        const f2 q = f2_mul(g[0][s], prev[0][s]);
+        dA[0][s] = f2_fma(q, delta, dA[0][s]);
+        sq = s ? f2_fma(q, A[0][s], sq) : f2_mul(q, A[0][s]);
       }
-      sum_over_channels<SL>(v, p, sm.red[k][p.warp]);
-      if (first >= 0 && a.dh0) store_final<SL>(a, p, a.dh0, first, g);
+      float yg[4], qa[2];
+      f2_split(sy, yg[0], yg[1]);
+      f2_split(sb, yg[2], yg[3]);
+      f2_split(sq, qa[0], qa[1]);
+      const float ygsum = sum_over_states<SL>(yg, p.sl);        // lanes 0, 1: y's; 2, 3: g . b
+      const float qsum = sum_over_states<SL>(qa, p.sl) * kLn2;  // A carries log2(e)
+      const int64_t at = (t0 + k) * a.d.E + e_mine;
+      if (owns_x) {
+        const float xo = sm.r.x[k][col], uo = sm.r.up[k][col];
+        const float ddt = fmaf(xo, ygsum, qsum) * sm.r.slope[k][col];
+        static_cast<T *>(a.dx)[at] = from_f32<T>(fmaf(skip, uo, sm.r.delta[k][col] * ygsum));
+        static_cast<T *>(a.ddt)[at] = from_f32<T>(ddt);
+        dd = fmaf(uo, xo, dd);
+        dbias += ddt;
+      } else if (owns_z && a.dz) {
+        static_cast<T *>(a.dz)[at] = from_f32<T>(sm.r.zf[k][col] * fmaf(skip, sm.r.x[k][col], ygsum));
+      }
+      sum_over_channels(v, p, sm.red[k][p.warp]);
+      if (first >= 0 && a.dh0) store_final(a, p, a.dh0, first, g);
     }
     __syncthreads();
     // db and dc of these tokens over the block's channels
     float *out = a.part_bc + ((int64_t)(blockIdx.x % (unsigned)a.ctiles) * a.M + t0) * (2 * P::SP);
-    for (int i = tid; i < nt * 2 * P::SP; i += kSsmThreads) {
+    for (int i = tid; i < nt * 2 * P::SP; i += P::kThreads) {
       const int k = i / (2 * P::SP), s = i % (2 * P::SP);
-      out[i] = (sm.red[k][0][s] + sm.red[k][1][s]) + (sm.red[k][2][s] + sm.red[k][3][s]);
+      float o = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) o += sm.red[k][w][s];
+      out[i] = o;
     }
   }
-  store_chunk<SL>(a, p, a.hloc, p.chunk, dA);  // this block's states there have been read
-  if (owner) {
+  store_chunk(a, p, a.hloc, p.chunk, dA);  // this block's states there have been read
+  if (owns_x) {
     a.part_e[p.chunk * 2 * a.d.E + e_mine] = dd;
     a.part_e[(p.chunk * 2 + 1) * a.d.E + e_mine] = dbias;
   }
@@ -458,7 +491,8 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 template <typename T, int SL>
 int launch_sl(const SsmArgs &a, void *db, void *dc, cudaStream_t st) {
   const unsigned grid = (unsigned)(a.chunks * a.ctiles);
-  constexpr int smem = sizeof(MainShared<SL>);
+  constexpr int smem = sizeof(MainShared<MainPlace<SL>>);
+  static_assert(MainPlace<SL>::CB == Place<SL>::CB, "one grid for both kernels");
   const cudaError_t e =
       cudaFuncSetAttribute(ssm_bwd_main_kernel<T, SL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_error(e, "ssm_bwd_main_kernel shared memory");
@@ -467,7 +501,7 @@ int launch_sl(const SsmArgs &a, void *db, void *dc, cudaStream_t st) {
   if (rc != GDR_OK) return rc;
   ssm_bwd_carry_kernel<<<dim3((unsigned)cdiv(a.d.E * 4 * SL, 128), 2), 128, 0, st>>>(a, 4 * SL);
   if ((rc = launched("ssm_bwd_carry_kernel")) != GDR_OK) return rc;
-  ssm_bwd_main_kernel<T, SL><<<grid, kSsmThreads, smem, st>>>(a);
+  ssm_bwd_main_kernel<T, SL><<<grid, 256, smem, st>>>(a);
   if ((rc = launched("ssm_bwd_main_kernel")) != GDR_OK) return rc;
   if (a.M > 0) {
     ssm_sum_bc_kernel<T><<<(unsigned)cdiv(a.M * a.d.G * a.d.S, 256), 256, 0, st>>>(a, 4 * SL, (T *)db, (T *)dc);
