@@ -36,6 +36,9 @@ __device__ __forceinline__ void store_fp8(uint8_t *p, const float (&v)[VEC], flo
     const uint32_t lo = pack_e4m3(v[0] * inv, v[1] * inv) | (pack_e4m3(v[2] * inv, v[3] * inv) << 16);
     const uint32_t hi = pack_e4m3(v[4] * inv, v[5] * inv) | (pack_e4m3(v[6] * inv, v[7] * inv) << 16);
     *reinterpret_cast<uint2 *>(p) = make_uint2(lo, hi);
+  } else if constexpr (VEC == 4) {
+    *reinterpret_cast<uint32_t *>(p) =
+        pack_e4m3(v[0] * inv, v[1] * inv) | (pack_e4m3(v[2] * inv, v[3] * inv) << 16);
   } else {
     p[0] = (uint8_t)(pack_e4m3(v[0] * inv, 0.f) & 0xffu);
   }
@@ -67,12 +70,13 @@ __device__ __forceinline__ float row_reduce(float v, float *red) {
   return v;
 }
 
-// Column of this thread's k-th vector.  VEC == 8: vectors of neighbouring
-// threads follow one another.  VEC == 1: a warp owns NV * 32 columns in a run,
+// Column of this thread's k-th vector.  VEC 8 (all bf16) or 4 (fp32 among the
+// types): 16 bytes of the widest, vectors of neighbouring threads follow one
+// another.  VEC 1: a warp owns NV * 32 columns in a run,
 // so that a scale group of 128 columns is four steps of one warp.
 template <int NT, int VEC, int NV>
 __device__ __forceinline__ int64_t col_of(int tid, int k) {
-  if constexpr (VEC == 8) return ((int64_t)k * NT + tid) * 8;
+  if constexpr (VEC > 1) return ((int64_t)k * NT + tid) * VEC;
   else return (int64_t)(tid >> 5) * (NV * 32) + k * 32 + (tid & 31);
 }
 
@@ -156,7 +160,8 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) norm_fwd_kernel(NormArgs 
   } else {
     uint8_t *y = static_cast<uint8_t *>(a.y) + m * E;
     float *scale = a.scale + m * a.ngroups;
-    if constexpr (VEC == 8) {  // a group is 16 neighbouring lanes
+    if constexpr (VEC > 1) {  // a group is 16 or 32 neighbouring lanes
+      constexpr int kLanes = GDR_QUANT_GROUP_SIZE / VEC;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const int64_t c = col_of<NT, VEC, NV>(tid, k);
@@ -164,10 +169,10 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) norm_fwd_kernel(NormArgs 
 #pragma unroll
         for (int i = 0; i < VEC; ++i) g = max_nan(g, c < E ? fabsf(v[k][i]) : 0.f);
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) g = max_nan(g, __shfl_xor_sync(0xffffffffu, g, o));
+        for (int o = kLanes / 2; o > 0; o >>= 1) g = max_nan(g, __shfl_xor_sync(0xffffffffu, g, o));
         if (c < E) {
           store_fp8<VEC>(y + c, v[k], group_inv(g));
-          if ((tid & 15) == 0) scale[c / GDR_QUANT_GROUP_SIZE] = group_scale(g);
+          if ((tid & (kLanes - 1)) == 0) scale[c / GDR_QUANT_GROUP_SIZE] = group_scale(g);
         }
       }
     } else {  // a group is four steps of the warp
@@ -254,55 +259,41 @@ __global__ void __launch_bounds__(256) norm_fwd_long_kernel(NormArgs a) {
   }
 }
 
-// Backward.  A block takes rows b, b + grid, ...  Each thread owns eight columns
-// and copies its own part of the next row into its own shared memory while it
-// works on this one: 16-byte asynchronous copies that cost no registers and, as
-// no other thread reads them, no barrier.  Held in registers instead, the next
-// row took the kernel from two blocks of 512 threads per multiprocessor to one,
-// or spilled.  The weight gradient of the thread's columns stays in registers
-// over all its rows and ends in row b of the partials, which col_sum_kernel adds
-// in order.
+// Backward.  A block takes rows b, b + grid, ...  Each thread owns two runs of
+// four columns, 4 NT apart so that a warp's accesses are whole lines in either
+// type, and copies its own part of the next row into its own shared memory while
+// it works on this one: asynchronous copies that cost no registers and, as no
+// other thread reads them, no barrier.  Held in registers instead, the next row
+// took the kernel from two blocks of 512 threads per multiprocessor to one, or
+// spilled.  The weight gradient of the thread's columns stays in registers over
+// all its rows and ends in row b of the partials, which col_sum_kernel adds in
+// order.
+template <int BYTES>
 __device__ __forceinline__ void copy_async(void *smem, const void *global) {
   const uint32_t to = (uint32_t)__cvta_generic_to_shared(smem);
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(global) : "memory");
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(global) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(global) : "memory");
 }
 
-// A thread's eight elements of a row in shared memory: 16-byte pieces, NT apart.
+// A thread's part of a row in shared memory.
 template <typename T, int NT>
 struct Slot {
-  static constexpr int kPieces = sizeof(T) / 2;
-  uint4 v[kPieces][NT];
-  __device__ __forceinline__ void fetch(const T *p, int tid) {
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) copy_async(&v[i][tid], reinterpret_cast<const uint4 *>(p) + i);
-  }
-  __device__ __forceinline__ void get(int tid, float (&o)[8]) const {
-    if constexpr (kPieces == 1) {
-      unpack8(v[0][tid], o);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 u = v[i][tid];
-        o[4 * i] = __uint_as_float(u.x);
-        o[4 * i + 1] = __uint_as_float(u.y);
-        o[4 * i + 2] = __uint_as_float(u.z);
-        o[4 * i + 3] = __uint_as_float(u.w);
-      }
-    }
-  }
-  __device__ __forceinline__ void put(int tid, const float (&o)[8]) {  // T float only
+  T v[2][NT][4];
+  __device__ __forceinline__ void fetch(const T *row, int tid, const bool (&in)[2]) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      v[i][tid] = make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]), __float_as_uint(o[4 * i + 2]),
-                             __float_as_uint(o[4 * i + 3]));
+      if (in[i]) copy_async<4 * sizeof(T)>(v[i][tid], row + (i * NT + tid) * 4);
   }
+  __device__ __forceinline__ void get(int i, int tid, float (&o)[4]) const { load4(v[i][tid], o); }
 };
 template <typename T, typename R, int NT>
-struct BwdShared {
+struct __align__(16) BwdShared {
   Slot<float, NT> w;
   struct Row {
-    Slot<T, NT> dy;
     Slot<R, NT> s, ds;
+    Slot<T, NT> dy;
   } row[2];
   float2 red[2][32];
 };
@@ -313,25 +304,25 @@ __global__ void __launch_bounds__(NT, 1024 / NT) norm_bwd_kernel(NormArgs a) {
   BwdShared<T, R, NT> &sm = *reinterpret_cast<BwdShared<T, R, NT> *>(smem_raw);
   const int tid = threadIdx.x;
   const int64_t E = a.d.E;
-  const int c = tid * 8;
-  const bool in = c < E;
-  float dw[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) dw[i] = 0.f;
+  const bool in[2] = {tid * 4 < E, (NT + tid) * 4 < E};
+  float dw[2][4] = {};
   auto fetch = [&](int64_t m, int buf) {
-    if (!in) return;
     auto &row = sm.row[buf];
-    row.dy.fetch(static_cast<const T *>(a.x) + m * a.d.ld_x + c, tid);
-    row.s.fetch(static_cast<const R *>(a.res) + m * a.d.ld_res + c, tid);
-    if (a.ds) row.ds.fetch(static_cast<const R *>(a.ds) + m * a.d.ld_ds + c, tid);
+    row.dy.fetch(static_cast<const T *>(a.x) + m * a.d.ld_x, tid, in);
+    row.s.fetch(static_cast<const R *>(a.res) + m * a.d.ld_res, tid, in);
+    if (a.ds) row.ds.fetch(static_cast<const R *>(a.ds) + m * a.d.ld_ds, tid, in);
   };
   if (blockIdx.x < a.d.M) fetch(blockIdx.x, 0);
   asm volatile("cp.async.commit_group;" ::: "memory");
-  if (in) {
-    float w[8];
-    if (a.d.weight_dtype == GDR_F32) load8(static_cast<const float *>(a.weight) + c, w);
-    else load8(static_cast<const T *>(a.weight) + c, w);
-    sm.w.put(tid, w);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float w[4] = {};
+    const int c = (i * NT + tid) * 4;
+    if (in[i]) {
+      if (a.d.weight_dtype == GDR_F32) load4(static_cast<const float *>(a.weight) + c, w);
+      else load4(static_cast<const T *>(a.weight) + c, w);
+    }
+    store4(sm.w.v[i][tid], w);
   }
   int buf = 0;
   for (int64_t m = blockIdx.x; m < a.d.M; m += gridDim.x) {
@@ -340,15 +331,17 @@ __global__ void __launch_bounds__(NT, 1024 / NT) norm_bwd_kernel(NormArgs a) {
     asm volatile("cp.async.wait_group 1;" ::: "memory");  // this row is here, the next one on its way
     const auto &row = sm.row[buf];
     float ss = 0.f, ps = 0.f;
-    if (in) {
-      float v[8], g[8], w[8];
-      row.s.get(tid, v);
-      row.dy.get(tid, g);
-      sm.w.get(tid, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        ss = fmaf(v[i], v[i], ss);
-        ps = fmaf(v[i] * w[i], g[i], ps);
+    for (int i = 0; i < 2; ++i) {
+      if (!in[i]) continue;
+      float v[4], g[4], w[4];
+      row.s.get(i, tid, v);
+      row.dy.get(i, tid, g);
+      sm.w.get(i, tid, w);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        ss = fmaf(v[k], v[k], ss);
+        ps = fmaf(v[k] * w[k], g[k], ps);
       }
     }
 #pragma unroll
@@ -371,31 +364,33 @@ __global__ void __launch_bounds__(NT, 1024 / NT) norm_bwd_kernel(NormArgs a) {
     }
     const float rho = rsqrtf(ss / (float)E + a.d.eps);
     const float mix = rho * rho * (ps / (float)E);
-    if (in) {
-      float v[8], g[8], w[8], o[8];
-      row.s.get(tid, v);
-      row.dy.get(tid, g);
-      sm.w.get(tid, w);
-      if (a.ds) {
-        row.ds.get(tid, o);
-      } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = 0.f;
-      }
+    for (int i = 0; i < 2; ++i) {
+      if (!in[i]) continue;
+      float v[4], g[4], w[4], o[4] = {};
+      row.s.get(i, tid, v);
+      row.dy.get(i, tid, g);
+      sm.w.get(i, tid, w);
+      if (a.ds) row.ds.get(i, tid, o);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        dw[i] = fmaf(g[i] * rho, v[i], dw[i]);
-        o[i] = fmaf(rho, fmaf(w[i], g[i], -v[i] * mix), o[i]);
+      for (int k = 0; k < 4; ++k) {
+        dw[i][k] = fmaf(g[k] * rho, v[k], dw[i][k]);
+        o[k] = fmaf(rho, fmaf(w[k], g[k], -v[k] * mix), o[k]);
       }
-      if (a.y) store8(static_cast<T *>(a.y) + m * E + c, o);
-      if (a.s) store8(static_cast<R *>(a.s) + m * E + c, o);
+      const int64_t at = m * E + (i * NT + tid) * 4;
+      if (a.y) store4(static_cast<T *>(a.y) + at, o);
+      if (a.s) store4(static_cast<R *>(a.s) + at, o);
     }
     buf ^= 1;
   }
-  if (a.scale && in) store8(a.scale + (int64_t)blockIdx.x * E + c, dw);
+  if (a.scale) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (in[i]) store4(a.scale + (int64_t)blockIdx.x * E + (i * NT + tid) * 4, dw[i]);
+  }
 }
 
-// The same for rows that allow no 16-byte accesses: NV single columns of a thread.
+// The same for rows that allow no accesses of four columns: NV single columns of a thread.
 template <typename T, typename R, int NT, int NV>
 __global__ void __launch_bounds__(NT) norm_bwd_scalar_kernel(NormArgs a) {
   __shared__ __align__(16) float red[2][32];
@@ -491,12 +486,13 @@ int launch_fwd(const NormArgs &a, cudaStream_t st) {
   const bool vec = E % 8 == 0 && a.d.ld_x % 8 == 0 && (!RES || a.d.ld_res % 8 == 0) && is_aligned16(a.x) &&
                    is_aligned16(a.res) && is_aligned16(a.weight) && is_aligned16(a.y) && is_aligned16(a.s);
   if (vec) {
-    if (E <= 512) launch_fwd_q<T, R, 32, 8, 2, RES>(a, st);
-    else if (E <= 1024) launch_fwd_q<T, R, 128, 8, 1, RES>(a, st);
-    else if (E <= 2048) launch_fwd_q<T, R, 256, 8, 1, RES>(a, st);
-    else if (E <= 4096) launch_fwd_q<T, R, 256, 8, 2, RES>(a, st);
-    else if (E <= 8192) launch_fwd_q<T, R, 512, 8, 2, RES>(a, st);
-    else if (E <= 16384) launch_fwd_q<T, R, 1024, 8, 2, RES>(a, st);
+    constexpr int V = sizeof(T) == 4 || (RES && sizeof(R) == 4) ? 4 : 8, K = 8 / V;
+    if (E <= 512) launch_fwd_q<T, R, 32, V, 2 * K, RES>(a, st);
+    else if (E <= 1024) launch_fwd_q<T, R, 128, V, K, RES>(a, st);
+    else if (E <= 2048) launch_fwd_q<T, R, 256, V, K, RES>(a, st);
+    else if (E <= 4096) launch_fwd_q<T, R, 256, V, 2 * K, RES>(a, st);
+    else if (E <= 8192) launch_fwd_q<T, R, 512, V, 2 * K, RES>(a, st);
+    else if (E <= 16384) launch_fwd_q<T, R, 1024, V, 2 * K, RES>(a, st);
     else norm_fwd_long_kernel<T, R, RES><<<(unsigned)a.d.M, 256, 0, st>>>(a);
   } else {
     if (E <= 256) launch_fwd_q<T, R, 32, 1, 8, RES>(a, st);
@@ -510,7 +506,7 @@ int launch_fwd(const NormArgs &a, cudaStream_t st) {
 template <typename T, typename R>
 int launch_bwd(NormArgs a, float *dweight, cudaStream_t st) {
   const int64_t E = a.d.E;
-  const bool vec = E % 8 == 0 && a.d.ld_x % 8 == 0 && a.d.ld_res % 8 == 0 && (!a.ds || a.d.ld_ds % 8 == 0) &&
+  const bool vec = E % 4 == 0 && a.d.ld_x % 4 == 0 && a.d.ld_res % 4 == 0 && (!a.ds || a.d.ld_ds % 4 == 0) &&
                    is_aligned16(a.x) && is_aligned16(a.res) && is_aligned16(a.ds) && is_aligned16(a.weight) && is_aligned16(a.y) &&
                    is_aligned16(a.s);
   // blocks, and rows of partials: 1024 threads of them on each multiprocessor

@@ -209,47 +209,74 @@ __global__ void __launch_bounds__(128) ssm_carry_kernel(SsmArgs a, int SP) {
 // finishes that row's output.  The bound is HBM: each state is read and written
 // once.
 constexpr int kStepRows = 4;
+
+// Four elements of b or c as they lie in memory.
+template <typename T>
+struct Raw4;
+template <>
+struct Raw4<__nv_bfloat16> {
+  uint2 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p, int s0, int S, int vec) {
+    u = make_uint2(0, 0);
+    if (vec) {
+      if (s0 < S) u = *reinterpret_cast<const uint2 *>(p + s0);
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) w[q] = s0 + q < S ? __bfloat16_as_ushort(p[s0 + q]) : 0;
+      u = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+    }
+  }
+  __device__ __forceinline__ void expand(float (&v)[4]) const {
+    v[0] = __uint_as_float(u.x << 16);
+    v[1] = __uint_as_float(u.x & 0xffff0000u);
+    v[2] = __uint_as_float(u.y << 16);
+    v[3] = __uint_as_float(u.y & 0xffff0000u);
+  }
+};
+template <>
+struct Raw4<float> {
+  float u[4];
+  __device__ __forceinline__ void load(const float *p, int s0, int S, int vec) { load_states(p, s0, S, vec, u); }
+  __device__ __forceinline__ void expand(float (&v)[4]) const {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = u[q];
+  }
+};
+
 template <typename T, int SL>
-__global__ void __launch_bounds__(256) ssm_step_kernel(SsmArgs a, const int32_t *slots, float *state, unsigned tiles) {
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) ssm_step_kernel(SsmArgs a, const int32_t *slots,
+                                                                               float *state, unsigned tiles) {
   const int64_t r0 = (int64_t)(blockIdx.x / tiles) * kStepRows;
   const int64_t i = (int64_t)(blockIdx.x % tiles) * 256 + threadIdx.x;
   const int64_t e = i / SL;
   const int sl = (int)(i % SL), s0 = sl * 4, S = (int)a.d.S;
   const bool in = e < a.d.E;
-  float h[kStepRows][4], b[kStepRows][4], c[kStepRows][4], A[4] = {};
-  float *row[kStepRows];
-  const unsigned g = in ? (unsigned)e / (unsigned)(a.d.E / a.d.G) : 0;
+  int64_t slot[kStepRows];  // negative: nothing to do
 #pragma unroll
   for (int k = 0; k < kStepRows; ++k) {
     const int64_t r = r0 + k;
-    int64_t slot = -1;
-    if (r < a.d.B) {
-      slot = slots ? slots[r] : r;
-      if (slot >= a.d.N) {
-        if (threadIdx.x == 0) raise_status(a.status, GDR_ERR_SLOTS);
-        slot = -1;
-      }
+    slot[k] = r < a.d.B && in ? (slots ? slots[r] : r) : -1;
+    if (slot[k] >= a.d.N) {
+      raise_status(a.status, GDR_ERR_SLOTS);
+      slot[k] = -1;
     }
-    row[k] = slot >= 0 && in ? state + (slot * a.d.E + e) * S : nullptr;
+  }
+  auto row = [&](int k) { return state + (slot[k] * a.d.E + e) * S; };
+  float h[kStepRows][4], A[4] = {};
+  Raw4<T> b[kStepRows], c[kStepRows];
+  const int64_t g = in ? (unsigned)e / (unsigned)(a.d.E / a.d.G) : 0;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) h[k][q] = b[k][q] = c[k][q] = 0.f;
-    if (row[k]) {
-      load_states(row[k], s0, S, a.s4, h[k]);
-      const T *bp = static_cast<const T *>(a.b) + r * a.d.ld_b + (int64_t)g * S;
-      const T *cp = static_cast<const T *>(a.c) + r * a.d.ld_c + (int64_t)g * S;
-      if (a.bc4) {
-        if (s0 < S) {
-          load4(bp + s0, b[k]);
-          load4(cp + s0, c[k]);
-        }
-      } else {
+  for (int k = 0; k < kStepRows; ++k) {
+    if (slot[k] >= 0) {
+      load_states(row(k), s0, S, a.s4, h[k]);
+      b[k].load(static_cast<const T *>(a.b) + (r0 + k) * a.d.ld_b + g * S, s0, S, a.bc4);
+      c[k].load(static_cast<const T *>(a.c) + (r0 + k) * a.d.ld_c + g * S, s0, S, a.bc4);
+    } else {
+      b[k].load(nullptr, S, S, 1);
+      c[k].load(nullptr, S, S, 1);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (s0 + q < S) {
-            b[k][q] = to_f32(bp[s0 + q]);
-            c[k][q] = to_f32(cp[s0 + q]);
-          }
-      }
+      for (int q = 0; q < 4; ++q) h[k][q] = 0.f;
     }
   }
   const int64_t r = r0 + sl;  // the row this lane prepares and finishes
@@ -273,18 +300,21 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(SsmArgs a, const int32_t 
 #pragma unroll
   for (int k = 0; k < kStepRows; ++k) {
     const float dk = __shfl_sync(0xffffffffu, delta, k, SL), uk = __shfl_sync(0xffffffffu, u, k, SL);
+    float bk[4], ck[4];
+    b[k].expand(bk);
+    c[k].expand(ck);
     out[k] = 0.f;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      h[k][q] = fmaf(ex2(dk * A[q]), h[k][q], uk * b[k][q]);
-      out[k] = fmaf(c[k][q], h[k][q], out[k]);
+      h[k][q] = fmaf(ex2(dk * A[q]), h[k][q], uk * bk[q]);
+      out[k] = fmaf(ck[q], h[k][q], out[k]);
     }
-    if (row[k]) store_states(row[k], s0, S, a.s4, h[k]);
+    if (slot[k] >= 0) store_states(row(k), s0, S, a.s4, h[k]);
   }
   const float y = sum_over_states<SL>(out, sl);
   if (owner) {
-    const float *mine = sl == 0 ? row[0] : sl == 1 ? row[1] : sl == 2 ? row[2] : row[3];
-    static_cast<T *>(a.y)[r * a.d.E + e] = from_f32<T>(mine ? fmaf(skip, x, y) * gate : 0.f);
+    const int64_t mine = sl == 0 ? slot[0] : sl == 1 ? slot[1] : sl == 2 ? slot[2] : slot[3];
+    static_cast<T *>(a.y)[r * a.d.E + e] = from_f32<T>(mine >= 0 ? fmaf(skip, x, y) * gate : 0.f);
   }
 }
 
