@@ -133,6 +133,22 @@ __device__ __forceinline__ void store_vec(T *p, const float (&v)[VEC]) {
   else p[0] = from_f32<T>(v[0]);
 }
 
+// Asynchronous copy of 16 or 8 bytes into shared memory.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *smem, const void *global) {
+  const uint32_t to = (uint32_t)__cvta_generic_to_shared(smem);
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(global) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(global) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most N of the thread's committed groups are under way.
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // An element of a parameter vector that is fp32 or of the input dtype.
 template <typename T>
 __device__ __forceinline__ float param(const void *p, bool f32, int64_t i) {

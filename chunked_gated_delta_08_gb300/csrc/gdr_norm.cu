@@ -268,15 +268,6 @@ __global__ void __launch_bounds__(256) norm_fwd_long_kernel(NormArgs a) {
 // spilled.  The weight gradient of the thread's columns stays in registers over
 // all its rows and ends in row b of the partials, which col_sum_kernel adds in
 // order.
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void *smem, const void *global) {
-  const uint32_t to = (uint32_t)__cvta_generic_to_shared(smem);
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(global) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(global) : "memory");
-}
-
 // A thread's part of a row in shared memory.
 template <typename T, int NT>
 struct Slot {
@@ -313,7 +304,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) norm_bwd_kernel(NormArgs a) {
     if (a.ds) row.ds.fetch(static_cast<const R *>(a.ds) + m * a.d.ld_ds, tid, in);
   };
   if (blockIdx.x < a.d.M) fetch(blockIdx.x, 0);
-  asm volatile("cp.async.commit_group;" ::: "memory");
+  copy_commit();
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     float w[4] = {};
@@ -327,8 +318,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) norm_bwd_kernel(NormArgs a) {
   int buf = 0;
   for (int64_t m = blockIdx.x; m < a.d.M; m += gridDim.x) {
     if (m + gridDim.x < a.d.M) fetch(m + gridDim.x, buf ^ 1);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    asm volatile("cp.async.wait_group 1;" ::: "memory");  // this row is here, the next one on its way
+    copy_commit();
+    copy_wait<1>();  // this row is here, the next one on its way
     const auto &row = sm.row[buf];
     float ss = 0.f, ps = 0.f;
 #pragma unroll

@@ -17,59 +17,63 @@
 namespace gdr {
 namespace {
 
-template <typename P>
+template <typename T, typename P, bool VEC, bool MAIN>
 struct __align__(16) FwdShared {
-  float delta[kTile][P::CB], x[kTile][P::CB], gate[kTile][P::CB];
+  Ahead<T, VEC ? (MAIN ? 3 : 2) : 1, VEC ? Stager<kTile, P::CB, kSsmThreads>::kCount : 1, VEC ? kSsmThreads : 1> ahead;
+  float delta[kTile][P::CB], x[kTile][P::CB], gate[MAIN ? kTile : 1][P::CB];
   float bias[P::CB];
   float2 b[kTile * P::SP], c[kTile * P::SP];
   Borders<kTile> bd;
 };
 
-// What a thread stages of a tile, as loaded.
-template <typename T, bool VEC, bool MAIN, int COUNT, int NB>
-struct FwdTile {
-  Raw8<T, VEC> x[COUNT], dt[COUNT], z[MAIN ? COUNT : 1];
-  T b[NB], c[MAIN ? NB : 1];
-};
-
 // MAIN: y and ht from the states that enter the chunks (a.hloc, zero where
 // null).  Else: the chunk's own state and sum of delta.
 template <typename T, int SL, bool VEC, bool MAIN>
-__global__ void __launch_bounds__(kSsmThreads, 4) ssm_fwd_kernel(SsmArgs a) {
+__global__ void __launch_bounds__(kSsmThreads, SL == 4 ? 5 : 4) ssm_fwd_kernel(SsmArgs a) {
   using P = Place<SL>;
   constexpr int NB = kTile * P::SP / kSsmThreads;
-  // bf16 tiles are loaded while the one before is computed; fp32 ones would take twice the registers
   constexpr bool kAhead = VEC && sizeof(T) == 2;
-  __shared__ FwdShared<P> sm;
+  __shared__ FwdShared<T, P, VEC, MAIN> sm;
   if (!seqlens_ok(a.cu, a.d.N, a.M, a.status)) return;
   const P p(a);
   if (MAIN && p.chunk == 0) copy_empty_states(a, p, a.h0, a.ht);
   const Stager<kTile, P::CB, kSsmThreads> st(p);
-  FwdTile<T, VEC, MAIN, st.kCount, NB> tile;
   States A, h;
+  T next_b[NB], next_c[MAIN ? NB : 1];
   const int64_t begin = p.chunk * a.L, end = begin + a.L < a.M ? begin + a.L : a.M;
-  auto fetch = [&](int64_t t0) {
-    const int nt = end - t0 < kTile ? (int)(end - t0) : kTile;
-    const int64_t e = p.e0 + st.col;
+  auto columns = [&](int64_t t0, int k) {  // of the thread's k-th token of a tile: columns to load
+    return st.has(k) && st.token(k) < end - t0 ? st.n : 0;
+  };
+  auto source = [&](const void *p0, int64_t ld, int64_t t0, int k) {
+    return static_cast<const T *>(p0) + (t0 + st.token(k)) * ld + p.e0 + st.col;
+  };
+  auto fetch_ahead = [&](int64_t t0) {
 #pragma unroll
     for (int k = 0; k < st.kCount; ++k) {
-      const int n = st.has(k) && st.token(k) < nt ? st.n : 0;
-      const int64_t t = t0 + st.token(k);
-      tile.x[k].load(static_cast<const T *>(a.x) + t * a.d.ld_x + e, n);
-      tile.dt[k].load(static_cast<const T *>(a.dt) + t * a.d.ld_dt + e, n);
-      if (MAIN && a.z) tile.z[k].load(static_cast<const T *>(a.z) + t * a.d.ld_z + e, n);
+      const int n = columns(t0, k);
+      sm.ahead.fetch(0, k, source(a.x, a.d.ld_x, t0, k), n);
+      sm.ahead.fetch(1, k, source(a.dt, a.d.ld_dt, t0, k), n);
+      if (MAIN && a.z) sm.ahead.fetch(2, k, source(a.z, a.d.ld_z, t0, k), n);
     }
+    copy_commit();
+  };
+  auto fetch_states = [&](int64_t t0) {
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
       const int i = k * kSsmThreads + threadIdx.x, t = i / P::SP, s = i % P::SP;
-      const bool in = t < nt && s < a.d.S;
+      const bool in = t < end - t0 && s < a.d.S;
       const int64_t at = p.g * a.d.S + s;
-      tile.b[k] = in ? static_cast<const T *>(a.b)[(t0 + t) * a.d.ld_b + at] : from_f32<T>(0.f);
-      if (MAIN) tile.c[k] = in ? static_cast<const T *>(a.c)[(t0 + t) * a.d.ld_c + at] : from_f32<T>(0.f);
+      next_b[k] = in ? static_cast<const T *>(a.b)[(t0 + t) * a.d.ld_b + at] : from_f32<T>(0.f);
+      if (MAIN) next_c[k] = in ? static_cast<const T *>(a.c)[(t0 + t) * a.d.ld_c + at] : from_f32<T>(0.f);
     }
   };
-  if (kAhead && begin < end) fetch(begin);
-  stage_bias<P::CB, kSsmThreads>(a, p, sm.bias);
+  if constexpr (kAhead) {
+    if (begin < end) {
+      fetch_ahead(begin);
+      fetch_states(begin);
+    }
+  }
+  stage_row<P::CB, kSsmThreads>(p, a.dt_bias, sm.bias);
   load_a(a, p, A);
   load_chunk(a, p, MAIN ? a.hloc : nullptr, p.chunk, h);
   const int mine = p.sl & 3;  // of the thread's four channels, the one whose output it finishes
@@ -105,7 +109,7 @@ __global__ void __launch_bounds__(kSsmThreads, 4) ssm_fwd_kernel(SsmArgs a) {
   int64_t bos = -1, eos = -1;  // of the sequence that the tile begins in
   for (int64_t t0 = begin; t0 < end; t0 += kTile) {
     const int nt = end - t0 < kTile ? (int)(end - t0) : kTile;
-    if (!kAhead) fetch(t0);
+    if (!kAhead) fetch_states(t0);
     if (t0 >= eos) {
       const SeqRange r = seq_range(a.cu, seq_of_token(a.cu, a.d.N, a.d.T, t0), a.d.T);
       bos = r.bos;
@@ -116,19 +120,29 @@ __global__ void __launch_bounds__(kSsmThreads, 4) ssm_fwd_kernel(SsmArgs a) {
     if (borders) stage_borders(a, t0, nt, sm.bd);
     Eight bias;
     get8(&sm.bias[st.col], bias);
+    if (kAhead) copy_wait<0>();
+    auto get = [&](int array, const void *src, int64_t ld, int k, Eight &v) {
+      if constexpr (kAhead) {
+        sm.ahead.get(array, k, v);
+      } else {
+        Raw8<T, VEC> r;
+        r.load(source(src, ld, t0, k), columns(t0, k));
+        r.expand(v);
+      }
+    };
 #pragma unroll
     for (int k = 0; k < st.kCount; ++k) {
       if (!st.has(k)) continue;
       const int t = st.token(k);
       Eight v;
-      tile.x[k].expand(v);
+      get(0, a.x, a.d.ld_x, k, v);
       put8(&sm.x[t][st.col], v);
-      tile.dt[k].expand(v);
+      get(1, a.dt, a.d.ld_dt, k, v);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = f2_delta(f2_add(v[i], bias[i]), a.d.flags & GDR_SSM_SOFTPLUS);
       put8(&sm.delta[t][st.col], v);
       if (MAIN) {
-        if (a.z) tile.z[k].expand(v);
+        if (a.z) get(2, a.z, a.d.ld_z, k, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = a.z ? f2_silu(v[i]) : f2_both(1.f);
         put8(&sm.gate[t][st.col], v);
@@ -136,14 +150,19 @@ __global__ void __launch_bounds__(kSsmThreads, 4) ssm_fwd_kernel(SsmArgs a) {
     }
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
-      const float bv = to_f32(tile.b[k]);
+      const float bv = to_f32(next_b[k]);
       sm.b[k * kSsmThreads + threadIdx.x] = make_float2(bv, bv);
       if (MAIN) {
-        const float cv = to_f32(tile.c[k]);
+        const float cv = to_f32(next_c[k]);
         sm.c[k * kSsmThreads + threadIdx.x] = make_float2(cv, cv);
       }
     }
-    if (kAhead && t0 + kTile < end) fetch(t0 + kTile);
+    if constexpr (kAhead) {
+      if (t0 + kTile < end) {
+        fetch_ahead(t0 + kTile);
+        fetch_states(t0 + kTile);
+      }
+    }
     __syncthreads();
     if (!borders && nt == kTile) {
 #pragma unroll 4

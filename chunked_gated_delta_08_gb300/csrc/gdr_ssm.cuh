@@ -37,7 +37,7 @@ struct SsmArgs {
   float *ht, *dh0;
   // scratch: states per chunk [chunks, E, SP] and sums of delta [chunks, E]
   float *hloc, *sumd, *gloc;
-  // backward: partials of db and dc [ctiles, M, 2 SP]; of dd and ddt_bias [chunks, 2, E] (da's reuse hloc)
+  // backward: partials of db and dc [ctiles, M, 2 SP]; of ddt_bias and dd [chunks, 2, E] (da's reuse hloc)
   float *part_bc, *part_e;
   int vec;       // backward: 16-byte loads of x, dt, z, dy
   int64_t M, chunks;
@@ -256,11 +256,30 @@ struct Stager {
   __device__ __forceinline__ bool has(int k) const { return TT * kRow >= THREADS * (k + 1) || token(k) < TT; }
 };
 
-// The block's row of dt_bias as fp32, zero past the group.
+// A thread's part of the next tile on its way into shared memory while this one
+// is computed: bf16 with 16-byte accesses (fp32 tiles would take twice the room,
+// and are loaded when they are staged).  A thread reads only what it copied, so
+// its own wait is enough.
+template <typename T, int ARRAYS, int COUNT, int THREADS>
+struct Ahead {
+  static constexpr bool kUse = sizeof(T) == 2;
+  uint4 v[kUse ? ARRAYS : 1][kUse ? COUNT : 1][kUse ? THREADS : 1];
+  __device__ __forceinline__ void fetch(int array, int k, const T *p, int n) {
+    uint4 *to = &v[array][k][threadIdx.x];
+    if (n > 0) copy_async<16>(to, p);
+    else *to = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void get(int array, int k, Eight &o) const {
+    Raw8<__nv_bfloat16, true> r;
+    r.u = v[array][k][threadIdx.x];
+    r.expand(o);
+  }
+};
+
+// The block's columns of a row of E values (dt_bias, d): zero past the group, and where null.
 template <int CB, int THREADS, typename P>
-__device__ __forceinline__ void stage_bias(const SsmArgs &a, const P &p, float *bias) {
-  for (int i = threadIdx.x; i < CB; i += THREADS)
-    bias[i] = a.dt_bias && p.e0 + i < p.e_end ? a.dt_bias[p.e0 + i] : 0.f;
+__device__ __forceinline__ void stage_row(const P &p, const float *src, float *dst) {
+  for (int i = threadIdx.x; i < CB; i += THREADS) dst[i] = src && p.e0 + i < p.e_end ? src[p.e0 + i] : 0.f;
 }
 
 // b or c of a tile as fp32 [TT][SP], each twice, zero past S and past the tokens.

@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_bwd_local_kernel(SsmArgs a) {
   if (!seqlens_ok(a.cu, a.d.N, a.M, a.status)) return;
   const P p(a);
   const Stager<kTile, P::CB, P::kThreads> st(p);
-  stage_bias<P::CB, P::kThreads>(a, p, sm.bias);
+  stage_row<P::CB, P::kThreads>(p, a.dt_bias, sm.bias);
   __syncthreads();
   States A, h, g, pass;  // pass: product of the decays since the chunk began; zero once a sequence started
   load_a(a, p, A);
@@ -214,7 +214,7 @@ using MainPlace = Place<SL, 1, 8>;
 
 template <typename P>
 struct MainShared {
-  ulonglong2 ckpt[kSubs][2][P::kThreads];  // a thread's states before each run of kSub tokens
+  ulonglong2 ckpt[kSubs - 1][2][P::kThreads];  // a thread's states before each run of kSub tokens but the first
   union {
     struct {
       float delta[kTile][P::CB], x[kTile][P::CB];
@@ -225,9 +225,12 @@ struct MainShared {
       float2 b[kSub * P::SP], c[kSub * P::SP];
     } r;
   };
-  float bias[P::CB];
+  float sums[3][kSub][P::CB];  // per channel and token, over the states: c . h, b . g, a . q
+  float bias[P::CB], skip[P::CB];
+  float total[2][kSub][P::CB];  // ddt and up x over the chunk, by column and thread row
   float red[kSub][8][2 * P::SP];  // db, dc of a token by warp
   Borders<kMaxL> bd;
+  unsigned border_mask[kMaxL / 32];
 };
 
 template <typename T, typename P, bool VEC>
@@ -280,6 +283,63 @@ __device__ __forceinline__ void stage_reverse(const SsmArgs &a, const P &p, int6
   }
 }
 
+// Eight columns to memory, n of them inside the group.
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_columns(T *p, int n, const Eight &v) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f2_split(v[i], f[2 * i], f[2 * i + 1]);
+  if (VEC) {
+    if (n > 0) store8(p, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = from_f32<T>(f[i]);
+  }
+}
+
+// The gradients of a run's tokens from the sums over states, by the threads that
+// staged them: dx and ddt by the first half of the block, dz by the second.
+template <typename T, typename P, bool VEC>
+__device__ __forceinline__ void finish(const SsmArgs &a, const P &p, int64_t t0, int nt, MainShared<P> &sm) {
+  constexpr int kHalf = P::kThreads / 2, kRow = P::CB / 8;
+  const int half = threadIdx.x / kHalf, i0 = threadIdx.x % kHalf, t = i0 / kRow, col = i0 % kRow * 8;
+  if (t >= nt) return;
+  const int64_t e = p.e0 + col, left = p.e_end - e, at = (t0 + t) * a.d.E + e;
+  const int n = left < 0 ? 0 : left < 8 ? (int)left : 8;
+  Eight x, up, o, v, w, skip, total;
+  get8(&sm.r.x[t][col], x);
+  get8(&sm.r.up[t][col], up);
+  get8(&sm.skip[col], skip);
+  get8(&sm.total[half][t][col], total);
+  if (half == 0) {
+    get8(&sm.r.delta[t][col], v);
+    get8(&sm.sums[1][t][col], w);  // b . g
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = f2_fma(skip[i], up[i], f2_mul(v[i], w[i]));
+    store_columns<T, VEC>(static_cast<T *>(a.dx) + at, n, o);
+    get8(&sm.sums[2][t][col], v);  // a . q, where a carries log2(e)
+    get8(&sm.r.slope[t][col], o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[i] = f2_mul(o[i], f2_fma(x[i], w[i], f2_mul(v[i], f2_both(kLn2))));
+      total[i] = f2_add(total[i], o[i]);
+    }
+    store_columns<T, VEC>(static_cast<T *>(a.ddt) + at, n, o);
+  } else {
+    if (a.dz) {
+      get8(&sm.sums[0][t][col], v);  // c . h
+      get8(&sm.r.zf[t][col], o);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = f2_mul(o[i], f2_fma(skip[i], x[i], v[i]));
+      store_columns<T, VEC>(static_cast<T *>(a.dz) + at, n, o);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) total[i] = f2_fma(up[i], x[i], total[i]);
+  }
+  put8(&sm.total[half][t][col], total);
+}
+
 // Sums v[0..7] (db of the thread's four states, then dc) over the channel lanes
 // of a warp, halving the values a lane holds at each step, and leaves them in
 // out[2 * SP] (db, then dc).
@@ -326,21 +386,24 @@ __global__ void __launch_bounds__(256, 2) ssm_bwd_main_kernel(SsmArgs a) {
   const int64_t begin = p.chunk * a.L, end = begin + a.L < a.M ? begin + a.L : a.M;
   const int len = end > begin ? (int)(end - begin) : 0;
   const int subs = (len + kSub - 1) / kSub;
-  // Of a channel pair's first four lanes, two finish dz and two dx and ddt, a channel each.
-  const int col = p.col + (p.sl & 1);
-  const int64_t e_mine = p.e0 + col;
-  const bool owner = p.sl < 4 && e_mine < p.e_end, owns_z = owner && p.sl < 2, owns_x = owner && p.sl >= 2;
-  const float skip = a.dskip && owner ? a.dskip[e_mine] : 0.f;
-  float dd = 0.f, dbias = 0.f;
-  stage_bias<P::CB, P::kThreads>(a, p, sm.bias);
-  stage_borders(a, begin, len, sm.bd);
+  stage_row<P::CB, P::kThreads>(p, a.dt_bias, sm.bias);
+  stage_row<P::CB, P::kThreads>(p, a.dskip, sm.skip);
+  for (int i = tid; i < 2 * kSub * P::CB; i += P::kThreads) (&sm.total[0][0][0])[i] = 0.f;
+  const bool borders = stage_borders(a, begin, len, sm.bd);
+  if (tid < 2) sm.border_mask[tid] = 0;
+  __syncthreads();
+  if (borders) atomicOr(&sm.border_mask[tid >> 5], 1u << (tid & 31));  // tokens that start or end a sequence
 
   auto keep = [&](int sub) {
-    sm.ckpt[sub][0][tid] = make_ulonglong2(h[0][0], h[0][1]);
-    sm.ckpt[sub][1][tid] = make_ulonglong2(h[0][2], h[0][3]);
+    sm.ckpt[sub - 1][0][tid] = make_ulonglong2(h[0][0], h[0][1]);
+    sm.ckpt[sub - 1][1][tid] = make_ulonglong2(h[0][2], h[0][3]);
   };
   auto back_to = [&](int sub, StatesOf<1> &to) {
-    const ulonglong2 u = sm.ckpt[sub][0][tid], v = sm.ckpt[sub][1][tid];
+    if (sub == 0) {
+      load_chunk(a, p, a.hloc, p.chunk, to);
+      return;
+    }
+    const ulonglong2 u = sm.ckpt[sub - 1][0][tid], v = sm.ckpt[sub - 1][1][tid];
     to[0][0] = u.x;
     to[0][1] = u.y;
     to[0][2] = v.x;
@@ -348,7 +411,6 @@ __global__ void __launch_bounds__(256, 2) ssm_bwd_main_kernel(SsmArgs a) {
   };
 
   // States at the start of every run of kSub tokens; the last run needs only its start.
-  keep(0);
   const int flen = subs > 0 ? (subs - 1) * kSub : 0;
   {
     const Stager<kTile, P::CB, P::kThreads> st(p);
@@ -382,32 +444,9 @@ __global__ void __launch_bounds__(256, 2) ssm_bwd_main_kernel(SsmArgs a) {
     stage_states<T, kSub, P::kThreads>(a, p, a.b, a.d.ld_b, t0, nt, sm.r.b);
     stage_states<T, kSub, P::kThreads>(a, p, a.c, a.d.ld_c, t0, nt, sm.r.c);
     __syncthreads();
-    StatesOf<1> after[kSub];  // after[k]: the state after token k (past the end: never read)
-    back_to(sub, h);
-#pragma unroll
-    for (int k = 0; k < kSub; ++k) {
-      if (k < nt) {
-        if (sm.bd.first[sub * kSub + k] >= 0) load_h0(a, p, a.h0, sm.bd.first[sub * kSub + k], h);
-        advance(h, A, Pairs<1>(&sm.r.delta[k][p.col]), Pairs<1>(&sm.r.x[k][p.col]),
-                Twice(&sm.r.b[k * P::SP + p.sl * 4]));
-      }
-#pragma unroll
-      for (int s = 0; s < 4; ++s) after[k][0][s] = h[0][s];
-    }
-#pragma unroll
-    for (int k = kSub - 1; k >= 0; --k) {
-      if (k >= nt) continue;
-      const int first = sm.bd.first[sub * kSub + k], last = sm.bd.last[sub * kSub + k];
-      if (last >= 0) load_h0(a, p, a.dht, last, g);
-      StatesOf<1> prev;
-      if (first >= 0) {
-        load_h0(a, p, a.h0, first, prev);
-      } else if (k == 0) {
-        back_to(sub, prev);
-      } else {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) prev[0][s] = after[k > 0 ? k - 1 : 0][0][s];
-      }
+    // the reverse recurrence at token k, from the states before and after it
+    auto reverse = [&](int k, const StatesOf<1> &prev, const StatesOf<1> &after) {
+      asm volatile("" ::: "memory");  // one token's values at a time: loads moved up from later ones spill
       const f2 delta = Pairs<1>(&sm.r.delta[k][p.col]).v[0], up = Pairs<1>(&sm.r.up[k][p.col]).v[0];
       const f2 u = f2_mul(delta, Pairs<1>(&sm.r.x[k][p.col]).v[0]);
       const Twice b(&sm.r.b[k * P::SP + p.sl * 4]), c(&sm.r.c[k * P::SP + p.sl * 4]);
@@ -419,9 +458,9 @@ __global__ void __launch_bounds__(256, 2) ssm_bwd_main_kernel(SsmArgs a) {
         g[0][s] = f2_fma(c.v[s], up, g[0][s]);
         f2_split(f2_mul(u, g[0][s]), lo, hi);
         v[s] = lo + hi;  // db
-        f2_split(f2_mul(up, after[k][0][s]), lo, hi);
+        f2_split(f2_mul(up, after[0][s]), lo, hi);
         v[4 + s] = lo + hi;  // dc
-        sy = s ? f2_fma(c.v[s], after[k][0][s], sy) : f2_mul(c.v[s], after[k][0][s]);
+        sy = s ? f2_fma(c.v[s], after[0][s], sy) : f2_mul(c.v[s], after[0][s]);
         sb = s ? f2_fma(b.v[s], g[0][s], sb) : f2_mul(b.v[s], g[0][s]);
         g[0][s] = f2_mul(g[0][s], f2_ex2(f2_mul(A[0][s], delta)));
         const f2 q = f2_mul(g[0][s], prev[0][s]);
@@ -432,21 +471,50 @@ __global__ void __launch_bounds__(256, 2) ssm_bwd_main_kernel(SsmArgs a) {
       f2_split(sy, yg[0], yg[1]);
       f2_split(sb, yg[2], yg[3]);
       f2_split(sq, qa[0], qa[1]);
-      const float ygsum = sum_over_states<SL>(yg, p.sl);        // lanes 0, 1: y's; 2, 3: g . b
-      const float qsum = sum_over_states<SL>(qa, p.sl) * kLn2;  // A carries log2(e)
-      const int64_t at = (t0 + k) * a.d.E + e_mine;
-      if (owns_x) {
-        const float xo = sm.r.x[k][col], uo = sm.r.up[k][col];
-        const float ddt = fmaf(xo, ygsum, qsum) * sm.r.slope[k][col];
-        static_cast<T *>(a.dx)[at] = from_f32<T>(fmaf(skip, uo, sm.r.delta[k][col] * ygsum));
-        static_cast<T *>(a.ddt)[at] = from_f32<T>(ddt);
-        dd = fmaf(uo, xo, dd);
-        dbias += ddt;
-      } else if (owns_z && a.dz) {
-        static_cast<T *>(a.dz)[at] = from_f32<T>(sm.r.zf[k][col] * fmaf(skip, sm.r.x[k][col], ygsum));
-      }
+      const float ygsum = sum_over_states<SL>(yg, p.sl);  // lanes 0, 1: c . h of the two channels; 2, 3: b . g
+      const float qsum = sum_over_states<SL>(qa, p.sl);
+      if (p.sl < 4) sm.sums[p.sl >> 1][k][p.col + (p.sl & 1)] = ygsum;
+      if (p.sl < 2) sm.sums[2][k][p.col + p.sl] = qsum;
       sum_over_channels(v, p, sm.red[k][p.warp]);
-      if (first >= 0 && a.dh0) store_final(a, p, a.dh0, first, g);
+    };
+    auto forward = [&](int k) {
+      asm volatile("" ::: "memory");
+      advance(h, A, Pairs<1>(&sm.r.delta[k][p.col]), Pairs<1>(&sm.r.x[k][p.col]),
+              Twice(&sm.r.b[k * P::SP + p.sl * 4]));
+    };
+    const int first_token = sub * kSub;
+    back_to(sub, h);
+    if (nt == kSub && !(sm.border_mask[first_token >> 5] >> (first_token & 31) & ((1u << kSub) - 1))) {
+      StatesOf<1> before[kSub];  // before[k]: the state before token k
+#pragma unroll
+      for (int k = 0; k < kSub; ++k) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) before[k][0][s] = h[0][s];
+        forward(k);
+      }
+#pragma unroll
+      for (int k = kSub - 1; k >= 0; --k) reverse(k, before[k], k == kSub - 1 ? h : before[k < kSub - 1 ? k + 1 : k]);
+    } else {
+      // A run that a sequence starts or ends in, or of fewer tokens: the states of each token over again.
+#pragma unroll 1
+      for (int k = nt - 1; k >= 0; --k) {
+        StatesOf<1> prev;
+        back_to(sub, h);
+#pragma unroll 1
+        for (int q = 0; q <= k; ++q) {
+          const int first = sm.bd.first[first_token + q];
+          if (first >= 0) load_h0(a, p, a.h0, first, h);
+          if (q == k) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) prev[0][s] = h[0][s];
+          }
+          forward(q);
+        }
+        const int first = sm.bd.first[first_token + k], last = sm.bd.last[first_token + k];
+        if (last >= 0) load_h0(a, p, a.dht, last, g);
+        reverse(k, prev, h);
+        if (first >= 0 && a.dh0) store_final(a, p, a.dh0, first, g);
+      }
     }
     __syncthreads();
     // db and dc of these tokens over the block's channels
@@ -458,12 +526,19 @@ __global__ void __launch_bounds__(256, 2) ssm_bwd_main_kernel(SsmArgs a) {
       for (int w = 0; w < 8; ++w) o += sm.red[k][w][s];
       out[i] = o;
     }
+    if (a.vec) finish<T, P, true>(a, p, t0, nt, sm);
+    else finish<T, P, false>(a, p, t0, nt, sm);
+  }
+  // ddt_bias and dd of the chunk
+  __syncthreads();
+  for (int i = tid; i < 2 * P::CB; i += P::kThreads) {
+    const int which = i / P::CB, c = i % P::CB;
+    float o = 0.f;
+#pragma unroll
+    for (int k = 0; k < kSub; ++k) o += sm.total[which][k][c];
+    if (p.e0 + c < p.e_end) a.part_e[(p.chunk * 2 + which) * a.d.E + p.e0 + c] = o;
   }
   store_chunk(a, p, a.hloc, p.chunk, dA);  // this block's states there have been read
-  if (owns_x) {
-    a.part_e[p.chunk * 2 * a.d.E + e_mine] = dd;
-    a.part_e[(p.chunk * 2 + 1) * a.d.E + e_mine] = dbias;
-  }
 }
 
 // db and dc [M, G, S] from the partials of the channel blocks of each group.
@@ -521,7 +596,8 @@ int run_bwd(SsmArgs a, float *da, void *db, void *dc, float *dd, float *ddt_bias
   int sl, rc;
   bool vec;
   if ((rc = ssm_prepare(a, true, &sl, &vec)) != GDR_OK) return rc;
-  a.vec = vec;
+  // the outputs' rows are E long: 16-byte stores where E and the pointers allow them
+  a.vec = vec && is_aligned16(a.dx) && is_aligned16(a.ddt) && is_aligned16(a.dz);
   a.L = kMaxL;
   while (a.L > 2 * kSub && cdiv(a.M, a.L) * a.ctiles < 2 * kSMs) a.L /= 2;
   a.chunks = std::max<int64_t>(1, cdiv(a.M, a.L));
@@ -542,8 +618,8 @@ int run_bwd(SsmArgs a, float *da, void *db, void *dc, float *dd, float *ddt_bias
   rc = a.d.dtype == GDR_BF16 ? launch_t<__nv_bfloat16>(a, sl, db, dc, st) : launch_t<float>(a, sl, db, dc, st);
   const SeqCheck seqs{a.cu, a.d.N, a.M, a.status};
   if (rc == GDR_OK) rc = launch_col_sum(a.hloc, a.chunks, E * SP, E * SP, SP, a.d.S, da, seqs, st);
-  if (rc == GDR_OK && dd) rc = launch_col_sum(a.part_e, a.chunks, 2 * E, E, E, E, dd, seqs, st);
-  if (rc == GDR_OK && ddt_bias) rc = launch_col_sum(a.part_e + E, a.chunks, 2 * E, E, E, E, ddt_bias, seqs, st);
+  if (rc == GDR_OK && dd) rc = launch_col_sum(a.part_e + E, a.chunks, 2 * E, E, E, E, dd, seqs, st);
+  if (rc == GDR_OK && ddt_bias) rc = launch_col_sum(a.part_e, a.chunks, 2 * E, E, E, E, ddt_bias, seqs, st);
   return scratch_end(base, st, "scan backward scratch", rc);
 }
 
