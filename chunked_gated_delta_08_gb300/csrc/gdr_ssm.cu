@@ -22,14 +22,14 @@ struct __align__(16) FwdShared {
   Ahead<T, VEC ? (MAIN ? 3 : 2) : 1, VEC ? Stager<kTile, P::CB, kSsmThreads>::kCount : 1, VEC ? kSsmThreads : 1> ahead;
   float delta[kTile][P::CB], x[kTile][P::CB], gate[MAIN ? kTile : 1][P::CB];
   float bias[P::CB];
-  float2 b[kTile * P::SP], c[kTile * P::SP];
+  float b[kTile * P::SP], c[kTile * P::SP];
   Borders<kTile> bd;
 };
 
 // MAIN: y and ht from the states that enter the chunks (a.hloc, zero where
 // null).  Else: the chunk's own state and sum of delta.
 template <typename T, int SL, bool VEC, bool MAIN>
-__global__ void __launch_bounds__(kSsmThreads, SL == 4 ? 5 : 4) ssm_fwd_kernel(SsmArgs a) {
+__global__ void __launch_bounds__(kSsmThreads, 4) ssm_fwd_kernel(SsmArgs a) {
   using P = Place<SL>;
   constexpr int NB = kTile * P::SP / kSsmThreads;
   constexpr bool kAhead = VEC && sizeof(T) == 2;
@@ -151,10 +151,10 @@ __global__ void __launch_bounds__(kSsmThreads, SL == 4 ? 5 : 4) ssm_fwd_kernel(S
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
       const float bv = to_f32(next_b[k]);
-      sm.b[k * kSsmThreads + threadIdx.x] = make_float2(bv, bv);
+      sm.b[k * kSsmThreads + threadIdx.x] = bv;
       if (MAIN) {
         const float cv = to_f32(next_c[k]);
-        sm.c[k * kSsmThreads + threadIdx.x] = make_float2(cv, cv);
+        sm.c[k * kSsmThreads + threadIdx.x] = cv;
       }
     }
     if constexpr (kAhead) {
@@ -395,20 +395,38 @@ int validate(const gdr_ssm_desc *d, const int64_t *cu, bool step) {
   return GDR_OK;
 }
 
-// Chunk length: long chunks cost less carry, short ones fill the GPU.
-int64_t chunk_length(const SsmArgs &a, int64_t lo, int64_t hi) {
-  int64_t L = hi;
-  while (L > lo && cdiv(a.M, L) * a.ctiles < 8 * kSMs) L /= 2;
-  return L;
+// Chunk length, in whole tiles.  The grid runs in waves of four blocks on each
+// multiprocessor; in units of a quarter of a token's time in one wave, a wave of
+// local and main takes 4 (L + 8), the chunk's start included, and the carry about
+// one per chunk (measured: 0.7 us a token, 0.2 us a chunk).  The last wave is
+// what matters: 16384 x 4096 channels in chunks of 256 tokens leave it a third
+// full and take 593 us, against 560 us with the length chosen here.
+constexpr int kWave = 4 * kSMs;
+int64_t chunk_cost(const SsmArgs &a, int64_t L) {
+  const int64_t chunks = cdiv(a.M, L);
+  return 4 * cdiv(chunks * a.ctiles, kWave) * (L + 8) + chunks;
+}
+int64_t chunk_length(const SsmArgs &a) {
+  int64_t best = kTile, least = chunk_cost(a, kTile);
+  for (int64_t L = 2 * kTile; L <= 512; L += kTile) {
+    const int64_t cost = chunk_cost(a, L);
+    if (cost < least) {
+      least = cost;
+      best = L;
+    }
+  }
+  return best;
 }
 
 int run_fwd(SsmArgs a, cudaStream_t st) {
   int sl, rc;
   bool vec;
   if ((rc = ssm_prepare(a, false, &sl, &vec)) != GDR_OK) return rc;
-  // Sequences that are short, or enough of them to fill the GPU: each is one chunk.
-  const bool whole = !a.cu && (a.d.T <= 64 || a.d.B * a.ctiles >= 4 * kSMs);
-  a.L = whole ? std::max<int64_t>(1, a.d.T) : chunk_length(a, 32, 256);
+  // A dense batch may take each sequence as one chunk: main alone, three fifths of the work per token.
+  a.L = chunk_length(a);
+  const bool whole =
+      !a.cu && (a.d.T <= 2 * kTile || 12 * cdiv(a.d.B * a.ctiles, kWave) * (a.d.T + 8) <= 5 * chunk_cost(a, a.L));
+  if (whole) a.L = std::max<int64_t>(1, a.d.T);
   a.chunks = std::max<int64_t>(1, cdiv(a.M, a.L));
   if (a.chunks * a.ctiles > 0x7fffffff) return set_error(GDR_ERR_SHAPE, "too many tokens and channels for one launch");
   if (whole || a.chunks == 1) return launch_fwd<true>(a, sl, vec, st);

@@ -285,7 +285,7 @@ __device__ __forceinline__ void stage_row(const P &p, const float *src, float *d
 // b or c of a tile as fp32 [TT][SP], each twice, zero past S and past the tokens.
 template <typename T, int TT, int THREADS, typename P>
 __device__ __forceinline__ void stage_states(const SsmArgs &a, const P &p, const void *src, int64_t ld, int64_t t0,
-                                             int nt, float2 *dst) {
+                                             int nt, float *dst) {
   constexpr int SP = P::SP;
   const T *row = static_cast<const T *>(src) + p.g * a.d.S;
 #pragma unroll
@@ -293,7 +293,7 @@ __device__ __forceinline__ void stage_states(const SsmArgs &a, const P &p, const
     const int i = i0 + threadIdx.x, t = i / SP, s = i % SP;
     if (TT * SP % THREADS != 0 && i >= TT * SP) break;
     const float v = t < nt && s < a.d.S ? to_f32(row[(t0 + t) * ld + s]) : 0.f;
-    dst[i] = make_float2(v, v);
+    dst[i] = v;
   }
 }
 
@@ -384,12 +384,12 @@ struct Pairs {
 // Four values of a staged row of b or c: the thread's states, each twice.
 struct Twice {
   f2 v[4];
-  __device__ __forceinline__ explicit Twice(const float2 *row) {
-    const ulonglong2 *u = reinterpret_cast<const ulonglong2 *>(row);
-    v[0] = u[0].x;
-    v[1] = u[0].y;
-    v[2] = u[1].x;
-    v[3] = u[1].y;
+  __device__ __forceinline__ explicit Twice(const float *row) {
+    const float4 u = *reinterpret_cast<const float4 *>(row);
+    v[0] = f2_both(u.x);
+    v[1] = f2_both(u.y);
+    v[2] = f2_both(u.z);
+    v[3] = f2_both(u.w);
   }
 };
 

@@ -35,7 +35,7 @@ template <typename P>
 struct __align__(16) LocalShared {
   float delta[kTile][P::CB], x[kTile][P::CB], up[kTile][P::CB];
   float bias[P::CB];
-  float2 b[kTile * P::SP], c[kTile * P::SP];
+  float b[kTile * P::SP], c[kTile * P::SP];
   Borders<kTile> bd;
 };
 
@@ -218,11 +218,11 @@ struct MainShared {
   union {
     struct {
       float delta[kTile][P::CB], x[kTile][P::CB];
-      float2 b[kTile * P::SP];
+      float b[kTile * P::SP];
     } f;
     struct {
       float delta[kSub][P::CB], x[kSub][P::CB], up[kSub][P::CB], slope[kSub][P::CB], zf[kSub][P::CB];
-      float2 b[kSub * P::SP], c[kSub * P::SP];
+      float b[kSub * P::SP], c[kSub * P::SP];
     } r;
   };
   float sums[3][kSub][P::CB];  // per channel and token, over the states: c . h, b . g, a . q
