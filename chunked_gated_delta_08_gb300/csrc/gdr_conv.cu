@@ -477,14 +477,14 @@ int with_taps(int64_t W, F &&f) {
 
 enum Dir { kFwd, kBwd, kStep };
 
-// Tokens in a run: long enough that the W - 1 tokens read again, the weights
-// and (backward) the partials are small beside it, short enough that the grid
-// fills the GPU.
-int run_length(int64_t M, int64_t E, int vec, int lo, int hi) {
-  const int64_t want = M * cdiv(E, vec) / ((int64_t)kSMs * 1024);
-  int L = lo;
-  while (L < hi && L < want) L *= 2;
-  return L;
+// Tokens in a run.  A run reads W - 1 tokens again, loads its weights and leaves
+// partials, so it is long; and the grid is whole waves of the five blocks that a
+// multiprocessor holds, as few as keep runs within `hi`.
+int64_t run_length(int64_t M, int64_t tiles, int64_t per, int64_t lo, int64_t hi) {
+  const int64_t slots = 5 * kSMs * per;  // runs of one wave, times tiles
+  int64_t L = hi + 1;
+  for (int64_t waves = 1; L > hi; ++waves) L = cdiv(M * tiles, slots * waves);
+  return std::max(L, lo);
 }
 
 // Four channels of a thread in the forward and the step.  The backward keeps
@@ -504,7 +504,7 @@ int launch(ConvArgs a, Dir dir, float *dweight, float *dbias, cudaStream_t st) {
       return launched("conv_step_kernel");
     });
   }
-  a.L = dir == kFwd ? run_length(a.M, d.E, vec, 8, 64) : run_length(a.M, d.E, vec, 16, 128);
+  a.L = (int)(dir == kFwd ? run_length(a.M, tiles, per, 8, 96) : run_length(a.M, tiles, per, 16, 384));
   a.runs = std::max<int64_t>(1, cdiv(a.M, a.L));
   const int64_t blocks = tiles * cdiv(a.runs, per);
   if (blocks > 0x7fffffff) return set_error(GDR_ERR_SHAPE, "too many tokens for one launch");

@@ -87,9 +87,9 @@ def _param_code(t, x, name):
 
 def _device(t, name):
     """The index of the current device, which must own the inputs."""
-    if not t.is_cuda:
+    dev = t.get_device()  # -1 on the CPU
+    if dev < 0:
         raise GdrError(GDR_ERR_NULLPTR, f"{name} must be a CUDA tensor")
-    dev = t.get_device()
     if dev != torch.cuda.current_device():
         raise GdrError(GDR_ERR_NULLPTR, f"{name} is on {t.device}, but cuda:{torch.cuda.current_device()} is current")
     return dev
@@ -97,9 +97,9 @@ def _device(t, name):
 
 def _on(t, dev, name):
     """t is on the GPU that the call runs on."""
-    if not t.is_cuda:
-        raise GdrError(GDR_ERR_NULLPTR, f"{name} must be a CUDA tensor")
     if t.get_device() != dev:
+        if not t.is_cuda:
+            raise GdrError(GDR_ERR_NULLPTR, f"{name} must be a CUDA tensor")
         raise GdrError(GDR_ERR_NULLPTR, f"{name} is on {t.device}, expected cuda:{dev}")
 
 
@@ -155,7 +155,16 @@ def _outputs_on(stream):
 
 
 def _stream(stream, dev):
-    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _like(t):
+    """An output of t's shape and dtype, contiguous."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def _new(t, shape, dtype=None):
+    return torch.empty(shape, dtype=t.dtype if dtype is None else dtype, device=t.device)
 
 
 def _call(fn, desc, *args):
@@ -192,14 +201,14 @@ def norm_fwd(x, weight, residual=None, eps=1e-6, quant=None, stream=None):
         ld_r = _rows(residual, "residual", dev, None, x.shape)
     desc = GdrNormDesc(M, E, ld_x, ld_r, E, code, rcode, _param_code(weight, x, "weight"), _QUANTS[quant], eps, 0)
     with _outputs_on(stream):
-        s = None if residual is None else residual.new_empty(x.shape)
+        s = None if residual is None else _new(residual, x.shape)
         scale = None
         if quant is None:
-            y = x.new_empty(x.shape)
+            y = _like(x)
         else:
-            y = x.new_empty(x.shape, dtype=torch.float8_e4m3fn)
+            y = _new(x, x.shape, torch.float8_e4m3fn)
             lead = x.shape[:-1]
-            scale = x.new_empty(lead if quant == "row" else (*lead, -(-E // GROUP_SIZE)), dtype=torch.float32)
+            scale = _new(x, lead if quant == "row" else (*lead, -(-E // GROUP_SIZE)), torch.float32)
     _call(_lib.gdr_norm_fwd, desc, x.data_ptr(), _addr(residual), weight.data_ptr(), y.data_ptr(), _addr(scale),
           _addr(s), _stream(stream, dev))
     return (y, s) if quant is None else (y, scale, s)
@@ -221,9 +230,9 @@ def norm_bwd(dy, s, weight, ds=None, eps=1e-6, stream=None):
     desc = GdrNormDesc(M, E, _rows(dy, "dy", dev), ld_s, ld_ds, code, rcode, _param_code(weight, dy, "weight"), 0, eps,
                        0)
     with _outputs_on(stream):
-        dx = dy.new_empty(dy.shape)
-        dres = dx if s.dtype == dy.dtype else s.new_empty(dy.shape)
-        dweight = dy.new_empty(E, dtype=torch.float32)
+        dx = _like(dy)
+        dres = dx if s.dtype == dy.dtype else _new(s, dy.shape)
+        dweight = _new(dy, E, torch.float32)
     _call(_lib.gdr_norm_bwd, desc, dy.data_ptr(), s.data_ptr(), _addr(ds), weight.data_ptr(), dx.data_ptr(),
           None if dres is dx else dres.data_ptr(), dweight.data_ptr(), _stream(stream, dev))
     return dx, dres, dweight
@@ -285,8 +294,8 @@ def conv_fwd(x, weight, bias=None, s0=None, cu_seqlens=None, activation="silu", 
     shape = (N, desc.W - 1, desc.E)
     _whole(s0, "s0", dev, x.dtype, shape)
     with _outputs_on(stream):
-        y = x.new_empty(x.shape)
-        st = x.new_empty(shape) if output_final_state else None
+        y = _like(x)
+        st = _new(x, shape) if output_final_state else None
     _call(_lib.gdr_conv_fwd, desc, x.data_ptr(), weight.data_ptr(), _addr(bias), _addr(s0), _addr(cu_seqlens),
           y.data_ptr(), _addr(st), _stream(stream, dev))
     return y, st
@@ -304,9 +313,9 @@ def conv_bwd(x, weight, dy, bias=None, s0=None, dst=None, cu_seqlens=None, activ
     _whole(s0, "s0", dev, x.dtype, shape)
     _whole(dst, "dst", dev, x.dtype, shape)
     with _outputs_on(stream):
-        dx, ds0 = x.new_empty(x.shape), x.new_empty(shape)
-        dweight = x.new_empty(weight.shape, dtype=torch.float32)
-        dbias = None if bias is None else x.new_empty(desc.E, dtype=torch.float32)
+        dx, ds0 = _like(x), _new(x, shape)
+        dweight = _new(x, weight.shape, torch.float32)
+        dbias = None if bias is None else _new(x, desc.E, torch.float32)
     _call(_lib.gdr_conv_bwd, desc, x.data_ptr(), weight.data_ptr(), _addr(bias), _addr(s0), _addr(cu_seqlens),
           dy.data_ptr(), _addr(dst), dx.data_ptr(), dweight.data_ptr(), _addr(dbias), ds0.data_ptr(),
           _stream(stream, dev))
@@ -323,7 +332,7 @@ def conv_step(x, state, weight, bias=None, activation="silu", slots=None, stream
     desc = _conv_desc(x, dev, weight, bias, activation, R, 1, P, x.shape[1])
     _whole(state, "state", dev, x.dtype, (P, desc.W - 1, desc.E))
     with _outputs_on(stream):
-        y = x.new_empty(x.shape)
+        y = _like(x)
     _call(_lib.gdr_conv_step, desc, x.data_ptr(), weight.data_ptr(), _addr(bias), _addr(slots), state.data_ptr(),
           y.data_ptr(), _stream(stream, dev))
     return y
@@ -360,8 +369,8 @@ def ssm_fwd(x, dt, a, b, c, d=None, z=None, dt_bias=None, h0=None, cu_seqlens=No
     shape = (N, desc.E, desc.S)
     _whole(h0, "h0", dev, torch.float32, shape)
     with _outputs_on(stream):
-        y = x.new_empty(x.shape)
-        ht = a.new_empty(shape) if output_final_state else None
+        y = _like(x)
+        ht = _new(a, shape) if output_final_state else None
     _call(_lib.gdr_ssm_fwd, desc, x.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(), _addr(d),
           _addr(z), _addr(dt_bias), _addr(h0), _addr(cu_seqlens), y.data_ptr(), _addr(ht), _stream(stream, dev))
     return y, ht
@@ -381,12 +390,12 @@ def ssm_bwd(x, dt, a, b, c, dy, d=None, z=None, dt_bias=None, h0=None, dht=None,
     _whole(h0, "h0", dev, torch.float32, shape)
     _whole(dht, "dht", dev, torch.float32, shape)
     with _outputs_on(stream):
-        dx, ddt = x.new_empty(x.shape), x.new_empty(x.shape)
-        db, dc = x.new_empty(b.shape), x.new_empty(b.shape)
-        dz = None if z is None else x.new_empty(x.shape)
-        da, dh0 = a.new_empty(a.shape), a.new_empty(shape)
-        dd = None if d is None else a.new_empty(desc.E)
-        ddt_bias = None if dt_bias is None else a.new_empty(desc.E)
+        dx, ddt = _like(x), _like(x)
+        db, dc = _new(x, b.shape), _new(x, b.shape)
+        dz = None if z is None else _like(x)
+        da, dh0 = _like(a), _new(a, shape)
+        dd = None if d is None else _new(a, desc.E)
+        ddt_bias = None if dt_bias is None else _new(a, desc.E)
     _call(_lib.gdr_ssm_bwd, desc, x.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(), _addr(d),
           _addr(z), _addr(dt_bias), _addr(h0), _addr(cu_seqlens), dy.data_ptr(), _addr(dht), dx.data_ptr(),
           ddt.data_ptr(), da.data_ptr(), db.data_ptr(), dc.data_ptr(), _addr(dd), _addr(dz), _addr(ddt_bias),
@@ -403,7 +412,7 @@ def ssm_step(x, dt, a, b, c, state, d=None, z=None, dt_bias=None, slots=None, dt
     desc = _ssm_desc(x, dev, dt, a, b, c, d, z, dt_bias, R, 1, P, dt_softplus, x.shape[1])
     _whole(state, "state", dev, torch.float32, (P, desc.E, desc.S))
     with _outputs_on(stream):
-        y = x.new_empty(x.shape)
+        y = _like(x)
     _call(_lib.gdr_ssm_step, desc, x.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(), _addr(d),
           _addr(z), _addr(dt_bias), _addr(slots), state.data_ptr(), y.data_ptr(), _stream(stream, dev))
     return y
