@@ -481,7 +481,7 @@ int launch_fwd(const NormArgs &a, cudaStream_t st) {
     if (E <= 512) launch_fwd_q<T, R, 32, V, 2 * K, RES>(a, st);
     else if (E <= 1024) launch_fwd_q<T, R, 128, V, K, RES>(a, st);
     else if (E <= 2048) launch_fwd_q<T, R, 256, V, K, RES>(a, st);
-    else if (E <= 4096) launch_fwd_q<T, R, 256, V, 2 * K, RES>(a, st);
+    else if (E <= 4096) launch_fwd_q<T, R, 512, V, K, RES>(a, st);
     else if (E <= 8192) launch_fwd_q<T, R, 512, V, 2 * K, RES>(a, st);
     else if (E <= 16384) launch_fwd_q<T, R, 1024, V, 2 * K, RES>(a, st);
     else norm_fwd_long_kernel<T, R, RES><<<(unsigned)a.d.M, 256, 0, st>>>(a);
