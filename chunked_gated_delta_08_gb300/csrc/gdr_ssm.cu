@@ -220,120 +220,181 @@ __global__ void __launch_bounds__(128) ssm_carry_kernel(SsmArgs a, int SP) {
   }
 }
 
-// One token per row.  A block takes four rows and 256 / SL channels; SL lanes
-// share a channel, four states each, so that a warp's states are consecutive
-// 16-byte groups, and the four rows' states are in flight together.  Of a
-// channel's first four lanes, lane k works out delta, delta x and the gate of
-// row k for all (they cost more than the four recurrences of a lane), and
-// finishes that row's output.  The bound is HBM: each state is read and written
-// once.
+// One token per row.  A block takes 256 / SL channels and goes through rows, four
+// at a time; SL lanes share a channel, four states each, so that a warp's states
+// are consecutive 16-byte groups.  The states of the next four rows are on their
+// way into shared memory (a thread copies what it alone reads) while these are
+// computed.  Of a channel's first four lanes, lane k works out delta, delta x and
+// the gate of row k for all (they cost more than the four recurrences of a lane),
+// and finishes that row's output.  The bound is HBM: each state is read and
+// written once.
 constexpr int kStepRows = 4;
 
-// Four elements of b or c as they lie in memory.
-template <typename T>
-struct Raw4;
-template <>
-struct Raw4<__nv_bfloat16> {
-  uint2 u;
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p, int s0, int S, int vec) {
-    u = make_uint2(0, 0);
-    if (vec) {
-      if (s0 < S) u = *reinterpret_cast<const uint2 *>(p + s0);
+// Four states of a thread, in pairs, and four elements of b or c as they lie in
+// memory.  AL: by 16-byte (bf16: 8-byte) accesses, all four or none inside S;
+// else one by one.
+template <bool AL>
+__device__ __forceinline__ void load_quad(const float *p, int s0, int S, f2 (&v)[2]) {
+  float f[4] = {};
+  if (AL) {
+    if (s0 < S) load4(p, f);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (s0 + q < S) f[q] = p[q];
+  }
+  v[0] = f2_pack(f[0], f[1]);
+  v[1] = f2_pack(f[2], f[3]);
+}
+template <bool AL>
+__device__ __forceinline__ void store_quad(float *p, int s0, int S, const f2 (&v)[2]) {
+  float f[4];
+  f2_split(v[0], f[0], f[1]);
+  f2_split(v[1], f[2], f[3]);
+  if (AL) {
+    if (s0 < S) store4(p, f);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (s0 + q < S) p[q] = f[q];
+  }
+}
+template <typename T, bool AL>
+struct Quad;
+template <bool AL>
+struct Quad<__nv_bfloat16, AL> {
+  uint2 u = {0, 0};
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p, int s0, int S) {
+    if (AL) {
+      if (s0 < S) u = *reinterpret_cast<const uint2 *>(p);
     } else {
       uint32_t w[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) w[q] = s0 + q < S ? __bfloat16_as_ushort(p[s0 + q]) : 0;
+      for (int q = 0; q < 4; ++q) w[q] = s0 + q < S ? __bfloat16_as_ushort(p[q]) : 0;
       u = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
     }
   }
-  __device__ __forceinline__ void expand(float (&v)[4]) const {
-    v[0] = __uint_as_float(u.x << 16);
-    v[1] = __uint_as_float(u.x & 0xffff0000u);
-    v[2] = __uint_as_float(u.y << 16);
-    v[3] = __uint_as_float(u.y & 0xffff0000u);
+  __device__ __forceinline__ void expand(f2 (&v)[2]) const {
+    v[0] = f2_pack(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u));
+    v[1] = f2_pack(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
   }
 };
-template <>
-struct Raw4<float> {
-  float u[4];
-  __device__ __forceinline__ void load(const float *p, int s0, int S, int vec) { load_states(p, s0, S, vec, u); }
-  __device__ __forceinline__ void expand(float (&v)[4]) const {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = u[q];
+template <bool AL>
+struct Quad<float, AL> {
+  f2 u[2] = {0, 0};
+  __device__ __forceinline__ void load(const float *p, int s0, int S) { load_quad<AL>(p, s0, S, u); }
+  __device__ __forceinline__ void expand(f2 (&v)[2]) const {
+    v[0] = u[0];
+    v[1] = u[1];
   }
 };
 
-template <typename T, int SL>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) ssm_step_kernel(SsmArgs a, const int32_t *slots,
-                                                                               float *state, unsigned tiles) {
-  const int64_t r0 = (int64_t)(blockIdx.x / tiles) * kStepRows;
-  const int64_t i = (int64_t)(blockIdx.x % tiles) * 256 + threadIdx.x;
-  const int64_t e = i / SL;
-  const int sl = (int)(i % SL), s0 = sl * 4, S = (int)a.d.S;
-  const bool in = e < a.d.E;
-  int64_t slot[kStepRows];  // negative: nothing to do
-#pragma unroll
-  for (int k = 0; k < kStepRows; ++k) {
-    const int64_t r = r0 + k;
-    slot[k] = r < a.d.B && in ? (slots ? slots[r] : r) : -1;
-    if (slot[k] >= a.d.N) {
+// AL: states, a, b and c allow their whole accesses.
+template <typename T, int SL, bool AL>
+__global__ void __launch_bounds__(256, 4) ssm_step_kernel(SsmArgs a, const int32_t *slots, float *state,
+                                                          unsigned tiles, int groups) {
+  __shared__ __align__(16) float ahead[2][kStepRows][256][4];
+  // rows, channels and leading dimensions are below 2^31; products of two are 64-bit
+  const int rows = (int)a.d.B, E = (int)a.d.E, S = (int)a.d.S;
+  const int i = (int)(blockIdx.x % tiles) * 256 + threadIdx.x;
+  const int e = i / SL, sl = i % SL, s0 = sl * 4;
+  const bool in = e < E;
+  const int es = E * S, mine_s = e * S + s0;  // at most 2^30
+  const int at = (in ? (unsigned)e / (unsigned)(a.d.E / a.d.G) : 0) * S + s0;
+  auto slot_of = [&](int g, int k) {  // negative: nothing to do
+    const int r = g * kStepRows + k;
+    int slot = g < groups && r < rows && in ? (slots ? slots[r] : r) : -1;
+    if (slot >= a.d.N) {
       raise_status(a.status, GDR_ERR_SLOTS);
-      slot[k] = -1;
+      slot = -1;
     }
-  }
-  auto row = [&](int k) { return state + (slot[k] * a.d.E + e) * S; };
-  float h[kStepRows][4], A[4] = {};
-  Raw4<T> b[kStepRows], c[kStepRows];
-  const int64_t g = in ? (unsigned)e / (unsigned)(a.d.E / a.d.G) : 0;
+    return slot;
+  };
+  auto fetch = [&](int slot, int buf, int k) {
+    float *to = ahead[buf][k][threadIdx.x];
+    const float *from = state + (int64_t)slot * es + mine_s;
+    if (AL) {
+      if (slot >= 0 && s0 < S) copy_async<16>(to, from);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (slot >= 0 && s0 + q < S) to[q] = from[q];
+    }
+  };
+  int g = (int)(blockIdx.x / tiles);
+  const int stride = (int)(gridDim.x / tiles);
+  int slot[kStepRows];
 #pragma unroll
   for (int k = 0; k < kStepRows; ++k) {
-    if (slot[k] >= 0) {
-      load_states(row(k), s0, S, a.s4, h[k]);
-      b[k].load(static_cast<const T *>(a.b) + (r0 + k) * a.d.ld_b + g * S, s0, S, a.bc4);
-      c[k].load(static_cast<const T *>(a.c) + (r0 + k) * a.d.ld_c + g * S, s0, S, a.bc4);
-    } else {
-      b[k].load(nullptr, S, S, 1);
-      c[k].load(nullptr, S, S, 1);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) h[k][q] = 0.f;
-    }
+    *reinterpret_cast<float4 *>(ahead[0][k][threadIdx.x]) = make_float4(0.f, 0.f, 0.f, 0.f);
+    *reinterpret_cast<float4 *>(ahead[1][k][threadIdx.x]) = make_float4(0.f, 0.f, 0.f, 0.f);
+    slot[k] = slot_of(g, k);
+    fetch(slot[k], 0, k);
   }
-  const int64_t r = r0 + sl;  // the row this lane prepares and finishes
-  const bool owner = sl < kStepRows && in && r < a.d.B;
-  float x = 0.f, delta = 0.f, gate = 1.f, skip = 0.f;
-  if (owner) {
-    x = to_f32(static_cast<const T *>(a.x)[r * a.d.ld_x + e]);
-    delta = ssm_delta(to_f32(static_cast<const T *>(a.dt)[r * a.d.ld_dt + e]) + (a.dt_bias ? a.dt_bias[e] : 0.f),
-                      a.d.flags & GDR_SSM_SOFTPLUS);
-    if (a.z) {
-      const float z = to_f32(static_cast<const T *>(a.z)[r * a.d.ld_z + e]);
-      gate = z * sigmoid_fast(z);
-    }
+  copy_commit();
+  f2 A[2] = {0, 0};
+  float bias = 0.f, skip = 0.f;
+  if (in) {
+    load_quad<AL>(a.a + mine_s, s0, S, A);
+    if (a.dt_bias) bias = a.dt_bias[e];
     if (a.dskip) skip = a.dskip[e];
   }
-  if (in) load_states(a.a + e * S, s0, S, a.s4, A);
+  A[0] = f2_mul(A[0], f2_both(kLog2e));
+  A[1] = f2_mul(A[1], f2_both(kLog2e));
+
+  int buf = 0;
+  for (; g < groups; g += stride, buf ^= 1) {
+    int next[kStepRows];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) A[q] *= kLog2e;
-  const float u = delta * x;
-  float out[kStepRows];
+    for (int k = 0; k < kStepRows; ++k) next[k] = slot_of(g + stride, k);
+    Quad<T, AL> b[kStepRows], c[kStepRows];
 #pragma unroll
-  for (int k = 0; k < kStepRows; ++k) {
-    const float dk = __shfl_sync(0xffffffffu, delta, k, SL), uk = __shfl_sync(0xffffffffu, u, k, SL);
-    float bk[4], ck[4];
-    b[k].expand(bk);
-    c[k].expand(ck);
-    out[k] = 0.f;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      h[k][q] = fmaf(ex2(dk * A[q]), h[k][q], uk * bk[q]);
-      out[k] = fmaf(ck[q], h[k][q], out[k]);
+    for (int k = 0; k < kStepRows; ++k) {
+      if (slot[k] >= 0) {
+        const int64_t r = g * kStepRows + k;
+        b[k].load(static_cast<const T *>(a.b) + r * (int)a.d.ld_b + at, s0, S);
+        c[k].load(static_cast<const T *>(a.c) + r * (int)a.d.ld_c + at, s0, S);
+      }
     }
-    if (slot[k] >= 0) store_states(row(k), s0, S, a.s4, h[k]);
-  }
-  const float y = sum_over_states<SL>(out, sl);
-  if (owner) {
-    const int64_t mine = sl == 0 ? slot[0] : sl == 1 ? slot[1] : sl == 2 ? slot[2] : slot[3];
-    static_cast<T *>(a.y)[r * a.d.E + e] = from_f32<T>(mine >= 0 ? fmaf(skip, x, y) * gate : 0.f);
+    const int r = g * kStepRows + sl;  // the row this lane prepares and finishes
+    const bool owner = sl < kStepRows && in && r < rows;
+    float x = 0.f, delta = 0.f, gate = 1.f;
+    if (owner) {
+      x = to_f32(static_cast<const T *>(a.x)[(int64_t)r * (int)a.d.ld_x + e]);
+      delta = to_f32(static_cast<const T *>(a.dt)[(int64_t)r * (int)a.d.ld_dt + e]) + bias;
+      if (a.z) gate = to_f32(static_cast<const T *>(a.z)[(int64_t)r * (int)a.d.ld_z + e]);
+    }
+#pragma unroll
+    for (int k = 0; k < kStepRows; ++k) fetch(next[k], buf ^ 1, k);
+    copy_commit();
+    if (owner) {
+      delta = ssm_delta(delta, a.d.flags & GDR_SSM_SOFTPLUS);
+      if (a.z) gate *= sigmoid_fast(gate);
+    }
+    const float u = delta * x;
+    copy_wait<1>();  // these rows' states are here
+    float out[kStepRows];
+#pragma unroll
+    for (int k = 0; k < kStepRows; ++k) {
+      const f2 dk = f2_both(__shfl_sync(0xffffffffu, delta, k, SL)), uk = f2_both(__shfl_sync(0xffffffffu, u, k, SL));
+      const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(ahead[buf][k][threadIdx.x]);
+      f2 h[2] = {v.x, v.y}, bk[2], ck[2];
+      b[k].expand(bk);
+      c[k].expand(ck);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) h[q] = f2_fma(f2_ex2(f2_mul(dk, A[q])), h[q], f2_mul(uk, bk[q]));
+      float lo, hi;
+      f2_split(f2_fma(ck[1], h[1], f2_mul(ck[0], h[0])), lo, hi);
+      out[k] = lo + hi;
+      if (slot[k] >= 0) store_quad<AL>(state + (int64_t)slot[k] * es + mine_s, s0, S, h);
+    }
+    const float y = sum_over_states<SL>(out, sl);
+    if (owner) {
+      const int mine = sl == 0 ? slot[0] : sl == 1 ? slot[1] : sl == 2 ? slot[2] : slot[3];
+      static_cast<T *>(a.y)[(int64_t)r * E + e] = from_f32<T>(mine >= 0 ? fmaf(skip, x, y) * gate : 0.f);
+    }
+#pragma unroll
+    for (int k = 0; k < kStepRows; ++k) slot[k] = next[k];
   }
 }
 
@@ -363,9 +424,11 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 template <typename T>
 int launch_step(const SsmArgs &a, const int32_t *slots, float *state, cudaStream_t st) {
   auto go = [&](auto SL) {
-    const int64_t tiles = cdiv(a.d.E * decltype(SL)::value, 256), blocks = tiles * cdiv(a.d.B, kStepRows);
-    if (blocks > 0x7fffffff) return set_error(GDR_ERR_SHAPE, "too many rows for one launch");
-    ssm_step_kernel<T, decltype(SL)::value><<<(unsigned)blocks, 256, 0, st>>>(a, slots, state, (unsigned)tiles);
+    const int64_t tiles = cdiv(a.d.E * decltype(SL)::value, 256), groups = cdiv(a.d.B, kStepRows);
+    // one wave of blocks, each through its share of the rows
+    const int64_t across = std::min(groups, std::max<int64_t>(1, 4 * kSMs / tiles));
+    auto *kernel = a.s4 && a.bc4 ? ssm_step_kernel<T, decltype(SL)::value, true> : ssm_step_kernel<T, decltype(SL)::value, false>;
+    kernel<<<(unsigned)(tiles * across), 256, 0, st>>>(a, slots, state, (unsigned)tiles, (int)groups);
     return launched("ssm_step_kernel");
   };
   const int sl = lanes_of(a.d.S);
@@ -386,6 +449,10 @@ int validate(const gdr_ssm_desc *d, const int64_t *cu, bool step) {
   if (d->ld_x < d->E || d->ld_dt < d->E || d->ld_z < d->E || d->ld_dy < d->E || d->ld_b < d->G * d->S ||
       d->ld_c < d->G * d->S)
     return set_error(GDR_ERR_SHAPE, "leading dimensions must be at least E, or G * S");
+  constexpr int64_t kMost = 0x7fffffff;
+  if (d->ld_x > kMost || d->ld_dt > kMost || d->ld_z > kMost || d->ld_b > kMost || d->ld_c > kMost || d->ld_dy > kMost)
+    return set_error(GDR_ERR_SHAPE, "leading dimensions must be below 2^31");
+  if (step && d->B > kMost - 4) return set_error(GDR_ERR_SHAPE, "too many rows for one launch");
   if (step) return d->T == 1 ? GDR_OK : set_error(GDR_ERR_SHAPE, "a step takes one token per row: T must be 1");
   if (cu) {
     if (d->B != 1) return set_error(GDR_ERR_SHAPE, "cu_seqlens requires B == 1");
