@@ -149,6 +149,8 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // An element of a parameter vector that is fp32 or of the input dtype.
 template <typename T>
 __device__ __forceinline__ float param(const void *p, bool f32, int64_t i) {

@@ -31,8 +31,9 @@ constexpr int kMaxL = 64;    // tokens of a chunk
 constexpr int kSubs = kMaxL / kSub;
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <typename P>
+template <typename T, typename P, bool VEC>
 struct __align__(16) LocalShared {
+  Ahead<T, VEC ? 4 : 1, VEC ? Stager<kTile, P::CB, P::kThreads>::kCount : 1, VEC ? P::kThreads : 1> ahead;
   float delta[kTile][P::CB], x[kTile][P::CB], up[kTile][P::CB];
   float bias[P::CB];
   float b[kTile * P::SP], c[kTile * P::SP];
@@ -56,38 +57,31 @@ __device__ __forceinline__ void fetch_delta(const SsmArgs &a, int64_t t, int64_t
   for (int i = 0; i < 4; ++i) v[i] = f2_add(v[i], w[i]);
 }
 
-template <typename T, typename P, bool VEC>
-__device__ __forceinline__ void stage_local(const SsmArgs &a, const P &p, const Stager<kTile, P::CB, P::kThreads> &st,
-                                            int64_t t0, int nt, LocalShared<P> &sm) {
-  const int64_t e = p.e0 + st.col;
-#pragma unroll
-  for (int k = 0; k < st.kCount; ++k) {
-    if (!st.has(k)) continue;
-    const int t = st.token(k), n = t < nt ? st.n : 0;
-    Eight v, w;
-    fetch8<T, VEC>(a.x, a.d.ld_x, t0 + t, e, n, v);
-    put8(&sm.x[t][st.col], v);
-    fetch_delta<T, VEC>(a, t0 + t, e, n, &sm.bias[st.col], v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = f2_delta(v[i], a.d.flags & GDR_SSM_SOFTPLUS);
-    put8(&sm.delta[t][st.col], v);
-    fetch8<T, VEC>(a.dy, a.d.ld_dy, t0 + t, e, n, v);
-    if (a.z) {
-      fetch8<T, VEC>(a.z, a.d.ld_z, t0 + t, e, n, w);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = f2_mul(v[i], f2_silu(w[i]));
-    }
-    put8(&sm.up[t][st.col], v);
-  }
-}
-
-template <typename T, int SL>
-__global__ void __launch_bounds__(kSsmThreads) ssm_bwd_local_kernel(SsmArgs a) {
+template <typename T, int SL, bool VEC>
+__global__ void __launch_bounds__(kSsmThreads, 4) ssm_bwd_local_kernel(SsmArgs a) {
   using P = Place<SL>;
-  __shared__ LocalShared<P> sm;
+  constexpr bool kAhead = VEC && sizeof(T) == 2;
+  __shared__ LocalShared<T, P, VEC> sm;
   if (!seqlens_ok(a.cu, a.d.N, a.M, a.status)) return;
   const P p(a);
   const Stager<kTile, P::CB, P::kThreads> st(p);
+  const int64_t begin = p.chunk * a.L, end = begin + a.L < a.M ? begin + a.L : a.M;
+  const void *const src[4] = {a.x, a.dt, a.dy, a.z};
+  const int64_t lds[4] = {a.d.ld_x, a.d.ld_dt, a.d.ld_dy, a.d.ld_z};
+  auto columns = [&](int64_t t0, int k) { return st.has(k) && st.token(k) < end - t0 ? st.n : 0; };
+  auto fetch_ahead = [&](int64_t t0) {
+#pragma unroll
+    for (int k = 0; k < st.kCount; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (src[i])
+          sm.ahead.fetch(i, k, static_cast<const T *>(src[i]) + (t0 + st.token(k)) * lds[i] + p.e0 + st.col,
+                         columns(t0, k));
+    copy_commit();
+  };
+  if constexpr (kAhead) {
+    if (begin < end) fetch_ahead(begin);
+  }
   stage_row<P::CB, P::kThreads>(p, a.dt_bias, sm.bias);
   __syncthreads();
   States A, h, g, pass;  // pass: product of the decays since the chunk began; zero once a sequence started
@@ -99,7 +93,6 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_bwd_local_kernel(SsmArgs a) {
       h[i][s] = g[i][s] = 0;
       pass[i][s] = f2_pack(1.f, 1.f);
     }
-  const int64_t begin = p.chunk * a.L, end = begin + a.L < a.M ? begin + a.L : a.M;
   f2 sum[2] = {0, 0};
   bool started = false;
   auto token = [&](int t) {
@@ -129,10 +122,36 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_bwd_local_kernel(SsmArgs a) {
     const bool borders = bos >= t0 || eos <= t0 + nt;  // a sequence starts or ends in the tile
     __syncthreads();                                   // the previous tile is consumed
     if (borders) stage_borders(a, t0, nt, sm.bd);
-    if (a.vec) stage_local<T, P, true>(a, p, st, t0, nt, sm);
-    else stage_local<T, P, false>(a, p, st, t0, nt, sm);
+    if (kAhead) copy_wait<0>();
+    auto get = [&](int i, int k, Eight &v) {
+      if constexpr (kAhead) sm.ahead.get(i, k, v);
+      else fetch8<T, VEC>(src[i], lds[i], t0 + st.token(k), p.e0 + st.col, columns(t0, k), v);
+    };
+#pragma unroll
+    for (int k = 0; k < st.kCount; ++k) {
+      if (!st.has(k)) continue;
+      const int t = st.token(k);
+      Eight v, w;
+      get(0, k, v);
+      put8(&sm.x[t][st.col], v);
+      get(1, k, v);
+      get8(&sm.bias[st.col], w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = f2_delta(f2_add(v[i], w[i]), a.d.flags & GDR_SSM_SOFTPLUS);
+      put8(&sm.delta[t][st.col], v);
+      get(2, k, v);
+      if (a.z) {
+        get(3, k, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = f2_mul(v[i], f2_silu(w[i]));
+      }
+      put8(&sm.up[t][st.col], v);
+    }
     stage_states<T, kTile, P::kThreads>(a, p, a.b, a.d.ld_b, t0, nt, sm.b);
     stage_states<T, kTile, P::kThreads>(a, p, a.c, a.d.ld_c, t0, nt, sm.c);
+    if constexpr (kAhead) {
+      if (t0 + kTile < end) fetch_ahead(t0 + kTile);
+    }
     __syncthreads();
     if (!borders && nt == kTile) {
 #pragma unroll 4
@@ -377,6 +396,19 @@ __global__ void __launch_bounds__(256, 2) ssm_bwd_main_kernel(SsmArgs a) {
   const P p(a);
   const int tid = threadIdx.x;
   if (p.chunk == 0) copy_empty_states(a, p, a.dht, a.dh0);
+  {  // The runs below wait for their rows one after the other: ask L2 for all of them now.
+    constexpr int kLine = 128 / sizeof(T), kLines = (P::CB + kLine - 1) / kLine;
+    const int64_t t0 = p.chunk * a.L, left = a.M - t0;
+    const int tokens = left < a.L ? (left > 0 ? (int)left : 0) : (int)a.L;
+    for (int i = tid; i < tokens * kLines; i += P::kThreads) {
+      const int64_t t = t0 + i / kLines, e = p.e0 + i % kLines * kLine;
+      if (e >= p.e_end) continue;
+      prefetch_l2(static_cast<const T *>(a.x) + t * a.d.ld_x + e);
+      prefetch_l2(static_cast<const T *>(a.dt) + t * a.d.ld_dt + e);
+      prefetch_l2(static_cast<const T *>(a.dy) + t * a.d.ld_dy + e);
+      if (a.z) prefetch_l2(static_cast<const T *>(a.z) + t * a.d.ld_z + e);
+    }
+  }
   StatesOf<1> A, h, g, dA;
   load_a(a, p, A);
   load_chunk(a, p, a.hloc, p.chunk, h);
@@ -571,7 +603,8 @@ int launch_sl(const SsmArgs &a, void *db, void *dc, cudaStream_t st) {
   const cudaError_t e =
       cudaFuncSetAttribute(ssm_bwd_main_kernel<T, SL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_error(e, "ssm_bwd_main_kernel shared memory");
-  ssm_bwd_local_kernel<T, SL><<<grid, kSsmThreads, 0, st>>>(a);
+  if (a.vec) ssm_bwd_local_kernel<T, SL, true><<<grid, kSsmThreads, 0, st>>>(a);
+  else ssm_bwd_local_kernel<T, SL, false><<<grid, kSsmThreads, 0, st>>>(a);
   int rc = launched("ssm_bwd_local_kernel");
   if (rc != GDR_OK) return rc;
   ssm_bwd_carry_kernel<<<dim3((unsigned)cdiv(a.d.E * 4 * SL, 128), 2), 128, 0, st>>>(a, 4 * SL);
@@ -598,8 +631,16 @@ int run_bwd(SsmArgs a, float *da, void *db, void *dc, float *dd, float *ddt_bias
   if ((rc = ssm_prepare(a, true, &sl, &vec)) != GDR_OK) return rc;
   // the outputs' rows are E long: 16-byte stores where E and the pointers allow them
   a.vec = vec && is_aligned16(a.dx) && is_aligned16(a.ddt) && is_aligned16(a.dz);
-  a.L = kMaxL;
-  while (a.L > 2 * kSub && cdiv(a.M, a.L) * a.ctiles < 2 * kSMs) a.L /= 2;
+  // Chunks of up to kMaxL tokens such that main's waves, of two blocks on each
+  // multiprocessor, are few: a chunk costs its tokens and some eight more to begin.
+  int64_t least = 0;
+  for (int64_t L = kTile; L <= kMaxL; L += kTile) {
+    const int64_t cost = cdiv(cdiv(a.M, L) * a.ctiles, 2 * kSMs) * (L + 8);
+    if (L == kTile || cost <= least) {
+      least = cost;
+      a.L = L;
+    }
+  }
   a.chunks = std::max<int64_t>(1, cdiv(a.M, a.L));
   const int64_t SP = 4 * sl, E = a.d.E;
   if (a.chunks * a.ctiles > 0x7fffffff || cdiv(a.M * a.d.G * a.d.S, 256) > 0x7fffffff)
