@@ -47,16 +47,6 @@ __device__ __forceinline__ void fetch8(const void *src, int64_t ld, int64_t t, i
   r.load(static_cast<const T *>(src) + t * ld + e, n);
   r.expand(v);
 }
-template <typename T, bool VEC>
-__device__ __forceinline__ void fetch_delta(const SsmArgs &a, int64_t t, int64_t e, int n, const float *bias,
-                                            Eight &v) {
-  Eight w;
-  fetch8<T, VEC>(a.dt, a.d.ld_dt, t, e, n, v);
-  get8(bias, w);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = f2_add(v[i], w[i]);
-}
-
 template <typename T, int SL, bool VEC>
 __global__ void __launch_bounds__(kSsmThreads, 4) ssm_bwd_local_kernel(SsmArgs a) {
   using P = Place<SL>;
@@ -224,15 +214,19 @@ __global__ void __launch_bounds__(128) ssm_bwd_carry_kernel(SsmArgs a, int SP) {
   }
 }
 
-// Main: two channels to a thread and eight warps to a block, against four and
-// four before: half the registers for the eight states held back, so that two
-// blocks of 256 threads fit a multiprocessor where two of 128 did, and half the
-// unrolled code.
+// Main: two channels to a thread, where the other kernels have four: the states
+// of eight tokens held back take half the registers and the unrolled code half
+// the instructions.  Blocks of four warps, three on a multiprocessor at 168
+// registers, take 1178 us on 16384 tokens of 2048 channels; four at 128, which
+// spill, 1198 us; two of eight warps 1219 us.
+constexpr int kMainWarps = 4;
 template <int SL>
-using MainPlace = Place<SL, 1, 8>;
+using MainPlace = Place<SL, 1, kMainWarps>;
 
-template <typename P>
+template <typename T, typename P, bool VEC>
 struct MainShared {
+  // x and dt, or dy and z, of the thread's eight columns in the next run
+  Ahead<T, VEC ? 2 : 1, 1, VEC ? P::kThreads : 1> ahead;
   ulonglong2 ckpt[kSubs - 1][2][P::kThreads];  // a thread's states before each run of kSub tokens but the first
   union {
     struct {
@@ -247,59 +241,50 @@ struct MainShared {
   float sums[3][kSub][P::CB];  // per channel and token, over the states: c . h, b . g, a . q
   float bias[P::CB], skip[P::CB];
   float total[2][kSub][P::CB];  // ddt and up x over the chunk, by column and thread row
-  float red[kSub][8][2 * P::SP];  // db, dc of a token by warp
+  float red[kSub][kMainWarps][2 * P::SP];  // db, dc of a token by warp
   Borders<kMaxL> bd;
   unsigned border_mask[kMaxL / 32];
 };
 
+// A thread's token and eight columns of a run or tile, and their loads: two
+// arrays p0 and p1, ahead of their use where that is worth it (gdr_ssm.cuh).
 template <typename T, typename P, bool VEC>
-__device__ __forceinline__ void stage_forward(const SsmArgs &a, const P &p,
-                                              const Stager<kTile, P::CB, P::kThreads> &st, int64_t t0, int nt,
-                                              MainShared<P> &sm) {
-  const int64_t e = p.e0 + st.col;
-#pragma unroll
-  for (int k = 0; k < st.kCount; ++k) {
-    if (!st.has(k)) continue;
-    const int t = st.token(k), n = t < nt ? st.n : 0;
-    Eight v;
-    fetch8<T, VEC>(a.x, a.d.ld_x, t0 + t, e, n, v);
-    put8(&sm.f.x[t][st.col], v);
-    fetch_delta<T, VEC>(a, t0 + t, e, n, &sm.bias[st.col], v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = f2_delta(v[i], a.d.flags & GDR_SSM_SOFTPLUS);
-    put8(&sm.f.delta[t][st.col], v);
+struct MainLoads {
+  static constexpr bool kAhead = VEC && sizeof(T) == 2;
+  const SsmArgs &a;
+  const P &p;
+  MainShared<T, P, VEC> &sm;
+  int t, col;
+  __device__ __forceinline__ int columns(int nt) const {
+    const int64_t left = p.e_end - p.e0 - col;
+    return t >= nt || left < 0 ? 0 : left < 8 ? (int)left : 8;
   }
-}
-
-// The first half of the block stages x and dt, the second dy and z.
-template <typename T, typename P, bool VEC>
-__device__ __forceinline__ void stage_reverse(const SsmArgs &a, const P &p, int64_t t0, int nt, MainShared<P> &sm) {
-  constexpr int kHalf = P::kThreads / 2, kRow = P::CB / 8;
-  const int half = threadIdx.x / kHalf, i0 = threadIdx.x % kHalf, t = i0 / kRow, col = i0 % kRow * 8;
-  if (t >= kSub) return;
-  const int64_t e = p.e0 + col, left = p.e_end - e;
-  const int n = t >= nt || left < 0 ? 0 : left < 8 ? (int)left : 8;
-  Eight v, w, o;
-  if (half == 0) {
-    fetch8<T, VEC>(a.x, a.d.ld_x, t0 + t, e, n, v);
-    put8(&sm.r.x[t][col], v);
-    fetch_delta<T, VEC>(a, t0 + t, e, n, &sm.bias[col], v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = f2_delta<true>(v[i], a.d.flags & GDR_SSM_SOFTPLUS, &w[i]);
-    put8(&sm.r.delta[t][col], o);
-    put8(&sm.r.slope[t][col], w);
-  } else {
-    fetch8<T, VEC>(a.dy, a.d.ld_dy, t0 + t, e, n, v);
-    if (a.z) {
-      fetch8<T, VEC>(a.z, a.d.ld_z, t0 + t, e, n, w);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = f2_mul(v[i], f2_silu_grad(w[i]));
-      put8(&sm.r.zf[t][col], o);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = f2_mul(v[i], f2_silu(w[i]));
+  __device__ __forceinline__ const T *at(const void *src, int64_t ld, int64_t t0) const {
+    return static_cast<const T *>(src) + (t0 + t) * ld + p.e0 + col;
+  }
+  __device__ __forceinline__ void fetch(const void *p0, int64_t ld0, const void *p1, int64_t ld1, int64_t t0,
+                                        int nt) const {
+    if constexpr (kAhead) {
+      const int n = columns(nt);
+      sm.ahead.fetch(0, 0, at(p0, ld0, t0), n);
+      if (p1) sm.ahead.fetch(1, 0, at(p1, ld1, t0), n);
+      copy_commit();
     }
-    put8(&sm.r.up[t][col], v);
   }
+  __device__ __forceinline__ void get(int which, const void *src, int64_t ld, int64_t t0, int nt, Eight &v) const {
+    if constexpr (kAhead) sm.ahead.get(which, 0, v);
+    else fetch8<T, VEC>(src, ld, t0 + t, p.e0 + col, columns(nt), v);
+  }
+};
+
+// dt as it is read becomes delta, and where asked its slope.
+template <bool SLOPE, typename P>
+__device__ __forceinline__ void to_delta(const SsmArgs &a, const float *bias, Eight &v, Eight &slope) {
+  Eight w;
+  get8(bias, w);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = f2_delta<SLOPE>(f2_add(v[i], w[i]), a.d.flags & GDR_SSM_SOFTPLUS, &slope[i]);
 }
 
 // Eight columns to memory, n of them inside the group.
@@ -320,7 +305,7 @@ __device__ __forceinline__ void store_columns(T *p, int n, const Eight &v) {
 // The gradients of a run's tokens from the sums over states, by the threads that
 // staged them: dx and ddt by the first half of the block, dz by the second.
 template <typename T, typename P, bool VEC>
-__device__ __forceinline__ void finish(const SsmArgs &a, const P &p, int64_t t0, int nt, MainShared<P> &sm) {
+__device__ __forceinline__ void finish(const SsmArgs &a, const P &p, int64_t t0, int nt, MainShared<T, P, VEC> &sm) {
   constexpr int kHalf = P::kThreads / 2, kRow = P::CB / 8;
   const int half = threadIdx.x / kHalf, i0 = threadIdx.x % kHalf, t = i0 / kRow, col = i0 % kRow * 8;
   if (t >= nt) return;
@@ -387,11 +372,11 @@ __device__ __forceinline__ void sum_over_channels(float (&v)[8], const P &p, flo
   }
 }
 
-template <typename T, int SL>
-__global__ void __launch_bounds__(256, 2) ssm_bwd_main_kernel(SsmArgs a) {
+template <typename T, int SL, bool VEC>
+__global__ void __launch_bounds__(32 * kMainWarps, 3) ssm_bwd_main_kernel(SsmArgs a) {
   using P = MainPlace<SL>;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  MainShared<P> &sm = *reinterpret_cast<MainShared<P> *>(smem_raw);
+  MainShared<T, P, VEC> &sm = *reinterpret_cast<MainShared<T, P, VEC> *>(smem_raw);
   if (!seqlens_ok(a.cu, a.d.N, a.M, a.status)) return;
   const P p(a);
   const int tid = threadIdx.x;
@@ -444,14 +429,25 @@ __global__ void __launch_bounds__(256, 2) ssm_bwd_main_kernel(SsmArgs a) {
 
   // States at the start of every run of kSub tokens; the last run needs only its start.
   const int flen = subs > 0 ? (subs - 1) * kSub : 0;
+  constexpr int kRow = P::CB / 8, kHalf = P::kThreads / 2;
   {
-    const Stager<kTile, P::CB, P::kThreads> st(p);
+    const MainLoads<T, P, VEC> ld{a, p, sm, tid / kRow, tid % kRow * 8};
+    if (flen > 0) ld.fetch(a.x, a.d.ld_x, a.dt, a.d.ld_dt, begin, flen < kTile ? flen : kTile);
     for (int f0 = 0; f0 < flen; f0 += kTile) {
       const int nt = flen - f0 < kTile ? flen - f0 : kTile;
       __syncthreads();
-      if (a.vec) stage_forward<T, P, true>(a, p, st, begin + f0, nt, sm);
-      else stage_forward<T, P, false>(a, p, st, begin + f0, nt, sm);
+      if (ld.kAhead) copy_wait<0>();
+      if (ld.t < kTile) {
+        Eight v, none;
+        ld.get(0, a.x, a.d.ld_x, begin + f0, nt, v);
+        put8(&sm.f.x[ld.t][ld.col], v);
+        ld.get(1, a.dt, a.d.ld_dt, begin + f0, nt, v);
+        to_delta<false, P>(a, &sm.bias[ld.col], v, none);
+        put8(&sm.f.delta[ld.t][ld.col], v);
+      }
       stage_states<T, kTile, P::kThreads>(a, p, a.b, a.d.ld_b, begin + f0, nt, sm.f.b);
+      const int rest = flen - f0 - kTile;
+      if (rest > 0) ld.fetch(a.x, a.d.ld_x, a.dt, a.d.ld_dt, begin + f0 + kTile, rest < kTile ? rest : kTile);
       __syncthreads();
 #pragma unroll 1
       for (int t1 = 0; t1 < nt; t1 += kSub) {
@@ -466,15 +462,46 @@ __global__ void __launch_bounds__(256, 2) ssm_bwd_main_kernel(SsmArgs a) {
     }
   }
 
+  // The first half of the block stages x and dt of a run, the second dy and z.
+  const int half = tid / kHalf;
+  const MainLoads<T, P, VEC> ld{a, p, sm, tid % kHalf / kRow, tid % kHalf % kRow * 8};
+  auto fetch = [&](int sub) {
+    const int nt = len - sub * kSub < kSub ? len - sub * kSub : kSub;
+    if (half == 0) ld.fetch(a.x, a.d.ld_x, a.dt, a.d.ld_dt, begin + sub * kSub, nt);
+    else ld.fetch(a.dy, a.d.ld_dy, a.z, a.d.ld_z, begin + sub * kSub, nt);
+  };
+  if (subs > 0) fetch(subs - 1);
 #pragma unroll 1
   for (int sub = subs - 1; sub >= 0; --sub) {
     const int64_t t0 = begin + sub * kSub;
     const int nt = len - sub * kSub < kSub ? len - sub * kSub : kSub;
     __syncthreads();  // the previous run's staging and partials are consumed
-    if (a.vec) stage_reverse<T, P, true>(a, p, t0, nt, sm);
-    else stage_reverse<T, P, false>(a, p, t0, nt, sm);
+    if (ld.kAhead) copy_wait<0>();
+    if (ld.t < kSub) {
+      Eight v, w, o;
+      if (half == 0) {
+        ld.get(0, a.x, a.d.ld_x, t0, nt, v);
+        put8(&sm.r.x[ld.t][ld.col], v);
+        ld.get(1, a.dt, a.d.ld_dt, t0, nt, v);
+        to_delta<true, P>(a, &sm.bias[ld.col], v, w);
+        put8(&sm.r.delta[ld.t][ld.col], v);
+        put8(&sm.r.slope[ld.t][ld.col], w);
+      } else {
+        ld.get(0, a.dy, a.d.ld_dy, t0, nt, v);
+        if (a.z) {
+          ld.get(1, a.z, a.d.ld_z, t0, nt, w);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = f2_mul(v[i], f2_silu_grad(w[i]));
+          put8(&sm.r.zf[ld.t][ld.col], o);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = f2_mul(v[i], f2_silu(w[i]));
+        }
+        put8(&sm.r.up[ld.t][ld.col], v);
+      }
+    }
     stage_states<T, kSub, P::kThreads>(a, p, a.b, a.d.ld_b, t0, nt, sm.r.b);
     stage_states<T, kSub, P::kThreads>(a, p, a.c, a.d.ld_c, t0, nt, sm.r.c);
+    if (sub > 0) fetch(sub - 1);
     __syncthreads();
     // the reverse recurrence at token k, from the states before and after it
     auto reverse = [&](int k, const StatesOf<1> &prev, const StatesOf<1> &after) {
@@ -555,11 +582,10 @@ __global__ void __launch_bounds__(256, 2) ssm_bwd_main_kernel(SsmArgs a) {
       const int k = i / (2 * P::SP), s = i % (2 * P::SP);
       float o = 0.f;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) o += sm.red[k][w][s];
+      for (int w = 0; w < kMainWarps; ++w) o += sm.red[k][w][s];
       out[i] = o;
     }
-    if (a.vec) finish<T, P, true>(a, p, t0, nt, sm);
-    else finish<T, P, false>(a, p, t0, nt, sm);
+    finish<T, P, VEC>(a, p, t0, nt, sm);
   }
   // ddt_bias and dd of the chunk
   __syncthreads();
@@ -598,21 +624,28 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 template <typename T, int SL>
 int launch_sl(const SsmArgs &a, void *db, void *dc, cudaStream_t st) {
   const unsigned grid = (unsigned)(a.chunks * a.ctiles);
-  constexpr int smem = sizeof(MainShared<MainPlace<SL>>);
-  static_assert(MainPlace<SL>::CB == Place<SL>::CB, "one grid for both kernels");
-  const cudaError_t e =
-      cudaFuncSetAttribute(ssm_bwd_main_kernel<T, SL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return cuda_error(e, "ssm_bwd_main_kernel shared memory");
+  SsmArgs m = a;  // main's blocks have half the channels
+  m.tpg = (int)cdiv(a.d.E / a.d.G, MainPlace<SL>::CB);
+  m.ctiles = (int)(a.d.G * m.tpg);
+  auto launch_main = [&](auto vec) {
+    constexpr bool VEC = decltype(vec)::value;
+    constexpr int smem = sizeof(MainShared<T, MainPlace<SL>, VEC>);
+    const cudaError_t e =
+        cudaFuncSetAttribute(ssm_bwd_main_kernel<T, SL, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return cuda_error(e, "ssm_bwd_main_kernel shared memory");
+    ssm_bwd_main_kernel<T, SL, VEC><<<(unsigned)(m.chunks * m.ctiles), 32 * kMainWarps, smem, st>>>(m);
+    return launched("ssm_bwd_main_kernel");
+  };
   if (a.vec) ssm_bwd_local_kernel<T, SL, true><<<grid, kSsmThreads, 0, st>>>(a);
   else ssm_bwd_local_kernel<T, SL, false><<<grid, kSsmThreads, 0, st>>>(a);
   int rc = launched("ssm_bwd_local_kernel");
   if (rc != GDR_OK) return rc;
   ssm_bwd_carry_kernel<<<dim3((unsigned)cdiv(a.d.E * 4 * SL, 128), 2), 128, 0, st>>>(a, 4 * SL);
   if ((rc = launched("ssm_bwd_carry_kernel")) != GDR_OK) return rc;
-  ssm_bwd_main_kernel<T, SL><<<grid, 256, smem, st>>>(a);
-  if ((rc = launched("ssm_bwd_main_kernel")) != GDR_OK) return rc;
+  rc = a.vec ? launch_main(std::true_type{}) : launch_main(std::false_type{});
+  if (rc != GDR_OK) return rc;
   if (a.M > 0) {
-    ssm_sum_bc_kernel<T><<<(unsigned)cdiv(a.M * a.d.G * a.d.S, 256), 256, 0, st>>>(a, 4 * SL, (T *)db, (T *)dc);
+    ssm_sum_bc_kernel<T><<<(unsigned)cdiv(a.M * a.d.G * a.d.S, 256), 256, 0, st>>>(m, 4 * SL, (T *)db, (T *)dc);
     rc = launched("ssm_sum_bc_kernel");
   }
   return rc;
@@ -631,11 +664,11 @@ int run_bwd(SsmArgs a, float *da, void *db, void *dc, float *dd, float *ddt_bias
   if ((rc = ssm_prepare(a, true, &sl, &vec)) != GDR_OK) return rc;
   // the outputs' rows are E long: 16-byte stores where E and the pointers allow them
   a.vec = vec && is_aligned16(a.dx) && is_aligned16(a.ddt) && is_aligned16(a.dz);
-  // Chunks of up to kMaxL tokens such that main's waves, of two blocks on each
+  // Chunks of up to kMaxL tokens such that main's waves, of three blocks on each
   // multiprocessor, are few: a chunk costs its tokens and some eight more to begin.
   int64_t least = 0;
   for (int64_t L = kTile; L <= kMaxL; L += kTile) {
-    const int64_t cost = cdiv(cdiv(a.M, L) * a.ctiles, 2 * kSMs) * (L + 8);
+    const int64_t cost = cdiv(cdiv(a.M, L) * 2 * a.ctiles, 3 * kSMs) * (L + 8);
     if (L == kTile || cost <= least) {
       least = cost;
       a.L = L;
@@ -643,11 +676,11 @@ int run_bwd(SsmArgs a, float *da, void *db, void *dc, float *dd, float *ddt_bias
   }
   a.chunks = std::max<int64_t>(1, cdiv(a.M, a.L));
   const int64_t SP = 4 * sl, E = a.d.E;
-  if (a.chunks * a.ctiles > 0x7fffffff || cdiv(a.M * a.d.G * a.d.S, 256) > 0x7fffffff)
+  if (2 * a.chunks * a.ctiles > 0x7fffffff || cdiv(a.M * a.d.G * a.d.S, 256) > 0x7fffffff)
     return set_error(GDR_ERR_SHAPE, "too many tokens and channels for one launch");
   const size_t states = align256(sizeof(float) * (size_t)(a.chunks * E * SP));
   const size_t sums = align256(sizeof(float) * (size_t)(a.chunks * E));
-  const size_t bc = align256(sizeof(float) * (size_t)(a.ctiles * a.M * 2 * SP));
+  const size_t bc = align256(sizeof(float) * (size_t)(2 * a.ctiles * a.M * 2 * SP));
   char *base = nullptr;
   rc = scratch_begin(2 * states + 3 * sums + bc, st, "scan backward scratch", &base);
   if (rc != GDR_OK) return rc;
