@@ -481,10 +481,8 @@ enum Dir { kFwd, kBwd, kStep };
 // partials, so it is long; and the grid is whole waves of the five blocks that a
 // multiprocessor holds, as few as keep runs within `hi`.
 int64_t run_length(int64_t M, int64_t tiles, int64_t per, int64_t lo, int64_t hi) {
-  const int64_t slots = 5 * kSMs * per;  // runs of one wave, times tiles
-  int64_t L = hi + 1;
-  for (int64_t waves = 1; L > hi; ++waves) L = cdiv(M * tiles, slots * waves);
-  return std::max(L, lo);
+  const int64_t wave = std::max<int64_t>(1, 5 * kSMs / tiles) * per;  // runs at once
+  return std::max(lo, cdiv(M, wave * std::max<int64_t>(1, cdiv(M, wave * hi))));
 }
 
 // Four channels of a thread in the forward and the step.  The backward keeps

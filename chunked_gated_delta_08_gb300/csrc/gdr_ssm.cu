@@ -524,10 +524,11 @@ int ssm_prepare(SsmArgs &a, bool backward, int *sl, bool *vec) {
   *sl = lanes_of(a.d.S);
   a.tpg = (int)cdiv(a.d.E / a.d.G, 512 / *sl);
   a.ctiles = (int)(a.d.G * a.tpg);
-  *vec = (a.d.E / a.d.G) % 8 == 0 && a.d.ld_x % 8 == 0 && a.d.ld_dt % 8 == 0 && (!a.z || a.d.ld_z % 8 == 0) &&
+  const int64_t unit = a.d.dtype == GDR_BF16 ? 8 : 4;  // elements of a 16-byte access
+  *vec = (a.d.E / a.d.G) % unit == 0 && a.d.ld_x % unit == 0 && a.d.ld_dt % unit == 0 && (!a.z || a.d.ld_z % unit == 0) &&
          is_aligned16(a.x) && is_aligned16(a.dt) && is_aligned16(a.z);
   a.s4 = a.d.S % 4 == 0 && is_aligned16(a.a) && is_aligned16(a.h0) && is_aligned16(a.ht) && is_aligned16(a.dht) && is_aligned16(a.dh0);
-  if (backward) *vec = *vec && a.d.ld_dy % 8 == 0 && is_aligned16(a.dy);
+  if (backward) *vec = *vec && a.d.ld_dy % unit == 0 && is_aligned16(a.dy);
   return GDR_OK;
 }
 

@@ -190,8 +190,10 @@ __device__ __forceinline__ void get8(const float *p, Eight &v) {
   v[2] = b.x;
   v[3] = b.y;
 }
-// Eight elements as they lie in memory.  VEC: by 16-byte accesses; else one by
-// one, those of the first n columns (zero past them).
+// Eight elements as they lie in memory, those of the first n columns (zero past
+// them).  VEC: by 16-byte accesses, which the host allows where groups of
+// channels are a multiple of the 8 (bf16) or 4 (fp32) elements of one; else one by
+// one.
 template <typename T, bool VEC>
 struct Raw8;
 template <>
@@ -207,19 +209,18 @@ struct Raw8<__nv_bfloat16, true> {
   }
 };
 template <>
-struct Raw8<float, true> {
-  Eight u;
+struct Raw8<float, true> {  // n is 0, 4 or 8
+  ulonglong2 u[2];
   __device__ __forceinline__ void load(const float *p, int n) {
-    if (n > 0) {
-      get8(p, u);
-    } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] = 0;
-    }
+    for (int i = 0; i < 2; ++i)
+      u[i] = n > 4 * i ? reinterpret_cast<const ulonglong2 *>(p)[i] : make_ulonglong2(0, 0);
   }
   __device__ __forceinline__ void expand(Eight &v) const {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = u[i];
+    v[0] = u[0].x;
+    v[1] = u[0].y;
+    v[2] = u[1].x;
+    v[3] = u[1].y;
   }
 };
 template <typename T>

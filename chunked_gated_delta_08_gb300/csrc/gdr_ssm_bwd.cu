@@ -293,7 +293,11 @@ __device__ __forceinline__ void store_columns(T *p, int n, const Eight &v) {
   float f[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) f2_split(v[i], f[2 * i], f[2 * i + 1]);
-  if (VEC) {
+  if (VEC && sizeof(T) == 4) {
+    const float lo[4] = {f[0], f[1], f[2], f[3]}, hi[4] = {f[4], f[5], f[6], f[7]};
+    if (n > 0) store4(p, lo);
+    if (n > 4) store4(p + 4, hi);
+  } else if (VEC) {
     if (n > 0) store8(p, f);
   } else {
 #pragma unroll
