@@ -18,7 +18,6 @@ contiguous; outputs are.  Activations are bf16 or fp32.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -90,7 +89,7 @@ def _device(t, name):
     dev = t.get_device()  # -1 on the CPU
     if dev < 0:
         raise GdrError(GDR_ERR_NULLPTR, f"{name} must be a CUDA tensor")
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         raise GdrError(GDR_ERR_NULLPTR, f"{name} is on {t.device}, but cuda:{torch.cuda.current_device()} is current")
     return dev
 
@@ -146,18 +145,6 @@ def _rows(t, name, dev, dtype=None, shape=None, row_dims=1):
     return width if ld is None else ld
 
 
-_HERE = contextlib.nullcontext()
-
-
-def _outputs_on(stream):
-    """Outputs belong to the launching stream: their memory is taken while it is current."""
-    return _HERE if stream is None else torch.cuda.stream(stream)
-
-
-def _stream(stream, dev):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
 def _like(t):
     """An output of t's shape and dtype, contiguous."""
     return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
@@ -167,8 +154,8 @@ def _new(t, shape, dtype=None):
     return torch.empty(shape, dtype=t.dtype if dtype is None else dtype, device=t.device)
 
 
-def _call(fn, desc, *args):
-    rc = fn(desc, *args)
+def _call(fn, dev, desc, *args):
+    rc = fn(desc, *args, torch._C._cuda_getCurrentRawStream(dev))
     if rc:
         _check(rc)
 
@@ -190,6 +177,9 @@ def norm_fwd(x, weight, residual=None, eps=1e-6, quant=None, stream=None):
     without a residual.  ``quant`` "row" or "group" (128 columns) returns
     ``(y8, scale, s)`` with y8 in float8_e4m3fn and ``y ~ y8 * scale``.
     """
+    if stream is not None:  # outputs are taken while it is current, so that they belong to it
+        with torch.cuda.stream(stream):
+            return norm_fwd(x, weight, residual, eps, quant)
     code = _dtype_code(x, "x")
     dev = _device(x, "x")
     M, E = _norm_shape(x, weight, dev, "x")
@@ -200,17 +190,16 @@ def norm_fwd(x, weight, residual=None, eps=1e-6, quant=None, stream=None):
         rcode = _param_code(residual, x, "residual")
         ld_r = _rows(residual, "residual", dev, None, x.shape)
     desc = GdrNormDesc(M, E, ld_x, ld_r, E, code, rcode, _param_code(weight, x, "weight"), _QUANTS[quant], eps, 0)
-    with _outputs_on(stream):
-        s = None if residual is None else _new(residual, x.shape)
-        scale = None
-        if quant is None:
-            y = _like(x)
-        else:
-            y = _new(x, x.shape, torch.float8_e4m3fn)
-            lead = x.shape[:-1]
-            scale = _new(x, lead if quant == "row" else (*lead, -(-E // GROUP_SIZE)), torch.float32)
-    _call(_lib.gdr_norm_fwd, desc, x.data_ptr(), _addr(residual), weight.data_ptr(), y.data_ptr(), _addr(scale),
-          _addr(s), _stream(stream, dev))
+    s = None if residual is None else _like(residual)
+    scale = None
+    if quant is None:
+        y = _like(x)
+    else:
+        y = _new(x, x.shape, torch.float8_e4m3fn)
+        lead = x.shape[:-1]
+        scale = _new(x, lead if quant == "row" else (*lead, -(-E // GROUP_SIZE)), torch.float32)
+    _call(_lib.gdr_norm_fwd, dev, desc, x.data_ptr(), _addr(residual), weight.data_ptr(), y.data_ptr(), _addr(scale),
+          _addr(s))
     return (y, s) if quant is None else (y, scale, s)
 
 
@@ -220,6 +209,9 @@ def norm_bwd(dy, s, weight, ds=None, eps=1e-6, stream=None):
     Returns ``(dx, dres, dweight)``: dx in dy's dtype, dres in s's (the same
     tensor where the two agree), dweight fp32.
     """
+    if stream is not None:  # outputs are taken while it is current, so that they belong to it
+        with torch.cuda.stream(stream):
+            return norm_bwd(dy, s, weight, ds, eps)
     code = _dtype_code(dy, "dy")
     dev = _device(dy, "dy")
     M, E = _norm_shape(dy, weight, dev, "dy")
@@ -229,12 +221,11 @@ def norm_bwd(dy, s, weight, ds=None, eps=1e-6, stream=None):
         ld_ds = _rows(ds, "ds", dev, s.dtype, dy.shape)
     desc = GdrNormDesc(M, E, _rows(dy, "dy", dev), ld_s, ld_ds, code, rcode, _param_code(weight, dy, "weight"), 0, eps,
                        0)
-    with _outputs_on(stream):
-        dx = _like(dy)
-        dres = dx if s.dtype == dy.dtype else _new(s, dy.shape)
-        dweight = _new(dy, E, torch.float32)
-    _call(_lib.gdr_norm_bwd, desc, dy.data_ptr(), s.data_ptr(), _addr(ds), weight.data_ptr(), dx.data_ptr(),
-          None if dres is dx else dres.data_ptr(), dweight.data_ptr(), _stream(stream, dev))
+    dx = _like(dy)
+    dres = dx if s.dtype == dy.dtype else _new(s, dy.shape)
+    dweight = _new(dy, E, torch.float32)
+    _call(_lib.gdr_norm_bwd, dev, desc, dy.data_ptr(), s.data_ptr(), _addr(ds), weight.data_ptr(), dx.data_ptr(),
+          None if dres is dx else dres.data_ptr(), dweight.data_ptr())
     return dx, dres, dweight
 
 
@@ -289,15 +280,17 @@ def conv_fwd(x, weight, bias=None, s0=None, cu_seqlens=None, activation="silu", 
     each sequence (zero when None).  Returns ``(y, st)``, st the last W - 1
     inputs of each sequence (None unless requested).
     """
+    if stream is not None:  # outputs are taken while it is current, so that they belong to it
+        with torch.cuda.stream(stream):
+            return conv_fwd(x, weight, bias, s0, cu_seqlens, activation, output_final_state)
     dev, B, T, N = _sequences(x, cu_seqlens)
     desc = _conv_desc(x, dev, weight, bias, activation, B, T, N, x.shape[-1])
     shape = (N, desc.W - 1, desc.E)
     _whole(s0, "s0", dev, x.dtype, shape)
-    with _outputs_on(stream):
-        y = _like(x)
-        st = _new(x, shape) if output_final_state else None
-    _call(_lib.gdr_conv_fwd, desc, x.data_ptr(), weight.data_ptr(), _addr(bias), _addr(s0), _addr(cu_seqlens),
-          y.data_ptr(), _addr(st), _stream(stream, dev))
+    y = _like(x)
+    st = _new(x, shape) if output_final_state else None
+    _call(_lib.gdr_conv_fwd, dev, desc, x.data_ptr(), weight.data_ptr(), _addr(bias), _addr(s0), _addr(cu_seqlens),
+          y.data_ptr(), _addr(st))
     return y, st
 
 
@@ -307,18 +300,19 @@ def conv_bwd(x, weight, dy, bias=None, s0=None, dst=None, cu_seqlens=None, activ
     Returns ``(dx, dweight, dbias, ds0)``: dx and ds0 in x's dtype, dweight and
     dbias fp32 (dbias None without a bias).
     """
+    if stream is not None:  # outputs are taken while it is current, so that they belong to it
+        with torch.cuda.stream(stream):
+            return conv_bwd(x, weight, dy, bias, s0, dst, cu_seqlens, activation)
     dev, B, T, N = _sequences(x, cu_seqlens)
     desc = _conv_desc(x, dev, weight, bias, activation, B, T, N, _rows(dy, "dy", dev, x.dtype, x.shape))
     shape = (N, desc.W - 1, desc.E)
     _whole(s0, "s0", dev, x.dtype, shape)
     _whole(dst, "dst", dev, x.dtype, shape)
-    with _outputs_on(stream):
-        dx, ds0 = _like(x), _new(x, shape)
-        dweight = _new(x, weight.shape, torch.float32)
-        dbias = None if bias is None else _new(x, desc.E, torch.float32)
-    _call(_lib.gdr_conv_bwd, desc, x.data_ptr(), weight.data_ptr(), _addr(bias), _addr(s0), _addr(cu_seqlens),
-          dy.data_ptr(), _addr(dst), dx.data_ptr(), dweight.data_ptr(), _addr(dbias), ds0.data_ptr(),
-          _stream(stream, dev))
+    dx, ds0 = _like(x), _new(x, shape)
+    dweight = _new(x, weight.shape, torch.float32)
+    dbias = None if bias is None else _new(x, desc.E, torch.float32)
+    _call(_lib.gdr_conv_bwd, dev, desc, x.data_ptr(), weight.data_ptr(), _addr(bias), _addr(s0), _addr(cu_seqlens),
+          dy.data_ptr(), _addr(dst), dx.data_ptr(), dweight.data_ptr(), _addr(dbias), ds0.data_ptr())
     return dx, dweight, dbias, ds0
 
 
@@ -328,13 +322,15 @@ def conv_step(x, state, weight, bias=None, activation="silu", slots=None, stream
     Row r uses ``state[slots[r]]`` (slots int32; None: slot r).  A negative slot
     is a padding row with a zero output.  Slots of one call must differ.
     """
+    if stream is not None:  # outputs are taken while it is current, so that they belong to it
+        with torch.cuda.stream(stream):
+            return conv_step(x, state, weight, bias, activation, slots)
     dev, R, P = _step_rows(x, state, slots)
     desc = _conv_desc(x, dev, weight, bias, activation, R, 1, P, x.shape[1])
     _whole(state, "state", dev, x.dtype, (P, desc.W - 1, desc.E))
-    with _outputs_on(stream):
-        y = _like(x)
-    _call(_lib.gdr_conv_step, desc, x.data_ptr(), weight.data_ptr(), _addr(bias), _addr(slots), state.data_ptr(),
-          y.data_ptr(), _stream(stream, dev))
+    y = _like(x)
+    _call(_lib.gdr_conv_step, dev, desc, x.data_ptr(), weight.data_ptr(), _addr(bias), _addr(slots), state.data_ptr(),
+          y.data_ptr())
     return y
 
 
@@ -364,15 +360,17 @@ def ssm_fwd(x, dt, a, b, c, d=None, z=None, dt_bias=None, h0=None, cu_seqlens=No
     x, dt, z [B, T, E]; a [E, S] fp32, S in 1..64; b, c [B, T, G, S]; h0
     [N, E, S] fp32.  Returns ``(y, ht)`` (ht None unless requested).
     """
+    if stream is not None:  # outputs are taken while it is current, so that they belong to it
+        with torch.cuda.stream(stream):
+            return ssm_fwd(x, dt, a, b, c, d, z, dt_bias, h0, cu_seqlens, dt_softplus, output_final_state)
     dev, B, T, N = _sequences(x, cu_seqlens)
     desc = _ssm_desc(x, dev, dt, a, b, c, d, z, dt_bias, B, T, N, dt_softplus, x.shape[-1])
     shape = (N, desc.E, desc.S)
     _whole(h0, "h0", dev, torch.float32, shape)
-    with _outputs_on(stream):
-        y = _like(x)
-        ht = _new(a, shape) if output_final_state else None
-    _call(_lib.gdr_ssm_fwd, desc, x.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(), _addr(d),
-          _addr(z), _addr(dt_bias), _addr(h0), _addr(cu_seqlens), y.data_ptr(), _addr(ht), _stream(stream, dev))
+    y = _like(x)
+    ht = _new(a, shape) if output_final_state else None
+    _call(_lib.gdr_ssm_fwd, dev, desc, x.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(), _addr(d),
+          _addr(z), _addr(dt_bias), _addr(h0), _addr(cu_seqlens), y.data_ptr(), _addr(ht))
     return y, ht
 
 
@@ -384,22 +382,24 @@ def ssm_bwd(x, dt, a, b, c, dy, d=None, z=None, dt_bias=None, h0=None, dht=None,
     dz in x's dtype, the others fp32; dd, dz and ddt_bias are None where d, z
     and dt_bias are.  The forward is recomputed inside the call.
     """
+    if stream is not None:  # outputs are taken while it is current, so that they belong to it
+        with torch.cuda.stream(stream):
+            return ssm_bwd(x, dt, a, b, c, dy, d, z, dt_bias, h0, dht, cu_seqlens, dt_softplus)
     dev, B, T, N = _sequences(x, cu_seqlens)
     desc = _ssm_desc(x, dev, dt, a, b, c, d, z, dt_bias, B, T, N, dt_softplus, _rows(dy, "dy", dev, x.dtype, x.shape))
     shape = (N, desc.E, desc.S)
     _whole(h0, "h0", dev, torch.float32, shape)
     _whole(dht, "dht", dev, torch.float32, shape)
-    with _outputs_on(stream):
-        dx, ddt = _like(x), _like(x)
-        db, dc = _new(x, b.shape), _new(x, b.shape)
-        dz = None if z is None else _like(x)
-        da, dh0 = _like(a), _new(a, shape)
-        dd = None if d is None else _new(a, desc.E)
-        ddt_bias = None if dt_bias is None else _new(a, desc.E)
-    _call(_lib.gdr_ssm_bwd, desc, x.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(), _addr(d),
+    dx, ddt = _like(x), _like(x)
+    db, dc = _new(x, b.shape), _new(x, b.shape)
+    dz = None if z is None else _like(x)
+    da, dh0 = _like(a), _new(a, shape)
+    dd = None if d is None else _new(a, desc.E)
+    ddt_bias = None if dt_bias is None else _new(a, desc.E)
+    _call(_lib.gdr_ssm_bwd, dev, desc, x.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(), _addr(d),
           _addr(z), _addr(dt_bias), _addr(h0), _addr(cu_seqlens), dy.data_ptr(), _addr(dht), dx.data_ptr(),
           ddt.data_ptr(), da.data_ptr(), db.data_ptr(), dc.data_ptr(), _addr(dd), _addr(dz), _addr(ddt_bias),
-          dh0.data_ptr(), _stream(stream, dev))
+          dh0.data_ptr())
     return dx, ddt, da, db, dc, dd, dz, ddt_bias, dh0
 
 
@@ -408,11 +408,13 @@ def ssm_step(x, dt, a, b, c, state, d=None, z=None, dt_bias=None, slots=None, dt
 
     ``slots`` as in ``conv_step``.
     """
+    if stream is not None:  # outputs are taken while it is current, so that they belong to it
+        with torch.cuda.stream(stream):
+            return ssm_step(x, dt, a, b, c, state, d, z, dt_bias, slots, dt_softplus)
     dev, R, P = _step_rows(x, state, slots)
     desc = _ssm_desc(x, dev, dt, a, b, c, d, z, dt_bias, R, 1, P, dt_softplus, x.shape[1])
     _whole(state, "state", dev, torch.float32, (P, desc.E, desc.S))
-    with _outputs_on(stream):
-        y = _like(x)
-    _call(_lib.gdr_ssm_step, desc, x.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(), _addr(d),
-          _addr(z), _addr(dt_bias), _addr(slots), state.data_ptr(), y.data_ptr(), _stream(stream, dev))
+    y = _like(x)
+    _call(_lib.gdr_ssm_step, dev, desc, x.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(), _addr(d),
+          _addr(z), _addr(dt_bias), _addr(slots), state.data_ptr(), y.data_ptr())
     return y
