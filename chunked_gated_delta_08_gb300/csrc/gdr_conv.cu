@@ -406,25 +406,26 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvArgs a) {
   O::store(part + W * a.d.E, p.n, db);
 }
 
-// dweight [E, W] and dbias [E] from the runs' partials: 32 columns a block, 32
+// dweight [E, W] and dbias [E] from the runs' partials: 32 columns a block, SETS
 // interleaved sets of runs, each added in order, then the sets in order.
-__global__ void __launch_bounds__(1024) conv_sum_kernel(const float *__restrict__ part, int64_t runs, int64_t E, int W,
-                                                        float *__restrict__ dweight, float *__restrict__ dbias,
-                                                        SeqCheck seqs) {
-  __shared__ float sm[32][33];
+template <int SETS>
+__global__ void __launch_bounds__(32 * SETS) conv_sum_kernel(const float *__restrict__ part, int64_t runs, int64_t E,
+                                                             int W, float *__restrict__ dweight,
+                                                             float *__restrict__ dbias, SeqCheck seqs) {
+  __shared__ float sm[SETS][33];
   if (!seqlens_ok(seqs)) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, j = blockIdx.y;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float acc = 0.f;
   if (c < E) {
 #pragma unroll 4
-    for (int64_t r = w; r < runs; r += 32) acc += part[(r * (W + 1) + j) * E + c];
+    for (int64_t r = w; r < runs; r += SETS) acc += part[(r * (W + 1) + j) * E + c];
   }
   sm[w][lane] = acc;
   __syncthreads();
   if (w == 0 && c < E) {
 #pragma unroll
-    for (int i = 1; i < 32; ++i) acc += sm[i][lane];
+    for (int i = 1; i < SETS; ++i) acc += sm[i][lane];
     if (j < W) dweight[c * W + j] = acc;
     else if (dbias) dbias[c] = acc;
   }
@@ -524,8 +525,13 @@ int launch(ConvArgs a, Dir dir, float *dweight, float *dbias, cudaStream_t st) {
     return launched("conv_bwd_kernel");
   });
   if (rc == GDR_OK) {
-    conv_sum_kernel<<<dim3((unsigned)cdiv(d.E, 32), (unsigned)(d.W + (dbias ? 1 : 0))), 1024, 0, st>>>(
-        a.part, a.runs, d.E, (int)d.W, dweight, dbias, SeqCheck{a.cu, d.N, a.M, a.status});
+    const dim3 grid((unsigned)cdiv(d.E, 32), (unsigned)(d.W + (dbias ? 1 : 0)));
+    const SeqCheck seqs{a.cu, d.N, a.M, a.status};
+    // small blocks where the columns fill the GPU, else the runs further apart
+    if ((int64_t)grid.x * grid.y >= 4 * kSMs)
+      conv_sum_kernel<8><<<grid, 256, 0, st>>>(a.part, a.runs, d.E, (int)d.W, dweight, dbias, seqs);
+    else
+      conv_sum_kernel<32><<<grid, 1024, 0, st>>>(a.part, a.runs, d.E, (int)d.W, dweight, dbias, seqs);
     rc = launched("conv_sum_kernel");
   }
   return scratch_end(base, st, "convolution backward scratch", rc);

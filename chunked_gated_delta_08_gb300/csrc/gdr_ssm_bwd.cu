@@ -697,9 +697,9 @@ int run_bwd(SsmArgs a, float *da, void *db, void *dc, float *dd, float *ddt_bias
   a.part_bc = (float *)(base + 2 * states + 3 * sums);
   rc = a.d.dtype == GDR_BF16 ? launch_t<__nv_bfloat16>(a, sl, db, dc, st) : launch_t<float>(a, sl, db, dc, st);
   const SeqCheck seqs{a.cu, a.d.N, a.M, a.status};
-  if (rc == GDR_OK) rc = launch_col_sum(a.hloc, a.chunks, E * SP, E * SP, SP, a.d.S, da, seqs, st);
-  if (rc == GDR_OK && dd) rc = launch_col_sum(a.part_e + E, a.chunks, 2 * E, E, E, E, dd, seqs, st);
-  if (rc == GDR_OK && ddt_bias) rc = launch_col_sum(a.part_e, a.chunks, 2 * E, E, E, E, ddt_bias, seqs, st);
+  if (rc == GDR_OK) rc = launch_col_sum(a.hloc, a.chunks, E * SP, E * SP, SP, a.d.S, da, E * SP, nullptr, seqs, st);
+  if (rc == GDR_OK && (dd || ddt_bias))
+    rc = launch_col_sum(a.part_e, a.chunks, 2 * E, 2 * E, E, E, ddt_bias, E, dd, seqs, st);
   return scratch_end(base, st, "scan backward scratch", rc);
 }
 
