@@ -13,7 +13,7 @@
 // Runs are cut from the flat token axis; a sequence's border inside one reloads
 // the window.  The bound is HBM: 16384 x 4096 bf16 take 51.5 us, 77 % of the copy
 // rate, where eight channels to a thread, at 155 registers, took 104.  The
-// backward takes 100 us, 60 %: at 58 instructions per token and pair of channels
+// backward takes 99 us, 60 %: at 58 instructions per token and pair of channels
 // it issues on half of the cycles.
 #include <algorithm>
 
@@ -160,12 +160,14 @@ __device__ __forceinline__ void load_window(const ConvArgs &a, const Seq &s, int
   }
 }
 
-// States of sequences without tokens: `to` = `from` (zero where null).
+// States of sequences without tokens: `to` = `from` (zero where null).  Run r
+// looks after sequences r, r + runs, ...
 template <typename T, int NP, bool AL, int W>
-__device__ __forceinline__ void copy_empty(const ConvArgs &a, int64_t e, int n, const void *from, void *to) {
+__device__ __forceinline__ void copy_empty(const ConvArgs &a, int64_t run, int64_t e, int n, const void *from,
+                                           void *to) {
   using I = Io<T, NP, AL>;
   if (!to) return;
-  for (int64_t q = 0; q < a.d.N; ++q) {
+  for (int64_t q = run; q < a.d.N; q += a.runs) {
     const SeqRange r = seq_range(a.cu, q, a.d.T);
     if (r.eos > r.bos) continue;
 #pragma unroll
@@ -202,8 +204,8 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvArgs a) {
   using I = Io<T, NP, AL>;
   if (!seqlens_ok(a.cu, a.d.N, a.M, a.status)) return;
   const Place p(a, 2 * NP);
-  if (p.n <= 0) return;
-  if (p.run == 0) copy_empty<T, NP, AL, W>(a, p.e, p.n, a.s0, a.st);
+  if (p.n <= 0 || p.run >= a.runs) return;
+  copy_empty<T, NP, AL, W>(a, p.run, p.e, p.n, a.s0, a.st);
   int64_t t = p.run * a.L;
   const int64_t end = t + a.L < a.M ? t + a.L : a.M;
   if (t >= end) return;
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvArgs a) {
   if (!seqlens_ok(a.cu, a.d.N, a.M, a.status)) return;
   const Place p(a, 2 * NP);
   if (p.n <= 0 || p.run >= a.runs) return;
-  if (p.run == 0) copy_empty<T, NP, AL, W>(a, p.e, p.n, a.dst, a.st);
+  copy_empty<T, NP, AL, W>(a, p.run, p.e, p.n, a.dst, a.st);
   const int64_t t0 = p.run * a.L, end = t0 + a.L < a.M ? t0 + a.L : a.M;
   const bool silu = a.d.activation == GDR_ACT_SILU;
   Taps<T, NP, W> taps;

@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kSsmThreads, 4) ssm_fwd_kernel(SsmArgs a) {
   __shared__ FwdShared<T, P, VEC, MAIN> sm;
   if (!seqlens_ok(a.cu, a.d.N, a.M, a.status)) return;
   const P p(a);
-  if (MAIN && p.chunk == 0) copy_empty_states(a, p, a.h0, a.ht);
+  if (MAIN) copy_empty_states(a, p, a.h0, a.ht);
   const Stager<kTile, P::CB, kSsmThreads> st(p);
   States A, h;
   T next_b[NB], next_c[MAIN ? NB : 1];

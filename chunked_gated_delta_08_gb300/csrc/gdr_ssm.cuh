@@ -405,11 +405,12 @@ __device__ __forceinline__ void advance(f2 (&h)[NP][4], const f2 (&A)[NP][4], co
   }
 }
 
-// States of sequences without tokens: `to` = `from` (zero where null).
+// States of sequences without tokens: `to` = `from` (zero where null).  Chunk c
+// looks after sequences c, c + chunks, ...
 template <typename P>
 __device__ __forceinline__ void copy_empty_states(const SsmArgs &a, const P &p, const float *from, float *to) {
   if (!to) return;
-  for (int64_t n = 0; n < a.d.N; ++n) {
+  for (int64_t n = p.chunk; n < a.d.N; n += a.chunks) {
     const SeqRange r = seq_range(a.cu, n, a.d.T);
     if (r.eos > r.bos) continue;
     StatesOf<P::NP> h;

@@ -20,7 +20,7 @@
 // small a_t has forgotten.  The bound is arithmetic: four exponentials and about
 // 25 fp32 operations per channel, state and token, some 250 instructions per
 // token of a thread's eight states.  16384 tokens x 2048 channels x 16 states take
-// 1135 us, four fifths of it main, which issues on 49 % of cycles.
+// 1127 us, four fifths of it main, which issues on 49 % of cycles.
 #include <algorithm>
 
 #include "gdr_ssm.cuh"
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(32 * kMainWarps, 3) ssm_bwd_main_kernel(SsmArg
   if (!seqlens_ok(a.cu, a.d.N, a.M, a.status)) return;
   const P p(a);
   const int tid = threadIdx.x;
-  if (p.chunk == 0) copy_empty_states(a, p, a.dht, a.dh0);
+  copy_empty_states(a, p, a.dht, a.dh0);
   {  // The runs below wait for their rows one after the other: ask L2 for all of them now.
     constexpr int kLine = 128 / sizeof(T), kLines = (P::CB + kLine - 1) / kLine;
     const int64_t t0 = p.chunk * a.L, left = a.M - t0;

@@ -228,8 +228,10 @@ int gdr_fwd_noalloc(const gdr_desc *desc, const void *q, const void *k, const vo
  * elements (ld at least the row's length; a slice of a wider projection output
  * needs no copy); every output is contiguous.  And a bad state slot is treated
  * as padding and reported by gdr_device_status as GDR_ERR_SLOTS.
- * Sums, statistics and states are fp32 throughout.  Results do not depend on
- * the order in which blocks run: no atomics add anywhere.
+ * Outputs must not overlap inputs (the states of the single-token calls apart,
+ * which are updated in place): blocks read s0 and h0 while others write.  Sums,
+ * statistics and states are fp32 throughout.  Results do not depend on the order
+ * in which blocks run: no atomics add anywhere.
  */
 
 typedef enum gdr_quant { GDR_QUANT_NONE = 0, GDR_QUANT_ROW = 1, GDR_QUANT_GROUP = 2 } gdr_quant;
