@@ -114,12 +114,6 @@ struct SeqCheck {
   int64_t N, T;
   int *status;
 };
-// Column sums of part [rows, cols] (rows ld apart) in a fixed order; of each
-// `width` columns the first `keep` are written, those from column `split` on to
-// out2 (either output may be null), none where `seqs` is invalid (gdr_norm.cu).
-int launch_col_sum(const float *part, int64_t rows, int64_t ld, int64_t cols, int64_t width, int64_t keep, float *out,
-                   int64_t split, float *out2, const SeqCheck &seqs, cudaStream_t stream);
-
 // The per-token form (gdr_recurrent.cu): reads q, k, v, g, beta, h0, cu,
 // chunk_offsets (varlen only, from launch_chunk_index), writes o and ht.
 int launch_recurrent_fwd(const ChunkedArgs &a);

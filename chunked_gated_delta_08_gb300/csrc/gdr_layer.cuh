@@ -190,4 +190,38 @@ __device__ __forceinline__ int64_t seq_of_token(const int64_t *cu, int64_t N, in
   return lo;
 }
 
+// Column sums of part [rows, cols], rows ld apart, by a block of 32 SETS threads:
+// columns 32 block and on, SETS interleaved sets of rows, each added in order,
+// then the sets in order.  Columns come in groups of `width`, of which the first
+// `keep` go to the output, close together; columns from `split` on to the second.
+struct ColSum {
+  const float *part;
+  int64_t rows, ld, cols, width, keep;
+  float *out;
+  int64_t split;
+  float *out2;
+};
+template <int SETS>
+__device__ __forceinline__ void col_sum_block(const ColSum &q, int64_t block, float (&sm)[SETS][33]) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int64_t c = block * 32 + lane;
+  float acc = 0.f;
+  if (c < q.cols) {
+#pragma unroll 4
+    for (int64_t r = w; r < q.rows; r += SETS) acc += q.part[r * q.ld + c];
+  }
+  sm[w][lane] = acc;
+  __syncthreads();
+  if (w == 0 && c < q.cols && c % q.width < q.keep) {
+#pragma unroll
+    for (int i = 1; i < SETS; ++i) acc += sm[i][lane];
+    float *to = q.out;
+    if (c >= q.split) {
+      c -= q.split;
+      to = q.out2;
+    }
+    if (to) to[c / q.width * q.keep + c % q.width] = acc;
+  }
+}
+
 }  // namespace gdr

@@ -496,6 +496,21 @@ int launch_fwd(const NormArgs &a, cudaStream_t st) {
   return launched("norm_fwd_kernel");
 }
 
+template <int SETS>
+__global__ void __launch_bounds__(32 * SETS) col_sum_kernel(ColSum q) {
+  __shared__ float sm[SETS][33];
+  col_sum_block<SETS>(q, blockIdx.x, sm);
+}
+
+// Many columns fill the GPU with small blocks; few need their rows apart (64 rows
+// of 32768 columns: 6 us against 12, 304 of 4096: 11 against 6).
+int launch_col_sum(const ColSum &q, cudaStream_t stream) {
+  const unsigned grid = (unsigned)cdiv(q.cols, 32);
+  if (grid >= 4 * kSMs) col_sum_kernel<8><<<grid, 256, 0, stream>>>(q);
+  else col_sum_kernel<32><<<grid, 1024, 0, stream>>>(q);
+  return launched("col_sum_kernel");
+}
+
 template <typename T, typename R>
 int launch_bwd(NormArgs a, float *dweight, cudaStream_t st) {
   const int64_t E = a.d.E;
@@ -532,7 +547,7 @@ int launch_bwd(NormArgs a, float *dweight, cudaStream_t st) {
   }
   rc = launched("norm_bwd_kernel");
   if (dweight) {
-    if (rc == GDR_OK) rc = launch_col_sum((const float *)base, grid, E, E, E, E, dweight, E, nullptr, SeqCheck{}, st);
+    if (rc == GDR_OK) rc = launch_col_sum(ColSum{(const float *)base, grid, E, E, E, E, dweight, E, nullptr}, st);
     rc = scratch_end(base, st, "norm backward scratch", rc);
   }
   return rc;
@@ -555,51 +570,7 @@ int validate(const gdr_norm_desc *d) {
   return GDR_OK;
 }
 
-// Column sums of part [rows, cols], rows ld apart: 32 columns a block, SETS
-// interleaved sets of rows, each added in order, then the sets in order.
-// Columns come in groups of `width`, of which the first `keep` go to the output,
-// close together; columns from `split` on to the second output.
-template <int SETS>
-__global__ void __launch_bounds__(32 * SETS) col_sum_kernel(const float *__restrict__ part, int64_t rows, int64_t ld,
-                                                            int64_t cols, int64_t width, int64_t keep,
-                                                            float *__restrict__ out, int64_t split,
-                                                            float *__restrict__ out2, SeqCheck seqs) {
-  __shared__ float sm[SETS][33];
-  if (!seqlens_ok(seqs)) return;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  int64_t c = (int64_t)blockIdx.x * 32 + lane;
-  float acc = 0.f;
-  if (c < cols) {
-#pragma unroll 4
-    for (int64_t r = w; r < rows; r += SETS) acc += part[r * ld + c];
-  }
-  sm[w][lane] = acc;
-  __syncthreads();
-  if (w == 0 && c < cols && c % width < keep) {
-#pragma unroll
-    for (int i = 1; i < SETS; ++i) acc += sm[i][lane];
-    float *to = out;
-    if (c >= split) {
-      c -= split;
-      to = out2;
-    }
-    if (to) to[c / width * keep + c % width] = acc;
-  }
-}
-
 }  // namespace
-
-int launch_col_sum(const float *part, int64_t rows, int64_t ld, int64_t cols, int64_t width, int64_t keep, float *out,
-                   int64_t split, float *out2, const SeqCheck &seqs, cudaStream_t stream) {
-  const unsigned grid = (unsigned)cdiv(cols, 32);
-  // many columns fill the GPU with small blocks; few need their rows apart (64 x 32768 values: 6 against 12 us,
-  // 304 x 4096: 11 against 6)
-  if (grid >= 4 * kSMs)
-    col_sum_kernel<8><<<grid, 256, 0, stream>>>(part, rows, ld, cols, width, keep, out, split, out2, seqs);
-  else
-    col_sum_kernel<32><<<grid, 1024, 0, stream>>>(part, rows, ld, cols, width, keep, out, split, out2, seqs);
-  return launched("col_sum_kernel");
-}
 
 }  // namespace gdr
 

@@ -501,6 +501,7 @@ int run_fwd(SsmArgs a, cudaStream_t st) {
   const bool whole =
       !a.cu && (a.d.T <= 2 * kTile || 12 * cdiv(a.d.B * a.ctiles, kWave) * (a.d.T + 8) <= 5 * chunk_cost(a, a.L));
   if (whole) a.L = std::max<int64_t>(1, a.d.T);
+  else if (a.M <= 4 * kTile) a.L = 4 * kTile;  // so few tokens take less than the launches that would share them out
   a.chunks = std::max<int64_t>(1, cdiv(a.M, a.L));
   if (a.chunks * a.ctiles > 0x7fffffff) return set_error(GDR_ERR_SHAPE, "too many tokens and channels for one launch");
   if (whole || a.chunks == 1) return launch_fwd<true>(a, sl, vec, st);

@@ -16,6 +16,7 @@
 //           memory; then 8 tokens at a time from the last: the states once more,
 //           in registers, and the reverse recurrence with all products
 //   sums    the partials of db and dc over channels, of da, dd and ddt_bias over chunks
+// (one chunk needs no local and carry).
 // States are recomputed, never inverted: h_{t-1} = (h_t - ..) / a_t loses what a
 // small a_t has forgotten.  The bound is arithmetic: four exponentials and about
 // 25 fp32 operations per channel, state and token, some 250 instructions per
@@ -402,8 +403,9 @@ __global__ void __launch_bounds__(32 * kMainWarps, 3) ssm_bwd_main_kernel(SsmArg
   }
   StatesOf<1> A, h, g, dA;
   load_a(a, p, A);
-  load_chunk(a, p, a.hloc, p.chunk, h);
-  load_chunk(a, p, a.gloc, p.chunk, g);
+  const float *entering = a.chunks > 1 ? a.hloc : nullptr;
+  load_chunk(a, p, entering, p.chunk, h);
+  load_chunk(a, p, a.chunks > 1 ? a.gloc : nullptr, p.chunk, g);
 #pragma unroll
   for (int s = 0; s < 4; ++s) dA[0][s] = 0;
   const int64_t begin = p.chunk * a.L, end = begin + a.L < a.M ? begin + a.L : a.M;
@@ -423,7 +425,7 @@ __global__ void __launch_bounds__(32 * kMainWarps, 3) ssm_bwd_main_kernel(SsmArg
   };
   auto back_to = [&](int sub, StatesOf<1> &to) {
     if (sub == 0) {
-      load_chunk(a, p, a.hloc, p.chunk, to);
+      load_chunk(a, p, entering, p.chunk, to);
       return;
     }
     const ulonglong2 u = sm.ckpt[sub - 1][0][tid], v = sm.ckpt[sub - 1][1][tid];
@@ -605,10 +607,19 @@ __global__ void __launch_bounds__(32 * kMainWarps, 3) ssm_bwd_main_kernel(SsmArg
   store_chunk(a, p, a.hloc, p.chunk, dA);  // this block's states there have been read
 }
 
-// db and dc [M, G, S] from the partials of the channel blocks of each group.
+// All sums over blocks in one launch: db and dc [M, G, S] from the partials of the
+// channel blocks of each group, da and (ddt_bias, dd) from those of the chunks.
 template <typename T>
-__global__ void __launch_bounds__(256) ssm_sum_bc_kernel(SsmArgs a, int SP, T *db, T *dc) {
+__global__ void __launch_bounds__(256) ssm_sums_kernel(SsmArgs a, int SP, T *db, T *dc, unsigned bc_blocks, ColSum da,
+                                                       unsigned da_blocks, ColSum per_channel) {
+  __shared__ float sm[8][33];
   if (!seqlens_ok(a.cu, a.d.N, a.M, a.status)) return;
+  if (blockIdx.x >= bc_blocks) {
+    const unsigned block = blockIdx.x - bc_blocks;
+    if (block < da_blocks) col_sum_block<8>(da, block, sm);
+    else col_sum_block<8>(per_channel, block - da_blocks, sm);
+    return;
+  }
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t per = a.d.G * a.d.S;
   if (i >= a.M * per) return;
@@ -627,8 +638,13 @@ __global__ void __launch_bounds__(256) ssm_sum_bc_kernel(SsmArgs a, int SP, T *d
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
+struct Sums {
+  void *db, *dc;
+  float *da, *dd, *ddt_bias;
+};
+
 template <typename T, int SL>
-int launch_sl(const SsmArgs &a, void *db, void *dc, cudaStream_t st) {
+int launch_sl(const SsmArgs &a, const Sums &out, cudaStream_t st) {
   const unsigned grid = (unsigned)(a.chunks * a.ctiles);
   SsmArgs m = a;  // main's blocks have half the channels
   m.tpg = (int)cdiv(a.d.E / a.d.G, MainPlace<SL>::CB);
@@ -642,47 +658,52 @@ int launch_sl(const SsmArgs &a, void *db, void *dc, cudaStream_t st) {
     ssm_bwd_main_kernel<T, SL, VEC><<<(unsigned)(m.chunks * m.ctiles), 32 * kMainWarps, smem, st>>>(m);
     return launched("ssm_bwd_main_kernel");
   };
-  if (a.vec) ssm_bwd_local_kernel<T, SL, true><<<grid, kSsmThreads, 0, st>>>(a);
-  else ssm_bwd_local_kernel<T, SL, false><<<grid, kSsmThreads, 0, st>>>(a);
-  int rc = launched("ssm_bwd_local_kernel");
-  if (rc != GDR_OK) return rc;
-  ssm_bwd_carry_kernel<<<dim3((unsigned)cdiv(a.d.E * 4 * SL, 128), 2), 128, 0, st>>>(a, 4 * SL);
-  if ((rc = launched("ssm_bwd_carry_kernel")) != GDR_OK) return rc;
+  int rc = GDR_OK;
+  if (a.chunks > 1) {  // else nothing enters or leaves but by the sequences' borders
+    if (a.vec) ssm_bwd_local_kernel<T, SL, true><<<grid, kSsmThreads, 0, st>>>(a);
+    else ssm_bwd_local_kernel<T, SL, false><<<grid, kSsmThreads, 0, st>>>(a);
+    if ((rc = launched("ssm_bwd_local_kernel")) != GDR_OK) return rc;
+    ssm_bwd_carry_kernel<<<dim3((unsigned)cdiv(a.d.E * 4 * SL, 128), 2), 128, 0, st>>>(a, 4 * SL);
+    if ((rc = launched("ssm_bwd_carry_kernel")) != GDR_OK) return rc;
+  }
   rc = a.vec ? launch_main(std::true_type{}) : launch_main(std::false_type{});
   if (rc != GDR_OK) return rc;
-  if (a.M > 0) {
-    ssm_sum_bc_kernel<T><<<(unsigned)cdiv(a.M * a.d.G * a.d.S, 256), 256, 0, st>>>(m, 4 * SL, (T *)db, (T *)dc);
-    rc = launched("ssm_sum_bc_kernel");
-  }
-  return rc;
+  const int64_t E = a.d.E, SP = 4 * SL;
+  const unsigned bc_blocks = (unsigned)cdiv(a.M * a.d.G * a.d.S, 256), da_blocks = (unsigned)cdiv(E * SP, 32);
+  const ColSum da{a.hloc, a.chunks, E * SP, E * SP, SP, a.d.S, out.da, E * SP, nullptr};
+  const ColSum per_channel{a.part_e, a.chunks, 2 * E, 2 * E, E, E, out.ddt_bias, E, out.dd};
+  const unsigned blocks = bc_blocks + da_blocks + (unsigned)cdiv(2 * E, 32);
+  ssm_sums_kernel<T><<<blocks, 256, 0, st>>>(m, 4 * SL, (T *)out.db, (T *)out.dc, bc_blocks, da, da_blocks, per_channel);
+  return launched("ssm_sums_kernel");
 }
 
 template <typename T>
-int launch_t(const SsmArgs &a, int sl, void *db, void *dc, cudaStream_t st) {
-  if (sl == 4) return launch_sl<T, 4>(a, db, dc, st);
-  if (sl == 8) return launch_sl<T, 8>(a, db, dc, st);
-  return launch_sl<T, 16>(a, db, dc, st);
+int launch_t(const SsmArgs &a, int sl, const Sums &out, cudaStream_t st) {
+  if (sl == 4) return launch_sl<T, 4>(a, out, st);
+  if (sl == 8) return launch_sl<T, 8>(a, out, st);
+  return launch_sl<T, 16>(a, out, st);
 }
 
-int run_bwd(SsmArgs a, float *da, void *db, void *dc, float *dd, float *ddt_bias, cudaStream_t st) {
+int run_bwd(SsmArgs a, const Sums &out, cudaStream_t st) {
   int sl, rc;
   bool vec;
   if ((rc = ssm_prepare(a, true, &sl, &vec)) != GDR_OK) return rc;
   // the outputs' rows are E long: 16-byte stores where E and the pointers allow them
   a.vec = vec && is_aligned16(a.dx) && is_aligned16(a.ddt) && is_aligned16(a.dz);
-  // Chunks of up to kMaxL tokens such that main's waves, of three blocks on each
+  // A few tokens are one chunk: two launches fewer than they would save.  Else
+  // chunks of up to kMaxL tokens such that main's waves, of three blocks on each
   // multiprocessor, are few: a chunk costs its tokens and some eight more to begin.
   int64_t least = 0;
   for (int64_t L = kTile; L <= kMaxL; L += kTile) {
     const int64_t cost = cdiv(cdiv(a.M, L) * 2 * a.ctiles, 3 * kSMs) * (L + 8);
-    if (L == kTile || cost <= least) {
+    if (L == kTile || cost <= least || a.M <= kMaxL) {
       least = cost;
       a.L = L;
     }
   }
   a.chunks = std::max<int64_t>(1, cdiv(a.M, a.L));
   const int64_t SP = 4 * sl, E = a.d.E;
-  if (2 * a.chunks * a.ctiles > 0x7fffffff || cdiv(a.M * a.d.G * a.d.S, 256) > 0x7fffffff)
+  if (2 * a.chunks * a.ctiles > 0x7fffffff || cdiv(a.M * a.d.G * a.d.S, 256) > 0x3fffffff)
     return set_error(GDR_ERR_SHAPE, "too many tokens and channels for one launch");
   const size_t states = align256(sizeof(float) * (size_t)(a.chunks * E * SP));
   const size_t sums = align256(sizeof(float) * (size_t)(a.chunks * E));
@@ -695,11 +716,7 @@ int run_bwd(SsmArgs a, float *da, void *db, void *dc, float *dd, float *ddt_bias
   a.sumd = (float *)(base + 2 * states);
   a.part_e = (float *)(base + 2 * states + sums);
   a.part_bc = (float *)(base + 2 * states + 3 * sums);
-  rc = a.d.dtype == GDR_BF16 ? launch_t<__nv_bfloat16>(a, sl, db, dc, st) : launch_t<float>(a, sl, db, dc, st);
-  const SeqCheck seqs{a.cu, a.d.N, a.M, a.status};
-  if (rc == GDR_OK) rc = launch_col_sum(a.hloc, a.chunks, E * SP, E * SP, SP, a.d.S, da, E * SP, nullptr, seqs, st);
-  if (rc == GDR_OK && (dd || ddt_bias))
-    rc = launch_col_sum(a.part_e, a.chunks, 2 * E, 2 * E, E, E, ddt_bias, E, dd, seqs, st);
+  rc = a.d.dtype == GDR_BF16 ? launch_t<__nv_bfloat16>(a, sl, out, st) : launch_t<float>(a, sl, out, st);
   return scratch_end(base, st, "scan backward scratch", rc);
 }
 
@@ -721,5 +738,5 @@ extern "C" int gdr_ssm_bwd(const gdr_ssm_desc *desc, const void *x, const void *
   s.d = *desc;
   s.x = x; s.dt = dt; s.a = a; s.b = b; s.c = c; s.dskip = d; s.z = z; s.dt_bias = dt_bias; s.h0 = h0;
   s.cu = cu_seqlens; s.dy = dy; s.dht = dht; s.dx = dx; s.ddt = ddt; s.dz = dz; s.dh0 = dh0;
-  return run_bwd(s, da, db, dc, dd, ddt_bias, (cudaStream_t)stream);
+  return run_bwd(s, Sums{db, dc, da, dd, ddt_bias}, (cudaStream_t)stream);
 }
