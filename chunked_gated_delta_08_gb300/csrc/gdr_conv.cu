@@ -13,7 +13,7 @@
 // Runs are cut from the flat token axis; a sequence's border inside one reloads
 // the window.  The bound is HBM: 16384 x 4096 bf16 take 51.5 us, 77 % of the copy
 // rate, where eight channels to a thread, at 155 registers, took 104.  The
-// backward takes 99 us, 60 %: at 58 instructions per token and pair of channels
+// backward takes 98 us, 61 %: at 58 instructions per token and pair of channels
 // it issues on half of the cycles.
 #include <algorithm>
 
@@ -29,6 +29,7 @@ struct ConvArgs {
   const int32_t *slots;
   void *y, *st;  // backward: dx, ds0; step: st is the pool
   float *part;   // backward: [runs, W + 1, E]
+  float *dweight, *dbias;
   int64_t M, runs;
   int L, cx;     // tokens in a run; threads across channels in a block
   unsigned tiles;  // blocks across channels
@@ -401,6 +402,23 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvArgs a) {
     }
     ta = tb;
   }
+  if (a.runs == 1) {  // nothing to add up
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      float lo, hi;
+      const int64_t e = p.e + 2 * i;
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        f2_split(dw[j][i], lo, hi);
+        if (2 * i < p.n) a.dweight[e * W + j] = lo;
+        if (2 * i + 1 < p.n) a.dweight[(e + 1) * W + j] = hi;
+      }
+      f2_split(db[i], lo, hi);
+      if (a.dbias && 2 * i < p.n) a.dbias[e] = lo;
+      if (a.dbias && 2 * i + 1 < p.n) a.dbias[e + 1] = hi;
+    }
+    return;
+  }
   using O = Io<float, NP, AL>;
   float *part = a.part + p.run * (W + 1) * a.d.E + p.e;
 #pragma unroll
@@ -509,6 +527,7 @@ int launch(ConvArgs a, Dir dir, float *dweight, float *dbias, cudaStream_t st) {
     });
   }
   a.L = (int)(dir == kFwd ? run_length(a.M, tiles, per, 8, 96) : run_length(a.M, tiles, per, 16, 384));
+  if (dir == kBwd && a.M <= 64) a.L = 64;  // one run: a second launch and scratch take longer than 64 tokens in a row
   a.runs = std::max<int64_t>(1, cdiv(a.M, a.L));
   const int64_t blocks = tiles * cdiv(a.runs, per);
   if (blocks > 0x7fffffff) return set_error(GDR_ERR_SHAPE, "too many tokens for one launch");
@@ -518,14 +537,20 @@ int launch(ConvArgs a, Dir dir, float *dweight, float *dbias, cudaStream_t st) {
       return launched("conv_fwd_kernel");
     });
   }
+  a.dweight = dweight;
+  a.dbias = dbias;
+  auto go = [&] {
+    return with_taps(d.W, [&](auto w) {
+      conv_bwd_kernel<T, 1, AL, decltype(w)::value><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+      return launched("conv_bwd_kernel");
+    });
+  };
+  if (a.runs == 1) return go();
   char *base = nullptr;
   int rc = scratch_begin(sizeof(float) * (size_t)(a.runs * (d.W + 1) * d.E), st, "convolution backward scratch", &base);
   if (rc != GDR_OK) return rc;
   a.part = (float *)base;
-  rc = with_taps(d.W, [&](auto w) {
-    conv_bwd_kernel<T, 1, AL, decltype(w)::value><<<(unsigned)blocks, kThreads, 0, st>>>(a);
-    return launched("conv_bwd_kernel");
-  });
+  rc = go();
   if (rc == GDR_OK) {
     const dim3 grid((unsigned)cdiv(d.E, 32), (unsigned)(d.W + (dbias ? 1 : 0)));
     const SeqCheck seqs{a.cu, d.N, a.M, a.status};

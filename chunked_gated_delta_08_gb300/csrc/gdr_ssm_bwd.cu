@@ -21,7 +21,7 @@
 // small a_t has forgotten.  The bound is arithmetic: four exponentials and about
 // 25 fp32 operations per channel, state and token, some 250 instructions per
 // token of a thread's eight states.  16384 tokens x 2048 channels x 16 states take
-// 1127 us, four fifths of it main, which issues on 49 % of cycles.
+// 1122 us, four fifths of it main, which issues on 49 % of cycles.
 #include <algorithm>
 
 #include "gdr_ssm.cuh"
