@@ -195,3 +195,19 @@ def test_refusals(gdr, call, error):
     x = torch.zeros(2, 6, 16, dtype=BF16, device="cuda")
     with pytest.raises(error):
         call(gdr, x, torch.zeros(16, 4, dtype=BF16, device="cuda"))
+
+
+def test_thousands_of_short_sequences(gdr):
+    g = torch.Generator().manual_seed(12)
+    lens = torch.randint(0, 7, (2500,), generator=g).tolist()
+    p = ref.conv_inputs(lens, 20, 4, F32, seed=12)
+    q, cu = put(p), ref.cu_of(lens, "cuda")
+    fn = lambda x, w, b, s0: ref.conv(x, w, b, s0, lens)  # noqa: E731
+    y, st = gdr.conv_fwd(q["x"][None], q["weight"], bias=q["bias"], s0=q["s0"], cu_seqlens=cu)
+    want_y, want_st = fn(*[ref.f64(p[k]) for k in ("x", "weight", "bias", "s0")])
+    ref.close(y[0], want_y, 4, "y")
+    assert torch.equal(st.cpu().double(), want_st)
+    got = gdr.conv_bwd(q["x"][None], q["weight"], q["dy"][None], bias=q["bias"], s0=q["s0"], dst=q["dst"], cu_seqlens=cu)
+    want = ref.grads(fn, [p[k] for k in ("x", "weight", "bias", "s0")], (p["dy"].double(), p["dst"].double()))
+    for u, v, n, what in zip(got, want, (4, sum(lens), sum(lens), 4), ("dx", "dweight", "dbias", "ds0")):
+        ref.close(u[0] if what == "dx" else u, v, n, what)

@@ -277,3 +277,10 @@ def test_refusals(gdr, change, error):
     gdr.ssm_fwd(**q)
     with pytest.raises(error):
         gdr.ssm_fwd(**{k: change.get(k, lambda t: t)(v) for k, v in q.items()})
+
+
+def test_thousands_of_short_sequences(gdr):
+    g = torch.Generator().manual_seed(12)
+    lens = torch.randint(0, 4, (2500,), generator=g).tolist()
+    p = ref.scan_inputs(lens, 10, 4, 1, F32, seed=12)
+    check(gdr, p, put(p), lens)
