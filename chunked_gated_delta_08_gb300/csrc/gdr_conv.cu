@@ -502,10 +502,10 @@ int with_taps(int64_t W, F &&f) {
 enum Dir { kFwd, kBwd, kStep };
 
 // Tokens in a run.  A run reads W - 1 tokens again, loads its weights and leaves
-// partials, so it is long; and the grid is whole waves of the five blocks that a
-// multiprocessor holds, as few as keep runs within `hi`.
-int64_t run_length(int64_t M, int64_t tiles, int64_t per, int64_t lo, int64_t hi) {
-  const int64_t wave = std::max<int64_t>(1, 5 * kSMs / tiles) * per;  // runs at once
+// partials, so it is long; and the grid is whole waves of the blocks that the
+// multiprocessors hold at once, as few as keep runs within `hi`.
+int64_t run_length(int64_t M, int64_t tiles, int64_t per, int64_t resident, int64_t lo, int64_t hi) {
+  const int64_t wave = std::max<int64_t>(1, resident * kSMs / tiles) * per;  // runs at once
   return std::max(lo, cdiv(M, wave * std::max<int64_t>(1, cdiv(M, wave * hi))));
 }
 
@@ -526,7 +526,10 @@ int launch(ConvArgs a, Dir dir, float *dweight, float *dbias, cudaStream_t st) {
       return launched("conv_step_kernel");
     });
   }
-  a.L = (int)(dir == kFwd ? run_length(a.M, tiles, per, 8, 96) : run_length(a.M, tiles, per, 16, 384));
+  // blocks on a multiprocessor, by registers: bf16 in whole accesses 96, else up to 117 backward and 154 forward
+  constexpr bool kLean = AL && sizeof(T) == 2;
+  a.L = (int)(dir == kFwd ? run_length(a.M, tiles, per, kLean ? 5 : 3, 8, 96)
+                          : run_length(a.M, tiles, per, kLean ? 5 : 4, 16, 384));
   if (dir == kBwd && a.M <= 64) a.L = 64;  // one run: a second launch and scratch take longer than 64 tokens in a row
   a.runs = std::max<int64_t>(1, cdiv(a.M, a.L));
   const int64_t blocks = tiles * cdiv(a.runs, per);

@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) norm_bwd_kernel(NormArgs a) {
 
 // The same for rows that allow no accesses of four columns: NV single columns of a thread.
 template <typename T, typename R, int NT, int NV>
-__global__ void __launch_bounds__(NT) norm_bwd_scalar_kernel(NormArgs a) {
+__global__ void __launch_bounds__(NT, 1024 / NT) norm_bwd_scalar_kernel(NormArgs a) {
   __shared__ __align__(16) float red[2][32];
   const int tid = threadIdx.x;
   const int64_t E = a.d.E;
