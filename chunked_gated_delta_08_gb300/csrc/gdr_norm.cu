@@ -46,8 +46,17 @@ __device__ __forceinline__ void store_fp8(uint8_t *p, const float (&v)[VEC], flo
   }
 }
 
-__device__ __forceinline__ float group_inv(float amax) { return amax == 0.f ? 1.f : kFp8Max / amax; }
-__device__ __forceinline__ float group_scale(float amax) { return amax == 0.f ? 1.f : amax / kFp8Max; }
+// The multiplier 448 / amax passes fp32's range below 1.32e-36, and an infinite one
+// makes NaN of the zeros beside such values.  Smaller groups take the scale of this
+// least amax, so that multiplier and scale agree: their bytes are below 448.
+constexpr float kLeastAmax = 0x1.c00002p-120f;
+static_assert(kFp8Max / kLeastAmax <= 3.402823466e38f, "448 / kLeastAmax is an fp32 number");
+__device__ __forceinline__ float group_inv(float amax) {
+  return amax == 0.f ? 1.f : kFp8Max / max_nan(amax, kLeastAmax);
+}
+__device__ __forceinline__ float group_scale(float amax) {
+  return amax == 0.f ? 1.f : max_nan(amax, kLeastAmax) / kFp8Max;
+}
 
 // Sums (or maxima) over the NT threads of a row.  NT == 32: a warp, no barrier.
 template <int NT, bool MAX>

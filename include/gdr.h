@@ -259,7 +259,9 @@ typedef struct gdr_norm_desc {
  *                byte = e4m3(y * (448 / amax)), round to nearest even.
  *   quant GROUP  the same over groups of 128 columns (the last one may be
  *                shorter), scale [M, ceil(E / 128)].
- * A group of zeros has scale 1; a NaN makes its scale and its bytes NaN.
+ * A group of zeros has scale 1; a NaN makes its scale and its bytes NaN.  An
+ * amax below 1.32e-36, whose 448 / amax is past fp32's range, counts as that:
+ * y ~ byte * scale holds, to half an e4m3 step or 2^-10 of the scale.
  */
 int gdr_norm_fwd(const gdr_norm_desc *desc, const void *x, const void *residual, const void *weight, void *y,
                  float *scale, void *s, void *stream);
