@@ -77,7 +77,10 @@ __global__ void __launch_bounds__(kSsmThreads, 4) ssm_bwd_local_kernel(SsmArgs a
   }
   stage_row<P::CB, P::kThreads>(p, a.dt_bias, sm.bias);
   __syncthreads();
-  States A, h, g, pass;  // pass: product of the decays since the chunk began; zero once a sequence started
+  // pass: product of the decays since the chunk began.  What a sequence that starts
+  // in the chunk holds is no part of the gradient entering it, and is left out, not
+  // multiplied by zero: it need not be finite.
+  States A, h, g, pass;
   load_a(a, p, A);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -88,7 +91,7 @@ __global__ void __launch_bounds__(kSsmThreads, 4) ssm_bwd_local_kernel(SsmArgs a
     }
   f2 sum[2] = {0, 0};
   bool started = false;
-  auto token = [&](int t) {
+  auto token = [&](int t) {  // before a sequence has started
     const Pairs<2> delta(&sm.delta[t][p.col]), x(&sm.x[t][p.col]), up(&sm.up[t][p.col]);
     const Twice b(&sm.b[t * P::SP + p.sl * 4]), c(&sm.c[t * P::SP + p.sl * 4]);
 #pragma unroll
@@ -103,6 +106,9 @@ __global__ void __launch_bounds__(kSsmThreads, 4) ssm_bwd_local_kernel(SsmArgs a
       }
       sum[i] = f2_add(sum[i], delta.v[i]);
     }
+  };
+  auto state_only = [&](int t) {
+    advance(h, A, Pairs<2>(&sm.delta[t][p.col]), Pairs<2>(&sm.x[t][p.col]), Twice(&sm.b[t * P::SP + p.sl * 4]));
   };
   int64_t bos = -1, eos = -1;  // of the sequence that the tile begins in
   for (int64_t t0 = begin; t0 < end; t0 += kTile) {
@@ -146,7 +152,7 @@ __global__ void __launch_bounds__(kSsmThreads, 4) ssm_bwd_local_kernel(SsmArgs a
       if (t0 + kTile < end) fetch_ahead(t0 + kTile);
     }
     __syncthreads();
-    if (!borders && nt == kTile) {
+    if (!borders && nt == kTile && !started) {
 #pragma unroll 4
       for (int t = 0; t < kTile; ++t) token(t);
     } else {
@@ -155,12 +161,9 @@ __global__ void __launch_bounds__(kSsmThreads, 4) ssm_bwd_local_kernel(SsmArgs a
         if (borders && sm.bd.first[t] >= 0) {
           load_h0(a, p, a.h0, sm.bd.first[t], h);
           started = true;
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int s = 0; s < 4; ++s) pass[i][s] = 0;
         }
-        token(t);
+        if (started) state_only(t);
+        else token(t);
         if (a.dht && !started && borders && sm.bd.last[t] >= 0) {
           States dh;
           load_h0(a, p, a.dht, sm.bd.last[t], dh);
