@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(128) ssm_carry_kernel(SsmArgs a, int SP) {
       const int64_t c = c0 + k;
       if (c < a.chunks) {
         a.hloc[c * row + i] = h;
-        h = isnan(sum[k]) ? loc[k] : fmaf(ex2(A * sum[k]), h, loc[k]);
+        h = isnan(sum[k]) ? loc[k] : carry_over(A * sum[k], h, loc[k]);
       }
     }
   }

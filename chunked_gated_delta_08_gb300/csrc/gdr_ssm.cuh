@@ -419,6 +419,18 @@ __device__ __forceinline__ void copy_empty_states(const SsmArgs &a, const P &p, 
   }
 }
 
+// What a chunk makes of the value v that enters it: 2^e v + loc.  Where a state
+// grows (a > 0, or a negative delta) the factor may leave fp32's range and the
+// product not, zero above all: such a factor is multiplied in three parts, each in
+// range, of which more than 2^381 in all take any v but zero past the range as well.
+// Selects, as lanes of a warp have near and far factors: a branch took 4 us more in
+// the backward of 16384 x 2048 x 16.
+__device__ __forceinline__ float carry_over(float e, float v, float loc) {
+  const bool far = !(fabsf(e) <= 126.f);
+  const float third = e * (1.f / 3.f), r = ex2(far ? (third > 127.f ? 127.f : third) : e), m = far ? r : 1.f;
+  return fmaf(r, (m * v) * m, loc);
+}
+
 // Host side, shared by the forward and the backward.
 int ssm_validate(const gdr_ssm_desc *d, const int64_t *cu);
 int ssm_prepare(SsmArgs &a, bool backward, int *sl, bool *vec);

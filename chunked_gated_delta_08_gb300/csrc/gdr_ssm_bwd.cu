@@ -9,7 +9,8 @@
 //
 // Launches (chunks of L <= 64 tokens, gdr_ssm.cuh):
 //   local   per (chunk, channels): the chunk's state from zero, and what its own
-//           tokens give to the gradient of the state entering it
+//           tokens give to the gradient of the state entering it (forwards, times the
+//           product of decays; backwards where that leaves fp32's range)
 //   carry   per (channel, state): the state entering each chunk (forwards) and the
 //           gradient reaching its end from later chunks (backwards), in order
 //   main    per (chunk, channels): the states again, kept every 8 tokens in shared
@@ -41,7 +42,20 @@ struct __align__(16) LocalShared {
   float bias[P::CB];
   float b[kTile * P::SP], c[kTile * P::SP];
   Borders<kTile> bd;
+  unsigned signs;  // of the deltas, where they come without softplus: 1 some are negative, 2 some positive
 };
+
+// Keeps the signs of eight deltas.
+__device__ __forceinline__ void note_signs(const Eight &v, unsigned *signs) {
+  unsigned found = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x, y;
+    f2_split(v[i], x, y);
+    found |= (x < 0.f || y < 0.f ? 1u : 0u) | (x > 0.f || y > 0.f ? 2u : 0u);
+  }
+  atomicOr(signs, found);
+}
 
 // Eight columns of token t, n of them inside the group.
 template <typename T, bool VEC>
@@ -50,8 +64,80 @@ __device__ __forceinline__ void fetch8(const void *src, int64_t ld, int64_t t, i
   r.load(static_cast<const T *>(src) + t * ld + e, n);
   r.expand(v);
 }
+
+// The sequence that enters a chunk, and its tokens [begin, stop) there (none where a
+// sequence starts with the chunk).
+struct Entering {
+  int64_t n, begin, stop;
+  bool ends;  // in the chunk
+  __device__ __forceinline__ Entering(const SsmArgs &a, int64_t chunk) {
+    begin = chunk * a.L;
+    const int64_t end = begin + a.L < a.M ? begin + a.L : a.M;
+    n = seq_of_token(a.cu, a.d.N, a.d.T, begin);
+    const SeqRange r = seq_range(a.cu, n, a.d.T);
+    stop = r.bos == begin ? begin : r.eos < end ? r.eos : end;
+    ends = r.bos < begin && r.eos <= end;
+  }
+};
+
+// The local pass sums the gradient entering a chunk forwards, each token's part times
+// the product of the decays so far.  Where a state grows, that product can leave
+// fp32's range and the gradient not.  Such gradients of a thread's channels and states
+// are worked out again from the last token back, one decay at a time, as main does it:
+// all of them where one is not finite (`all`); else, of raw deltas with both signs,
+// those whose product may have been below fp32's range and come back with what was left
+// of it.  A call that finds its place again, so that local holds no registers for it.
+template <typename T, int SL>
+__device__ __noinline__ void redo_entering(const SsmArgs &a, bool all) {
+  const Place<SL> p(a);
+  const Entering in(a, p.chunk);
+  const int s0 = p.sl * 4;
+  const T *c = static_cast<const T *>(a.c) + p.g * a.d.S + s0;
+  for (int64_t e = p.e0 + p.col; e < p.e0 + p.col + 4 && e < p.e_end; ++e) {
+    const float bias = a.dt_bias ? a.dt_bias[e] : 0.f;
+    auto raw = [&](int64_t t) { return to_f32(static_cast<const T *>(a.dt)[t * a.d.ld_dt + e]) + bias; };
+    float reach = CUDART_INF_F;
+    if (!all) {  // the furthest from zero that the sums of delta come
+      float sum = 0.f, far = 0.f, low = 0.f, high = 0.f;
+#pragma unroll 4
+      for (int64_t t = in.begin; t < in.stop; ++t) {
+        const float v = raw(t);
+        low = fminf(low, v);
+        high = fmaxf(high, v);
+        sum += v;
+        far = fmaxf(far, fabsf(sum));
+      }
+      reach = low < 0.f && high > 0.f ? far : 0.f;
+    }
+    float A[4], g[4] = {};
+    bool some = false;
+    load_states(a.a + e * a.d.S, s0, (int)a.d.S, 0, A);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      A[s] *= kLog2e;
+      some |= !(fabsf(A[s]) * reach < 126.f);
+    }
+    if (!some) continue;
+    if (a.dht && in.ends) load_states(a.dht + (in.n * a.d.E + e) * a.d.S, s0, (int)a.d.S, 0, g);
+    for (int64_t t = in.stop - 1; t >= in.begin; --t) {
+      const float delta = ssm_delta(raw(t), a.d.flags & GDR_SSM_SOFTPLUS);
+      float up = to_f32(static_cast<const T *>(a.dy)[t * a.d.ld_dy + e]);
+      if (a.z) {
+        const float z = to_f32(static_cast<const T *>(a.z)[t * a.d.ld_z + e]);
+        up *= z * sigmoid_fast(z);
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        if (s0 + s < a.d.S) g[s] = ex2(A[s] * delta) * fmaf(to_f32(c[t * a.d.ld_c + s]), up, g[s]);
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      if (!(fabsf(A[s]) * reach < 126.f)) a.gloc[(p.chunk * a.d.E + e) * p.SP + s0 + s] = g[s];
+  }
+}
+
 template <typename T, int SL, bool VEC>
-__global__ void __launch_bounds__(kSsmThreads, 4) ssm_bwd_local_kernel(SsmArgs a) {
+__global__ void __launch_bounds__(kSsmThreads, 4) ssm_bwd_local_kernel(const __grid_constant__ SsmArgs a) {
   using P = Place<SL>;
   constexpr bool kAhead = VEC && sizeof(T) == 2;
   __shared__ LocalShared<T, P, VEC> sm;
@@ -76,6 +162,7 @@ __global__ void __launch_bounds__(kSsmThreads, 4) ssm_bwd_local_kernel(SsmArgs a
     if (begin < end) fetch_ahead(begin);
   }
   stage_row<P::CB, P::kThreads>(p, a.dt_bias, sm.bias);
+  if (threadIdx.x == 0) sm.signs = 0;
   __syncthreads();
   // pass: product of the decays since the chunk began.  What a sequence that starts
   // in the chunk holds is no part of the gradient entering it, and is left out, not
@@ -138,6 +225,7 @@ __global__ void __launch_bounds__(kSsmThreads, 4) ssm_bwd_local_kernel(SsmArgs a
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = f2_delta(f2_add(v[i], w[i]), a.d.flags & GDR_SSM_SOFTPLUS);
       put8(&sm.delta[t][st.col], v);
+      if (!(a.d.flags & GDR_SSM_SOFTPLUS)) note_signs(v, &sm.signs);
       get(2, k, v);
       if (a.z) {
         get(3, k, w);
@@ -177,6 +265,14 @@ __global__ void __launch_bounds__(kSsmThreads, 4) ssm_bwd_local_kernel(SsmArgs a
   }
   store_chunk(a, p, a.hloc, p.chunk, h);
   store_chunk(a, p, a.gloc, p.chunk, g);
+  f2 zero = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int s = 0; s < 4; ++s) zero = f2_fma(g[i][s], 0, zero);
+  float lo, hi;
+  f2_split(zero, lo, hi);
+  const bool all = !(lo == 0.f && hi == 0.f);  // some g is not finite
   const int mine = p.sl & 3;
   const int64_t e_mine = p.e0 + p.col + mine;
   if (p.sl < 4 && e_mine < p.e_end) {
@@ -186,6 +282,7 @@ __global__ void __launch_bounds__(kSsmThreads, 4) ssm_bwd_local_kernel(SsmArgs a
     const float mine_sum = mine == 0 ? s[0] : mine == 1 ? s[1] : mine == 2 ? s[2] : s[3];
     a.sumd[p.chunk * a.d.E + e_mine] = started ? CUDART_NAN_F : mine_sum;  // NaN: nothing passes through
   }
+  if (all || sm.signs == 3) redo_entering<T, SL>(a, all);
 }
 
 // In place: blockIdx.y 0 turns hloc[c] into the state entering chunk c, 1 turns
@@ -214,7 +311,7 @@ __global__ void __launch_bounds__(128) ssm_bwd_carry_kernel(SsmArgs a, int SP) {
       const int64_t c = back ? a.chunks - 1 - (c0 + k) : c0 + k;
       if (c0 + k < a.chunks) {
         v[c * row] = acc;
-        acc = isnan(sum[k]) ? loc[k] : fmaf(ex2(A * sum[k]), acc, loc[k]);
+        acc = isnan(sum[k]) ? loc[k] : carry_over(A * sum[k], acc, loc[k]);
       }
     }
   }

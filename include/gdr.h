@@ -326,6 +326,9 @@ typedef struct gdr_ssm_desc {
  * x, dt, z, y [B, T, E]; a [E, S] fp32; b, c [B, T, G, S]; d, dt_bias [E] fp32;
  * h0, ht [N, E, S] fp32.  d, z, dt_bias, h0 may be NULL (no such term), ht NULL
  * is not wanted.
+ * States may grow (a > 0, or a negative delta without the softplus): a token's
+ * exp(delta_t a), the states and their gradients have to be fp32 numbers, the
+ * products of decays over several tokens need not.
  */
 int gdr_ssm_fwd(const gdr_ssm_desc *desc, const void *x, const void *dt, const float *a, const void *b,
                 const void *c, const float *d, const void *z, const float *dt_bias, const float *h0,
