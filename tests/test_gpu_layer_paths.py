@@ -193,3 +193,44 @@ def test_conv_slices_and_unaligned_bases(gdr, lens, dtype, offset):
     want = ref.grads(fn, [p[k] for k in ("x", "weight", "bias", "s0")], (p["dy"].double(), p["dst"].double()))
     for u, v, n, what in zip(got, want, (4, M, M, 4), ("dx", "dweight", "dbias", "ds0")):
         ref.close(u[0] if what == "dx" else u, v, n, what)
+
+
+@both_types
+@pytest.mark.parametrize("value", [float("nan"), float("inf")], ids=str)
+@pytest.mark.parametrize("where", ["x", "dt", "b", "c", "z", "dy", "dht", "h0"])
+def test_scan_sequences_keep_to_themselves_in_one_chunk(gdr, dtype, where, value):
+    lens = [20, 12, 30]
+    p = put(ref.scan_inputs(lens, 24, 12, 2, dtype, seed=6))
+    clean = scan(gdr, p, lens)
+    q = dict(p)
+    q[where] = p[where].clone()
+    q[where][1 if where in ("dht", "h0") else slice(20, 32)] = value
+    got = scan(gdr, q, lens)
+    for n, i, j in ref.spans(lens):
+        for k in ("y", "dx", "ddt", "db", "dc", "dz", "ht", "dh0"):
+            mine, want = (v[n] if k in ("ht", "dh0") else v[0, i:j] for v in (got[k], clean[k]))
+            assert n == 1 or torch.equal(mine, want), (k, n)
+
+
+@both_types
+@pytest.mark.parametrize("lens", [[20, 12, 30], [100, 30, 90]], ids=["one_run", "runs"])
+@pytest.mark.parametrize("where", ["x", "dy", "s0", "dst"])
+def test_conv_sequences_keep_to_themselves(gdr, lens, dtype, where):
+    E = 24
+    p, cu = put(ref.conv_inputs(lens, E, 4, dtype, seed=6)), ref.cu_of(lens, "cuda")
+
+    def call(q):
+        y, st = gdr.conv_fwd(q["x"][None], q["weight"], bias=q["bias"], s0=q["s0"], cu_seqlens=cu)
+        with Launches(gdr, 2 if sum(lens) > 64 else 1):
+            dx, _, _, ds0 = gdr.conv_bwd(q["x"][None], q["weight"], q["dy"][None], bias=q["bias"], s0=q["s0"],
+                                         dst=q["dst"], cu_seqlens=cu)
+        return dict(y=y[0], dx=dx[0], st=st, ds0=ds0)
+    clean, q = call(p), dict(p)
+    for value in (float("nan"), float("inf")):
+        q[where] = p[where].clone()
+        q[where][1 if where in ("s0", "dst") else slice(lens[0], lens[0] + lens[1])] = value
+        got = call(q)
+        for n, i, j in ref.spans(lens):
+            for k, v in got.items():
+                mine, want = (u[n] if k in ("st", "ds0") else u[i:j] for u in (v, clean[k]))
+                assert n == 1 or torch.equal(mine, want), (k, n)
