@@ -11,10 +11,11 @@
 // registers, so every input is read from HBM once (the W - 1 tokens around a run
 // come from L2 again).  The next batch of tokens is loaded while one is computed.
 // Runs are cut from the flat token axis; a sequence's border inside one reloads
-// the window.  The bound is HBM: 16384 x 4096 bf16 take 51.5 us, 77 % of the copy
+// the window.  The bound is HBM: 16384 x 4096 bf16 take 51.5 us, 78 % of the copy
 // rate, where eight channels to a thread, at 155 registers, took 104.  The
-// backward takes 98 us, 61 %: at 58 instructions per token and pair of channels
-// it issues on half of the cycles.
+// backward takes 98 us, 61 %, and issues on 53 % of the cycles: neither is full.  A
+// thread has four tokens of two arrays under way, 20 KB a multiprocessor, half of what
+// the forward has (41 KB), and its warps wait for loads more than for anything else.
 #include <algorithm>
 
 #include "gdr_layer.cuh"

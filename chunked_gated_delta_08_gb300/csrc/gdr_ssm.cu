@@ -7,12 +7,13 @@
 //   main    per (chunk, channels): the recurrence again from there, y and ht
 // The recurrence runs twice so that chunks run at once; where one chunk covers
 // a sequence (short ones, or enough sequences to fill the GPU) main runs alone.
-// The bound is arithmetic: per channel, state and token one exponential and
+// The work is arithmetic: per channel, state and token one exponential and
 // four fp32 operations in each pass, against 8 bytes of HBM traffic per channel
-// and token in bf16.  16384 tokens x 4096 channels x 16 states take 572 us (local
-// and main issue on 60 % of cycles; the fp32 pipe is 50 to 58 % and the
-// exponential unit 39 to 54 % busy), where one exponential each would take 115 us
-// and the bytes 80.  Four blocks of 128 registers on a multiprocessor are the best
+// and token in bf16.  16384 tokens x 4096 channels x 16 states take 577 us, where one
+// exponential each would take 115 us and the bytes 81.  Nothing is full: local and
+// main issue on 60 % of cycles, the fp32 pipe is 50 to 58 % and the exponential unit
+// 39 to 55 % busy; the 14 warps of a multiprocessor wait about as often for a value
+// just computed as for a pipe.  Four blocks of 128 registers on a multiprocessor are the best
 // of four, five (+2 %) and six (+17 %, spilling); eight channels to a thread, which
 // halve the reads of b and c, took 5 % longer.
 #include <algorithm>
@@ -232,8 +233,9 @@ __global__ void __launch_bounds__(128) ssm_carry_kernel(SsmArgs a, int SP) {
 // computed.  Of a channel's first four lanes, lane k works out delta, delta x and
 // the gate of row k for all (they cost more than the four recurrences of a lane),
 // and finishes that row's output.  The bound is HBM: each state is read and
-// written once, 256 rows of 4096 x 16 in 31 us, 68 % of the copy rate.  One row
-// group to a block took 37 us, and 66 us at 92 registers.
+// written once, 256 rows of 4096 x 16 in 31 us, 69 % of the copy rate.  One row
+// group to a block took 37 us, and 66 us at 92 registers.  With fp32 inputs, whose b
+// and c take twice the registers and spill 16 to 28 bytes, 42 us against 33 with cold caches.
 constexpr int kStepRows = 4;
 
 // Four states of a thread, in pairs, and four elements of b or c as they lie in

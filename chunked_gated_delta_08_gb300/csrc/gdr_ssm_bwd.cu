@@ -19,10 +19,12 @@
 //   sums    the partials of db and dc over channels, of da, dd and ddt_bias over chunks
 // (one chunk needs no local and carry).
 // States are recomputed, never inverted: h_{t-1} = (h_t - ..) / a_t loses what a
-// small a_t has forgotten.  The bound is arithmetic: four exponentials and about
+// small a_t has forgotten.  The work is arithmetic: four exponentials and about
 // 25 fp32 operations per channel, state and token, some 250 instructions per
 // token of a thread's eight states.  16384 tokens x 2048 channels x 16 states take
-// 1122 us, four fifths of it main, which issues on 49 % of cycles.
+// 1129 us, four fifths of it main, which issues on 49 % of cycles with the fp32 pipe
+// 36 % and the exponential unit 20 % busy: its 12 warps a multiprocessor wait for
+// shared memory, shuffles and values just computed.
 #include <algorithm>
 
 #include "gdr_ssm.cuh"
@@ -320,8 +322,9 @@ __global__ void __launch_bounds__(128) ssm_bwd_carry_kernel(SsmArgs a, int SP) {
 // Main: two channels to a thread, where the other kernels have four: the states
 // of eight tokens held back take half the registers and the unrolled code half
 // the instructions.  Blocks of four warps, three on a multiprocessor at 168
-// registers, take 1178 us on 16384 tokens of 2048 channels; four at 128, which
-// spill, 1198 us; two of eight warps 1219 us.
+// registers, were the best of three on 16384 tokens of 2048 channels, before rows were
+// copied ahead: the whole backward took 1178 us, with four at 128, which spill, 1198 us,
+// with two of eight warps 1219 us.
 constexpr int kMainWarps = 4;
 template <int SL>
 using MainPlace = Place<SL, 1, kMainWarps>;
