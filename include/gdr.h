@@ -254,6 +254,8 @@ typedef struct gdr_norm_desc {
  *   y = s / sqrt(mean(s^2) + eps) * weight
  * s [M, E] (res_dtype) is the new residual stream; y is of the sum as stored,
  * so that gdr_norm_bwd differentiates exactly what was computed.
+ * The squares are summed in fp32: a row of values about 1e19 passes its range
+ * (y is then 0, or NaN where s is not finite).
  *   quant NONE   y [M, E] in dtype, scale NULL.
  *   quant ROW    y holds e4m3 bytes, scale [M] fp32 with scale = amax(y) / 448:
  *                byte = e4m3(y * (448 / amax)), round to nearest even.
