@@ -10,7 +10,9 @@ this module raises.
     dq, dk, dv, dg, dbeta, dh0 = bwd(q, k, v, g, beta, do, dht=None, h0=None, ...)
 
 The operators around the recurrence (norm_fwd, conv_fwd, ssm_fwd and their
-backward and single-token forms) are described in ``layer_ops``.
+backward and single-token forms) are described in ``layer_ops``; linear
+attention with a decay for each head and the norm of its queries and keys
+(la_fwd, qk_norm_fwd and theirs) in ``attention_ops``.
 
 Layouts: q, k [B,T,H,K]; v [B,T,HV,V]; g [B,T,HV] (GDN) or [B,T,HV,K] (KDA),
 fp32; beta [B,T,HV]; h0 [N,HV,K,V] fp32; cu_seqlens [N+1] int64 (B == 1).
@@ -37,6 +39,7 @@ GDR_ERR_TIMEOUT = -7
 GDR_ERR_SEQLENS = -8
 GDR_ERR_UNSUPPORTED = -9
 GDR_ERR_SLOTS = -10
+GDR_ERR_POSITION = -11
 
 GDR_F32, GDR_BF16 = 0, 1
 GDR_GATE_SCALAR, GDR_GATE_PER_K = 0, 1
@@ -46,7 +49,8 @@ ALGOS = {"auto": 0, "chunked": 1, "fused": 2, "recurrent": 3, "split": 4}
 EXPORTED = ["gdr_fwd", "gdr_bwd", "gdr_fwd_noalloc", "gdr_chunked_sizes_get", "gdr_chunk_index", "gdr_chunk_prepare", "gdr_chunk_fwd_h",
             "gdr_chunk_fwd_o", "gdr_device_status", "gdr_last_error", "gdr_launch_count", "gdr_version",
             "gdr_norm_fwd", "gdr_norm_bwd", "gdr_conv_fwd", "gdr_conv_bwd", "gdr_conv_step", "gdr_ssm_fwd",
-            "gdr_ssm_bwd", "gdr_ssm_step"]
+            "gdr_ssm_bwd", "gdr_ssm_step", "gdr_la_fwd", "gdr_la_bwd", "gdr_la_step", "gdr_qk_norm_fwd",
+            "gdr_qk_norm_bwd"]
 
 
 class GdrDesc(ctypes.Structure):
@@ -362,3 +366,4 @@ def device_status(stream=None, clear=True) -> int:
 
 from .layer_ops import (conv_bwd, conv_fwd, conv_step, norm_bwd, norm_fwd, ssm_bwd, ssm_fwd,  # noqa: E402,F401
                         ssm_step)
+from .attention_ops import la_bwd, la_fwd, la_step, qk_norm_bwd, qk_norm_fwd, rotation_table  # noqa: E402,F401

@@ -1,0 +1,495 @@
+// gdr_la.cu -- linear attention with a decay for each head: the entry points,
+// the form for every type and size, and the single-token form.
+#include <algorithm>
+
+#include "gdr_la.cuh"
+#include "gdr_sm100.cuh"
+
+namespace gdr {
+namespace la {
+namespace {
+
+// --------------------------------------------------------------------- any type, any size
+// One block per (segment, value head, 32 columns of c), 8 warps.  Operands lie in
+// shared memory in fp32; products are warp-level tensor-core products of values
+// split into three tf32 parts (2^-21 of a product; bf16 inputs are exact in one).
+// Rows past the segment's end and channels past the width are zeros in shared memory.
+constexpr int kThreads = 256;
+constexpr int kCols = 32;       // columns of c in a block
+constexpr int LDC = kCols + 4;  // row strides in shared memory, chosen off multiples of 32 banks
+constexpr int LDP = C + 4;
+
+inline int pad16(int n) { return (n + 15) & ~15; }
+inline size_t smem_bytes(int Da) {
+  const int D = pad16(Da);
+  return sizeof(float) * ((size_t)2 * C * (D + 4) + C * LDC + C * LDP + D * LDC + 2 * (C + 4));
+}
+
+// rows x D elements of one head into dst [C][ld], zeros past `rows` and from D to Dp.
+template <typename T>
+__device__ __forceinline__ void load_tile(float *dst, int ld, const LaRows &r, int64_t row0, int head, int rows, int col0,
+                                          int cols, int Dp, bool vec) {
+  const T *src = static_cast<const T *>(r.p) + row0 * r.ld + (int64_t)(head / r.group) * r.D + col0;
+  if (vec) {
+    const int per = Dp / 4;
+    for (int i = threadIdx.x; i < C * per; i += kThreads) {
+      const int row = i / per, c = i % per * 4;
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      if (row < rows && c < cols) load4(src + row * r.ld + c, v);  // cols is a multiple of 4
+      store4(dst + row * ld + c, v);
+    }
+  } else {
+    for (int i = threadIdx.x; i < C * Dp; i += kThreads) {
+      const int row = i / Dp, c = i % Dp;
+      dst[row * ld + c] = row < rows && c < cols ? to_f32(src[row * r.ld + c]) : 0.f;
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ bool vec4_ok(const LaRows &r) {
+  return r.D % 4 == 0 && r.ld % 4 == 0 && (reinterpret_cast<uintptr_t>(r.p) & (4 * sizeof(T) - 1)) == 0;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) la_any_kernel(const __grid_constant__ LaArgs p) {
+  extern __shared__ __align__(16) float sm[];
+  if (!seqlens_ok(p.cu, p.N, p.cu ? p.tokens : p.T, p.status)) return;
+  const LaPass &q = p.pass[blockIdx.z];
+  const int64_t hv = blockIdx.x % p.HV, slot = blockIdx.x / p.HV;
+  const int Da = q.a.D, Dc = q.c.D, col0 = blockIdx.y * kCols;
+  if (col0 >= Dc) return;
+  const bool bw = q.backwards;
+  if (p.mode == kWhole && slot >= p.N) return;  // no sequences: the block has checked cu_seqlens
+  const Segment s = segment_of(p, slot, bw);
+  if (!s.some) return;
+  if (p.mode == kStates && s.last) return;  // nobody reads the state behind the last segment
+  const int D = (Da + 15) & ~15, LDA = D + 4, cols = min(kCols, Dc - col0);
+  float *A = sm, *B = A + C * LDA, *Cm = B + C * LDA, *P = Cm + C * LDC, *S = P + C * LDP, *pw = S + D * LDC,
+        *wt = pw + C + 4;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gr = lane >> 2, tg = lane & 3;
+  const float g = p.g[hv];
+  const bool va = vec4_ok<T>(q.a), vb = vec4_ok<T>(q.b), vc = vec4_ok<T>(q.c);
+
+  for (int i = tid; i <= C; i += kThreads) pw[i] = decay_power(g, i);
+  // the state the segment starts from
+  const int64_t at = (p.mode == kWhole ? s.n : slot) * p.HV + hv;
+  const float *from = p.mode == kStates || !q.s_in ? nullptr : q.s_in + at * p.KV;
+  for (int i = tid; i < D * kCols; i += kThreads) {
+    const int r = i / kCols, c = i % kCols;
+    S[r * LDC + c] = from && r < Da && c < cols ? from[r * q.si + (col0 + c) * q.sj] : 0.f;
+  }
+  const int64_t len = s.eos - s.bos;
+  const int chunks = (int)((len + C - 1) / C);
+  for (int u = 0; u < chunks; ++u) {
+    const int64_t t0 = s.bos + (int64_t)(bw ? chunks - 1 - u : u) * C;
+    const int n = (int)min((int64_t)C, s.eos - t0);
+    __syncthreads();
+    if (p.mode != kStates) load_tile<T>(A, LDA, q.a, t0, (int)hv, n, 0, Da, D, va);
+    load_tile<T>(B, LDA, q.b, t0, (int)hv, n, 0, Da, D, vb);
+    load_tile<T>(Cm, LDC, q.c, t0, (int)hv, n, col0, cols, kCols, vc);
+    if (tid < C) wt[tid] = tid < n ? pw[bw ? tid + 1 : n - 1 - tid] * q.wscale : 0.f;
+    __syncthreads();
+    if (p.mode != kStates) {
+      // P = (A B^T) r^|i-j|: a warp takes 16 rows and 32 columns
+      const int r0 = (warp >> 1) * 16, c0 = (warp & 1) * 32;
+      float acc[4][4] = {};
+      for (int k = 0; k < D; k += 8) {
+        const float *ap = A + (r0 + gr) * LDA + k + tg;
+        const float a[4] = {ap[0], ap[8 * LDA], ap[4], ap[8 * LDA + 4]};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float *bp = B + (c0 + 8 * j + gr) * LDA + k + tg;
+          const float b[2] = {bp[0], bp[4]};
+          sm100::mma_3xtf32(acc[j], a, b);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = r0 + gr + (e >> 1) * 8, c = c0 + 8 * j + 2 * tg + (e & 1);
+          const bool in = bw ? c >= r : c <= r;
+          P[r * LDP + c] = in ? acc[j][e] * (pw[abs(r - c)] * q.pscale) : 0.f;
+        }
+      }
+      // y = iscale r^e(i) A S + P C: a warp takes 16 rows and 16 columns
+      const int oc = (warp & 1) * 16;
+      float o[2][4] = {};
+      for (int k = 0; k < D; k += 8) {
+        const float *ap = A + (r0 + gr) * LDA + k + tg;
+        const float a[4] = {ap[0], ap[8 * LDA], ap[4], ap[8 * LDA + 4]};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float *bp = S + (k + tg) * LDC + oc + 8 * j + gr;
+          const float b[2] = {bp[0], bp[4 * LDC]};
+          sm100::mma_3xtf32(o[j], a, b);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = r0 + gr + (e >> 1) * 8;
+          o[j][e] *= r < n ? pw[bw ? n - 1 - r : r + 1] * q.iscale : 0.f;
+        }
+      __syncthreads();
+      for (int k = 0; k < C; k += 8) {
+        const float *ap = P + (r0 + gr) * LDP + k + tg;
+        const float a[4] = {ap[0], ap[8 * LDP], ap[4], ap[8 * LDP + 4]};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float *bp = Cm + (k + tg) * LDC + oc + 8 * j + gr;
+          const float b[2] = {bp[0], bp[4 * LDC]};
+          sm100::mma_3xtf32(o[j], a, b);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = r0 + gr + (e >> 1) * 8, c = oc + 8 * j + 2 * tg + (e & 1);
+          if (r < n && c < cols) {
+            const int64_t to = ((t0 + r) * p.HV + hv) * Dc + col0 + c;
+            if (q.out_f32) static_cast<float *>(q.out)[to] = o[j][e];
+            else static_cast<T *>(q.out)[to] = from_f32<T>(o[j][e]);
+          }
+        }
+    }
+    // S = r^n S + (w B)^T C: a warp takes rows of S, 16 at a time
+    const float less1 = decay_less1(g, n);
+    for (int r0 = warp * 16; r0 < D; r0 += 8 * 16) {
+      float acc[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float old = S[(r0 + gr + (e >> 1) * 8) * LDC + 8 * j + 2 * tg + (e & 1)];
+          acc[j][e] = fmaf(old, less1, old);
+        }
+      for (int k = 0; k < C; k += 8) {
+        const float *ap = B + (k + tg) * LDA + r0 + gr;
+        const float w0 = wt[k + tg], w1 = wt[k + tg + 4];
+        const float a[4] = {ap[0] * w0, ap[8] * w0, ap[4 * LDA] * w1, ap[4 * LDA + 8] * w1};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float *bp = Cm + (k + tg) * LDC + 8 * j + gr;
+          const float b[2] = {bp[0], bp[4 * LDC]};
+          sm100::mma_3xtf32(acc[j], a, b);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          S[(r0 + gr + (e >> 1) * 8) * LDC + 8 * j + 2 * tg + (e & 1)] = acc[j][e];
+    }
+  }
+  if (!q.s_out || (p.mode != kStates && !s.last)) return;
+  __syncthreads();
+  float *to = q.s_out + (p.mode == kStates ? slot * p.HV + hv : s.n * p.HV + hv) * p.KV;
+  for (int i = tid; i < Da * kCols; i += kThreads) {
+    const int r = i / kCols, c = i % kCols;
+    if (c < cols) to[r * q.si + (col0 + c) * q.sj] = S[r * LDC + c];
+  }
+}
+
+// ------------------------------------------------------------------------------ carry, sums
+// The states that segments start from, in place of their own: over a sequence's
+// segments in the pass's order, S enters and leaves as r^len S + own.  One thread
+// per element of a head's state; the next segment's element is on its way meanwhile.
+__global__ void __launch_bounds__(256) la_carry_kernel(const __grid_constant__ LaArgs p) {
+  if (!seqlens_ok(p.cu, p.N, p.cu ? p.tokens : p.T, p.status)) return;
+  const LaPass &q = p.pass[blockIdx.z];
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t n = blockIdx.y / p.HV, hv = blockIdx.y % p.HV;
+  if (e >= p.KV) return;
+  const SeqRange r = seq_range(p.cu, n, p.T);
+  const int64_t len = r.eos - r.bos, segs = len > 0 ? (len + p.L - 1) / p.L : 1;
+  const float g = p.g[hv];
+  float S = q.s_in ? q.s_in[(n * p.HV + hv) * p.KV + e] : 0.f;
+  float *own = q.s_out + (first_slot(p, n) * p.HV + hv) * p.KV + e;
+  const int64_t step = p.HV * p.KV;
+  const float full = decay_less1(g, p.L), tail = decay_less1(g, len - (segs - 1) * p.L);
+  for (int64_t u = 0; u < segs; ++u) {
+    const int64_t i = q.backwards ? segs - 1 - u : u;
+    const float mine = u + 1 < segs ? own[i * step] : 0.f;  // of the last there is none
+    own[i * step] = S;
+    S = fmaf(S, i == segs - 1 ? tail : full, S) + mine;
+  }
+}
+
+// out [M, H, D] = sums over groups of G value heads of part [M, H G, D], in order.
+template <typename T>
+__global__ void __launch_bounds__(256) la_sum_kernel(const float *part0, const float *part1, T *out0, T *out1, int64_t n,
+                                                     int G, int D, SeqCheck check) {
+  if (!seqlens_ok(check)) return;
+  const float *part = blockIdx.y ? part1 : part0;
+  T *out = blockIdx.y ? out1 : out0;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  const float *src = part + (i / D) * G * D + i % D;
+  float s = src[0];
+  for (int j = 1; j < G; ++j) s += src[(int64_t)j * D];
+  out[i] = from_f32<T>(s);
+}
+
+// -------------------------------------------------------------------------------- host side
+// Tokens in a segment, or 0 for none.  A block walks a sequence chunk by chunk; where
+// there are fewer blocks than multiprocessors the rest stand idle, and forming
+// segments' states takes half as much again.
+int64_t segment_length(const LaArgs &p, int blocks_per_pair) {
+  const int64_t pairs = p.N * p.HV * blocks_per_pair;
+  if (p.tokens <= 4 * C || p.N == 0 || pairs >= 2 * kSMs) return 0;
+  const int64_t want = std::max<int64_t>(1, cdiv(2 * kSMs, p.HV * blocks_per_pair));  // segments over all sequences
+  const int64_t L = std::max<int64_t>(4 * C, cdiv(cdiv(p.tokens, want), C) * C);
+  return !p.cu && L >= p.T ? 0 : L;
+}
+
+template <typename T>
+int launch_any(const LaArgs &p, int passes, cudaStream_t st) {
+  int Da = 0, Dc = 0;
+  for (int i = 0; i < passes; ++i) {
+    Da = std::max(Da, p.pass[i].a.D);
+    Dc = std::max(Dc, p.pass[i].c.D);
+  }
+  const size_t smem = smem_bytes(Da);
+  const cudaError_t e = cudaFuncSetAttribute(la_any_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return cuda_error(e, "cudaFuncSetAttribute(la_any_kernel)");
+  const int64_t items = std::max<int64_t>(1, (p.mode == kWhole ? p.N : p.slots) * p.HV);
+  if (items > 0x7fffffff) return set_error(GDR_ERR_SHAPE, "too many sequences and heads for one launch");
+  la_any_kernel<T><<<dim3((unsigned)items, (unsigned)cdiv(Dc, kCols), passes), kThreads, smem, st>>>(p);
+  return launched("la_any_kernel");
+}
+
+int launch(const LaArgs &p, int passes, int dtype, bool tc, cudaStream_t st) {
+  if (tc) return launch_tc(p, passes, st);
+  return dtype == GDR_BF16 ? launch_any<__nv_bfloat16>(p, passes, st) : launch_any<float>(p, passes, st);
+}
+
+// Runs `passes` of p; states (nstates of them, in passes st_pass, with natural strides) are
+// formed and carried first where sequences are cut.  from[i]: which state pass i starts from.
+int run(LaArgs p, int passes, const LaPass *st_pass, int nstates, const int *from, int dtype, cudaStream_t st) {
+  const bool tc = tc_takes(p, passes, dtype);
+  p.mode = kWhole;
+  int widest = 1;
+  for (int i = 0; i < passes; ++i) widest = std::max(widest, (int)cdiv(p.pass[i].c.D, kCols));
+  p.L = segment_length(p, tc ? passes : passes * widest);
+  if (!p.L) return launch(p, passes, dtype, tc, st);
+  p.slots = slot_count(p.tokens, p.N, p.L);
+  const int64_t one = p.slots * p.HV * p.KV;
+  char *base = nullptr;
+  int rc = scratch_begin(sizeof(float) * (size_t)(one * nstates), st, "linear attention states", &base);
+  if (rc != GDR_OK) return rc;
+  LaArgs s = p;
+  s.mode = kStates;
+  for (int i = 0; i < nstates; ++i) {
+    s.pass[i] = st_pass[i];
+    s.pass[i].s_out = (float *)base + i * one;
+  }
+  rc = launch(s, nstates, dtype, tc_takes(s, nstates, dtype), st);
+  if (rc == GDR_OK) {
+    la_carry_kernel<<<dim3((unsigned)cdiv(p.KV, 256), (unsigned)(p.N * p.HV), nstates), 256, 0, st>>>(s);
+    rc = launched("la_carry_kernel");
+  }
+  p.mode = kFromStates;
+  for (int i = 0; i < passes; ++i) p.pass[i].s_in = (float *)base + from[i] * one;
+  if (rc == GDR_OK) rc = launch(p, passes, dtype, tc, st);
+  return scratch_end(base, st, "linear attention states", rc);
+}
+
+int validate(const gdr_la_desc *d, const int64_t *cu, bool step) {
+  if (!d) return set_error(GDR_ERR_NULLPTR, "desc is NULL");
+  if (d->dtype != GDR_F32 && d->dtype != GDR_BF16) return set_error(GDR_ERR_DTYPE, "dtype must be GDR_F32 or GDR_BF16");
+  if (d->flags) return set_error(GDR_ERR_DTYPE, "unknown bits in flags");
+  constexpr int64_t kMost = 0x7fffffff;
+  if (d->B < 0 || d->T < 0 || d->N < 0 || d->N > kMost || d->B > kMost || d->T > kMost ||
+      (d->T > 0 && d->B > kMost / d->T))
+    return set_error(GDR_ERR_SHAPE, "B, T and N must be >= 0, N and B * T below 2^31");
+  if (d->H < 1 || d->HV < 1 || d->HV % d->H != 0 || d->HV > 65535)
+    return set_error(GDR_ERR_SHAPE, "HV must be a multiple of H, at most 65535");
+  if (d->K < 1 || d->K > 256 || d->V < 1 || d->V > 256) return set_error(GDR_ERR_SHAPE, "K and V must be in [1, 256]");
+  if (d->ld_q < d->H * d->K || d->ld_k < d->H * d->K || d->ld_v < d->HV * d->V || d->ld_do < d->HV * d->V)
+    return set_error(GDR_ERR_SHAPE, "leading dimensions must be at least H * K, or HV * V");
+  if (d->ld_q > kMost || d->ld_k > kMost || d->ld_v > kMost || d->ld_do > kMost)
+    return set_error(GDR_ERR_SHAPE, "leading dimensions must be below 2^31");
+  if (!(d->scale - d->scale == 0.f)) return set_error(GDR_ERR_SHAPE, "scale must be finite");
+  if (step) return d->T == 1 ? GDR_OK : set_error(GDR_ERR_SHAPE, "a step takes one token per row: T must be 1");
+  if (cu) {
+    if (d->B != 1) return set_error(GDR_ERR_SHAPE, "cu_seqlens requires B == 1");
+  } else if (d->N != d->B) {
+    return set_error(GDR_ERR_SHAPE, "N must equal B when cu_seqlens is NULL");
+  }
+  return GDR_OK;
+}
+
+LaArgs base_args(const gdr_la_desc &d, const float *g, const int64_t *cu, int *status) {
+  LaArgs p{};
+  p.g = g;
+  p.cu = cu;
+  p.status = status;
+  p.N = d.N;
+  p.T = d.T;
+  p.HV = d.HV;
+  p.tokens = d.B * d.T;
+  p.KV = d.K * d.V;
+  return p;
+}
+
+// ------------------------------------------------------------------------------ single tokens
+// One block per (row, value head) walks the K x V state once: S = r S + k v^T is
+// written back and o = scale S^T q summed on the way.  Eight bytes of state a
+// multiply-add: HBM bound.  A thread keeps VEC columns; the block's row groups'
+// partial sums of o meet in shared memory.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) la_step_kernel(gdr_la_desc d, const T *q, const T *k, const T *v, const float *g,
+                                                      const int32_t *slots, float *state, T *o, int *status) {
+  __shared__ float sq[256], sk[256];
+  __shared__ __align__(16) float part[256 * VEC];
+  const int K = (int)d.K, V = (int)d.V, tid = threadIdx.x;
+  const int64_t row = blockIdx.x / d.HV, hv = blockIdx.x % d.HV, h = hv / (d.HV / d.H);
+  int64_t slot = slots ? slots[row] : row;
+  if (slot >= d.N) {
+    if (tid == 0 && hv == 0) raise_status(status, GDR_ERR_SLOTS);
+    slot = -1;
+  }
+  T *to = o + (row * d.HV + hv) * V;
+  if (slot < 0) {
+    for (int c = tid; c < V; c += 256) to[c] = from_f32<T>(0.f);
+    return;
+  }
+  if (tid < K) {
+    sq[tid] = to_f32(q[row * d.ld_q + h * K + tid]) * d.scale;
+    sk[tid] = to_f32(k[row * d.ld_k + h * K + tid]);
+  }
+  __syncthreads();
+  const int across = (V + VEC - 1) / VEC, groups = 256 / across;  // V <= 256
+  const int c = tid % across * VEC, r0 = tid / across;
+  const float r = expf(g[hv]);
+  float acc[VEC] = {};
+  if (r0 < groups) {
+    float vv[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) vv[i] = to_f32(v[row * d.ld_v + hv * V + c + i]);
+    float *S = state + (slot * d.HV + hv) * (int64_t)K * V + c;
+#pragma unroll 4
+    for (int i = r0; i < K; i += groups) {
+      float s[VEC];
+      load_vec<VEC>(S + (int64_t)i * V, s);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        s[j] = fmaf(sk[i], vv[j], r * s[j]);
+        acc[j] = fmaf(sq[i], s[j], acc[j]);
+      }
+      store_vec<VEC>(S + (int64_t)i * V, s);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) part[tid * VEC + j] = acc[j];
+  __syncthreads();
+  for (int i = tid; i < V; i += 256) {
+    float s = 0.f;
+    for (int gq = 0; gq < groups; ++gq) s += part[gq * across * VEC + i];
+    to[i] = from_f32<T>(s);
+  }
+}
+
+template <typename T>
+int launch_step(const gdr_la_desc &d, const void *q, const void *k, const void *v, const float *g, const int32_t *slots,
+                float *state, void *o, int *status, cudaStream_t st) {
+  const int64_t blocks = d.B * d.HV;
+  if (blocks > 0x7fffffff) return set_error(GDR_ERR_SHAPE, "too many rows and heads for one launch");
+  const bool vec = d.V % 4 == 0 && is_aligned16(state);
+  const auto kernel = vec ? la_step_kernel<T, 4> : la_step_kernel<T, 1>;
+  kernel<<<(unsigned)blocks, 256, 0, st>>>(d, (const T *)q, (const T *)k, (const T *)v, g, slots, state, (T *)o, status);
+  return launched("la_step_kernel");
+}
+
+}  // namespace
+}  // namespace la
+}  // namespace gdr
+
+using namespace gdr;
+using namespace gdr::la;
+
+extern "C" {
+
+int gdr_la_fwd(const gdr_la_desc *desc, const void *q, const void *k, const void *v, const float *g, const float *h0,
+               const int64_t *cu_seqlens, void *o, float *ht, void *stream) {
+  int rc = validate(desc, cu_seqlens, false);
+  if (rc != GDR_OK) return rc;
+  const gdr_la_desc &d = *desc;
+  if (d.N == 0 && !cu_seqlens) return GDR_OK;
+  if (!g || (d.B * d.T > 0 && (!q || !k || !v || !o)))
+    return set_error(GDR_ERR_NULLPTR, "q, k, v, g and o must be non-NULL");
+  int *status = current_status_word(&rc);
+  if (!status) return rc;
+  LaArgs p = base_args(d, g, cu_seqlens, status);
+  const int G = (int)(d.HV / d.H);
+  const LaRows rq{q, d.ld_q, (int)d.K, G}, rk{k, d.ld_k, (int)d.K, G}, rv{v, d.ld_v, (int)d.V, 1};
+  p.pass[0] = {rq, rk, rv, o, h0, ht, d.V, 1, d.scale, d.scale, 1.f, 0, 0};
+  const LaPass state = p.pass[0];
+  const int from[1] = {0};
+  return run(p, 1, &state, 1, from, d.dtype, (cudaStream_t)stream);
+}
+
+int gdr_la_bwd(const gdr_la_desc *desc, const void *q, const void *k, const void *v, const float *g, const float *h0,
+               const int64_t *cu_seqlens, const void *d_o, const float *dht, void *dq, void *dk, void *dv, float *dh0,
+               void *stream) {
+  int rc = validate(desc, cu_seqlens, false);
+  if (rc != GDR_OK) return rc;
+  const gdr_la_desc &d = *desc;
+  if (d.N == 0 && !cu_seqlens) return GDR_OK;
+  if (!g || (d.B * d.T > 0 && (!q || !k || !v || !d_o || !dq || !dk || !dv)))
+    return set_error(GDR_ERR_NULLPTR, "q, k, v, g, d_o, dq, dk and dv must be non-NULL");
+  int *status = current_status_word(&rc);
+  if (!status) return rc;
+  LaArgs p = base_args(d, g, cu_seqlens, status);
+  const cudaStream_t st = (cudaStream_t)stream;
+  const int G = (int)(d.HV / d.H);
+  const int64_t n = d.B * d.T * d.HV * d.K;
+  // grouped value heads: their parts of dq and dk meet in fp32
+  char *base = nullptr;
+  if (G > 1 && n > 0) {
+    rc = scratch_begin(sizeof(float) * 2 * (size_t)n, st, "parts of dq and dk", &base);
+    if (rc != GDR_OK) return rc;
+  }
+  float *pq = (float *)base, *pk = base ? pq + n : nullptr;
+  const LaRows rq{q, d.ld_q, (int)d.K, G}, rk{k, d.ld_k, (int)d.K, G}, rv{v, d.ld_v, (int)d.V, 1},
+      rd{d_o, d.ld_do, (int)d.V, 1};
+  const int parts = base != nullptr;
+  // passes of the same direction side by side: dk and dv read the same rows
+  p.pass[0] = {rk, rq, rd, dv, dht, dh0, d.V, 1, d.scale, 1.f, d.scale, 1, 0};
+  p.pass[1] = {rv, rd, rq, parts ? pk : dk, dht, nullptr, 1, d.V, d.scale, 1.f, d.scale, 1, parts};
+  p.pass[2] = {rd, rv, rk, parts ? pq : dq, h0, nullptr, 1, d.V, d.scale, d.scale, 1.f, 0, parts};
+  LaPass states[2] = {p.pass[0], {rq, rk, rv, nullptr, h0, nullptr, d.V, 1, d.scale, d.scale, 1.f, 0, 0}};
+  const int from[3] = {0, 0, 1};
+  rc = run(p, 3, states, 2, from, d.dtype, st);
+  if (!base) return rc;
+  if (rc == GDR_OK) {
+    const int64_t m = n / G;
+    const dim3 grid((unsigned)cdiv(m, 256), 2);
+    const SeqCheck check{cu_seqlens, d.N, d.B * d.T, status};
+    if (d.dtype == GDR_BF16)
+      la_sum_kernel<<<grid, 256, 0, st>>>(pq, pk, (__nv_bfloat16 *)dq, (__nv_bfloat16 *)dk, m, G, (int)d.K, check);
+    else la_sum_kernel<<<grid, 256, 0, st>>>(pq, pk, (float *)dq, (float *)dk, m, G, (int)d.K, check);
+    rc = launched("la_sum_kernel");
+  }
+  return scratch_end(base, st, "parts of dq and dk", rc);
+}
+
+int gdr_la_step(const gdr_la_desc *desc, const void *q, const void *k, const void *v, const float *g,
+                const int32_t *slots, float *state, void *o, void *stream) {
+  int rc = validate(desc, nullptr, true);
+  if (rc != GDR_OK) return rc;
+  if (desc->B == 0) return GDR_OK;
+  if (!q || !k || !v || !g || !state || !o)
+    return set_error(GDR_ERR_NULLPTR, "q, k, v, g, state and o must be non-NULL");
+  int *status = current_status_word(&rc);
+  if (!status) return rc;
+  const cudaStream_t st = (cudaStream_t)stream;
+  return desc->dtype == GDR_BF16 ? launch_step<__nv_bfloat16>(*desc, q, k, v, g, slots, state, o, status, st)
+                                 : launch_step<float>(*desc, q, k, v, g, slots, state, o, status, st);
+}
+
+}  // extern "C"

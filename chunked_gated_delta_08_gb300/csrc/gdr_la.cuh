@@ -1,0 +1,125 @@
+// gdr_la.cuh -- what the forms of linear attention with a decay for each head
+// share: the pass that all of them run, and how sequences are cut into segments.
+//
+// One pass.  With rows a_t, b_t (Da channels) and c_t (Dc channels) of one head,
+// r = e^g and S a Da x Dc state,
+//
+//   forwards    S_t = r S_{t-1} + b_t c_t^T,            y_t = S_t^T a_t
+//   backwards   R_t = r R_{t+1} + b_t c_t^T,  R_{T+1} = S_in / r,  y_t = R_t^T a_t
+//
+// and the attention and its three gradients are such passes:
+//
+//   o  = pass(q, k, v)   from h0                dq = pass(do, v, k)  from h0^T
+//   dv = pass(k, q, do)  backwards from dht     dk = pass(v, do, q)  backwards from dht^T
+//
+// A chunk of n rows (i of 0 .. n-1, in the tokens' order both ways) takes
+//
+//   y_i  = pscale sum_j r^|i-j| (a_i . b_j) c_j + iscale r^e(i) S^T a_i     j <= i, backwards j >= i
+//   S'   = r^n S + wscale sum_j r^w(j) b_j c_j^T
+//   e(i) = i + 1,  w(j) = n - 1 - j;    backwards  e(i) = n - 1 - i,  w(j) = j + 1
+//
+// so that no factor exceeds 1 where g <= 0, and the state at a border of chunks
+// is the forward's state there, or that state's gradient.
+//
+// Segments.  Few heads and long sequences leave multiprocessors idle, so a
+// sequence is cut into segments of L tokens: one launch forms each segment's own
+// state, one carries them along the sequence, one runs the passes from there.
+#pragma once
+
+#include "gdr_layer.cuh"
+
+namespace gdr {
+namespace la {
+
+constexpr int C = 64;  // tokens in a chunk
+
+// One operand: [tokens, heads, D], rows ld apart; value head hv reads head hv / group.
+struct LaRows {
+  const void *p;
+  int64_t ld;
+  int D, group;
+};
+
+struct LaPass {
+  LaRows a, b, c;
+  void *out;          // [tokens, HV, Dc] contiguous; fp32 where out_f32, else of the inputs' type
+  const float *s_in;  // state that a sequence (or segment) starts from, null: zero
+  float *s_out;       // state behind the sequence's last chunk (or the segment's own), null: not wanted
+  int64_t si, sj;     // element (i, j) of a Da x Dc state lies at i si + j sj
+  float pscale, iscale, wscale;
+  int backwards, out_f32;
+};
+
+// What a launch does with segments: none (a sequence is one), their own states, the passes from carried states.
+enum LaMode { kWhole = 0, kStates = 1, kFromStates = 2 };
+
+struct LaArgs {
+  LaPass pass[3];
+  const float *g;  // [HV]
+  const int64_t *cu;
+  int *status;
+  int64_t N, T, HV, tokens;
+  int64_t KV;    // elements of a state
+  int64_t L;     // tokens in a segment, a multiple of C (unused in kWhole)
+  int64_t slots; // segment slots over all sequences
+  int mode;
+};
+
+// Segment slot of (sequence n, its segment s) = first token / L + n + s.  Sequences
+// take up disjoint ranges of slots, at least one each, whatever their lengths:
+// ceil(len / L) <= last / L - first / L + 1.
+__host__ __device__ __forceinline__ int64_t slot_count(int64_t tokens, int64_t N, int64_t L) {
+  return tokens / L + N;
+}
+__device__ __forceinline__ int64_t first_slot(const LaArgs &p, int64_t n) {
+  return (p.cu ? p.cu[n] : n * p.T) / p.L + n;
+}
+
+struct Segment {
+  int64_t n;         // sequence
+  int64_t bos, eos;  // tokens of the segment
+  int first, last;   // in the pass's order of time
+  bool some;         // false: the slot is not in use
+};
+__device__ __forceinline__ Segment segment_of(const LaArgs &p, int64_t slot, bool backwards) {
+  Segment s;
+  if (p.mode == kWhole) {
+    const SeqRange r = seq_range(p.cu, slot, p.T);
+    s.n = slot;
+    s.bos = r.bos;
+    s.eos = r.eos;
+    s.first = s.last = 1;
+    s.some = true;
+    return s;
+  }
+  int64_t lo = 0, hi = p.N;  // first_slot(lo) <= slot < first_slot(hi)
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (first_slot(p, mid) <= slot) lo = mid;
+    else hi = mid;
+  }
+  const SeqRange r = seq_range(p.cu, lo, p.T);
+  const int64_t len = r.eos - r.bos, i = slot - first_slot(p, lo);
+  const int64_t segs = len > 0 ? (len + p.L - 1) / p.L : 1;
+  s.n = lo;
+  s.bos = r.bos + i * p.L;
+  s.eos = r.eos - s.bos < p.L ? r.eos : s.bos + p.L;
+  s.some = i < segs;
+  s.first = backwards ? i == segs - 1 : i == 0;
+  s.last = backwards ? i == 0 : i == segs - 1;
+  return s;
+}
+
+// r^n of a whole number n >= 0; r^0 is 1 for every g, -inf (each token forgets all before it) included.
+__device__ __forceinline__ float decay_power(float g, int n) { return n == 0 ? 1.f : expf(g * (float)n); }
+
+// r^n - 1: a state is decayed as S + S (r^n - 1), so that factors close to 1 are not rounded
+// over and over (r^64 of g = -1e-5, rounded to 24 bits, is off by 4e-5 after 512 chunks).
+__device__ __forceinline__ float decay_less1(float g, int64_t n) { return n == 0 ? 0.f : expm1f(g * (float)n); }
+
+// The tensor-core form (gdr_la_tc.cu): whether it takes these passes, and its launch.
+bool tc_takes(const LaArgs &p, int passes, int dtype);
+int launch_tc(const LaArgs &p, int passes, cudaStream_t st);
+
+}  // namespace la
+}  // namespace gdr

@@ -56,7 +56,8 @@ typedef enum gdr_status {
   GDR_ERR_TIMEOUT = -7,     /* a bounded device-side wait expired (reported by gdr_device_status) */
   GDR_ERR_SEQLENS = -8,     /* cu_seqlens not monotone or not spanning [0, T] (gdr_device_status) */
   GDR_ERR_UNSUPPORTED = -9, /* valid request that the chosen algorithm does not implement */
-  GDR_ERR_SLOTS = -10       /* a state slot past the end of the pool (gdr_device_status) */
+  GDR_ERR_SLOTS = -10,      /* a state slot past the end of the pool (gdr_device_status) */
+  GDR_ERR_POSITION = -11    /* a position past the end of the rotation table (gdr_device_status) */
 } gdr_status;
 
 typedef enum gdr_dtype { GDR_F32 = 0, GDR_BF16 = 1 } gdr_dtype;
@@ -347,9 +348,79 @@ int gdr_ssm_step(const gdr_ssm_desc *desc, const void *x, const void *dt, const 
                  float *state, void *y, void *stream);
 
 /*
+ * Linear attention with a decay for each head, and the norm of its queries and
+ * keys.  The conventions of the operators above hold: token-major inputs may be
+ * slices of wider rows, outputs are contiguous, sums and states are fp32, no
+ * atomics add.
+ */
+
+typedef struct gdr_la_desc {
+  int64_t B, T, H, HV, K, V; /* as in gdr_desc; value head hv reads q/k head hv / (HV / H); K, V in [1, 256] */
+  int64_t N;                 /* sequences, as in gdr_desc; gdr_la_step: slots in the pool */
+  int64_t ld_q, ld_k, ld_v, ld_do; /* elements between tokens of q, k, v, d_o */
+  float scale;
+  int32_t dtype;             /* of q, k, v, o and their gradients */
+  int32_t flags;             /* must be 0 */
+} gdr_la_desc;
+
+/*
+ * gdr_la_fwd -- per sequence and value head, with S a K x V state:
+ *   S_t = exp(g) S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+ * q, k [B, T, H, K]; v, o [B, T, HV, V]; g [HV] fp32, one natural-log decay for
+ * each value head; h0, ht [N, HV, K, V] fp32 (h0 NULL: zero; ht NULL: not
+ * wanted); cu_seqlens as in gdr_fwd.  g may be 0 (no decay) or -inf (each token
+ * forgets all before it).  It may be positive as long as exp(64 g) and the
+ * states are fp32 numbers.
+ * Tokens are taken in chunks of 64: what is not finite in a token may reach every
+ * output of its own sequence from the start of its chunk on (in the gradients:
+ * all of the sequence), but no other sequence and no other head's outputs.
+ * With bf16 inputs, scores and states are rounded to bf16 where they are
+ * multiplied for o; the states themselves are not (they take each product to 2^-17).
+ */
+int gdr_la_fwd(const gdr_la_desc *desc, const void *q, const void *k, const void *v, const float *g, const float *h0,
+               const int64_t *cu_seqlens, void *o, float *ht, void *stream);
+/* Gradients of L = sum(o * d_o) + sum(ht * dht) (dht NULL: zero).  dq, dk [B,T,H,K] (sums over the value heads that
+ * share a q/k head) and dv [B,T,HV,V] in dtype; dh0 [N,HV,K,V] fp32, NULL when not wanted.  g is a constant of the
+ * layer: it has no gradient. */
+int gdr_la_bwd(const gdr_la_desc *desc, const void *q, const void *k, const void *v, const float *g, const float *h0,
+               const int64_t *cu_seqlens, const void *d_o, const float *dht, void *dq, void *dk, void *dv, float *dh0,
+               void *stream);
+/* One token for each of B rows (T must be 1), states [N, HV, K, V] fp32 updated in place; slots as in gdr_conv_step. */
+int gdr_la_step(const gdr_la_desc *desc, const void *q, const void *k, const void *v, const float *g,
+                const int32_t *slots, float *state, void *o, void *stream);
+
+typedef struct gdr_qk_norm_desc {
+  int64_t M, H, HK, D;   /* tokens; heads of q and of k (HK 0: no k); channels of a head, 1 to 256 */
+  int64_t P, R;          /* the rotation's table: positions, and pairs turned (2 R <= D; 0: no rotation) */
+  int64_t ld_q, ld_k, ld_dyq, ld_dyk; /* elements between tokens */
+  float eps;
+  int32_t dtype;         /* of q, k, yq, yk and their gradients */
+  int32_t weight_dtype;  /* of wq, wk: dtype or GDR_F32 */
+  int32_t interleaved;   /* 0: channel i is turned with i + R; 1: channel 2 i with 2 i + 1 */
+  int32_t flags;         /* must be 0 */
+} gdr_qk_norm_desc;
+
+/*
+ * gdr_qk_norm_fwd -- root-mean-square norm of each head, and the rotation by the
+ * token's position, for queries and keys in one launch:
+ *   n = x / sqrt(mean(x^2) + eps) * w
+ *   (a, b) -> (a cos - b sin, b cos + a sin)   for the R pairs of n, angles [positions[m], i]
+ * q, yq [M, H, D]; k, yk [M, HK, D]; wq, wk [D]; cos, sin [P, R] fp32; positions
+ * [M] int64.  Channels from 2 R on are normed only.  A negative position is a
+ * padding token: its rows are zero, its gradients too.  One past the table is
+ * treated so and reported by gdr_device_status as GDR_ERR_POSITION.
+ */
+int gdr_qk_norm_fwd(const gdr_qk_norm_desc *desc, const void *q, const void *k, const void *wq, const void *wk,
+                    const float *cos, const float *sin, const int64_t *positions, void *yq, void *yk, void *stream);
+/* Gradients of L = sum(yq * dyq) + sum(yk * dyk): dq, dk in dtype; dwq, dwk [D] fp32. */
+int gdr_qk_norm_bwd(const gdr_qk_norm_desc *desc, const void *dyq, const void *dyk, const void *q, const void *k,
+                    const void *wq, const void *wk, const float *cos, const float *sin, const int64_t *positions,
+                    void *dq, void *dk, float *dwq, float *dwk, void *stream);
+
+/*
  * gdr_device_status -- synchronizes `stream`, then returns (and, if `clear`,
  * resets) the library's device-side status word for the current device:
- * GDR_OK, GDR_ERR_SEQLENS, GDR_ERR_SLOTS or GDR_ERR_TIMEOUT.  Also returns GDR_ERR_CUDA if
+ * GDR_OK, GDR_ERR_SEQLENS, GDR_ERR_SLOTS, GDR_ERR_POSITION or GDR_ERR_TIMEOUT.  Also returns GDR_ERR_CUDA if
  * the stream itself reports an error.
  */
 int gdr_device_status(void *stream, int clear);
