@@ -1,11 +1,494 @@
-// gdr_la_tc.cu -- linear attention on the tcgen05 tensor cores (not built yet: every pass takes gdr_la.cu's form).
+// gdr_la_tc.cu -- linear attention with a decay for each head on the sm_103a
+// tensor cores: the passes of gdr_la.cuh for bf16 rows of up to 128 channels.
+//
+// One block per (segment, value head, pass) walks its tokens in chunks of 64 with the
+// state on chip: rows of a, b and c are read once, y is written once.  Per chunk of n
+// rows, with r = e^g and the state held transposed, Dc x Da, in tensor memory:
+//
+//   Sc   = A B^T                                    M=64  N=64   K=Da
+//   P_ij = pscale r^|i-j| Sc_ij  (j <= i; backwards j >= i), bf16
+//   B'_j = wscale r^w(j) B_j = hi + lo, two bf16    (2^-17 of each product; one would leave 2^-9 in the states)
+//   O1^T = C^T P^T                                  M=128 N=64   K=64
+//   O2^T = S^T A^T, S^T as bf16 in tensor memory    M=128 N=64   K=Da
+//   S^T  = S^T + (r^n - 1) S^T, then += C^T B'hi + C^T B'lo        M=128 N=Da K=64
+//   y_i  = O1_i + iscale r^e(i) O2_i
+//
+// Every factor is a power of r with an exponent that the place in the chunk gives, so
+// the threads keep them in registers; only a ragged last chunk works them out anew.
+//
+// Warp roles (448 threads):
+//   warps 0-3    state: the bf16 copy and the decay of the fp32 state in tensor memory
+//   warps 4-7    scores: P, B' (over B in place, its lower half beside), rows past a ragged end cleared
+//   warps 8-11   output: y through shared memory and a tensor store
+//   warp 12      producer: TMA loads into a ring of three stages
+//   warp 13      one thread issues every tcgen05.mma
+// Hand-offs are mbarriers with bounded waits (about two seconds); when one runs out
+// the block records GDR_ERR_TIMEOUT, lets its copies and MMAs finish, frees its tensor
+// memory and returns.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "gdr_fused_common.cuh"
 #include "gdr_la.cuh"
+#include "gdr_sm100.cuh"
 
 namespace gdr {
 namespace la {
+namespace {
 
-bool tc_takes(const LaArgs &, int, int) { return false; }
-int launch_tc(const LaArgs &, int, cudaStream_t) { return GDR_ERR_UNSUPPORTED; }
+using namespace sm100;
+using fused::ld_sw128_chunk;
+using fused::st_sw128_chunk;
+using fused::sw128_chunk_off;
+
+constexpr int kStages = 3;
+constexpr int kTcThreads = 448;
+constexpr int kProducer = 12, kMma = 13;
+constexpr int kBarState = 1, kBarScore = 2, kBarOut = 3;
+
+// shared memory, from a 1024-byte aligned base; tiles are two panels of 64 rows x 64 channels
+constexpr uint32_t SZ_TILE = 16384, SZ_PANEL = 8192;
+constexpr uint32_t SZ_STAGE = 3 * SZ_TILE;  // A | B | C
+constexpr uint32_t OFF_LO = kStages * SZ_STAGE;   // lower halves of B', two buffers
+constexpr uint32_t OFF_P = OFF_LO + 2 * SZ_TILE;  // P, two buffers
+constexpr uint32_t OFF_Y = OFF_P + 2 * SZ_PANEL;  // y on its way out
+constexpr uint32_t OFF_SMALL = OFF_Y + SZ_TILE;
+
+// TMEM columns
+constexpr uint32_t TM_SC = 0, TM_O = 64 /* O1, O2, twice */, TM_S = 320, TM_SB = 448, TM_COLS = 512;
+
+struct Small {
+  float pw[C + 4];  // r^0 .. r^64
+  uint64_t full[kStages], empty[kStages];
+  // single arrivals, one completion per chunk (or per second chunk where there are two)
+  uint64_t b_sc, b_p[2], b_bs[2], b_buf[2], b_st, b_state, b_o[2], b_ofree[2], b_final;
+  uint32_t tmem_slot;
+  int err;
+};
+constexpr uint32_t SMEM_BYTES = OFF_SMALL + sizeof(Small) + 1024;
+static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+
+struct Maps {
+  CUtensorMap a[3], b[3], c[3], y[3];
+};
+
+__global__ void __launch_bounds__(kTcThreads, 1)
+    la_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LaArgs p, int passes, int64_t items) {
+  extern __shared__ uint8_t smem_raw[];
+  if (!seqlens_ok(p.cu, p.N, p.cu ? p.tokens : p.T, p.status)) return;
+  uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Small &S = *reinterpret_cast<Small *>(sm + OFF_SMALL);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // two passes that read the same rows run side by side (their second reads come from L2); a third follows
+  const int64_t unit = blockIdx.x;
+  const int side = passes < 2 ? 1 : 2;
+  const int pi = unit < side * items ? (int)(unit % side) : 2;
+  const int64_t item = unit < side * items ? unit / side : unit - side * items;
+  const LaPass &q = p.pass[pi];
+  const int64_t hv = item % p.HV, slot = item / p.HV;
+  if (p.mode == kWhole && slot >= p.N) return;  // no sequences: the block has checked cu_seqlens
+  const bool bw = q.backwards, states = p.mode == kStates;
+  const Segment s = segment_of(p, slot, bw);
+  if (!s.some || (states && s.last)) return;  // nobody reads the state behind the last segment
+  const int Da = q.a.D, Dc = q.c.D, ka = Da > 64 ? 2 : 1, kc = Dc > 64 ? 2 : 1;
+  const int64_t len = s.eos - s.bos;
+  const int nch = (int)((len + C - 1) / C);
+  const float g = p.g[hv];
+  auto chunk_start = [&](int c) { return s.bos + (int64_t)(bw ? nch - 1 - c : c) * C; };
+  auto chunk_rows = [&](int64_t t0) { return (int)(s.eos - t0 < C ? s.eos - t0 : C); };
+
+  if (tid < C + 1) S.pw[tid] = decay_power(g, tid);
+  if (tid == 0) {
+    S.err = 0;
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&S.full[i]), 1);
+      mbar_init(smem_u32(&S.empty[i]), 1);
+    }
+    for (uint64_t *b = &S.b_sc; b <= &S.b_final; ++b) mbar_init(smem_u32(b), 1);
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(&S.tmem_slot), TM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = S.tmem_slot;
+  volatile int *err = &S.err;
+  constexpr uint64_t tmo = 1ull << 32;  // cycles
+  uint8_t *const sLo = sm + OFF_LO, *const sP = sm + OFF_P, *const sY = sm + OFF_Y;
+  const uint32_t lane_addr = tbase + ((uint32_t)((warp & 3) * 32) << 16);
+  const int gt = tid & 127;  // thread of a group of four warps
+  // one thread polls; the others sleep in the named barrier that shares its verdict
+  auto vote_wait = [&](int id, uint64_t *bar, uint32_t parity) -> bool {
+    const bool ok = gt == 0 ? mbar_wait(smem_u32(bar), parity, err, tmo) : true;
+    return named_bar_and(id, 128, ok);
+  };
+
+  if (warp < 4) {
+    // ================================================================ state
+    const int j = gt;  // TMEM lane: channel of c
+    const int64_t head = (p.mode == kWhole ? s.n : slot) * p.HV + hv;
+    const float *from = states || !q.s_in || j >= Dc ? nullptr : q.s_in + head * p.KV + j * q.sj;
+    float *to = q.s_out && (states || s.last) && j < Dc
+                    ? q.s_out + ((states ? slot : s.n) * p.HV + hv) * p.KV + j * q.sj
+                    : nullptr;
+    bool ok = true;
+    for (int c = 0; c < nch; ++c) {
+      if (c > 0 && !(ok = vote_wait(kBarState, &S.b_state, (c - 1) & 1))) break;
+      tc_fence_after();
+      const float less1 = decay_less1(g, chunk_rows(chunk_start(c)));
+#pragma unroll 1
+      for (int i0 = 0; i0 < 64 * ka; i0 += 32) {
+        float r[32];
+        if (c > 0) {
+          tmem_ld32(lane_addr + TM_S + i0, r);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[i] = from && i0 + i < Da ? from[(int64_t)(i0 + i) * q.si] : 0.f;
+        }
+        uint32_t u[16], d[32];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) u[i] = gdr::pack_bf16(r[2 * i], r[2 * i + 1]);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) d[i] = __float_as_uint(fmaf(r[i], less1, r[i]));
+        if (!states) tmem_st16u(lane_addr + TM_SB + i0 / 2, u);
+        tmem_st32(lane_addr + TM_S + i0, d);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      named_bar(kBarState, 128);
+      if (gt == 0) mbar_arrive(smem_u32(&S.b_st));
+    }
+    if (ok && nch > 0) ok = vote_wait(kBarState, &S.b_state, (nch - 1) & 1);
+    if (named_bar_and(kBarState, 128, ok && *err == 0)) {
+      tc_fence_after();
+#pragma unroll 1
+      for (int i0 = 0; i0 < 64 * ka; i0 += 32) {
+        float r[32];
+        if (nch > 0) {
+          tmem_ld32(lane_addr + TM_S + i0, r);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[i] = from && i0 + i < Da ? from[(int64_t)(i0 + i) * q.si] : 0.f;
+        }
+        if (to) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (i0 + i < Da) to[(int64_t)(i0 + i) * q.si] = r[i];
+        }
+      }
+    }
+  } else if (warp < 8) {
+    // ================================================================ scores
+    const int w = warp - 4;
+    // this thread's scores: rows r0 and r0 + 8, columns 8 b + c0 and the next, b of 0 .. 7
+    const int r0 = 16 * w + (lane >> 2), c0 = 2 * (lane & 3);
+    float f[8][4];
+#pragma unroll
+    for (int b = 0; b < 8; ++b)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = r0 + 8 * (e >> 1), c = 8 * b + c0 + (e & 1);
+        f[b][e] = (bw ? c >= r : c <= r) ? S.pw[abs(r - c)] * q.pscale : 0.f;
+      }
+    // of B: a row and half of its channels
+    const int row = 16 * w + (lane & 15), half = lane >> 4;
+    const int panel = ka == 2 ? half : 0, ch0 = ka == 2 ? 0 : 4 * half, ch1 = ka == 2 ? 8 : ch0 + 4;
+    for (int c = 0; c < nch; ++c) {
+      const int st = c % kStages, buf = c & 1;
+      const int n = chunk_rows(chunk_start(c));
+      uint8_t *tile = sm + st * SZ_STAGE;
+      if (!vote_wait(kBarScore, &S.full[st], (c / kStages) & 1)) break;
+      if (n < C) {  // rows past the end may hold the next sequence
+        for (int i = gt; i < (C - n) * 8 * kc; i += 128)
+          st_sw128_chunk(tile + 2 * SZ_TILE + (kc == 2 && (i & 8) ? SZ_PANEL : 0), n + (kc == 2 ? i >> 4 : i >> 3), i & 7,
+                         make_uint4(0, 0, 0, 0));
+      }
+      // buffers of the chunk before the last: its MMAs are done
+      if (c > 1 && !vote_wait(kBarScore, &S.b_buf[buf], ((c >> 1) - 1) & 1)) break;
+      if (!states) {
+        if (!vote_wait(kBarScore, &S.b_sc, c & 1)) break;
+        tc_fence_after();
+        float r[4][8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld_16x256b_x2(lane_addr + TM_SC + 16 * i, r[i]);
+        tmem_ld_wait();
+        tc_fence_before();
+        uint8_t *P = sP + buf * SZ_PANEL;
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] = r[b >> 1][4 * (b & 1) + e] * f[b][e];
+            if (n < C && 8 * b + c0 + (e & 1) >= n) v[e] = 0.f;
+          }
+          *reinterpret_cast<uint32_t *>(P + sw128_chunk_off(r0, b) + 2 * c0) = gdr::pack_bf16(v[0], v[1]);
+          *reinterpret_cast<uint32_t *>(P + sw128_chunk_off(r0 + 8, b) + 2 * c0) = gdr::pack_bf16(v[2], v[3]);
+        }
+        fence_proxy_async_smem();
+        named_bar(kBarScore, 128);
+        if (gt == 0) mbar_arrive(smem_u32(&S.b_p[buf]));
+      }
+      // B' over B (the scores' product has read it), its lower half beside
+      const float wt = row < n ? S.pw[bw ? row + 1 : n - 1 - row] * q.wscale : 0.f;
+      uint8_t *hi = tile + SZ_TILE + panel * SZ_PANEL, *lo = sLo + buf * SZ_TILE + panel * SZ_PANEL;
+#pragma unroll 4
+      for (int ch = ch0; ch < ch1; ++ch) {
+        float v[8];
+        unpack8(ld_sw128_chunk(hi, row, ch), v);
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = row < n ? v[2 * e] * wt : 0.f, y = row < n ? v[2 * e + 1] * wt : 0.f;
+          h[e] = gdr::pack_bf16(x, y);
+          l[e] = gdr::pack_bf16(x - __uint_as_float(h[e] << 16), y - __uint_as_float(h[e] & 0xffff0000u));
+        }
+        st_sw128_chunk(hi, row, ch, make_uint4(h[0], h[1], h[2], h[3]));
+        st_sw128_chunk(lo, row, ch, make_uint4(l[0], l[1], l[2], l[3]));
+      }
+      fence_proxy_async_smem();
+      named_bar(kBarScore, 128);
+      if (gt == 0) mbar_arrive(smem_u32(&S.b_bs[buf]));
+    }
+  } else if (warp < 12) {
+    // ================================================================ output
+    const int w = warp - 8;
+    const int tok0 = 2 * (lane & 3);  // this thread's tokens: 8 b + tok0 and the next
+    float f[8][2];
+    int fn = 0;  // the rows that f is for
+    for (int c = 0; c < (states ? 0 : nch); ++c) {
+      const int buf = c & 1;
+      const int64_t t0 = chunk_start(c);
+      const int n = chunk_rows(t0);
+      if (n != fn) {
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int i = 8 * b + tok0 + e;
+            f[b][e] = i < n ? S.pw[bw ? n - 1 - i : i + 1] * q.iscale : 0.f;
+          }
+        fn = n;
+      }
+      const bool stage = n == C && !q.out_f32;
+      if (gt == 0) bulk_wait_read0();  // the last chunk's y has been read
+      if (!vote_wait(kBarOut, &S.b_o[buf], (c >> 1) & 1)) break;
+      tc_fence_after();
+      if (w < 2 * kc) {
+        const uint32_t o1 = lane_addr + TM_O + buf * 128, o2 = o1 + 64;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float x[4][8], y[4][8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            tmem_ld_16x256b_x2(o1 + ((16u * h) << 16) + 16 * i, x[i]);
+            tmem_ld_16x256b_x2(o2 + ((16u * h) << 16) + 16 * i, y[i]);
+          }
+          tmem_ld_wait();
+          // channels of this thread: d0 and d0 + 8
+          const int d0 = 32 * w + 16 * h + (lane >> 2);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[i][e] = fmaf(y[i][e], f[2 * i + (e >> 2)][e & 1], x[i][e]);
+            if (stage) {
+              // matrix m of four: channels 8 (m & 1), tokens 8 (m >> 1) of the 16 x 16 here; lane 8 m + r gives
+              // the address of token r of it
+              const int m = lane >> 3, tok = 16 * i + 8 * (m >> 1) + (lane & 7);
+              const int chunk = (32 * w + 16 * h + 8 * (m & 1)) >> 3;
+              const uint32_t at = smem_u32(sY + (chunk >> 3) * SZ_PANEL) + sw128_chunk_off(tok, chunk & 7);
+              stmatrix_x4_trans(at, gdr::pack_bf16(x[i][0], x[i][1]), gdr::pack_bf16(x[i][2], x[i][3]),
+                                gdr::pack_bf16(x[i][4], x[i][5]), gdr::pack_bf16(x[i][6], x[i][7]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int tok = 16 * i + 8 * (e >> 2) + tok0 + (e & 1), d = d0 + ((e >> 1) & 1) * 8;
+                if (tok < n && d < Dc) {
+                  const int64_t at = ((t0 + tok) * p.HV + hv) * Dc + d;
+                  if (q.out_f32) static_cast<float *>(q.out)[at] = x[i][e];
+                  else static_cast<__nv_bfloat16 *>(q.out)[at] = __float2bfloat16_rn(x[i][e]);
+                }
+              }
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      if (stage) fence_proxy_async_smem();
+      named_bar(kBarOut, 128);
+      if (gt == 0) {
+        mbar_arrive(smem_u32(&S.b_ofree[buf]));
+        if (stage) {
+          for (int i = 0; i < kc; ++i) tma_store_3d(&maps.y[pi], smem_u32(sY + i * SZ_PANEL), 64 * i, (int)hv, (int)t0);
+          bulk_commit();
+        }
+      }
+    }
+    if (gt == 0) bulk_wait0();  // every store has landed before the block can exit
+  } else if (warp == kProducer && lane == 0) {
+    // ================================================================ producer
+    const int ha = (int)(hv / q.a.group), hb = (int)(hv / q.b.group), hc = (int)(hv / q.c.group);
+    const uint32_t bytes = SZ_PANEL * ((states ? 0 : ka) + ka + kc);
+    int issued = 0;
+    for (int c = 0; c < nch; ++c) {
+      const int st = c % kStages;
+      if (c >= kStages && !mbar_wait(smem_u32(&S.empty[st]), (c / kStages - 1) & 1, err, tmo)) break;
+      const int t0 = (int)chunk_start(c);
+      const uint32_t tile = smem_u32(sm + st * SZ_STAGE), bar = smem_u32(&S.full[st]);
+      mbar_arrive_expect_tx(bar, bytes);
+      for (int i = 0; i < ka; ++i) {
+        if (!states) tma_load_3d(tile + i * SZ_PANEL, &maps.a[pi], 64 * i, ha, t0, bar);
+        tma_load_3d(tile + SZ_TILE + i * SZ_PANEL, &maps.b[pi], 64 * i, hb, t0, bar);
+      }
+      for (int i = 0; i < kc; ++i) tma_load_3d(tile + 2 * SZ_TILE + i * SZ_PANEL, &maps.c[pi], 64 * i, hc, t0, bar);
+      issued = c + 1;
+    }
+    // let every copy issued land before the block can exit
+    for (int c = issued > kStages ? issued - kStages : 0; c < issued; ++c)
+      mbar_wait_drain(smem_u32(&S.full[c % kStages]), (c / kStages) & 1, tmo);
+  } else if (warp == kMma && lane == 0) {
+    // ================================================================ MMA issuer
+    constexpr uint32_t id_sc = idesc_bf16(64, 64, 0, 0), id_o1 = idesc_bf16(128, 64, 1, 0),
+                       id_o2 = idesc_bf16(128, 64, 0, 0);
+    const uint32_t id_s = idesc_bf16(128, 64 * ka, 1, 1);
+    auto wt = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_spin(smem_u32(bar), parity, err, tmo); };
+    // an operand at base + off has the base's descriptor plus off / 16 in its address field
+    auto at = [](uint64_t base, uint32_t off) { return base + (uint64_t)(off >> 4); };
+    const uint32_t t0 = smem_u32(sm);
+    const uint64_t dk = smem_desc(t0, 16, 1024), dmn = smem_desc(t0, SZ_PANEL, 1024);
+    auto issue_sc = [&](int c) {
+      const uint32_t off = (c % kStages) * SZ_STAGE;
+      for (int ks = 0; ks < 4 * ka; ++ks) {
+        const uint32_t k = off + (ks >> 2) * SZ_PANEL + (ks & 3) * 32;
+        mma_bf16(tbase + TM_SC, at(dk, k), at(dk, k + SZ_TILE), id_sc, ks > 0);
+      }
+      mma_commit(smem_u32(&S.b_sc));
+    };
+    int scored = 0;  // chunks whose scores have been issued
+    if (!states && nch > 0 && wt(&S.full[0], 0)) {
+      tc_fence_after();
+      issue_sc(0);
+      scored = 1;
+    }
+    for (int c = 0; c < nch; ++c) {
+      const int st = c % kStages, buf = c & 1;
+      const uint32_t off = st * SZ_STAGE, o1 = tbase + TM_O + buf * 128;
+      if (!states) {
+        // (scores of chunk c are under way)
+        if (!(wt(&S.b_p[buf], (c >> 1) & 1) && (c < 2 || wt(&S.b_ofree[buf], ((c >> 1) - 1) & 1)))) break;
+        tc_fence_after();
+        // the next chunk's scores first where its rows have come (b_p says that these have been read)
+        if (c + 1 < nch && mbar_test_wait(smem_u32(&S.full[(c + 1) % kStages]), ((c + 1) / kStages) & 1)) {
+          issue_sc(c + 1);
+          scored = c + 2;
+        }
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          mma_bf16(o1, at(dmn, off + 2 * SZ_TILE + ks * 2048), at(dk, OFF_P + buf * SZ_PANEL + ks * 32), id_o1, ks > 0);
+        if (!wt(&S.b_st, c & 1)) break;
+        tc_fence_after();
+        for (int ks = 0; ks < 4 * ka; ++ks)
+          mma_bf16_ta(o1 + 64, tbase + TM_SB + 8 * ks, at(dk, off + (ks >> 2) * SZ_PANEL + (ks & 3) * 32), id_o2, ks > 0);
+        mma_commit(smem_u32(&S.b_o[buf]));
+      } else if (!(wt(&S.full[st], (c / kStages) & 1) && wt(&S.b_st, c & 1))) break;
+      if (!wt(&S.b_bs[buf], (c >> 1) & 1)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        const uint64_t a = at(dmn, off + 2 * SZ_TILE + ks * 2048);
+        mma_bf16(tbase + TM_S, a, at(dmn, off + SZ_TILE + ks * 2048), id_s, 1);
+        mma_bf16(tbase + TM_S, a, at(dmn, OFF_LO + buf * SZ_TILE + ks * 2048), id_s, 1);
+      }
+      mma_commit(smem_u32(&S.b_state));
+      mma_commit(smem_u32(&S.b_buf[buf]));
+      mma_commit(smem_u32(&S.empty[st]));
+      if (!states && c + 1 < nch && scored < c + 2) {
+        if (!wt(&S.full[(c + 1) % kStages], ((c + 1) / kStages) & 1)) break;
+        tc_fence_after();
+        issue_sc(c + 1);
+        scored = c + 2;
+      }
+    }
+    // wait for every MMA issued so far before the tensor memory is released
+    mma_commit(smem_u32(&S.b_final));
+    mbar_wait_drain(smem_u32(&S.b_final), 0, tmo);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tbase, TM_COLS);
+  if (tid == 0 && S.err) raise_status(p.status, GDR_ERR_TIMEOUT);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) == cudaSuccess &&
+        r == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// [tokens, heads, D] with tokens ld apart, in boxes of 64 channels of one head and 64 tokens; channels
+// from D on read as zeros and are not written.
+int make_map(CUtensorMap *m, const LaRows &r, int64_t heads, int64_t tokens) {
+  const auto fn = encode_fn();
+  if (!fn) return set_error(GDR_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const cuuint64_t dims[3] = {(cuuint64_t)r.D, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)r.D * 2, (cuuint64_t)r.ld * 2};
+  const cuuint32_t box[3] = {64, 1, 64}, es[3] = {1, 1, 1};
+  const CUresult e = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(r.p), dims, strides, box, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return e == CUDA_SUCCESS ? GDR_OK : set_error(GDR_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+}
+
+// What TMA can describe: 16-byte aligned bases, rows and heads.
+bool tma_ok(const LaRows &r) { return r.D <= 128 && r.D % 8 == 0 && r.ld % 8 == 0 && is_aligned16(r.p); }
+
+}  // namespace
+
+bool tc_takes(const LaArgs &p, int passes, int dtype) {
+  if (dtype != GDR_BF16 || p.tokens == 0 || p.N == 0) return false;
+  for (int i = 0; i < passes; ++i) {
+    const LaPass &q = p.pass[i];
+    if (!tma_ok(q.a) || !tma_ok(q.b) || !tma_ok(q.c) || !is_aligned16(q.out)) return false;
+  }
+  return true;
+}
+
+int launch_tc(const LaArgs &p, int passes, cudaStream_t st) {
+  Maps maps{};
+  for (int i = 0; i < passes; ++i) {
+    const LaPass &q = p.pass[i];
+    const LaRows y{q.out, p.HV * q.c.D, q.c.D, 1};
+    const auto map = [&](CUtensorMap *m, const LaRows &r) { return make_map(m, r, p.HV / r.group, p.tokens); };
+    int rc;
+    if ((rc = map(&maps.b[i], q.b)) != GDR_OK || (rc = map(&maps.c[i], q.c)) != GDR_OK) return rc;
+    if (p.mode == kStates) continue;
+    if ((rc = map(&maps.a[i], q.a)) != GDR_OK) return rc;
+    if (!q.out_f32 && (rc = map(&maps.y[i], y)) != GDR_OK) return rc;
+  }
+  const int64_t items = std::max<int64_t>(1, (p.mode == kWhole ? p.N : p.slots) * p.HV);
+  if (items * passes > 0x7fffffff) return set_error(GDR_ERR_SHAPE, "too many sequences and heads for one launch");
+  const cudaError_t e =
+      cudaFuncSetAttribute(la_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+  if (e != cudaSuccess) return cuda_error(e, "cudaFuncSetAttribute(la_tc_kernel)");
+  la_tc_kernel<<<(unsigned)(items * passes), kTcThreads, SMEM_BYTES, st>>>(maps, p, passes, items);
+  return launched("la_tc_kernel");
+}
 
 }  // namespace la
 }  // namespace gdr
