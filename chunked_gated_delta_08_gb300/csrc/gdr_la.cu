@@ -235,13 +235,16 @@ __global__ void __launch_bounds__(256) la_sum_kernel(const float *part0, const f
 }
 
 // -------------------------------------------------------------------------------- host side
-// Tokens in a segment, or 0 for none.  A block walks a sequence chunk by chunk; where
-// there are fewer blocks than multiprocessors the rest stand idle, and forming
-// segments' states takes half as much again.
+// Tokens in a segment, or 0 for none.  A block walks a sequence chunk by chunk, one block to a
+// multiprocessor.  Uncut, a launch takes as long as its waves of whole sequences; of a packed
+// batch the lengths are on the device, and one sequence may hold nearly all tokens.  Cut, the
+// work spreads evenly, but forming the segments' states takes half as much again.
 int64_t segment_length(const LaArgs &p, int blocks_per_pair) {
-  const int64_t pairs = p.N * p.HV * blocks_per_pair;
-  if (p.tokens <= 4 * C || p.N == 0 || pairs >= 2 * kSMs) return 0;
-  const int64_t want = std::max<int64_t>(1, cdiv(2 * kSMs, p.HV * blocks_per_pair));  // segments over all sequences
+  if (p.tokens <= 4 * C || p.N == 0) return 0;
+  const int64_t blocks = p.HV * blocks_per_pair;  // to a sequence
+  const int64_t uncut = p.cu ? p.tokens : cdiv(p.N * blocks, kSMs) * p.T;
+  if (3 * cdiv(p.tokens * blocks, kSMs) >= 2 * uncut) return 0;
+  const int64_t want = std::max<int64_t>(1, cdiv(2 * kSMs, blocks));  // segments over all sequences
   const int64_t L = std::max<int64_t>(4 * C, cdiv(cdiv(p.tokens, want), C) * C);
   return !p.cu && L >= p.T ? 0 : L;
 }

@@ -7,7 +7,8 @@
 //
 //   Sc   = A B^T                                    M=64  N=64   K=Da
 //   P_ij = pscale r^|i-j| Sc_ij  (j <= i; backwards j >= i), bf16
-//   B'_j = wscale r^w(j) B_j = hi + lo, two bf16    (2^-17 of each product; one would leave 2^-9 in the states)
+//   B'_j = wscale r^w(j) B_j = hi + lo, two bf16    (2^-17 of each product; hi alone, 2^-9, where no state leaves the
+//                                                    kernel: S is rounded to bf16 for y in any case)
 //   O1^T = C^T P^T                                  M=128 N=64   K=64
 //   O2^T = S^T A^T, S^T as bf16 in tensor memory    M=128 N=64   K=Da
 //   S^T  = S^T + (r^n - 1) S^T, then += C^T B'hi + C^T B'lo        M=128 N=Da K=64
@@ -16,15 +17,23 @@
 // Every factor is a power of r with an exponent that the place in the chunk gives, so
 // the threads keep them in registers; only a ragged last chunk works them out anew.
 //
-// Warp roles (448 threads):
-//   warps 0-3    state: the bf16 copy and the decay of the fp32 state in tensor memory
-//   warps 4-7    scores: P, B' (over B in place, its lower half beside), rows past a ragged end cleared
-//   warps 8-11   output: y through shared memory and a tensor store
-//   warp 12      producer: TMA loads into a ring of three stages
-//   warp 13      one thread issues every tcgen05.mma
-// Hand-offs are mbarriers with bounded waits (about two seconds); when one runs out
-// the block records GDR_ERR_TIMEOUT, lets its copies and MMAs finish, frees its tensor
-// memory and returns.
+// What follows one chunk after the other is the state alone: its decay and bf16 copy
+// (warps 0-7), then the update's MMAs.  An issuing thread stands still for some 200 cycles
+// at each burst of MMAs and each commit, so the three kinds have a thread each: one thread
+// for all of them was late for the update (3080 cycles a chunk, 2.7 us; see the end of the file).
+//
+// Warp roles (896 threads):
+//   warps 0-7    state: the decay of the fp32 state in tensor memory, its bf16 copy
+//   warps 8-15   scores: P, B' (over B in place, its lower half beside), rows past a ragged end cleared
+//   warps 16-23  output: y through shared memory and a tensor store
+//   warp 24      producer: TMA loads into a ring of three stages
+//   warp 25      issues the scores' MMAs
+//   warp 26      issues the state's
+//   warp 27      issues the outputs'
+// Hand-offs are mbarriers.  Every wait is bounded (about two seconds): where one runs out
+// the block's error flag makes all others return at once, the producer and the MMA thread
+// stop, the rest run to their end on what is there (in bounds), the block lets its copies
+// and MMAs finish, frees its tensor memory and reports GDR_ERR_TIMEOUT.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -45,31 +54,63 @@ using fused::st_sw128_chunk;
 using fused::sw128_chunk_off;
 
 constexpr int kStages = 3;
-constexpr int kTcThreads = 448;
-constexpr int kProducer = 12, kMma = 13;
-constexpr int kBarState = 1, kBarScore = 2, kBarOut = 3;
+constexpr int kTcThreads = 896;
+constexpr int kProducer = 24, kScoreMma = 25, kStateMma = 26;  // and one more for the outputs' MMAs
+constexpr int kBarOut = 1;  // named barrier of the output warps
 
 // shared memory, from a 1024-byte aligned base; tiles are two panels of 64 rows x 64 channels
 constexpr uint32_t SZ_TILE = 16384, SZ_PANEL = 8192;
 constexpr uint32_t SZ_STAGE = 3 * SZ_TILE;  // A | B | C
 constexpr uint32_t OFF_LO = kStages * SZ_STAGE;   // lower halves of B', two buffers
 constexpr uint32_t OFF_P = OFF_LO + 2 * SZ_TILE;  // P, two buffers
-constexpr uint32_t OFF_Y = OFF_P + 2 * SZ_PANEL;  // y on its way out
-constexpr uint32_t OFF_SMALL = OFF_Y + SZ_TILE;
+constexpr uint32_t OFF_Y = OFF_P + 2 * SZ_PANEL;  // y on its way out, two buffers
+constexpr uint32_t OFF_SMALL = OFF_Y + 2 * SZ_TILE;
 
 // TMEM columns
-constexpr uint32_t TM_SC = 0, TM_O = 64 /* O1, O2, twice */, TM_S = 320, TM_SB = 448, TM_COLS = 512;
+constexpr uint32_t TM_SC = 0 /* twice */, TM_O = 128 /* O1, O2 */, TM_S = 256, TM_SB = 384 /* twice */, TM_COLS = 512;
 
 struct Small {
   float pw[C + 4];  // r^0 .. r^64
   uint64_t full[kStages], empty[kStages];
-  // single arrivals, one completion per chunk (or per second chunk where there are two)
-  uint64_t b_sc, b_p[2], b_bs[2], b_buf[2], b_st, b_state, b_o[2], b_ofree[2], b_final;
+  // (a stage is empty when its chunk's state and output MMAs are done, which frees P, B' and the bf16 state too)
+  uint64_t b_sc[2], b_state, b_o, b_final[3];  // MMAs done
+  uint64_t b_p[2], b_bs[2], b_s[2], b_ofree;   // arrivals of eight warps: P, B', state and its copy, O1 and O2 read
   uint32_t tmem_slot;
   int err;
 };
 constexpr uint32_t SMEM_BYTES = OFF_SMALL + sizeof(Small) + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+
+// One thread of a converged warp, in a form that the compiler knows to be one thread.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
+constexpr uint64_t kTimeout = 1ull << 32;  // cycles: about two seconds at the GB300's clocks
+
+// Waits for the phase of the given parity; returns without it once the block's error flag is set, which a wait
+// that runs out of time does.
+__device__ __forceinline__ void wait_or_err(uint32_t bar, uint32_t parity, volatile int *err) {
+  if (mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = clock64();
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+    if ((i & 15u) == 0) {
+      if (*err) return;
+      if ((uint64_t)clock64() - t0 > kTimeout) {
+        *err = 1;
+        return;
+      }
+    }
+  }
+}
+
+// Waits until at most N of the thread's bulk stores still read shared memory.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
 
 struct Maps {
   CUtensorMap a[3], b[3], c[3], y[3];
@@ -91,6 +132,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int64_t hv = item % p.HV, slot = item / p.HV;
   if (p.mode == kWhole && slot >= p.N) return;  // no sequences: the block has checked cu_seqlens
   const bool bw = q.backwards, states = p.mode == kStates;
+  const bool exact = q.s_out != nullptr;  // B' in two parts
   const Segment s = segment_of(p, slot, bw);
   if (!s.some || (states && s.last)) return;  // nobody reads the state behind the last segment
   const int Da = q.a.D, Dc = q.c.D, ka = Da > 64 ? 2 : 1, kc = Dc > 64 ? 2 : 1;
@@ -98,16 +140,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int nch = (int)((len + C - 1) / C);
   const float g = p.g[hv];
   auto chunk_start = [&](int c) { return s.bos + (int64_t)(bw ? nch - 1 - c : c) * C; };
-  auto chunk_rows = [&](int64_t t0) { return (int)(s.eos - t0 < C ? s.eos - t0 : C); };
+  const int ragged = bw ? 0 : nch - 1, rest = (int)(len - (int64_t)(nch - 1) * C);  // the sequence's last chunk, its rows
+  auto chunk_rows = [&](int c) { return c == ragged ? rest : C; };
 
   if (tid < C + 1) S.pw[tid] = decay_power(g, tid);
   if (tid == 0) {
     S.err = 0;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&S.full[i]), 1);
-      mbar_init(smem_u32(&S.empty[i]), 1);
+      mbar_init(smem_u32(&S.empty[i]), p.mode == kStates ? 1 : 2);
     }
-    for (uint64_t *b = &S.b_sc; b <= &S.b_final; ++b) mbar_init(smem_u32(b), 1);
+    for (uint64_t *b = S.b_sc; b <= &S.b_final[2]; ++b) mbar_init(smem_u32(b), 1);
+    for (uint64_t *b = S.b_p; b <= &S.b_ofree; ++b) mbar_init(smem_u32(b), 8);
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -119,228 +163,246 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_after();
   const uint32_t tbase = S.tmem_slot;
   volatile int *err = &S.err;
-  constexpr uint64_t tmo = 1ull << 32;  // cycles
   uint8_t *const sLo = sm + OFF_LO, *const sP = sm + OFF_P, *const sY = sm + OFF_Y;
   const uint32_t lane_addr = tbase + ((uint32_t)((warp & 3) * 32) << 16);
-  const int gt = tid & 127;  // thread of a group of four warps
-  // one thread polls; the others sleep in the named barrier that shares its verdict
-  auto vote_wait = [&](int id, uint64_t *bar, uint32_t parity) -> bool {
-    const bool ok = gt == 0 ? mbar_wait(smem_u32(bar), parity, err, tmo) : true;
-    return named_bar_and(id, 128, ok);
+  auto wait = [&](uint64_t &bar, uint32_t parity) { wait_or_err(smem_u32(&bar), parity, err); };
+  // the same without sleeping, for single threads (eight warps of the state group polling took 7 % longer)
+  auto spin = [&](uint64_t &bar, uint32_t parity) { mbar_wait_spin(smem_u32(&bar), parity, err, kTimeout); };
+  auto arrive = [&](uint64_t &bar) {  // of a warp
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bar));
   };
 
-  if (warp < 4) {
+  if (warp < 8) {
     // ================================================================ state
-    const int j = gt;  // TMEM lane: channel of c
-    const int64_t head = (p.mode == kWhole ? s.n : slot) * p.HV + hv;
-    const float *from = states || !q.s_in || j >= Dc ? nullptr : q.s_in + head * p.KV + j * q.sj;
-    float *to = q.s_out && (states || s.last) && j < Dc
-                    ? q.s_out + ((states ? slot : s.n) * p.HV + hv) * p.KV + j * q.sj
-                    : nullptr;
-    bool ok = true;
-    for (int c = 0; c < nch; ++c) {
-      if (c > 0 && !(ok = vote_wait(kBarState, &S.b_state, (c - 1) & 1))) break;
-      tc_fence_after();
-      const float less1 = decay_less1(g, chunk_rows(chunk_start(c)));
+    const int j = 32 * (warp & 3) + lane;                 // TMEM lane: channel of c
+    const int cols = 32 * ka, col0 = (warp >> 2) * cols;  // this thread's channels of a
+    const uint32_t aS = lane_addr + TM_S + col0, aSb = lane_addr + TM_SB + col0 / 2;
+    const bool mine = j < Dc;
+    {
+      const float *from = states || !q.s_in || !mine
+                              ? nullptr
+                              : q.s_in + ((p.mode == kWhole ? s.n : slot) * p.HV + hv) * p.KV + j * q.sj;
 #pragma unroll 1
-      for (int i0 = 0; i0 < 64 * ka; i0 += 32) {
-        float r[32];
-        if (c > 0) {
-          tmem_ld32(lane_addr + TM_S + i0, r);
+      for (int i0 = 0; i0 < cols; i0 += 16) {
+        float r[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) r[i] = from && col0 + i0 + i < Da ? from[(int64_t)(col0 + i0 + i) * q.si] : 0.f;
+        tmem_st16(aS + i0, r);
+      }
+    }
+    tmem_st_wait();
+    const float whole1 = decay_less1(g, C);
+#pragma unroll 1
+    for (int c = 0; c < nch; ++c) {
+      const int n = chunk_rows(c);
+      const float less1 = n == C ? whole1 : decay_less1(g, n);
+      if (c > 0) wait(S.b_state, (c - 1) & 1);
+      if (c > 1) wait(S.empty[(c - 2) % kStages], ((c - 2) / kStages) & 1);  // O2 has read the copy of two chunks before
+      tc_fence_after();
+#pragma unroll
+      for (int i0 = 0; i0 < 64; i0 += 32) {
+        if (i0 < cols) {
+          float r[32];
+          tmem_ld32(aS + i0, r);
           tmem_ld_wait();
-        } else {
+          uint32_t u[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) r[i] = from && i0 + i < Da ? from[(int64_t)(i0 + i) * q.si] : 0.f;
+          for (int i = 0; i < 16; ++i) u[i] = gdr::pack_bf16(r[2 * i], r[2 * i + 1]);
+          if (!states) tmem_st16u(aSb + (c & 1) * 64 + i0 / 2, u);
+          uint32_t d[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) d[i] = __float_as_uint(fmaf(r[i], less1, r[i]));
+          tmem_st32(aS + i0, d);
         }
-        uint32_t u[16], d[32];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) u[i] = gdr::pack_bf16(r[2 * i], r[2 * i + 1]);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) d[i] = __float_as_uint(fmaf(r[i], less1, r[i]));
-        if (!states) tmem_st16u(lane_addr + TM_SB + i0 / 2, u);
-        tmem_st32(lane_addr + TM_S + i0, d);
       }
       tmem_st_wait();
       tc_fence_before();
-      named_bar(kBarState, 128);
-      if (gt == 0) mbar_arrive(smem_u32(&S.b_st));
+      arrive(S.b_s[c & 1]);
     }
-    if (ok && nch > 0) ok = vote_wait(kBarState, &S.b_state, (nch - 1) & 1);
-    if (named_bar_and(kBarState, 128, ok && *err == 0)) {
-      tc_fence_after();
+    if (nch > 0) wait(S.b_state, (nch - 1) & 1);
+    tc_fence_after();
+    if (q.s_out && (states || s.last)) {
+      float *to = q.s_out + ((states ? slot : s.n) * p.HV + hv) * p.KV + j * q.sj;
 #pragma unroll 1
-      for (int i0 = 0; i0 < 64 * ka; i0 += 32) {
-        float r[32];
-        if (nch > 0) {
-          tmem_ld32(lane_addr + TM_S + i0, r);
-          tmem_ld_wait();
-        } else {
+      for (int i0 = 0; i0 < cols; i0 += 16) {
+        float r[16];
+        tmem_ld16(aS + i0, r);
+        tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) r[i] = from && i0 + i < Da ? from[(int64_t)(i0 + i) * q.si] : 0.f;
-        }
-        if (to) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (i0 + i < Da) to[(int64_t)(i0 + i) * q.si] = r[i];
-        }
+        for (int i = 0; i < 16; ++i)
+          if (mine && col0 + i0 + i < Da) to[(int64_t)(col0 + i0 + i) * q.si] = r[i];
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < 16) {
     // ================================================================ scores
-    const int w = warp - 4;
-    // this thread's scores: rows r0 and r0 + 8, columns 8 b + c0 and the next, b of 0 .. 7
+    const int gt = tid - 256, w = warp & 3, half = (warp - 8) >> 2;
+    // this thread's scores: rows r0 and r0 + 8, columns 32 half + 8 b + c0 and the next, b of 0 .. 3
     const int r0 = 16 * w + (lane >> 2), c0 = 2 * (lane & 3);
-    float f[8][4];
+    float f[4][4];
 #pragma unroll
-    for (int b = 0; b < 8; ++b)
+    for (int b = 0; b < 4; ++b)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int r = r0 + 8 * (e >> 1), c = 8 * b + c0 + (e & 1);
+        const int r = r0 + 8 * (e >> 1), c = 32 * half + 8 * b + c0 + (e & 1);
         f[b][e] = (bw ? c >= r : c <= r) ? S.pw[abs(r - c)] * q.pscale : 0.f;
       }
-    // of B: a row and half of its channels
-    const int row = 16 * w + (lane & 15), half = lane >> 4;
-    const int panel = ka == 2 ? half : 0, ch0 = ka == 2 ? 0 : 4 * half, ch1 = ka == 2 ? 8 : ch0 + 4;
+    // of B: a row and a quarter of its channels
+    const int row = 16 * w + (lane & 15), part = 2 * half + (lane >> 4);
+    const int panel = ka == 2 ? part >> 1 : 0, ch0 = ka == 2 ? 4 * (part & 1) : 2 * part, chunks = 2 * ka;
+    const float whole_wt = S.pw[bw ? row + 1 : C - 1 - row] * q.wscale, wscale = q.wscale;
+#pragma unroll 1
     for (int c = 0; c < nch; ++c) {
       const int st = c % kStages, buf = c & 1;
-      const int n = chunk_rows(chunk_start(c));
+      const int n = chunk_rows(c);
       uint8_t *tile = sm + st * SZ_STAGE;
-      if (!vote_wait(kBarScore, &S.full[st], (c / kStages) & 1)) break;
+      wait(S.full[st], (c / kStages) & 1);
       if (n < C) {  // rows past the end may hold the next sequence
-        for (int i = gt; i < (C - n) * 8 * kc; i += 128)
+        for (int i = gt; i < (C - n) * 8 * kc; i += 256)
           st_sw128_chunk(tile + 2 * SZ_TILE + (kc == 2 && (i & 8) ? SZ_PANEL : 0), n + (kc == 2 ? i >> 4 : i >> 3), i & 7,
                          make_uint4(0, 0, 0, 0));
       }
-      // buffers of the chunk before the last: its MMAs are done
-      if (c > 1 && !vote_wait(kBarScore, &S.b_buf[buf], ((c >> 1) - 1) & 1)) break;
+      if (c > 1) wait(S.empty[(c - 2) % kStages], ((c - 2) / kStages) & 1);  // the buffers' chunk before is done
       if (!states) {
-        if (!vote_wait(kBarScore, &S.b_sc, c & 1)) break;
+        wait(S.b_sc[buf], (c >> 1) & 1);
         tc_fence_after();
-        float r[4][8];
+        float r[2][8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld_16x256b_x2(lane_addr + TM_SC + 16 * i, r[i]);
+        for (int i = 0; i < 2; ++i) tmem_ld_16x256b_x2(lane_addr + TM_SC + 64 * buf + 32 * half + 16 * i, r[i]);
         tmem_ld_wait();
         tc_fence_before();
         uint8_t *P = sP + buf * SZ_PANEL;
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
+        for (int b = 0; b < 4; ++b) {
           float v[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             v[e] = r[b >> 1][4 * (b & 1) + e] * f[b][e];
-            if (n < C && 8 * b + c0 + (e & 1) >= n) v[e] = 0.f;
+            if (n < C && 32 * half + 8 * b + c0 + (e & 1) >= n) v[e] = 0.f;
           }
-          *reinterpret_cast<uint32_t *>(P + sw128_chunk_off(r0, b) + 2 * c0) = gdr::pack_bf16(v[0], v[1]);
-          *reinterpret_cast<uint32_t *>(P + sw128_chunk_off(r0 + 8, b) + 2 * c0) = gdr::pack_bf16(v[2], v[3]);
+          *reinterpret_cast<uint32_t *>(P + sw128_chunk_off(r0, 4 * half + b) + 2 * c0) = gdr::pack_bf16(v[0], v[1]);
+          *reinterpret_cast<uint32_t *>(P + sw128_chunk_off(r0 + 8, 4 * half + b) + 2 * c0) = gdr::pack_bf16(v[2], v[3]);
         }
         fence_proxy_async_smem();
-        named_bar(kBarScore, 128);
-        if (gt == 0) mbar_arrive(smem_u32(&S.b_p[buf]));
+        arrive(S.b_p[buf]);
       }
       // B' over B (the scores' product has read it), its lower half beside
-      const float wt = row < n ? S.pw[bw ? row + 1 : n - 1 - row] * q.wscale : 0.f;
+      const float wt = n == C ? whole_wt : row < n ? S.pw[bw ? row + 1 : n - 1 - row] * wscale : 0.f;
       uint8_t *hi = tile + SZ_TILE + panel * SZ_PANEL, *lo = sLo + buf * SZ_TILE + panel * SZ_PANEL;
-#pragma unroll 4
-      for (int ch = ch0; ch < ch1; ++ch) {
-        float v[8];
-        unpack8(ld_sw128_chunk(hi, row, ch), v);
-        uint32_t h[4], l[4];
+      uint4 in[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = row < n ? v[2 * e] * wt : 0.f, y = row < n ? v[2 * e + 1] * wt : 0.f;
-          h[e] = gdr::pack_bf16(x, y);
-          l[e] = gdr::pack_bf16(x - __uint_as_float(h[e] << 16), y - __uint_as_float(h[e] & 0xffff0000u));
+      for (int i = 0; i < 4; ++i)
+        if (i < chunks) in[i] = row < n ? ld_sw128_chunk(hi, row, ch0 + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i < chunks) {
+          float v[8];
+          unpack8(in[i], v);
+          uint32_t h[4], l[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = v[2 * e] * wt, y = v[2 * e + 1] * wt;
+            h[e] = gdr::pack_bf16(x, y);
+            l[e] = gdr::pack_bf16(x - __uint_as_float(h[e] << 16), y - __uint_as_float(h[e] & 0xffff0000u));
+          }
+          st_sw128_chunk(hi, row, ch0 + i, make_uint4(h[0], h[1], h[2], h[3]));
+          if (exact) st_sw128_chunk(lo, row, ch0 + i, make_uint4(l[0], l[1], l[2], l[3]));
         }
-        st_sw128_chunk(hi, row, ch, make_uint4(h[0], h[1], h[2], h[3]));
-        st_sw128_chunk(lo, row, ch, make_uint4(l[0], l[1], l[2], l[3]));
       }
       fence_proxy_async_smem();
-      named_bar(kBarScore, 128);
-      if (gt == 0) mbar_arrive(smem_u32(&S.b_bs[buf]));
+      arrive(S.b_bs[buf]);
     }
-  } else if (warp < 12) {
+  } else if (warp < 24) {
     // ================================================================ output
-    const int w = warp - 8;
-    const int tok0 = 2 * (lane & 3);  // this thread's tokens: 8 b + tok0 and the next
-    float f[8][2];
+    const int gt = tid - 512, w = warp & 3, half = (warp - 16) >> 2;
+    const int tok0 = 32 * half + 2 * (lane & 3);  // this thread's tokens: tok0 + 8 b and the next, b of 0 .. 3
+    // matrix m of a transposed store of four: channels 8 (m & 1), tokens 8 (m >> 1) of 16 x 16; lane 8 m + r gives the
+    // address of token r of it
+    const int m = lane >> 3, stok = 32 * half + 8 * (m >> 1) + (lane & 7);
+    float f[4][2];
     int fn = 0;  // the rows that f is for
+#pragma unroll 1
     for (int c = 0; c < (states ? 0 : nch); ++c) {
       const int buf = c & 1;
-      const int64_t t0 = chunk_start(c);
-      const int n = chunk_rows(t0);
+      const int n = chunk_rows(c);
       if (n != fn) {
 #pragma unroll
-        for (int b = 0; b < 8; ++b)
+        for (int b = 0; b < 4; ++b)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int i = 8 * b + tok0 + e;
+            const int i = tok0 + 8 * b + e;
             f[b][e] = i < n ? S.pw[bw ? n - 1 - i : i + 1] * q.iscale : 0.f;
           }
         fn = n;
       }
       const bool stage = n == C && !q.out_f32;
-      if (gt == 0) bulk_wait_read0();  // the last chunk's y has been read
-      if (!vote_wait(kBarOut, &S.b_o[buf], (c >> 1) & 1)) break;
+      if (gt == 0) bulk_wait_read<1>();  // the store before the last has read its buffer
+      named_bar(kBarOut, 256);
+      wait(S.b_o, c & 1);
       tc_fence_after();
-      if (w < 2 * kc) {
-        const uint32_t o1 = lane_addr + TM_O + buf * 128, o2 = o1 + 64;
+      const uint32_t o1 = lane_addr + TM_O + 32 * half, o2 = o1 + 64;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float x[4][8], y[4][8];
+      for (int h = 0; h < 2; ++h) {
+        float x[2][8], y[2][8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            tmem_ld_16x256b_x2(o1 + ((16u * h) << 16) + 16 * i, x[i]);
-            tmem_ld_16x256b_x2(o2 + ((16u * h) << 16) + 16 * i, y[i]);
-          }
-          tmem_ld_wait();
+        for (int i = 0; i < 2; ++i) {
+          tmem_ld_16x256b_x2(o1 + ((16u * h) << 16) + 16 * i, x[i]);
+          tmem_ld_16x256b_x2(o2 + ((16u * h) << 16) + 16 * i, y[i]);
+        }
+        tmem_ld_wait();
+        if (h == 1) {
+          tc_fence_before();
+          arrive(S.b_ofree);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[i][e] = fmaf(y[i][e], f[2 * i + (e >> 2)][e & 1], x[i][e]);
+        if (w >= 2 * kc) continue;
+        if (stage) {
+          const int chunk = (32 * w + 16 * h + 8 * (m & 1)) >> 3;
+          const uint32_t at = smem_u32(sY + buf * SZ_TILE + (chunk >> 3) * SZ_PANEL) + sw128_chunk_off(stok, chunk & 7);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            stmatrix_x4_trans(at + i * 2048, gdr::pack_bf16(x[i][0], x[i][1]), gdr::pack_bf16(x[i][2], x[i][3]),
+                              gdr::pack_bf16(x[i][4], x[i][5]), gdr::pack_bf16(x[i][6], x[i][7]));
+        } else {
           // channels of this thread: d0 and d0 + 8
           const int d0 = 32 * w + 16 * h + (lane >> 2);
+          const int64_t t0 = chunk_start(c);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[i][e] = fmaf(y[i][e], f[2 * i + (e >> 2)][e & 1], x[i][e]);
-            if (stage) {
-              // matrix m of four: channels 8 (m & 1), tokens 8 (m >> 1) of the 16 x 16 here; lane 8 m + r gives
-              // the address of token r of it
-              const int m = lane >> 3, tok = 16 * i + 8 * (m >> 1) + (lane & 7);
-              const int chunk = (32 * w + 16 * h + 8 * (m & 1)) >> 3;
-              const uint32_t at = smem_u32(sY + (chunk >> 3) * SZ_PANEL) + sw128_chunk_off(tok, chunk & 7);
-              stmatrix_x4_trans(at, gdr::pack_bf16(x[i][0], x[i][1]), gdr::pack_bf16(x[i][2], x[i][3]),
-                                gdr::pack_bf16(x[i][4], x[i][5]), gdr::pack_bf16(x[i][6], x[i][7]));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int tok = 16 * i + 8 * (e >> 2) + tok0 + (e & 1), d = d0 + ((e >> 1) & 1) * 8;
-                if (tok < n && d < Dc) {
-                  const int64_t at = ((t0 + tok) * p.HV + hv) * Dc + d;
-                  if (q.out_f32) static_cast<float *>(q.out)[at] = x[i][e];
-                  else static_cast<__nv_bfloat16 *>(q.out)[at] = __float2bfloat16_rn(x[i][e]);
-                }
+            for (int e = 0; e < 8; ++e) {
+              const int tok = tok0 + 16 * i + 8 * (e >> 2) + (e & 1), d = d0 + ((e >> 1) & 1) * 8;
+              if (tok < n && d < Dc) {
+                const int64_t at = ((t0 + tok) * p.HV + hv) * Dc + d;
+                if (q.out_f32) static_cast<float *>(q.out)[at] = x[i][e];
+                else static_cast<__nv_bfloat16 *>(q.out)[at] = __float2bfloat16_rn(x[i][e]);
               }
             }
-          }
         }
       }
-      tc_fence_before();
       if (stage) fence_proxy_async_smem();
-      named_bar(kBarOut, 128);
+      named_bar(kBarOut, 256);
       if (gt == 0) {
-        mbar_arrive(smem_u32(&S.b_ofree[buf]));
         if (stage) {
-          for (int i = 0; i < kc; ++i) tma_store_3d(&maps.y[pi], smem_u32(sY + i * SZ_PANEL), 64 * i, (int)hv, (int)t0);
-          bulk_commit();
+          for (int i = 0; i < kc; ++i)
+            tma_store_3d(&maps.y[pi], smem_u32(sY + buf * SZ_TILE + i * SZ_PANEL), 64 * i, (int)hv, (int)chunk_start(c));
         }
+        bulk_commit();  // one group a chunk, where nothing is staged an empty one
       }
     }
     if (gt == 0) bulk_wait0();  // every store has landed before the block can exit
-  } else if (warp == kProducer && lane == 0) {
+  } else if (warp == kProducer && elect_one()) {
     // ================================================================ producer
     const int ha = (int)(hv / q.a.group), hb = (int)(hv / q.b.group), hc = (int)(hv / q.c.group);
     const uint32_t bytes = SZ_PANEL * ((states ? 0 : ka) + ka + kc);
     int issued = 0;
     for (int c = 0; c < nch; ++c) {
       const int st = c % kStages;
-      if (c >= kStages && !mbar_wait(smem_u32(&S.empty[st]), (c / kStages - 1) & 1, err, tmo)) break;
+      if (c >= kStages) wait(S.empty[st], (c / kStages - 1) & 1);
+      if (*err) break;
       const int t0 = (int)chunk_start(c);
       const uint32_t tile = smem_u32(sm + st * SZ_STAGE), bar = smem_u32(&S.full[st]);
       mbar_arrive_expect_tx(bar, bytes);
@@ -353,73 +415,70 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     // let every copy issued land before the block can exit
     for (int c = issued > kStages ? issued - kStages : 0; c < issued; ++c)
-      mbar_wait_drain(smem_u32(&S.full[c % kStages]), (c / kStages) & 1, tmo);
-  } else if (warp == kMma && lane == 0) {
-    // ================================================================ MMA issuer
+      mbar_wait_drain(smem_u32(&S.full[c % kStages]), (c / kStages) & 1, kTimeout);
+  } else if (warp >= kScoreMma && elect_one()) {
+    // ================================================================ MMA issuers
     constexpr uint32_t id_sc = idesc_bf16(64, 64, 0, 0), id_o1 = idesc_bf16(128, 64, 1, 0),
                        id_o2 = idesc_bf16(128, 64, 0, 0);
     const uint32_t id_s = idesc_bf16(128, 64 * ka, 1, 1);
-    auto wt = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_spin(smem_u32(bar), parity, err, tmo); };
     // an operand at base + off has the base's descriptor plus off / 16 in its address field
     auto at = [](uint64_t base, uint32_t off) { return base + (uint64_t)(off >> 4); };
     const uint32_t t0 = smem_u32(sm);
     const uint64_t dk = smem_desc(t0, 16, 1024), dmn = smem_desc(t0, SZ_PANEL, 1024);
-    auto issue_sc = [&](int c) {
-      const uint32_t off = (c % kStages) * SZ_STAGE;
-      for (int ks = 0; ks < 4 * ka; ++ks) {
-        const uint32_t k = off + (ks >> 2) * SZ_PANEL + (ks & 3) * 32;
-        mma_bf16(tbase + TM_SC, at(dk, k), at(dk, k + SZ_TILE), id_sc, ks > 0);
-      }
-      mma_commit(smem_u32(&S.b_sc));
-    };
-    int scored = 0;  // chunks whose scores have been issued
-    if (!states && nch > 0 && wt(&S.full[0], 0)) {
-      tc_fence_after();
-      issue_sc(0);
-      scored = 1;
-    }
-    for (int c = 0; c < nch; ++c) {
+    const int last = states && warp != kStateMma ? 0 : nch;
+#pragma unroll 1
+    for (int c = 0; c < last; ++c) {
       const int st = c % kStages, buf = c & 1;
-      const uint32_t off = st * SZ_STAGE, o1 = tbase + TM_O + buf * 128;
-      if (!states) {
-        // (scores of chunk c are under way)
-        if (!(wt(&S.b_p[buf], (c >> 1) & 1) && (c < 2 || wt(&S.b_ofree[buf], ((c >> 1) - 1) & 1)))) break;
+      const uint32_t ph = (c >> 1) & 1, off = st * SZ_STAGE;
+      spin(S.full[st], (c / kStages) & 1);
+      if (warp == kScoreMma) {
+        if (c > 1) spin(S.b_p[buf], ((c >> 1) - 1) & 1);  // the scores of two chunks before have been read
+        if (*err) break;
         tc_fence_after();
-        // the next chunk's scores first where its rows have come (b_p says that these have been read)
-        if (c + 1 < nch && mbar_test_wait(smem_u32(&S.full[(c + 1) % kStages]), ((c + 1) / kStages) & 1)) {
-          issue_sc(c + 1);
-          scored = c + 2;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+          const uint32_t k = off + (ks >> 2) * SZ_PANEL + (ks & 3) * 32;
+          if (ks < 4 * ka) mma_bf16(tbase + TM_SC + 64 * buf, at(dk, k), at(dk, k + SZ_TILE), id_sc, ks > 0);
         }
+        mma_commit(smem_u32(&S.b_sc[buf]));
+      } else if (warp == kStateMma) {
+        spin(S.b_bs[buf], ph);
+        spin(S.b_s[buf], ph);
+        if (*err) break;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          const uint64_t a = at(dmn, off + 2 * SZ_TILE + ks * 2048);
+          mma_bf16(tbase + TM_S, a, at(dmn, off + SZ_TILE + ks * 2048), id_s, 1);
+          if (exact) mma_bf16(tbase + TM_S, a, at(dmn, OFF_LO + buf * SZ_TILE + ks * 2048), id_s, 1);
+        }
+        mma_commit(smem_u32(&S.b_state));
+        mma_commit(smem_u32(&S.empty[st]));
+      } else {
+        spin(S.b_p[buf], ph);
+        if (c > 0) spin(S.b_ofree, (c - 1) & 1);
+        if (*err) break;
+        tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          mma_bf16(o1, at(dmn, off + 2 * SZ_TILE + ks * 2048), at(dk, OFF_P + buf * SZ_PANEL + ks * 32), id_o1, ks > 0);
-        if (!wt(&S.b_st, c & 1)) break;
+          mma_bf16(tbase + TM_O, at(dmn, off + 2 * SZ_TILE + ks * 2048), at(dk, OFF_P + buf * SZ_PANEL + ks * 32), id_o1,
+                   ks > 0);
+        spin(S.b_s[buf], ph);
+        if (*err) break;
         tc_fence_after();
-        for (int ks = 0; ks < 4 * ka; ++ks)
-          mma_bf16_ta(o1 + 64, tbase + TM_SB + 8 * ks, at(dk, off + (ks >> 2) * SZ_PANEL + (ks & 3) * 32), id_o2, ks > 0);
-        mma_commit(smem_u32(&S.b_o[buf]));
-      } else if (!(wt(&S.full[st], (c / kStages) & 1) && wt(&S.b_st, c & 1))) break;
-      if (!wt(&S.b_bs[buf], (c >> 1) & 1)) break;
-      tc_fence_after();
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        const uint64_t a = at(dmn, off + 2 * SZ_TILE + ks * 2048);
-        mma_bf16(tbase + TM_S, a, at(dmn, off + SZ_TILE + ks * 2048), id_s, 1);
-        mma_bf16(tbase + TM_S, a, at(dmn, OFF_LO + buf * SZ_TILE + ks * 2048), id_s, 1);
-      }
-      mma_commit(smem_u32(&S.b_state));
-      mma_commit(smem_u32(&S.b_buf[buf]));
-      mma_commit(smem_u32(&S.empty[st]));
-      if (!states && c + 1 < nch && scored < c + 2) {
-        if (!wt(&S.full[(c + 1) % kStages], ((c + 1) / kStages) & 1)) break;
-        tc_fence_after();
-        issue_sc(c + 1);
-        scored = c + 2;
+        for (int ks = 0; ks < 8; ++ks)
+          if (ks < 4 * ka)
+            mma_bf16_ta(tbase + TM_O + 64, tbase + TM_SB + 64 * buf + 8 * ks,
+                        at(dk, off + (ks >> 2) * SZ_PANEL + (ks & 3) * 32), id_o2, ks > 0);
+        mma_commit(smem_u32(&S.b_o));
+        mma_commit(smem_u32(&S.empty[st]));
       }
     }
     // wait for every MMA issued so far before the tensor memory is released
-    mma_commit(smem_u32(&S.b_final));
-    mbar_wait_drain(smem_u32(&S.b_final), 0, tmo);
+    uint64_t *done = &S.b_final[warp - kScoreMma];
+    mma_commit(smem_u32(done));
+    mbar_wait_drain(smem_u32(done), 0, kTimeout);
   }
 
   tc_fence_before();
