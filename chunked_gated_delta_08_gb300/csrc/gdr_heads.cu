@@ -8,6 +8,7 @@
 // One pass over memory: a head's row is held in fp32 registers between its sum and
 // its output, queries and keys in one launch.  The bound is HBM.
 #include <algorithm>
+#include <type_traits>
 
 #include "gdr_layer.cuh"
 
@@ -21,55 +22,91 @@ struct HeadArgs {
   const void *q, *k, *wq, *wk, *dyq, *dyk;
   const float *cos, *sin;
   const int64_t *pos;
-  void *yq, *yk;   // backward: dq, dk
-  float *part;     // backward: [blocks, 2, D] sums of dw
+  void *yq, *yk;  // backward: dq, dk
+  float *part;    // backward: [blocks, D] sums of dw, the blocks of q before those of k
   int *status;
-  int64_t cq, ck;  // runs of heads of a token: of queries, of keys
+  int64_t bq;     // blocks of q; the others take k
 };
 
-// Eight channels of a thread, as two runs of four: the a and the b of four pairs
-// where halves are paired, neighbours otherwise; and the pairs' first index.
-// Thread t of a row; R % 4 == 0, D % 8 == 0.
-__device__ __forceinline__ void channels_of(const HeadArgs &p, int t, int &c0, int &c1, bool &turned) {
-  const int R = (int)p.d.R;
-  turned = 4 * t < R;
-  if (turned && !p.d.interleaved) {
-    c0 = 4 * t;
-    c1 = R + 4 * t;
-  } else {
-    c0 = 8 * t;
-    c1 = c0 + 4;
-  }
+// One of the two tensors.
+template <typename T>
+struct Side {
+  const T *x, *dy;
+  T *y;
+  const void *w;
+  int64_t ld, ld_dy, heads;
+};
+template <typename T>
+__device__ __forceinline__ Side<T> side_of(const HeadArgs &p, bool query) {
+  const gdr_qk_norm_desc &d = p.d;
+  if (query) return {(const T *)p.q, (const T *)p.dyq, (T *)p.yq, p.wq, d.ld_q, d.ld_dyq, d.H};
+  return {(const T *)p.k, (const T *)p.dyk, (T *)p.yk, p.wk, d.ld_k, d.ld_dyk, d.HK};
 }
 
-// The four cosines and sines of a thread's pairs.  `sign` -1 turns back.
+// Channels of thread t of a row: two runs of RUN (16 bytes of fp32 or of bf16, or 8 of bf16).  Where
+// halves are paired, the runs are the a and the b of RUN pairs; neighbours' pairs lie
+// within each run, and a row's threads take runs side by side.  R % RUN == 0, D % (2 RUN) == 0.
+template <int RUN, bool NEAR>
+struct Place {
+  int c0, c1;
+  bool on, turned0, turned1;
+  __device__ __forceinline__ Place(const HeadArgs &p, int t) {
+    const int R = (int)p.d.R, D = (int)p.d.D;
+    on = 2 * RUN * t < D;
+    if constexpr (NEAR) {
+      c0 = RUN * t;
+      c1 = D / 2 + c0;
+      turned0 = on && c0 < 2 * R;
+      turned1 = on && c1 < 2 * R;
+    } else {
+      turned0 = turned1 = on && RUN * t < R;
+      c0 = turned0 ? RUN * t : 2 * RUN * t;
+      c1 = turned0 ? R + RUN * t : c0 + RUN;
+    }
+  }
+};
+
+// Cosines and sines of a thread's RUN pairs.
+template <int RUN, bool NEAR>
 struct Turn {
-  float c[4], s[4];
+  float c[RUN], s[RUN];
+  __device__ __forceinline__ void load_run(const HeadArgs &p, int64_t pos, int first, int at, int n) {
+    const float *pc = p.cos + pos * p.d.R + first, *ps = p.sin + pos * p.d.R + first;
+#pragma unroll
+    for (int i = 0; i < RUN; i += 2) {
+      if (i < n) {
+        const float2 u = *reinterpret_cast<const float2 *>(pc + i), v = *reinterpret_cast<const float2 *>(ps + i);
+        c[at + i] = u.x; c[at + i + 1] = u.y;
+        s[at + i] = v.x; s[at + i + 1] = v.y;
+      }
+    }
+  }
+  __device__ __forceinline__ Turn(const HeadArgs &p, const Place<RUN, NEAR> &l, int64_t pos) {
+#pragma unroll
+    for (int i = 0; i < RUN; ++i) {
+      c[i] = 1.f;
+      s[i] = 0.f;
+    }
+    if constexpr (NEAR) {
+      if (l.turned0) load_run(p, pos, l.c0 / 2, 0, RUN / 2);
+      if (l.turned1) load_run(p, pos, l.c1 / 2, RUN / 2, RUN / 2);
+    } else if (l.turned0) {
+      load_run(p, pos, l.c0, 0, RUN);
+    }
+  }
+  // v: the first run, then the second.  BACK turns back.  Channels that are not turned are not touched.
+  template <bool BACK>
+  __device__ __forceinline__ void apply(float (&v)[2 * RUN], const Place<RUN, NEAR> &l) const {
+#pragma unroll
+    for (int i = 0; i < RUN; ++i) {
+      const int ia = NEAR ? 2 * i : i, ib = NEAR ? 2 * i + 1 : RUN + i;
+      const bool is = i < RUN / 2 ? l.turned0 : l.turned1;
+      const float a = v[ia], b = v[ib], si = BACK ? -s[i] : s[i];
+      v[ia] = is ? fmaf(a, c[i], -(b * si)) : a;
+      v[ib] = is ? fmaf(b, c[i], a * si) : b;
+    }
+  }
 };
-__device__ __forceinline__ Turn turn_of(const HeadArgs &p, int64_t pos, int t, bool turned, float sign) {
-  Turn u;
-  if (turned) {
-    load4(p.cos + pos * p.d.R + 4 * t, u.c);
-    load4(p.sin + pos * p.d.R + 4 * t, u.s);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    u.c[i] = turned ? u.c[i] : 1.f;
-    u.s[i] = turned ? u.s[i] * sign : 0.f;
-  }
-  return u;
-}
-// v[0..3] and v[4..7] are the two runs.
-__device__ __forceinline__ void turn(float (&v)[8], const Turn &u, bool turned, bool interleaved) {
-  if (!turned) return;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float &a = interleaved ? v[2 * i] : v[i], &b = interleaved ? v[2 * i + 1] : v[i + 4];
-    const float x = a, y = b;
-    a = fmaf(x, u.c[i], -(y * u.s[i]));
-    b = fmaf(y, u.c[i], x * u.s[i]);
-  }
-}
 
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v) {
@@ -78,56 +115,69 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-template <typename T>
-__device__ __forceinline__ void load_weight(const void *w, bool f32, int c0, int c1, float (&v)[8]) {
-  float a[4], b[4];
-  if (f32) {
-    load4(static_cast<const float *>(w) + c0, a);
-    load4(static_cast<const float *>(w) + c1, b);
-  } else {
-    load4(static_cast<const T *>(w) + c0, a);
-    load4(static_cast<const T *>(w) + c1, b);
+// Both runs of a thread as they lie in memory (half the registers of bf16 until they are used); zeros where `on` is false.
+template <typename T, int RUN>
+struct Raw {
+  static constexpr int kWords = RUN * sizeof(T) / 4;
+  uint32_t a[kWords], b[kWords];
+  static __device__ __forceinline__ void load_run(const T *p, uint32_t (&r)[kWords]) {
+    if constexpr (kWords == 4) {
+      const uint4 u = *reinterpret_cast<const uint4 *>(p);
+      r[0] = u.x; r[1] = u.y; r[2] = u.z; r[3] = u.w;
+    } else {
+      const uint2 u = *reinterpret_cast<const uint2 *>(p);
+      r[0] = u.x; r[1] = u.y;
+    }
   }
+  __device__ __forceinline__ void load(const T *p, int c0, int c1, bool on) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = a[i];
-    v[4 + i] = b[i];
+    for (int i = 0; i < kWords; ++i) a[i] = b[i] = 0;
+    if (on) {
+      load_run(p + c0, a);
+      load_run(p + c1, b);
+    }
   }
-}
-template <typename T>
-__device__ __forceinline__ void load_two(const T *p, int c0, int c1, float (&v)[8]) {
-  float a[4], b[4];
-  load4(p + c0, a);
-  load4(p + c1, b);
+  static __device__ __forceinline__ float at(const uint32_t (&r)[kWords], int i) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(r[i]);
+    else return __uint_as_float(i & 1 ? r[i / 2] & 0xffff0000u : r[i / 2] << 16);
+  }
+  __device__ __forceinline__ void get(float (&v)[2 * RUN]) const {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = a[i];
-    v[4 + i] = b[i];
+    for (int i = 0; i < RUN; ++i) {
+      v[i] = at(a, i);
+      v[RUN + i] = at(b, i);
+    }
   }
-}
-template <typename T>
-__device__ __forceinline__ void store_two(T *p, int c0, int c1, const float (&v)[8]) {
-  const float a[4] = {v[0], v[1], v[2], v[3]}, b[4] = {v[4], v[5], v[6], v[7]};
-  store4(p + c0, a);
-  store4(p + c1, b);
-}
-
-// The rows of one run of up to U heads of a token.
-struct Run {
-  int64_t m, h0;  // token, first head of the run
-  int heads;
-  bool query;
 };
-template <int U>
-__device__ __forceinline__ Run run_of(const HeadArgs &p, int64_t item) {
-  Run r;
-  r.m = item / (p.cq + p.ck);
-  int64_t c = item - r.m * (p.cq + p.ck);
-  r.query = c < p.cq;
-  if (!r.query) c -= p.cq;
-  r.h0 = c * U;
-  r.heads = (int)min((int64_t)U, (r.query ? p.d.H : p.d.HK) - r.h0);
-  return r;
+template <int RUN, typename T>
+__device__ __forceinline__ void load_two(const T *p, int c0, int c1, bool on, float (&v)[2 * RUN]) {
+  float a[RUN] = {}, b[RUN] = {};
+  if (on) {
+    load_vec<RUN>(p + c0, a);
+    load_vec<RUN>(p + c1, b);
+  }
+#pragma unroll
+  for (int i = 0; i < RUN; ++i) {
+    v[i] = a[i];
+    v[RUN + i] = b[i];
+  }
+}
+template <int RUN, typename T>
+__device__ __forceinline__ void store_two(T *p, int c0, int c1, const float (&v)[2 * RUN]) {
+  float a[RUN], b[RUN];
+#pragma unroll
+  for (int i = 0; i < RUN; ++i) {
+    a[i] = v[i];
+    b[i] = v[RUN + i];
+  }
+  store_vec<RUN>(p + c0, a);
+  store_vec<RUN>(p + c1, b);
+}
+template <typename T, int RUN, bool NEAR>
+__device__ __forceinline__ void load_weight(const HeadArgs &p, const void *w, const Place<RUN, NEAR> &l,
+                                            float (&v)[2 * RUN]) {
+  if (p.d.weight_dtype == GDR_F32) load_two<RUN>(static_cast<const float *>(w), l.c0, l.c1, l.on, v);
+  else load_two<RUN>(static_cast<const T *>(w), l.c0, l.c1, l.on, v);
 }
 
 // A token's position: -1 (or one past the table, which is reported) makes a padding row of zeros.
@@ -139,135 +189,116 @@ __device__ __forceinline__ int64_t position_of(const HeadArgs &p, int64_t m) {
   return -1;
 }
 
-// TPR threads to a row (a power of two, at least D / 8 and 4), U heads of a token to
-// each such group, all of whose rows are asked for before the first is used.
-template <typename T, int TPR, int U>
-__global__ void __launch_bounds__(kThreads) head_fwd_kernel(const __grid_constant__ HeadArgs p) {
-  const int D = (int)p.d.D, t = threadIdx.x % TPR;
-  const int64_t items = p.d.M * (p.cq + p.ck);
-  const int64_t item = (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
-  const Run r = run_of<U>(p, item < items ? item : items - 1);  // the last warp's spare groups: a copy of the last run
-  const bool on = 8 * t < D;
-  int c0, c1;
-  bool turned;
-  channels_of(p, t, c0, c1, turned);
-  const int64_t ld = r.query ? p.d.ld_q : p.d.ld_k, heads = r.query ? p.d.H : p.d.HK;
-  const T *x = static_cast<const T *>(r.query ? p.q : p.k) + r.m * ld + r.h0 * D;
-  float v[U][8];
+// TPR threads to a row (a power of two, at least D / (2 RUN)), so 32 / TPR rows to a warp at once; U such
+// sets of one token's heads to a warp, all of whose loads are on their way before the first is used.
+// A block belongs to q or to k: its weights stay in registers.  Warps go through the items
+// (token, run of heads) of their tensor.
+template <typename T, int RUN, int TPR, int U, bool NEAR>
+__global__ void __launch_bounds__(kThreads, 2) head_fwd_kernel(const __grid_constant__ HeadArgs p) {
+  constexpr int G = 32 / TPR, HI = G * U, kWarps = kThreads / 32;
+  const bool query = blockIdx.x < p.bq;
+  const Side<T> sd = side_of<T>(p, query);
+  const int64_t block = query ? blockIdx.x : blockIdx.x - p.bq, blocks = query ? p.bq : gridDim.x - p.bq;
+  const int lane = threadIdx.x & 31, D = (int)p.d.D, grp = lane / TPR;
+  const Place<RUN, NEAR> l(p, lane % TPR);
+  float w[2 * RUN];
+  load_weight<T>(p, sd.w, l, w);
+  const int64_t runs = (sd.heads + HI - 1) / HI, items = p.d.M * runs;
+  for (int64_t it = block * kWarps + (threadIdx.x >> 5); it < items; it += blocks * kWarps) {
+    const int64_t m = it / runs, h0 = (it - m * runs) * HI + grp;
+    const int64_t pos = position_of(p, m);
+    const T *x = sd.x + m * sd.ld + h0 * D;
+    Raw<T, RUN> rx[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (on && u < r.heads) load_two(x + u * D, c0, c1, v[u]);
-    else {
+    for (int u = 0; u < U; ++u) rx[u].load(x + u * G * D, l.c0, l.c1, l.on && h0 + u * G < sd.heads);
+    const Turn<RUN, NEAR> a(p, l, pos < 0 ? 0 : pos);
+    T *y = sd.y + (m * sd.heads + h0) * D;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
-    }
-  }
-  const int64_t pos = position_of(p, r.m);
-  const Turn a = turn_of(p, max(pos, (int64_t)0), t, turned && on && pos >= 0, 1.f);
-  float w[8];
-  if (on) load_weight<T>(r.query ? p.wq : p.wk, p.d.weight_dtype == GDR_F32, c0, c1, w);
-  T *y = static_cast<T *>(r.query ? p.yq : p.yk) + (r.m * heads + r.h0) * D;
+    for (int u = 0; u < U; ++u) {
+      float v[2 * RUN], ss = 0.f;
+      rx[u].get(v);
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    float ss = 0.f;
+      for (int i = 0; i < 2 * RUN; ++i) ss = fmaf(v[i], v[i], ss);
+      const float rho = rsqrtf(row_sum<TPR>(ss) / (float)D + p.d.eps);
+      if (l.on && h0 + u * G < sd.heads) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(v[u][i], v[u][i], ss);
-    const float rho = rsqrtf(row_sum<TPR>(ss) / (float)D + p.d.eps);
-    if (on && u < r.heads && item < items) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[u][i] = pos < 0 ? 0.f : v[u][i] * rho * w[i];
-      turn(v[u], a, turned, p.d.interleaved);
-      store_two(y + u * D, c0, c1, v[u]);
+        for (int i = 0; i < 2 * RUN; ++i) v[i] = pos < 0 ? 0.f : v[i] * rho * w[i];
+        a.template apply<false>(v, l);
+        store_two<RUN>(y + u * G * D, l.c0, l.c1, v);
+      }
     }
   }
 }
 
-// Blocks go through the runs; a thread sums its channels' dw of queries and of keys
-// over its runs, the block's groups meet in shared memory, the blocks in a second launch.
-template <typename T, int TPR, int U>
-__global__ void __launch_bounds__(kThreads) head_bwd_kernel(const __grid_constant__ HeadArgs p) {
-  __shared__ float red[kThreads / TPR][2][TPR * 8 + 1];
-  const int D = (int)p.d.D, t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
-  const int64_t items = p.d.M * (p.cq + p.ck), step = (int64_t)gridDim.x * (kThreads / TPR);
-  const bool on = 8 * t < D, f32 = p.d.weight_dtype == GDR_F32;
-  int c0, c1;
-  bool turned;
-  channels_of(p, t, c0, c1, turned);
-  float sq[8] = {}, sk[8] = {};
-  for (int64_t first = (int64_t)blockIdx.x * (kThreads / TPR); first < items; first += step) {  // all threads stay for the shuffles
-    const int64_t item = first + grp;
-    const bool real = item < items;
-    const Run r = run_of<U>(p, real ? item : items - 1);
-    const int64_t ld = r.query ? p.d.ld_q : p.d.ld_k, ldy = r.query ? p.d.ld_dyq : p.d.ld_dyk,
-                  heads = r.query ? p.d.H : p.d.HK;
-    const T *x = static_cast<const T *>(r.query ? p.q : p.k) + r.m * ld + r.h0 * D;
-    const T *dy = static_cast<const T *>(r.query ? p.dyq : p.dyk) + r.m * ldy + r.h0 * D;
-    float v[U][8], g[U][8];
+// The same with dy beside x; a thread sums dw of its channels over its items, a block's
+// warps and rows meet in shared memory, the blocks in a second launch.
+template <typename T, int RUN, int TPR, int U, bool NEAR>
+__global__ void __launch_bounds__(kThreads, 2) head_bwd_kernel(const __grid_constant__ HeadArgs p) {
+  constexpr int G = 32 / TPR, HI = G * U, kWarps = kThreads / 32;
+  __shared__ float red[kWarps * G][2 * RUN * TPR + 1];
+  const bool query = blockIdx.x < p.bq;
+  const Side<T> sd = side_of<T>(p, query);
+  const int64_t block = query ? blockIdx.x : blockIdx.x - p.bq, blocks = query ? p.bq : gridDim.x - p.bq;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = (int)p.d.D, grp = lane / TPR;
+  const Place<RUN, NEAR> l(p, lane % TPR);
+  float w[2 * RUN], sum[2 * RUN] = {};
+  load_weight<T>(p, sd.w, l, w);
+  const int64_t runs = (sd.heads + HI - 1) / HI, items = p.d.M * runs;
+  for (int64_t it = block * kWarps + warp; it < items; it += blocks * kWarps) {
+    const int64_t m = it / runs, h0 = (it - m * runs) * HI + grp;
+    const int64_t pos = position_of(p, m);
+    const T *x = sd.x + m * sd.ld + h0 * D, *dy = sd.dy + m * sd.ld_dy + h0 * D;
+    Raw<T, RUN> rx[U], rg[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (on && u < r.heads) {
-        load_two(x + u * D, c0, c1, v[u]);
-        load_two(dy + u * D, c0, c1, g[u]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[u][i] = g[u][i] = 0.f;
-      }
+      const bool on = l.on && h0 + u * G < sd.heads;
+      rx[u].load(x + u * G * D, l.c0, l.c1, on);
+      rg[u].load(dy + u * G * D, l.c0, l.c1, on);
     }
-    const int64_t pos = position_of(p, r.m);
-    const Turn a = turn_of(p, max(pos, (int64_t)0), t, turned && on && pos >= 0, -1.f);
-    float w[8];
-    if (on) load_weight<T>(r.query ? p.wq : p.wk, f32, c0, c1, w);
-    else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = 0.f;
-    }
-    T *dx = static_cast<T *>(r.query ? p.yq : p.yk) + (r.m * heads + r.h0) * D;
+    const Turn<RUN, NEAR> a(p, l, pos < 0 ? 0 : pos);
+    T *dx = sd.y + (m * sd.heads + h0) * D;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      turn(g[u], a, turned, p.d.interleaved);
-      float ss = 0.f, px = 0.f;
+      float v[2 * RUN], g[2 * RUN], ss = 0.f, px = 0.f;
+      rx[u].get(v);
+      rg[u].get(g);
+      a.template apply<true>(g, l);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        ss = fmaf(v[u][i], v[u][i], ss);
-        px = fmaf(w[i] * g[u][i], v[u][i], px);
+      for (int i = 0; i < 2 * RUN; ++i) {
+        ss = fmaf(v[i], v[i], ss);
+        px = fmaf(w[i] * g[i], v[i], px);
       }
-      ss = row_sum<TPR>(ss) / (float)D + p.d.eps;
-      const float rho = rsqrtf(ss), m = row_sum<TPR>(px) / (float)D * rho * rho;
-      if (on && u < r.heads && real) {
-        float o[8];
+      const float rho = rsqrtf(row_sum<TPR>(ss) / (float)D + p.d.eps);
+      const float mean = row_sum<TPR>(px) / (float)D * rho * rho;
+      if (l.on && h0 + u * G < sd.heads) {
+        float o[2 * RUN];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = pos < 0 ? 0.f : rho * (w[i] * g[u][i] - v[u][i] * m);
-        store_two(dx + u * D, c0, c1, o);
-        if (pos >= 0) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float dw = g[u][i] * (v[u][i] * rho);
-            if (r.query) sq[i] += dw;
-            else sk[i] += dw;
-          }
+        for (int i = 0; i < 2 * RUN; ++i) {
+          o[i] = pos < 0 ? 0.f : rho * (w[i] * g[i] - v[i] * mean);
+          sum[i] += pos < 0 ? 0.f : g[i] * (v[i] * rho);
         }
+        store_two<RUN>(dx + u * G * D, l.c0, l.c1, o);
       }
     }
   }
-  if (on) {
+  if (l.on) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = i < 4 ? c0 + i : c1 + i - 4;
-      red[grp][0][c] = sq[i];
-      red[grp][1][c] = sk[i];
+    for (int i = 0; i < RUN; ++i) {
+      red[warp * G + grp][l.c0 + i] = sum[i];
+      red[warp * G + grp][l.c1 + i] = sum[RUN + i];
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+  for (int i = threadIdx.x; i < D; i += kThreads) {
     float s = 0.f;
 #pragma unroll 4
-    for (int j = 0; j < kThreads / TPR; ++j) s += red[j][i / D][i % D];
-    p.part[(int64_t)blockIdx.x * 2 * D + i] = s;
+    for (int j = 0; j < kWarps * G; ++j) s += red[j][i];
+    p.part[(int64_t)blockIdx.x * D + i] = s;
   }
 }
 
-// Odd widths, pairs that four do not divide, or bases off the vectors' alignment: a
-// warp to a row, a lane to every 32nd pair (or channel past the pairs).
+// Odd widths, pairs that no run divides, or bases off the vectors' alignment: a warp to
+// a row, a lane to every 32nd pair (or channel past the pairs).
 constexpr int kMostUnits = 8;  // units of a lane: D <= 256
 __device__ __forceinline__ void unit_of(const HeadArgs &p, int u, int &ca, int &cb) {  // cb < 0: one channel
   const int R = (int)p.d.R;
@@ -276,20 +307,19 @@ __device__ __forceinline__ void unit_of(const HeadArgs &p, int u, int &ca, int &
 }
 template <typename T, bool BWD>
 __global__ void __launch_bounds__(kThreads) head_odd_kernel(const __grid_constant__ HeadArgs p) {
-  __shared__ float red[BWD ? kThreads / 32 : 1][2][256];
+  constexpr int kWarps = kThreads / 32;
+  __shared__ float red[BWD ? kWarps : 1][256];
+  const bool query = blockIdx.x < p.bq;
+  const Side<T> sd = side_of<T>(p, query);
+  const int64_t block = query ? blockIdx.x : blockIdx.x - p.bq, blocks = query ? p.bq : gridDim.x - p.bq;
   const int D = (int)p.d.D, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, units = D - (int)p.d.R;
-  const int64_t rows = p.d.M * (p.d.H + p.d.HK);
+  const int64_t rows = p.d.M * sd.heads;
   const bool f32 = p.d.weight_dtype == GDR_F32;
-  float sums[2][2][BWD ? kMostUnits : 1] = {};
-  for (int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + warp; row < rows; row += (int64_t)gridDim.x * (kThreads / 32)) {
-    const int64_t m = row / (p.d.H + p.d.HK);
-    int64_t h = row - m * (p.d.H + p.d.HK);
-    const bool query = h < p.d.H;
-    if (!query) h -= p.d.H;
-    const T *x = static_cast<const T *>(query ? p.q : p.k) + m * (query ? p.d.ld_q : p.d.ld_k) + h * D;
-    const T *dy = BWD ? static_cast<const T *>(query ? p.dyq : p.dyk) + m * (query ? p.d.ld_dyq : p.d.ld_dyk) + h * D : x;
-    const void *w = query ? p.wq : p.wk;
-    T *y = static_cast<T *>(query ? p.yq : p.yk) + (m * (query ? p.d.H : p.d.HK) + h) * D;
+  float sums[2][BWD ? kMostUnits : 1] = {};
+  for (int64_t row = block * kWarps + warp; row < rows; row += blocks * kWarps) {
+    const int64_t m = row / sd.heads, h = row - m * sd.heads;
+    const T *x = sd.x + m * sd.ld + h * D, *dy = sd.dy + (BWD ? m * sd.ld_dy + h * D : 0);
+    T *y = sd.y + row * D;
     const int64_t pos = position_of(p, m);
     float va[kMostUnits], vb[kMostUnits], ga[kMostUnits], gb[kMostUnits], ss = 0.f, px = 0.f;
 #pragma unroll
@@ -310,8 +340,8 @@ __global__ void __launch_bounds__(kThreads) head_odd_kernel(const __grid_constan
           ga[i] = fmaf(g0, c, g1 * s);
           gb[i] = fmaf(g1, c, -(g0 * s));
         }
-        px = fmaf(param<T>(w, f32, ca) * ga[i], va[i], px);
-        if (cb >= 0) px = fmaf(param<T>(w, f32, cb) * gb[i], vb[i], px);
+        px = fmaf(param<T>(sd.w, f32, ca) * ga[i], va[i], px);
+        if (cb >= 0) px = fmaf(param<T>(sd.w, f32, cb) * gb[i], vb[i], px);
       }
     }
     const float rho = rsqrtf(warp_sum(ss) / (float)D + p.d.eps);
@@ -324,21 +354,16 @@ __global__ void __launch_bounds__(kThreads) head_odd_kernel(const __grid_constan
       unit_of(p, u, ca, cb);
       float a, b = 0.f;
       if constexpr (BWD) {
-        a = rho * (param<T>(w, f32, ca) * ga[i] - va[i] * mean);
-        if (cb >= 0) b = rho * (param<T>(w, f32, cb) * gb[i] - vb[i] * mean);
+        a = rho * (param<T>(sd.w, f32, ca) * ga[i] - va[i] * mean);
+        if (cb >= 0) b = rho * (param<T>(sd.w, f32, cb) * gb[i] - vb[i] * mean);
         if (pos >= 0) {
-          if (query) {
-            sums[0][0][i] += ga[i] * (va[i] * rho);
-            sums[0][1][i] += gb[i] * (vb[i] * rho);
-          } else {
-            sums[1][0][i] += ga[i] * (va[i] * rho);
-            sums[1][1][i] += gb[i] * (vb[i] * rho);
-          }
+          sums[0][i] += ga[i] * (va[i] * rho);
+          sums[1][i] += gb[i] * (vb[i] * rho);
         }
       } else {
-        a = va[i] * rho * param<T>(w, f32, ca);
+        a = va[i] * rho * param<T>(sd.w, f32, ca);
         if (cb >= 0 && pos >= 0) {
-          b = vb[i] * rho * param<T>(w, f32, cb);
+          b = vb[i] * rho * param<T>(sd.w, f32, cb);
           const float c = p.cos[pos * p.d.R + u], s = p.sin[pos * p.d.R + u], n0 = a, n1 = b;
           a = fmaf(n0, c, -(n1 * s));
           b = fmaf(n1, c, n0 * s);
@@ -355,80 +380,119 @@ __global__ void __launch_bounds__(kThreads) head_odd_kernel(const __grid_constan
       if (u >= units) continue;
       int ca, cb;
       unit_of(p, u, ca, cb);
-      for (int z = 0; z < 2; ++z) {
-        red[warp][z][ca] = sums[z][0][i];
-        if (cb >= 0) red[warp][z][cb] = sums[z][1][i];
-      }
+      red[warp][ca] = sums[0][i];
+      if (cb >= 0) red[warp][cb] = sums[1][i];
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+    for (int i = threadIdx.x; i < D; i += kThreads) {
       float s = 0.f;
-      for (int j = 0; j < kThreads / 32; ++j) s += red[j][i / D][i % D];
-      p.part[(int64_t)blockIdx.x * 2 * D + i] = s;
+      for (int j = 0; j < kWarps; ++j) s += red[j][i];
+      p.part[(int64_t)blockIdx.x * D + i] = s;
     }
   }
 }
 
-__global__ void __launch_bounds__(1024) head_sum_kernel(ColSum q) {
+// dw of q and of k from the blocks' sums.
+__global__ void __launch_bounds__(1024) head_sum_kernel(ColSum q, ColSum k) {
   __shared__ float sm[32][33];
-  col_sum_block<32>(q, blockIdx.x, sm);
+  col_sum_block<32>(blockIdx.y ? k : q, blockIdx.x, sm);
 }
 
-bool vec_ok(const HeadArgs &a, bool bwd) {
+// Whether every row can be read in runs of `run` elements.
+bool runs_ok(const HeadArgs &a, int run, bool bwd) {
   const gdr_qk_norm_desc &d = a.d;
-  const uintptr_t bytes = d.dtype == GDR_BF16 ? 8 : 16;  // of four elements
-  const auto on = [&](const void *p, int64_t ld, uintptr_t n) { return (uintptr_t)p % n == 0 && ld % 4 == 0; };
-  const uintptr_t wb = d.weight_dtype == GDR_F32 ? 16 : bytes;
-  bool ok = d.D % 8 == 0 && d.R % 4 == 0 && on(a.q, d.ld_q, bytes) && on(a.k, d.ld_k, bytes) && on(a.wq, 0, wb) &&
-            on(a.wk, 0, wb) && on(a.yq, 0, bytes) && on(a.yk, 0, bytes) && on(a.cos, 0, 16) && on(a.sin, 0, 16);
+  const uintptr_t bytes = (d.dtype == GDR_BF16 ? 2 : 4) * run, wb = d.weight_dtype == GDR_F32 ? 16 : bytes;
+  const auto on = [&](const void *p, int64_t ld, uintptr_t n) { return (uintptr_t)p % n == 0 && ld % run == 0; };
+  bool ok = d.D % (2 * run) == 0 && d.R % run == 0 && on(a.q, d.ld_q, bytes) && on(a.k, d.ld_k, bytes) &&
+            on(a.wq, 0, wb) && on(a.wk, 0, wb) && on(a.yq, 0, bytes) && on(a.yk, 0, bytes) && on(a.cos, 0, 8) &&
+            on(a.sin, 0, 8);
   if (bwd) ok = ok && on(a.dyq, d.ld_dyq, bytes) && on(a.dyk, d.ld_dyk, bytes);
   return ok;
 }
 
-constexpr int kHeads = 4;     // heads of a run
-constexpr int kWaveBlocks = 4 * kSMs;  // blocks of the backward's grid
+// A launch's blocks: as many as its items fill, at most `most`; those of q and of k go by their items.
+struct Blocks {
+  int64_t q, all;
+};
+Blocks blocks_of(const gdr_qk_norm_desc &d, int heads_per_item, int64_t most) {
+  constexpr int kWarps = kThreads / 32;
+  const int64_t q = cdiv(d.M * cdiv(d.H, heads_per_item), kWarps), k = cdiv(d.M * cdiv(d.HK, heads_per_item), kWarps);
+  if (q + k <= most) return {q, q + k};
+  const int64_t bk = d.HK ? std::max<int64_t>(1, most * k / (q + k)) : 0;
+  return {most - bk, most};
+}
 
-template <typename T, int TPR>
+template <typename T, int RUN, int TPR, int U>
 int launch_vec(const HeadArgs &a, bool bwd, int64_t blocks, cudaStream_t st) {
-  if (bwd) head_bwd_kernel<T, TPR, kHeads><<<(unsigned)blocks, kThreads, 0, st>>>(a);
-  else head_fwd_kernel<T, TPR, kHeads><<<(unsigned)blocks, kThreads, 0, st>>>(a);
-  return launched(bwd ? "head_bwd_kernel" : "head_fwd_kernel");
+  const bool near = a.d.interleaved;
+  if constexpr (U < 4) if (bwd) {
+    const auto kernel = near ? head_bwd_kernel<T, RUN, TPR, U, true> : head_bwd_kernel<T, RUN, TPR, U, false>;
+    kernel<<<(unsigned)blocks, kThreads, 0, st>>>(a);
+    return launched("head_bwd_kernel");
+  }
+  if constexpr (U > 1) {
+    const auto kernel = near ? head_fwd_kernel<T, RUN, TPR, U, true> : head_fwd_kernel<T, RUN, TPR, U, false>;
+    kernel<<<(unsigned)blocks, kThreads, 0, st>>>(a);
+  }
+  return launched("head_fwd_kernel");
+}
+
+// Rows of a thread (U): four of x, or two of x and dy, are what the registers hold on their way; half
+// where the heads do not fill them.  16384 x 40 x 128 bf16: forward 79-84 us with four, 81-83 with two,
+// 116 with one; backward 112-120 with two, 142 with one.  16384 x 20 x 64: forward 36 with four, 24 with two.
+template <typename T, int RUN>
+int launch_runs(const HeadArgs &a, bool bwd, int tpr, bool half, int64_t blocks, cudaStream_t st) {
+  const auto go = [&](auto t) {
+    constexpr int TPR = decltype(t)::value;
+    if (bwd) return half ? launch_vec<T, RUN, TPR, 1>(a, bwd, blocks, st) : launch_vec<T, RUN, TPR, 2>(a, bwd, blocks, st);
+    return half ? launch_vec<T, RUN, TPR, 2>(a, bwd, blocks, st) : launch_vec<T, RUN, TPR, 4>(a, bwd, blocks, st);
+  };
+  if (tpr == 4) return go(std::integral_constant<int, 4>{});
+  if (tpr == 8) return go(std::integral_constant<int, 8>{});
+  if constexpr (RUN == 8) return go(std::integral_constant<int, 16>{});  // D <= 256
+  if (tpr == 16) return go(std::integral_constant<int, 16>{});
+  return go(std::integral_constant<int, 32>{});
 }
 
 template <typename T>
 int launch(HeadArgs a, bool bwd, float *dwq, float *dwk, cudaStream_t st) {
   const gdr_qk_norm_desc &d = a.d;
-  const bool vec = vec_ok(a, bwd);
-  int tpr = 4;
-  while (8 * tpr < d.D) tpr *= 2;
-  if (!vec) tpr = 32;
-  a.cq = vec ? cdiv(d.H, kHeads) : d.H;
-  a.ck = vec ? cdiv(d.HK, kHeads) : d.HK;
-  int64_t blocks = cdiv(d.M * (a.cq + a.ck), kThreads / tpr);
-  if (bwd || !vec) blocks = std::min<int64_t>(blocks, kWaveBlocks);
-  if (blocks > 0x7fffffff) return set_error(GDR_ERR_SHAPE, "too many rows for one launch");
+  constexpr int kWide = sizeof(T) == 2 ? 8 : 4;
+  const int run = runs_ok(a, kWide, bwd) ? kWide : runs_ok(a, 4, bwd) ? 4 : 1;
+  int tpr = run > 1 ? 4 : 32;
+  while (2 * run * tpr < d.D && run > 1) tpr *= 2;
+  // the backward's blocks stay and sum; more of them only leave more sums to add
+  const int64_t most = bwd || run == 1 ? 4 * kSMs : 0x7fffffff;
+  const int full = 32 / tpr * (bwd ? 2 : 4);  // heads of an item
+  const bool half = std::max(d.H, d.HK) <= full / 2;
+  const Blocks n = blocks_of(d, run > 1 ? full / (half ? 2 : 1) : 1, most);
+  if (n.all > 0x7fffffff) return set_error(GDR_ERR_SHAPE, "too many rows for one launch");
+  a.bq = n.q;
   char *base = nullptr;
-  int rc;
+  int rc = GDR_OK;
   if (bwd) {
-    rc = scratch_begin(sizeof(float) * (size_t)(std::max<int64_t>(1, blocks) * 2 * d.D), st, "head norm scratch", &base);
+    rc = scratch_begin(sizeof(float) * (size_t)(std::max<int64_t>(1, n.all) * d.D), st, "head norm scratch", &base);
     if (rc != GDR_OK) return rc;
     a.part = (float *)base;
   }
-  rc = GDR_OK;
-  if (blocks > 0) {
-    if (!vec) {
-      if (bwd) head_odd_kernel<T, true><<<(unsigned)blocks, kThreads, 0, st>>>(a);
-      else head_odd_kernel<T, false><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+  if (n.all > 0) {
+    if (run == 1) {
+      if (bwd) head_odd_kernel<T, true><<<(unsigned)n.all, kThreads, 0, st>>>(a);
+      else head_odd_kernel<T, false><<<(unsigned)n.all, kThreads, 0, st>>>(a);
       rc = launched("head_odd_kernel");
-    } else if (tpr == 4) rc = launch_vec<T, 4>(a, bwd, blocks, st);
-    else if (tpr == 8) rc = launch_vec<T, 8>(a, bwd, blocks, st);
-    else if (tpr == 16) rc = launch_vec<T, 16>(a, bwd, blocks, st);
-    else rc = launch_vec<T, 32>(a, bwd, blocks, st);
+    } else if (run == 8) {
+      if constexpr (sizeof(T) == 2) rc = launch_runs<T, 8>(a, bwd, tpr, half, n.all, st);
+    } else {
+      rc = launch_runs<T, 4>(a, bwd, tpr, half, n.all, st);
+    }
   }
   if (!bwd) return rc;
   if (rc == GDR_OK) {
-    const ColSum s{a.part, blocks, 2 * d.D, 2 * d.D, 2 * d.D, 2 * d.D, dwq, d.D, dwk};
-    head_sum_kernel<<<(unsigned)cdiv(2 * d.D, 32), 1024, 0, st>>>(s);
+    const auto sum = [&](int64_t first, int64_t rows, float *out) {
+      return ColSum{a.part + first * d.D, rows, d.D, d.D, d.D, d.D, out, d.D, nullptr};
+    };
+    head_sum_kernel<<<dim3((unsigned)cdiv(d.D, 32), d.HK ? 2 : 1), 1024, 0, st>>>(sum(0, n.q, dwq),
+                                                                                sum(n.q, n.all - n.q, dwk));
     rc = launched("head_sum_kernel");
   }
   return scratch_end(base, st, "head norm scratch", rc);

@@ -54,14 +54,14 @@ __device__ __forceinline__ bool vec4_ok(const LaRows &r) {
 template <typename T>
 __global__ void __launch_bounds__(kThreads) la_any_kernel(const __grid_constant__ LaArgs p) {
   extern __shared__ __align__(16) float sm[];
-  if (!seqlens_ok(p.cu, p.N, p.cu ? p.tokens : p.T, p.status)) return;
+  bool cut;
+  if (!sequences_ok(p, cut)) return;
   const LaPass &q = p.pass[blockIdx.z];
   const int64_t hv = blockIdx.x % p.HV, slot = blockIdx.x / p.HV;
   const int Da = q.a.D, Dc = q.c.D, col0 = blockIdx.y * kCols;
   if (col0 >= Dc) return;
   const bool bw = q.backwards;
-  if (p.mode == kWhole && slot >= p.N) return;  // no sequences: the block has checked cu_seqlens
-  const Segment s = segment_of(p, slot, bw);
+  const Segment s = segment_of(p, slot, bw, cut);
   if (!s.some) return;
   if (p.mode == kStates && s.last) return;  // nobody reads the state behind the last segment
   const int D = (Da + 15) & ~15, LDA = D + 4, cols = min(kCols, Dc - col0);
@@ -73,8 +73,7 @@ __global__ void __launch_bounds__(kThreads) la_any_kernel(const __grid_constant_
 
   for (int i = tid; i <= C; i += kThreads) pw[i] = decay_power(g, i);
   // the state the segment starts from
-  const int64_t at = (p.mode == kWhole ? s.n : slot) * p.HV + hv;
-  const float *from = p.mode == kStates || !q.s_in ? nullptr : q.s_in + at * p.KV;
+  const float *from = entering(p, q, s, slot, hv, cut);
   for (int i = tid; i < D * kCols; i += kThreads) {
     const int r = i / kCols, c = i % kCols;
     S[r * LDC + c] = from && r < Da && c < cols ? from[r * q.si + (col0 + c) * q.sj] : 0.f;
@@ -197,56 +196,87 @@ __global__ void __launch_bounds__(kThreads) la_any_kernel(const __grid_constant_
 // ------------------------------------------------------------------------------ carry, sums
 // The states that segments start from, in place of their own: over a sequence's
 // segments in the pass's order, S enters and leaves as r^len S + own.  One thread
-// per element of a head's state; the next segment's element is on its way meanwhile.
+// per element of a head's state, eight segments' elements on their way at once
+// (74 segments one after the other took 50 us).
 __global__ void __launch_bounds__(256) la_carry_kernel(const __grid_constant__ LaArgs p) {
-  if (!seqlens_ok(p.cu, p.N, p.cu ? p.tokens : p.T, p.status)) return;
+  bool cut;
+  if (!sequences_ok(p, cut) || !cut) return;
   const LaPass &q = p.pass[blockIdx.z];
   const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t n = blockIdx.y / p.HV, hv = blockIdx.y % p.HV;
   if (e >= p.KV) return;
   const SeqRange r = seq_range(p.cu, n, p.T);
-  const int64_t len = r.eos - r.bos, segs = len > 0 ? (len + p.L - 1) / p.L : 1;
+  const int64_t len = r.eos - r.bos, segs = segments_in(p, len, true);
   const float g = p.g[hv];
   float S = q.s_in ? q.s_in[(n * p.HV + hv) * p.KV + e] : 0.f;
-  float *own = q.s_out + (first_slot(p, n) * p.HV + hv) * p.KV + e;
-  const int64_t step = p.HV * p.KV;
+  const int64_t step = p.HV * p.KV * (q.backwards ? -1 : 1);
+  float *own = q.s_out + ((first_slot(p, n) + (q.backwards ? segs - 1 : 0)) * p.HV + hv) * p.KV + e;
   const float full = decay_less1(g, p.L), tail = decay_less1(g, len - (segs - 1) * p.L);
-  for (int64_t u = 0; u < segs; ++u) {
-    const int64_t i = q.backwards ? segs - 1 - u : u;
-    const float mine = u + 1 < segs ? own[i * step] : 0.f;  // of the last there is none
-    own[i * step] = S;
-    S = fmaf(S, i == segs - 1 ? tail : full, S) + mine;
+  constexpr int kAhead = 8;
+  for (int64_t u0 = 0; u0 < segs; u0 += kAhead, own += kAhead * step) {
+    float mine[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) mine[i] = u0 + i + 1 < segs ? own[i * step] : 0.f;  // of the last there is none
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (u0 + i < segs) {
+        own[i * step] = S;
+        // the ragged segment is a sequence's last: going back, the first of the pass
+        S = fmaf(S, q.backwards && u0 + i == 0 ? tail : full, S) + mine[i];
+      }
+    }
   }
 }
 
-// out [M, H, D] = sums over groups of G value heads of part [M, H G, D], in order.
-template <typename T>
+// out [M, H, D] = sums over groups of G value heads of part [M, H G, D], in order; VEC elements to a thread.
+template <typename T, int VEC>
 __global__ void __launch_bounds__(256) la_sum_kernel(const float *part0, const float *part1, T *out0, T *out1, int64_t n,
                                                      int G, int D, SeqCheck check) {
   if (!seqlens_ok(check)) return;
   const float *part = blockIdx.y ? part1 : part0;
   T *out = blockIdx.y ? out1 : out0;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * VEC;
   if (i >= n) return;
-  const float *src = part + (i / D) * G * D + i % D;
-  float s = src[0];
-  for (int j = 1; j < G; ++j) s += src[(int64_t)j * D];
-  out[i] = from_f32<T>(s);
+  const float *src = part + i / D * G * D + i % D;
+  float s[VEC];
+  load_vec<VEC>(src, s);
+#pragma unroll 4
+  for (int j = 1; j < G; ++j) {
+    float v[VEC];
+    load_vec<VEC>(src + (int64_t)j * D, v);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) s[e] += v[e];
+  }
+  store_vec<VEC>(out + i, s);
+}
+template <typename T>
+int launch_sum(const float *part0, const float *part1, void *out0, void *out1, int64_t n, int G, int D,
+               const SeqCheck &check, cudaStream_t st) {
+  const bool vec = D % 4 == 0 && is_aligned16(out0) && is_aligned16(out1);
+  const auto kernel = vec ? la_sum_kernel<T, 4> : la_sum_kernel<T, 1>;
+  const dim3 grid((unsigned)cdiv(n, vec ? 1024 : 256), 2);
+  kernel<<<grid, 256, 0, st>>>(part0, part1, (T *)out0, (T *)out1, n, G, D, check);
+  return launched("la_sum_kernel");
 }
 
 // -------------------------------------------------------------------------------- host side
-// Tokens in a segment, or 0 for none.  A block walks a sequence chunk by chunk, one block to a
-// multiprocessor.  Uncut, a launch takes as long as its waves of whole sequences; of a packed
-// batch the lengths are on the device, and one sequence may hold nearly all tokens.  Cut, the
-// work spreads evenly, but forming the segments' states takes half as much again.
-int64_t segment_length(const LaArgs &p, int blocks_per_pair) {
-  if (p.tokens <= 4 * C || p.N == 0) return 0;
-  const int64_t blocks = p.HV * blocks_per_pair;  // to a sequence
-  const int64_t uncut = p.cu ? p.tokens : cdiv(p.N * blocks, kSMs) * p.T;
-  if (3 * cdiv(p.tokens * blocks, kSMs) >= 2 * uncut) return 0;
-  const int64_t want = std::max<int64_t>(1, cdiv(2 * kSMs, blocks));  // segments over all sequences
-  const int64_t L = std::max<int64_t>(4 * C, cdiv(cdiv(p.tokens, want), C) * C);
-  return !p.cu && L >= p.T ? 0 : L;
+// How sequences are cut: p.L (0: not) and p.least.  A block walks a sequence chunk by chunk, `wave`
+// blocks at a time (a tensor-core block takes 1.6 us a chunk, one of the other form 3.5).  Uncut, a
+// launch takes as long as its longest sequence, or its waves of whole sequences.  Cut, the work
+// spreads evenly, but forming the segments' states adds three fifths of it, and two more launches
+// the time of `launches` chunks.
+void cut(LaArgs &p, int blocks_per_pair, int wave, int launches) {
+  const int64_t blocks = p.HV * blocks_per_pair;                // to a sequence
+  const int64_t even = cdiv(cdiv(p.tokens, C) * blocks, wave);  // chunks of work to a block of a wave
+  p.least = C * (launches + 8 * std::max<int64_t>(even, 4) / 5);
+  p.L = 0;
+  const int64_t longest = p.cu ? p.tokens : cdiv(p.N * blocks, wave) * p.T;
+  if (p.N == 0 || longest <= p.least) return;
+  // Where all sequences are alike, all segments in one wave; else half a wave's share, which packs better.
+  const int64_t alike = p.cu ? (p.N == 1 ? p.tokens : 0) : p.T, each = wave / (p.N * blocks);
+  const int64_t chunks = alike && each ? cdiv(cdiv(alike, C), each) : cdiv(even, 2);
+  p.L = C * std::max<int64_t>(4, chunks);
+  if (!p.cu && p.L >= p.T) p.L = 0;
 }
 
 template <typename T>
@@ -277,7 +307,8 @@ int run(LaArgs p, int passes, const LaPass *st_pass, int nstates, const int *fro
   p.mode = kWhole;
   int widest = 1;
   for (int i = 0; i < passes; ++i) widest = std::max(widest, (int)cdiv(p.pass[i].c.D, kCols));
-  p.L = segment_length(p, tc ? passes : passes * widest);
+  if (tc) cut(p, passes, kSMs, 10);
+  else cut(p, passes * widest, 2 * kSMs, 3);
   if (!p.L) return launch(p, passes, dtype, tc, st);
   p.slots = slot_count(p.tokens, p.N, p.L);
   const int64_t one = p.slots * p.HV * p.KV;
@@ -296,7 +327,7 @@ int run(LaArgs p, int passes, const LaPass *st_pass, int nstates, const int *fro
     rc = launched("la_carry_kernel");
   }
   p.mode = kFromStates;
-  for (int i = 0; i < passes; ++i) p.pass[i].s_in = (float *)base + from[i] * one;
+  for (int i = 0; i < passes; ++i) p.pass[i].carried = (float *)base + from[i] * one;
   if (rc == GDR_OK) rc = launch(p, passes, dtype, tc, st);
   return scratch_end(base, st, "linear attention states", rc);
 }
@@ -430,7 +461,7 @@ int gdr_la_fwd(const gdr_la_desc *desc, const void *q, const void *k, const void
   LaArgs p = base_args(d, g, cu_seqlens, status);
   const int G = (int)(d.HV / d.H);
   const LaRows rq{q, d.ld_q, (int)d.K, G}, rk{k, d.ld_k, (int)d.K, G}, rv{v, d.ld_v, (int)d.V, 1};
-  p.pass[0] = {rq, rk, rv, o, h0, ht, d.V, 1, d.scale, d.scale, 1.f, 0, 0};
+  p.pass[0] = {rq, rk, rv, o, h0, nullptr, ht, d.V, 1, d.scale, d.scale, 1.f, 0, 0};
   const LaPass state = p.pass[0];
   const int from[1] = {0};
   return run(p, 1, &state, 1, from, d.dtype, (cudaStream_t)stream);
@@ -462,21 +493,17 @@ int gdr_la_bwd(const gdr_la_desc *desc, const void *q, const void *k, const void
       rd{d_o, d.ld_do, (int)d.V, 1};
   const int parts = base != nullptr;
   // passes of the same direction side by side: dk and dv read the same rows
-  p.pass[0] = {rk, rq, rd, dv, dht, dh0, d.V, 1, d.scale, 1.f, d.scale, 1, 0};
-  p.pass[1] = {rv, rd, rq, parts ? pk : dk, dht, nullptr, 1, d.V, d.scale, 1.f, d.scale, 1, parts};
-  p.pass[2] = {rd, rv, rk, parts ? pq : dq, h0, nullptr, 1, d.V, d.scale, d.scale, 1.f, 0, parts};
-  LaPass states[2] = {p.pass[0], {rq, rk, rv, nullptr, h0, nullptr, d.V, 1, d.scale, d.scale, 1.f, 0, 0}};
+  p.pass[0] = {rk, rq, rd, dv, dht, nullptr, dh0, d.V, 1, d.scale, 1.f, d.scale, 1, 0};
+  p.pass[1] = {rv, rd, rq, parts ? pk : dk, dht, nullptr, nullptr, 1, d.V, d.scale, 1.f, d.scale, 1, parts};
+  p.pass[2] = {rd, rv, rk, parts ? pq : dq, h0, nullptr, nullptr, 1, d.V, d.scale, d.scale, 1.f, 0, parts};
+  LaPass states[2] = {p.pass[0], {rq, rk, rv, nullptr, h0, nullptr, nullptr, d.V, 1, d.scale, d.scale, 1.f, 0, 0}};
   const int from[3] = {0, 0, 1};
   rc = run(p, 3, states, 2, from, d.dtype, st);
   if (!base) return rc;
   if (rc == GDR_OK) {
-    const int64_t m = n / G;
-    const dim3 grid((unsigned)cdiv(m, 256), 2);
     const SeqCheck check{cu_seqlens, d.N, d.B * d.T, status};
-    if (d.dtype == GDR_BF16)
-      la_sum_kernel<<<grid, 256, 0, st>>>(pq, pk, (__nv_bfloat16 *)dq, (__nv_bfloat16 *)dk, m, G, (int)d.K, check);
-    else la_sum_kernel<<<grid, 256, 0, st>>>(pq, pk, (float *)dq, (float *)dk, m, G, (int)d.K, check);
-    rc = launched("la_sum_kernel");
+    rc = d.dtype == GDR_BF16 ? launch_sum<__nv_bfloat16>(pq, pk, dq, dk, n / G, G, (int)d.K, check, st)
+                             : launch_sum<float>(pq, pk, dq, dk, n / G, G, (int)d.K, check, st);
   }
   return scratch_end(base, st, "parts of dq and dk", rc);
 }

@@ -23,7 +23,10 @@
 //
 // Segments.  Few heads and long sequences leave multiprocessors idle, so a
 // sequence is cut into segments of L tokens: one launch forms each segment's own
-// state, one carries them along the sequence, one runs the passes from there.
+// state, one carries them along the sequence, one runs the passes from there.  Of a
+// packed batch the lengths are on the device, so the blocks themselves see whether
+// its longest sequence is worth that; if not, each sequence is one segment and the
+// first launch finds nothing to do.
 #pragma once
 
 #include "gdr_layer.cuh"
@@ -43,7 +46,8 @@ struct LaRows {
 struct LaPass {
   LaRows a, b, c;
   void *out;          // [tokens, HV, Dc] contiguous; fp32 where out_f32, else of the inputs' type
-  const float *s_in;  // state that a sequence (or segment) starts from, null: zero
+  const float *s_in;  // states that the sequences start from, null: zero
+  const float *carried;  // in kFromStates, where sequences are cut: those that the segments start from
   float *s_out;       // state behind the sequence's last chunk (or the segment's own), null: not wanted
   int64_t si, sj;     // element (i, j) of a Da x Dc state lies at i si + j sj
   float pscale, iscale, wscale;
@@ -61,6 +65,7 @@ struct LaArgs {
   int64_t N, T, HV, tokens;
   int64_t KV;    // elements of a state
   int64_t L;     // tokens in a segment, a multiple of C (unused in kWhole)
+  int64_t least; // sequences are cut where the longest has more tokens than this
   int64_t slots; // segment slots over all sequences
   int mode;
 };
@@ -75,21 +80,42 @@ __device__ __forceinline__ int64_t first_slot(const LaArgs &p, int64_t n) {
   return (p.cu ? p.cu[n] : n * p.T) / p.L + n;
 }
 
+// seqlens_ok, and whether sequences are cut.  Every thread of the block calls it.
+__device__ __forceinline__ bool sequences_ok(const LaArgs &p, bool &cut) {
+  __shared__ unsigned longest;
+  cut = p.mode != kWhole;
+  if (!p.cu) return true;
+  if (threadIdx.x == 0) longest = 0;
+  if (!seqlens_ok(p.cu, p.N, p.tokens, p.status)) return false;  // (a barrier)
+  if (!cut) return true;
+  unsigned most = 0;
+  for (int64_t n = threadIdx.x; n < p.N; n += blockDim.x) most = max(most, (unsigned)(p.cu[n + 1] - p.cu[n]));
+  if (most > p.least) atomicMax(&longest, most);
+  __syncthreads();
+  cut = longest > p.least;
+  return true;
+}
+
 struct Segment {
   int64_t n;         // sequence
   int64_t bos, eos;  // tokens of the segment
   int first, last;   // in the pass's order of time
   bool some;         // false: the slot is not in use
 };
-__device__ __forceinline__ Segment segment_of(const LaArgs &p, int64_t slot, bool backwards) {
+__device__ __forceinline__ int64_t segments_in(const LaArgs &p, int64_t len, bool cut) {
+  return cut && len > 0 ? (len + p.L - 1) / p.L : 1;
+}
+// Every thread of the block calls it.  Uncut, the longest sequences come first, so that none of them starts last.
+__device__ __forceinline__ Segment segment_of(const LaArgs &p, int64_t slot, bool backwards, bool cut) {
   Segment s;
-  if (p.mode == kWhole) {
-    const SeqRange r = seq_range(p.cu, slot, p.T);
-    s.n = slot;
+  if (!cut) {
+    s.some = slot < p.N;
+    if (!s.some) return s;
+    s.n = seq_of_rank(p.cu, p.N, slot);
+    const SeqRange r = seq_range(p.cu, s.n, p.T);
     s.bos = r.bos;
     s.eos = r.eos;
     s.first = s.last = 1;
-    s.some = true;
     return s;
   }
   int64_t lo = 0, hi = p.N;  // first_slot(lo) <= slot < first_slot(hi)
@@ -100,14 +126,22 @@ __device__ __forceinline__ Segment segment_of(const LaArgs &p, int64_t slot, boo
   }
   const SeqRange r = seq_range(p.cu, lo, p.T);
   const int64_t len = r.eos - r.bos, i = slot - first_slot(p, lo);
-  const int64_t segs = len > 0 ? (len + p.L - 1) / p.L : 1;
+  const int64_t segs = segments_in(p, len, cut);
   s.n = lo;
   s.bos = r.bos + i * p.L;
-  s.eos = r.eos - s.bos < p.L ? r.eos : s.bos + p.L;
+  s.eos = i == segs - 1 ? r.eos : s.bos + p.L;
   s.some = i < segs;
   s.first = backwards ? i == segs - 1 : i == 0;
   s.last = backwards ? i == 0 : i == segs - 1;
   return s;
+}
+
+// The state that a block starts from (null: zero).
+__device__ __forceinline__ const float *entering(const LaArgs &p, const LaPass &q, const Segment &s, int64_t slot,
+                                                 int64_t hv, bool cut) {
+  if (p.mode == kStates) return nullptr;
+  if (cut) return q.carried + (slot * p.HV + hv) * p.KV;
+  return q.s_in ? q.s_in + (s.n * p.HV + hv) * p.KV : nullptr;
 }
 
 // r^n of a whole number n >= 0; r^0 is 1 for every g, -inf (each token forgets all before it) included.

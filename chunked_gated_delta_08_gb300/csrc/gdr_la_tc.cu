@@ -63,7 +63,7 @@ constexpr uint32_t SZ_TILE = 16384, SZ_PANEL = 8192;
 constexpr uint32_t SZ_STAGE = 3 * SZ_TILE;  // A | B | C
 constexpr uint32_t OFF_LO = kStages * SZ_STAGE;   // lower halves of B', two buffers
 constexpr uint32_t OFF_P = OFF_LO + 2 * SZ_TILE;  // P, two buffers
-constexpr uint32_t OFF_Y = OFF_P + 2 * SZ_PANEL;  // y on its way out, two buffers
+constexpr uint32_t OFF_Y = OFF_P + 2 * SZ_PANEL;  // y on its way out: two buffers of bf16, one of fp32 (four panels of 32 channels)
 constexpr uint32_t OFF_SMALL = OFF_Y + 2 * SZ_TILE;
 
 // TMEM columns
@@ -116,10 +116,13 @@ struct Maps {
   CUtensorMap a[3], b[3], c[3], y[3];
 };
 
+// PARTS: some of the passes write fp32 parts (grouped value heads); their code costs the others 8 %.
+template <bool PARTS>
 __global__ void __launch_bounds__(kTcThreads, 1)
     la_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LaArgs p, int passes, int64_t items) {
   extern __shared__ uint8_t smem_raw[];
-  if (!seqlens_ok(p.cu, p.N, p.cu ? p.tokens : p.T, p.status)) return;
+  bool cut;
+  if (!sequences_ok(p, cut)) return;
   uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Small &S = *reinterpret_cast<Small *>(sm + OFF_SMALL);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -130,10 +133,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int64_t item = unit < side * items ? unit / side : unit - side * items;
   const LaPass &q = p.pass[pi];
   const int64_t hv = item % p.HV, slot = item / p.HV;
-  if (p.mode == kWhole && slot >= p.N) return;  // no sequences: the block has checked cu_seqlens
   const bool bw = q.backwards, states = p.mode == kStates;
   const bool exact = q.s_out != nullptr;  // B' in two parts
-  const Segment s = segment_of(p, slot, bw);
+  const Segment s = segment_of(p, slot, bw, cut);
   if (!s.some || (states && s.last)) return;  // nobody reads the state behind the last segment
   const int Da = q.a.D, Dc = q.c.D, ka = Da > 64 ? 2 : 1, kc = Dc > 64 ? 2 : 1;
   const int64_t len = s.eos - s.bos;
@@ -180,9 +182,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t aS = lane_addr + TM_S + col0, aSb = lane_addr + TM_SB + col0 / 2;
     const bool mine = j < Dc;
     {
-      const float *from = states || !q.s_in || !mine
-                              ? nullptr
-                              : q.s_in + ((p.mode == kWhole ? s.n : slot) * p.HV + hv) * p.KV + j * q.sj;
+      const float *from = mine ? entering(p, q, s, slot, hv, cut) : nullptr;
+      if (from) from += j * q.sj;
 #pragma unroll 1
       for (int i0 = 0; i0 < cols; i0 += 16) {
         float r[16];
@@ -321,6 +322,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int m = lane >> 3, stok = 32 * half + 8 * (m >> 1) + (lane & 7);
     float f[4][2];
     int fn = 0;  // the rows that f is for
+    const bool parts = PARTS && q.out_f32;
 #pragma unroll 1
     for (int c = 0; c < (states ? 0 : nch); ++c) {
       const int buf = c & 1;
@@ -335,8 +337,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         fn = n;
       }
-      const bool stage = n == C && !q.out_f32;
-      if (gt == 0) bulk_wait_read<1>();  // the store before the last has read its buffer
+      const bool stage = n == C;
+      if (gt == 0) {  // the store before this one's buffer has read it
+        if (parts) bulk_wait_read<0>();
+        else bulk_wait_read<1>();
+      }
       named_bar(kBarOut, 256);
       wait(S.b_o, c & 1);
       tc_fence_after();
@@ -359,7 +364,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[i][e] = fmaf(y[i][e], f[2 * i + (e >> 2)][e & 1], x[i][e]);
         if (w >= 2 * kc) continue;
-        if (stage) {
+        // channels of this thread: d0 and d0 + 8
+        const int d0 = 32 * w + 16 * h + (lane >> 2);
+        if (stage && parts) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int tok = tok0 + 16 * i + 8 * (e >> 2) + (e & 1), d = d0 + ((e >> 1) & 1) * 8;
+              *reinterpret_cast<float *>(sY + w * SZ_PANEL + sw128_chunk_off(tok, (d >> 2) & 7) + (d & 3) * 4) = x[i][e];
+            }
+        } else if (stage) {
           const int chunk = (32 * w + 16 * h + 8 * (m & 1)) >> 3;
           const uint32_t at = smem_u32(sY + buf * SZ_TILE + (chunk >> 3) * SZ_PANEL) + sw128_chunk_off(stok, chunk & 7);
 #pragma unroll
@@ -367,8 +382,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             stmatrix_x4_trans(at + i * 2048, gdr::pack_bf16(x[i][0], x[i][1]), gdr::pack_bf16(x[i][2], x[i][3]),
                               gdr::pack_bf16(x[i][4], x[i][5]), gdr::pack_bf16(x[i][6], x[i][7]));
         } else {
-          // channels of this thread: d0 and d0 + 8
-          const int d0 = 32 * w + 16 * h + (lane >> 2);
           const int64_t t0 = chunk_start(c);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
@@ -377,7 +390,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               const int tok = tok0 + 16 * i + 8 * (e >> 2) + (e & 1), d = d0 + ((e >> 1) & 1) * 8;
               if (tok < n && d < Dc) {
                 const int64_t at = ((t0 + tok) * p.HV + hv) * Dc + d;
-                if (q.out_f32) static_cast<float *>(q.out)[at] = x[i][e];
+                if (parts) static_cast<float *>(q.out)[at] = x[i][e];
                 else static_cast<__nv_bfloat16 *>(q.out)[at] = __float2bfloat16_rn(x[i][e]);
               }
             }
@@ -387,8 +400,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       named_bar(kBarOut, 256);
       if (gt == 0) {
         if (stage) {
-          for (int i = 0; i < kc; ++i)
-            tma_store_3d(&maps.y[pi], smem_u32(sY + buf * SZ_TILE + i * SZ_PANEL), 64 * i, (int)hv, (int)chunk_start(c));
+          const int wide = parts ? 32 : 64;  // channels of a panel
+          for (int i = 0; i < kc * 64 / wide; ++i)
+            tma_store_3d(&maps.y[pi], smem_u32(sY + (parts ? 0 : buf * SZ_TILE) + i * SZ_PANEL), wide * i, (int)hv,
+                         (int)chunk_start(c));
         }
         bulk_commit();  // one group a chunk, where nothing is staged an empty one
       }
@@ -500,15 +515,15 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// [tokens, heads, D] with tokens ld apart, in boxes of 64 channels of one head and 64 tokens; channels
-// from D on read as zeros and are not written.
-int make_map(CUtensorMap *m, const LaRows &r, int64_t heads, int64_t tokens) {
+// [tokens, heads, D] with tokens ld apart, in boxes of 128 bytes of one head's channels and 64 tokens;
+// channels from D on read as zeros and are not written.
+int make_map(CUtensorMap *m, const LaRows &r, int64_t heads, int64_t tokens, bool f32 = false) {
   const auto fn = encode_fn();
   if (!fn) return set_error(GDR_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
   const cuuint64_t dims[3] = {(cuuint64_t)r.D, (cuuint64_t)heads, (cuuint64_t)tokens};
-  const cuuint64_t strides[2] = {(cuuint64_t)r.D * 2, (cuuint64_t)r.ld * 2};
-  const cuuint32_t box[3] = {64, 1, 64}, es[3] = {1, 1, 1};
-  const CUresult e = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(r.p), dims, strides, box, es,
+  const cuuint64_t el = f32 ? 4 : 2, strides[2] = {(cuuint64_t)r.D * el, (cuuint64_t)r.ld * el};
+  const cuuint32_t box[3] = {f32 ? 32u : 64u, 1, 64}, es[3] = {1, 1, 1};
+  const CUresult e = fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(r.p), dims, strides, box, es,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return e == CUDA_SUCCESS ? GDR_OK : set_error(GDR_ERR_CUDA, "cuTensorMapEncodeTiled failed");
@@ -538,14 +553,16 @@ int launch_tc(const LaArgs &p, int passes, cudaStream_t st) {
     if ((rc = map(&maps.b[i], q.b)) != GDR_OK || (rc = map(&maps.c[i], q.c)) != GDR_OK) return rc;
     if (p.mode == kStates) continue;
     if ((rc = map(&maps.a[i], q.a)) != GDR_OK) return rc;
-    if (!q.out_f32 && (rc = map(&maps.y[i], y)) != GDR_OK) return rc;
+    if ((rc = make_map(&maps.y[i], y, p.HV, p.tokens, q.out_f32)) != GDR_OK) return rc;
   }
   const int64_t items = std::max<int64_t>(1, (p.mode == kWhole ? p.N : p.slots) * p.HV);
   if (items * passes > 0x7fffffff) return set_error(GDR_ERR_SHAPE, "too many sequences and heads for one launch");
-  const cudaError_t e =
-      cudaFuncSetAttribute(la_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+  bool parts = false;
+  for (int i = 0; i < passes; ++i) parts |= p.mode != kStates && p.pass[i].out_f32;
+  const auto kernel = parts ? la_tc_kernel<true> : la_tc_kernel<false>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
   if (e != cudaSuccess) return cuda_error(e, "cudaFuncSetAttribute(la_tc_kernel)");
-  la_tc_kernel<<<(unsigned)(items * passes), kTcThreads, SMEM_BYTES, st>>>(maps, p, passes, items);
+  kernel<<<(unsigned)(items * passes), kTcThreads, SMEM_BYTES, st>>>(maps, p, passes, items);
   return launched("la_tc_kernel");
 }
 

@@ -65,7 +65,7 @@ def test_dense(gdr, dtype, B, T, H, HV, K, V):
 
 @both_types
 @pytest.mark.parametrize("K,V", [(128, 128), (36, 20)], ids=str)
-@pytest.mark.parametrize("lens", [[1000], [300, 1, 0, 513, 256, 90]], ids=str)
+@pytest.mark.parametrize("lens", [[2500], [700, 1, 0, 1300, 256, 90], [200] * 8], ids=["one", "cut", "not_worth_it"])
 def test_sequences_cut_into_segments(gdr, dtype, K, V, lens):
     """Few heads: states of segments first, then carried, then the passes from there."""
     p = ref.attention_inputs(lens, 1, 1, K, V, dtype, seed=3)
