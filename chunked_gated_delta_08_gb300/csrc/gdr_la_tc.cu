@@ -81,6 +81,12 @@ struct Small {
 constexpr uint32_t SMEM_BYTES = OFF_SMALL + sizeof(Small) + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 
+__device__ __forceinline__ uint32_t pack_f2(f2 v) {
+  float lo, hi;
+  f2_split(v, lo, hi);
+  return gdr::pack_bf16(lo, hi);
+}
+
 // One thread of a converged warp, in a form that the compiler knows to be one thread.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -119,18 +125,16 @@ struct Maps {
 // PARTS: some of the passes write fp32 parts (grouped value heads); their code costs the others 8 %.
 template <bool PARTS>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    la_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LaArgs p, int passes, int64_t items) {
+    la_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LaArgs p, int passes) {
   extern __shared__ uint8_t smem_raw[];
   bool cut;
   if (!sequences_ok(p, cut)) return;
   uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Small &S = *reinterpret_cast<Small *>(sm + OFF_SMALL);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // two passes that read the same rows run side by side (their second reads come from L2); a third follows
-  const int64_t unit = blockIdx.x;
-  const int side = passes < 2 ? 1 : 2;
-  const int pi = unit < side * items ? (int)(unit % side) : 2;
-  const int64_t item = unit < side * items ? unit / side : unit - side * items;
+  // the passes over one item run side by side: the rows that two of them read come from L2 the second time
+  const int pi = (int)(blockIdx.x % passes);
+  const int64_t item = blockIdx.x / passes;
   const LaPass &q = p.pass[pi];
   const int64_t hv = item % p.HV, slot = item / p.HV;
   const bool bw = q.backwards, states = p.mode == kStates;
@@ -213,7 +217,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (!states) tmem_st16u(aSb + (c & 1) * 64 + i0 / 2, u);
           uint32_t d[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) d[i] = __float_as_uint(fmaf(r[i], less1, r[i]));
+          for (int i = 0; i < 32; i += 2) {
+            const f2 x = f2_pack(r[i], r[i + 1]);
+            float lo, hi;
+            f2_split(f2_fma(x, f2_both(less1), x), lo, hi);
+            d[i] = __float_as_uint(lo);
+            d[i + 1] = __float_as_uint(hi);
+          }
           tmem_st32(aS + i0, d);
         }
       }
@@ -272,17 +282,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int i = 0; i < 2; ++i) tmem_ld_16x256b_x2(lane_addr + TM_SC + 64 * buf + 32 * half + 16 * i, r[i]);
         tmem_ld_wait();
         tc_fence_before();
+        if (n < C) {  // columns past the end: what lies there is not multiplied
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (32 * half + 8 * (k >> 2) + c0 + (k & 1) >= n) r[k >> 3][k & 7] = 0.f;
+        }
         uint8_t *P = sP + buf * SZ_PANEL;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          float v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[e] = r[b >> 1][4 * (b & 1) + e] * f[b][e];
-            if (n < C && 32 * half + 8 * b + c0 + (e & 1) >= n) v[e] = 0.f;
-          }
-          *reinterpret_cast<uint32_t *>(P + sw128_chunk_off(r0, 4 * half + b) + 2 * c0) = gdr::pack_bf16(v[0], v[1]);
-          *reinterpret_cast<uint32_t *>(P + sw128_chunk_off(r0 + 8, 4 * half + b) + 2 * c0) = gdr::pack_bf16(v[2], v[3]);
+          const float *x = r[b >> 1] + 4 * (b & 1);
+          uint8_t *to = P + sw128_chunk_off(r0, 4 * half + b) + 2 * c0;
+          *reinterpret_cast<uint32_t *>(to) = pack_f2(f2_mul(f2_pack(x[0], x[1]), f2_pack(f[b][0], f[b][1])));
+          *reinterpret_cast<uint32_t *>(to + 1024) = pack_f2(f2_mul(f2_pack(x[2], x[3]), f2_pack(f[b][2], f[b][3])));
         }
         fence_proxy_async_smem();
         arrive(S.b_p[buf]);
@@ -302,9 +313,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           uint32_t h[4], l[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float x = v[2 * e] * wt, y = v[2 * e + 1] * wt;
-            h[e] = gdr::pack_bf16(x, y);
-            l[e] = gdr::pack_bf16(x - __uint_as_float(h[e] << 16), y - __uint_as_float(h[e] & 0xffff0000u));
+            const f2 x = f2_mul(f2_pack(v[2 * e], v[2 * e + 1]), f2_both(wt));
+            h[e] = pack_f2(x);
+            l[e] = pack_f2(f2_fma(f2_pack(__uint_as_float(h[e] << 16), __uint_as_float(h[e] & 0xffff0000u)), f2_both(-1.f), x));
           }
           st_sw128_chunk(hi, row, ch0 + i, make_uint4(h[0], h[1], h[2], h[3]));
           if (exact) st_sw128_chunk(lo, row, ch0 + i, make_uint4(l[0], l[1], l[2], l[3]));
@@ -362,7 +373,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[i][e] = fmaf(y[i][e], f[2 * i + (e >> 2)][e & 1], x[i][e]);
+          for (int e = 0; e < 8; e += 2) {
+            const float *fe = f[2 * i + (e >> 2)];
+            f2_split(f2_fma(f2_pack(y[i][e], y[i][e + 1]), f2_pack(fe[0], fe[1]), f2_pack(x[i][e], x[i][e + 1])), x[i][e],
+                     x[i][e + 1]);
+          }
         if (w >= 2 * kc) continue;
         // channels of this thread: d0 and d0 + 8
         const int d0 = 32 * w + 16 * h + (lane >> 2);
@@ -562,7 +577,7 @@ int launch_tc(const LaArgs &p, int passes, cudaStream_t st) {
   const auto kernel = parts ? la_tc_kernel<true> : la_tc_kernel<false>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
   if (e != cudaSuccess) return cuda_error(e, "cudaFuncSetAttribute(la_tc_kernel)");
-  kernel<<<(unsigned)(items * passes), kTcThreads, SMEM_BYTES, st>>>(maps, p, passes, items);
+  kernel<<<(unsigned)(items * passes), kTcThreads, SMEM_BYTES, st>>>(maps, p, passes);
   return launched("la_tc_kernel");
 }
 
