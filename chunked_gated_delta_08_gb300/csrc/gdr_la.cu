@@ -12,8 +12,13 @@ namespace {
 // --------------------------------------------------------------------- any type, any size
 // One block per (segment, value head, 32 columns of c), 8 warps.  Operands lie in
 // shared memory in fp32; products are warp-level tensor-core products of values
-// split into three tf32 parts (2^-21 of a product; bf16 inputs are exact in one).
-// Rows past the segment's end and channels past the width are zeros in shared memory.
+// split into two tf32 parts (2^-21 of a product is lost; bf16 inputs are exact in one
+// part).  The tensor cores cut off what they add to an accumulator, so the large
+// products and the small ones have one each, and a chunk's part of the state is
+// summed by itself: 4e-7 of a state after 16384 tokens, where one accumulator for
+// all left 5e-6.  Rows past the segment's end and channels past the width are zeros in
+// shared memory.  Two blocks a multiprocessor are bound by issue (40 %) and the
+// tensor pipe (37 %): 2 x 2048 x 8 x 64 fp32 take 79 us in three launches.
 constexpr int kThreads = 256;
 constexpr int kCols = 32;       // columns of c in a block
 constexpr int LDC = kCols + 4;  // row strides in shared memory, chosen off multiples of 32 banks
@@ -44,6 +49,51 @@ __device__ __forceinline__ void load_tile(float *dst, int ld, const LaRows &r, i
       dst[row * ld + c] = row < rows && c < cols ? to_f32(src[row * r.ld + c]) : 0.f;
     }
   }
+}
+
+// x in tf32 parts: hi its first 11 bits, lo 11 of the 13 that are left (2^-22 of x is lost; cut off, not rounded: adding
+// to the bits would turn some NaN into numbers).  EXACT: x has no more than 8 bits.
+template <bool EXACT>
+struct Split {
+  uint32_t hi, lo;
+  __device__ __forceinline__ explicit Split(float x) {
+    if constexpr (EXACT) {
+      hi = __float_as_uint(x);
+      lo = 0;
+    } else {
+      hi = __float_as_uint(x) & 0xffffe000u;
+      lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
+    }
+  }
+};
+// large += hi hi, small += the other products; a 16 x 8, b 8 x 8 fragments.
+template <bool EA, bool EB>
+__device__ __forceinline__ void mma_parts(float (&large)[4], float (&small)[4], const Split<EA> (&a)[4],
+                                          const Split<EB> (&b)[2]) {
+  if constexpr (!EA && !EB) sm100::mma_tf32(small, a[0].lo, a[1].lo, a[2].lo, a[3].lo, b[0].lo, b[1].lo);
+  if constexpr (!EA) sm100::mma_tf32(small, a[0].lo, a[1].lo, a[2].lo, a[3].lo, b[0].hi, b[1].hi);
+  if constexpr (!EB) sm100::mma_tf32(small, a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[0].lo, b[1].lo);
+  sm100::mma_tf32(large, a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[0].hi, b[1].hi);
+}
+// NT tiles of 8 columns: acc += a b over K, K a multiple of 8; fa(i, k) of 16 rows, fb(k, j) of 8 NT columns.
+template <bool EA, bool EB, int NT, typename FA, typename FB>
+__device__ __forceinline__ void tile_product(float (&acc)[NT][4], int K, FA fa, FB fb) {
+  const int lane = threadIdx.x & 31, gr = lane >> 2, tg = lane & 3;
+  float small[NT][4] = {};
+#pragma unroll 2
+  for (int k = 0; k < K; k += 8) {
+    const Split<EA> a[4] = {Split<EA>(fa(gr, k + tg)), Split<EA>(fa(gr + 8, k + tg)), Split<EA>(fa(gr, k + tg + 4)),
+                            Split<EA>(fa(gr + 8, k + tg + 4))};
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const Split<EB> b[2] = {Split<EB>(fb(k + tg, 8 * j + gr)), Split<EB>(fb(k + tg + 4, 8 * j + gr))};
+      mma_parts(acc[j], small[j], a, b);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[j][e] += small[j][e];
 }
 
 template <typename T>
@@ -89,20 +139,13 @@ __global__ void __launch_bounds__(kThreads) la_any_kernel(const __grid_constant_
     load_tile<T>(Cm, LDC, q.c, t0, (int)hv, n, col0, cols, kCols, vc);
     if (tid < C) wt[tid] = tid < n ? pw[bw ? tid + 1 : n - 1 - tid] * q.wscale : 0.f;
     __syncthreads();
+    constexpr bool EX = sizeof(T) == 2;
     if (p.mode != kStates) {
       // P = (A B^T) r^|i-j|: a warp takes 16 rows and 32 columns
       const int r0 = (warp >> 1) * 16, c0 = (warp & 1) * 32;
       float acc[4][4] = {};
-      for (int k = 0; k < D; k += 8) {
-        const float *ap = A + (r0 + gr) * LDA + k + tg;
-        const float a[4] = {ap[0], ap[8 * LDA], ap[4], ap[8 * LDA + 4]};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float *bp = B + (c0 + 8 * j + gr) * LDA + k + tg;
-          const float b[2] = {bp[0], bp[4]};
-          sm100::mma_3xtf32(acc[j], a, b);
-        }
-      }
+      tile_product<EX, EX>(acc, D, [&](int i, int k) { return A[(r0 + i) * LDA + k]; },
+                           [&](int k, int j) { return B[(c0 + j) * LDA + k]; });
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
 #pragma unroll
@@ -114,74 +157,38 @@ __global__ void __launch_bounds__(kThreads) la_any_kernel(const __grid_constant_
       }
       // y = iscale r^e(i) A S + P C: a warp takes 16 rows and 16 columns
       const int oc = (warp & 1) * 16;
-      float o[2][4] = {};
-      for (int k = 0; k < D; k += 8) {
-        const float *ap = A + (r0 + gr) * LDA + k + tg;
-        const float a[4] = {ap[0], ap[8 * LDA], ap[4], ap[8 * LDA + 4]};
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float *bp = S + (k + tg) * LDC + oc + 8 * j + gr;
-          const float b[2] = {bp[0], bp[4 * LDC]};
-          sm100::mma_3xtf32(o[j], a, b);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = r0 + gr + (e >> 1) * 8;
-          o[j][e] *= r < n ? pw[bw ? n - 1 - r : r + 1] * q.iscale : 0.f;
-        }
+      float o[2][4] = {}, o1[2][4] = {};
+      tile_product<EX, false>(o, D, [&](int i, int k) { return A[(r0 + i) * LDA + k]; },
+                              [&](int k, int j) { return S[k * LDC + oc + j]; });
       __syncthreads();
-      for (int k = 0; k < C; k += 8) {
-        const float *ap = P + (r0 + gr) * LDP + k + tg;
-        const float a[4] = {ap[0], ap[8 * LDP], ap[4], ap[8 * LDP + 4]};
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float *bp = Cm + (k + tg) * LDC + oc + 8 * j + gr;
-          const float b[2] = {bp[0], bp[4 * LDC]};
-          sm100::mma_3xtf32(o[j], a, b);
-        }
-      }
+      tile_product<false, EX>(o1, C, [&](int i, int k) { return P[(r0 + i) * LDP + k]; },
+                              [&](int k, int j) { return Cm[k * LDC + oc + j]; });
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int r = r0 + gr + (e >> 1) * 8, c = oc + 8 * j + 2 * tg + (e & 1);
           if (r < n && c < cols) {
+            const float y = fmaf(o[j][e], pw[bw ? n - 1 - r : r + 1] * q.iscale, o1[j][e]);
             const int64_t to = ((t0 + r) * p.HV + hv) * Dc + col0 + c;
-            if (q.out_f32) static_cast<float *>(q.out)[to] = o[j][e];
-            else static_cast<T *>(q.out)[to] = from_f32<T>(o[j][e]);
+            if (q.out_f32) static_cast<float *>(q.out)[to] = y;
+            else static_cast<T *>(q.out)[to] = from_f32<T>(y);
           }
         }
     }
     // S = r^n S + (w B)^T C: a warp takes rows of S, 16 at a time
     const float less1 = decay_less1(g, n);
     for (int r0 = warp * 16; r0 < D; r0 += 8 * 16) {
-      float acc[4][4];
+      float acc[4][4] = {};
+      tile_product<false, EX>(acc, C, [&](int i, int k) { return B[k * LDA + r0 + i] * wt[k]; },
+                              [&](int k, int j) { return Cm[k * LDC + j]; });
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float old = S[(r0 + gr + (e >> 1) * 8) * LDC + 8 * j + 2 * tg + (e & 1)];
-          acc[j][e] = fmaf(old, less1, old);
+          float &at = S[(r0 + gr + (e >> 1) * 8) * LDC + 8 * j + 2 * tg + (e & 1)];
+          at = fmaf(at, less1, at) + acc[j][e];
         }
-      for (int k = 0; k < C; k += 8) {
-        const float *ap = B + (k + tg) * LDA + r0 + gr;
-        const float w0 = wt[k + tg], w1 = wt[k + tg + 4];
-        const float a[4] = {ap[0] * w0, ap[8] * w0, ap[4 * LDA] * w1, ap[4 * LDA + 8] * w1};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float *bp = Cm + (k + tg) * LDC + 8 * j + gr;
-          const float b[2] = {bp[0], bp[4 * LDC]};
-          sm100::mma_3xtf32(acc[j], a, b);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          S[(r0 + gr + (e >> 1) * 8) * LDC + 8 * j + 2 * tg + (e & 1)] = acc[j][e];
     }
   }
   if (!q.s_out || (p.mode != kStates && !s.last)) return;
@@ -195,34 +202,39 @@ __global__ void __launch_bounds__(kThreads) la_any_kernel(const __grid_constant_
 
 // ------------------------------------------------------------------------------ carry, sums
 // The states that segments start from, in place of their own: over a sequence's
-// segments in the pass's order, S enters and leaves as r^len S + own.  One thread
-// per element of a head's state, eight segments' elements on their way at once
-// (74 segments one after the other took 50 us).
+// segments in the pass's order, S enters and leaves as r^len S + own.  A thread has
+// VEC elements of a head's state, and eight segments' of them on their way at once (74
+// segments one after the other took 50 us).
+template <int VEC>
 __global__ void __launch_bounds__(256) la_carry_kernel(const __grid_constant__ LaArgs p) {
   bool cut;
   if (!sequences_ok(p, cut) || !cut) return;
   const LaPass &q = p.pass[blockIdx.z];
-  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * VEC;
   const int64_t n = blockIdx.y / p.HV, hv = blockIdx.y % p.HV;
   if (e >= p.KV) return;
   const SeqRange r = seq_range(p.cu, n, p.T);
   const int64_t len = r.eos - r.bos, segs = segments_in(p, len, true);
   const float g = p.g[hv];
-  float S = q.s_in ? q.s_in[(n * p.HV + hv) * p.KV + e] : 0.f;
+  float S[VEC] = {};
+  if (q.s_in) load_vec<VEC>(q.s_in + (n * p.HV + hv) * p.KV + e, S);
   const int64_t step = p.HV * p.KV * (q.backwards ? -1 : 1);
   float *own = q.s_out + ((first_slot(p, n) + (q.backwards ? segs - 1 : 0)) * p.HV + hv) * p.KV + e;
   const float full = decay_less1(g, p.L), tail = decay_less1(g, len - (segs - 1) * p.L);
   constexpr int kAhead = 8;
   for (int64_t u0 = 0; u0 < segs; u0 += kAhead, own += kAhead * step) {
-    float mine[kAhead];
+    float mine[kAhead][VEC] = {};
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) mine[i] = u0 + i + 1 < segs ? own[i * step] : 0.f;  // of the last there is none
+    for (int i = 0; i < kAhead; ++i)
+      if (u0 + i + 1 < segs) load_vec<VEC>(own + i * step, mine[i]);  // of the last there is none
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (u0 + i < segs) {
-        own[i * step] = S;
+        store_vec<VEC>(own + i * step, S);
         // the ragged segment is a sequence's last: going back, the first of the pass
-        S = fmaf(S, q.backwards && u0 + i == 0 ? tail : full, S) + mine[i];
+        const float less1 = q.backwards && u0 + i == 0 ? tail : full;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) S[j] = fmaf(S[j], less1, S[j]) + mine[i][j];
       }
     }
   }
@@ -323,7 +335,10 @@ int run(LaArgs p, int passes, const LaPass *st_pass, int nstates, const int *fro
   }
   rc = launch(s, nstates, dtype, tc_takes(s, nstates, dtype), st);
   if (rc == GDR_OK) {
-    la_carry_kernel<<<dim3((unsigned)cdiv(p.KV, 256), (unsigned)(p.N * p.HV), nstates), 256, 0, st>>>(s);
+    bool vec = p.KV % 4 == 0;
+    for (int i = 0; i < nstates; ++i) vec = vec && is_aligned16(s.pass[i].s_in);
+    const auto kernel = vec ? la_carry_kernel<4> : la_carry_kernel<1>;
+    kernel<<<dim3((unsigned)cdiv(p.KV, vec ? 1024 : 256), (unsigned)(p.N * p.HV), nstates), 256, 0, st>>>(s);
     rc = launched("la_carry_kernel");
   }
   p.mode = kFromStates;

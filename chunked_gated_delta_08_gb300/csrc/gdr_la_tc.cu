@@ -160,6 +160,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (uint64_t *b = S.b_p; b <= &S.b_ofree; ++b) mbar_init(smem_u32(b), 8);
     fence_mbar_init();
   }
+  if (tid == 32 * kProducer) {
+    if (!states) tma_prefetch_desc(&maps.a[pi]);
+    tma_prefetch_desc(&maps.b[pi]);
+    tma_prefetch_desc(&maps.c[pi]);
+  }
   if (warp == 0) {
     tmem_alloc(smem_u32(&S.tmem_slot), TM_COLS);
     tmem_relinquish();
