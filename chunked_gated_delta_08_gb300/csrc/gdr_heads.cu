@@ -66,8 +66,11 @@ struct Place {
   }
 };
 
-// Cosines and sines of a thread's RUN pairs.
-template <int RUN, bool NEAR>
+// A thread's 2 RUN channels in packed pairs: those of the first run, then of the second.  (Single fp32 operations
+// and selects made 267 instructions of four rows of 128, and issue the bound: 51 %.)
+//
+// Cosines and sines of a thread's RUN pairs; BACK turns back.
+template <int RUN, bool NEAR, bool BACK>
 struct Turn {
   float c[RUN], s[RUN];
   __device__ __forceinline__ void load_run(const HeadArgs &p, int64_t pos, int first, int at, int n) {
@@ -76,17 +79,14 @@ struct Turn {
     for (int i = 0; i < RUN; i += 2) {
       if (i < n) {
         const float2 u = *reinterpret_cast<const float2 *>(pc + i), v = *reinterpret_cast<const float2 *>(ps + i);
-        c[at + i] = u.x; c[at + i + 1] = u.y;
-        s[at + i] = v.x; s[at + i + 1] = v.y;
+        c[at + i] = u.x;
+        c[at + i + 1] = u.y;
+        s[at + i] = BACK ? -v.x : v.x;
+        s[at + i + 1] = BACK ? -v.y : v.y;
       }
     }
   }
   __device__ __forceinline__ Turn(const HeadArgs &p, const Place<RUN, NEAR> &l, int64_t pos) {
-#pragma unroll
-    for (int i = 0; i < RUN; ++i) {
-      c[i] = 1.f;
-      s[i] = 0.f;
-    }
     if constexpr (NEAR) {
       if (l.turned0) load_run(p, pos, l.c0 / 2, 0, RUN / 2);
       if (l.turned1) load_run(p, pos, l.c1 / 2, RUN / 2, RUN / 2);
@@ -94,25 +94,37 @@ struct Turn {
       load_run(p, pos, l.c0, 0, RUN);
     }
   }
-  // v: the first run, then the second.  BACK turns back.  Channels that are not turned are not touched.
-  template <bool BACK>
-  __device__ __forceinline__ void apply(float (&v)[2 * RUN], const Place<RUN, NEAR> &l) const {
+  // Channels that are not turned are not touched.
+  __device__ __forceinline__ void apply(f2 (&v)[RUN], const Place<RUN, NEAR> &l) const {
+    if constexpr (NEAR) {
 #pragma unroll
-    for (int i = 0; i < RUN; ++i) {
-      const int ia = NEAR ? 2 * i : i, ib = NEAR ? 2 * i + 1 : RUN + i;
-      const bool is = i < RUN / 2 ? l.turned0 : l.turned1;
-      const float a = v[ia], b = v[ib], si = BACK ? -s[i] : s[i];
-      v[ia] = is ? fmaf(a, c[i], -(b * si)) : a;
-      v[ib] = is ? fmaf(b, c[i], a * si) : b;
+      for (int i = 0; i < RUN; ++i) {
+        if (i < RUN / 2 ? l.turned0 : l.turned1) {
+          float a, b;
+          f2_split(v[i], a, b);
+          v[i] = f2_pack(fmaf(a, c[i], -(b * s[i])), fmaf(b, c[i], a * s[i]));
+        }
+      }
+    } else if (l.turned0) {
+#pragma unroll
+      for (int i = 0; i < RUN / 2; ++i) {
+        const f2 cc = f2_pack(c[2 * i], c[2 * i + 1]), ss = f2_pack(s[2 * i], s[2 * i + 1]);
+        const f2 a = v[i], b = v[RUN / 2 + i];
+        v[i] = f2_fma(f2_mul(b, ss), f2_both(-1.f), f2_mul(a, cc));
+        v[RUN / 2 + i] = f2_fma(b, cc, f2_mul(a, ss));
+      }
     }
   }
 };
 
 template <int TPR>
-__device__ __forceinline__ float row_sum(float v) {
+__device__ __forceinline__ float row_sum(f2 v) {
+  float x, y;
+  f2_split(v, x, y);
+  x += y;
 #pragma unroll
-  for (int o = TPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int o = TPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
 }
 
 // Both runs of a thread as they lie in memory (half the registers of bf16 until they are used); zeros where `on` is false.
@@ -123,10 +135,14 @@ struct Raw {
   static __device__ __forceinline__ void load_run(const T *p, uint32_t (&r)[kWords]) {
     if constexpr (kWords == 4) {
       const uint4 u = *reinterpret_cast<const uint4 *>(p);
-      r[0] = u.x; r[1] = u.y; r[2] = u.z; r[3] = u.w;
+      r[0] = u.x;
+      r[1] = u.y;
+      r[2] = u.z;
+      r[3] = u.w;
     } else {
       const uint2 u = *reinterpret_cast<const uint2 *>(p);
-      r[0] = u.x; r[1] = u.y;
+      r[0] = u.x;
+      r[1] = u.y;
     }
   }
   __device__ __forceinline__ void load(const T *p, int c0, int c1, bool on) {
@@ -137,62 +153,83 @@ struct Raw {
       load_run(p + c1, b);
     }
   }
-  static __device__ __forceinline__ float at(const uint32_t (&r)[kWords], int i) {
-    if constexpr (sizeof(T) == 4) return __uint_as_float(r[i]);
-    else return __uint_as_float(i & 1 ? r[i / 2] & 0xffff0000u : r[i / 2] << 16);
+  static __device__ __forceinline__ f2 pair(const uint32_t (&r)[kWords], int i) {
+    if constexpr (sizeof(T) == 4) return f2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+    else return f2_pack(__uint_as_float(r[i] << 16), __uint_as_float(r[i] & 0xffff0000u));
   }
-  __device__ __forceinline__ void get(float (&v)[2 * RUN]) const {
+  __device__ __forceinline__ void get(f2 (&v)[RUN]) const {
 #pragma unroll
-    for (int i = 0; i < RUN; ++i) {
-      v[i] = at(a, i);
-      v[RUN + i] = at(b, i);
+    for (int i = 0; i < RUN / 2; ++i) {
+      v[i] = pair(a, i);
+      v[RUN / 2 + i] = pair(b, i);
     }
   }
 };
 template <int RUN, typename T>
-__device__ __forceinline__ void load_two(const T *p, int c0, int c1, bool on, float (&v)[2 * RUN]) {
-  float a[RUN] = {}, b[RUN] = {};
-  if (on) {
-    load_vec<RUN>(p + c0, a);
-    load_vec<RUN>(p + c1, b);
-  }
-#pragma unroll
-  for (int i = 0; i < RUN; ++i) {
-    v[i] = a[i];
-    v[RUN + i] = b[i];
-  }
-}
-template <int RUN, typename T>
-__device__ __forceinline__ void store_two(T *p, int c0, int c1, const float (&v)[2 * RUN]) {
+__device__ __forceinline__ void store_two(T *p, int c0, int c1, const f2 (&v)[RUN]) {
   float a[RUN], b[RUN];
 #pragma unroll
-  for (int i = 0; i < RUN; ++i) {
-    a[i] = v[i];
-    b[i] = v[RUN + i];
+  for (int i = 0; i < RUN / 2; ++i) {
+    f2_split(v[i], a[2 * i], a[2 * i + 1]);
+    f2_split(v[RUN / 2 + i], b[2 * i], b[2 * i + 1]);
   }
   store_vec<RUN>(p + c0, a);
   store_vec<RUN>(p + c1, b);
 }
 template <typename T, int RUN, bool NEAR>
-__device__ __forceinline__ void load_weight(const HeadArgs &p, const void *w, const Place<RUN, NEAR> &l,
-                                            float (&v)[2 * RUN]) {
-  if (p.d.weight_dtype == GDR_F32) load_two<RUN>(static_cast<const float *>(w), l.c0, l.c1, l.on, v);
-  else load_two<RUN>(static_cast<const T *>(w), l.c0, l.c1, l.on, v);
+__device__ __forceinline__ void load_weight(const HeadArgs &p, const void *w, const Place<RUN, NEAR> &l, f2 (&v)[RUN]) {
+  float a[RUN] = {}, b[RUN] = {};
+  if (l.on) {
+    if (p.d.weight_dtype == GDR_F32) {
+      load_vec<RUN>(static_cast<const float *>(w) + l.c0, a);
+      load_vec<RUN>(static_cast<const float *>(w) + l.c1, b);
+    } else {
+      load_vec<RUN>(static_cast<const T *>(w) + l.c0, a);
+      load_vec<RUN>(static_cast<const T *>(w) + l.c1, b);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < RUN / 2; ++i) {
+    v[i] = f2_pack(a[2 * i], a[2 * i + 1]);
+    v[RUN / 2 + i] = f2_pack(b[2 * i], b[2 * i + 1]);
+  }
 }
 
-// A token's position: -1 (or one past the table, which is reported) makes a padding row of zeros.
-__device__ __forceinline__ int64_t position_of(const HeadArgs &p, int64_t m) {
-  if (!p.d.R) return 0;
-  const int64_t pos = p.pos[m];
-  if (pos < p.d.P) return pos < 0 ? -1 : pos;
+// A token's position: -1 (or one past the table, which is reported) makes a padding row of zeros.  The load
+// and the check are apart, so that the rows' loads are on their way before the position has come.
+__device__ __forceinline__ int64_t load_position(const HeadArgs &p, int64_t m) { return p.d.R ? p.pos[m] : 0; }
+__device__ __forceinline__ int64_t checked(const HeadArgs &p, int64_t pos) {
+  if (!p.d.R || pos < p.d.P) return pos < 0 ? -1 : pos;
   raise_status(p.status, GDR_ERR_POSITION);
   return -1;
 }
 
+// A warp's items (token, run of heads): every `step`-th of its tensor, without a division on the way.
+struct Walk {
+  int64_t m, dm;
+  int run, dr, runs;
+  __device__ __forceinline__ Walk(int64_t first, int64_t step, int64_t heads, int per) {
+    runs = (int)((heads + per - 1) / per);
+    m = first / runs;
+    run = (int)(first - m * runs);
+    dm = step / runs;
+    dr = (int)(step - dm * runs);
+  }
+  __device__ __forceinline__ void next() {
+    m += dm;
+    run += dr;
+    if (run >= runs) {
+      run -= runs;
+      ++m;
+    }
+  }
+};
+
 // TPR threads to a row (a power of two, at least D / (2 RUN)), so 32 / TPR rows to a warp at once; U such
-// sets of one token's heads to a warp, all of whose loads are on their way before the first is used.
-// A block belongs to q or to k: its weights stay in registers.  Warps go through the items
-// (token, run of heads) of their tensor.
+// sets of one token's heads to a warp.  A block belongs to q or to k: its weights stay in registers.
+// Warps go through the items (token, run of heads) of their tensor, the next one's rows on their way:
+// 16384 x 40 x 128 bf16 in 66 us, 78 % of the copy rate (79 us with one item to a warp, 3 blocks at 80
+// registers 82).
 template <typename T, int RUN, int TPR, int U, bool NEAR>
 __global__ void __launch_bounds__(kThreads, 2) head_fwd_kernel(const __grid_constant__ HeadArgs p) {
   constexpr int G = 32 / TPR, HI = G * U, kWarps = kThreads / 32;
@@ -201,91 +238,154 @@ __global__ void __launch_bounds__(kThreads, 2) head_fwd_kernel(const __grid_cons
   const int64_t block = query ? blockIdx.x : blockIdx.x - p.bq, blocks = query ? p.bq : gridDim.x - p.bq;
   const int lane = threadIdx.x & 31, D = (int)p.d.D, grp = lane / TPR;
   const Place<RUN, NEAR> l(p, lane % TPR);
-  float w[2 * RUN];
+  f2 w[RUN];
   load_weight<T>(p, sd.w, l, w);
-  const int64_t runs = (sd.heads + HI - 1) / HI, items = p.d.M * runs;
-  for (int64_t it = block * kWarps + (threadIdx.x >> 5); it < items; it += blocks * kWarps) {
-    const int64_t m = it / runs, h0 = (it - m * runs) * HI + grp;
-    const int64_t pos = position_of(p, m);
-    const T *x = sd.x + m * sd.ld + h0 * D;
-    Raw<T, RUN> rx[U];
+  Walk it(block * kWarps + (threadIdx.x >> 5), blocks * kWarps, sd.heads, HI);
+  Raw<T, RUN> rx[U], nx[U];
+  int64_t at = 0, nat = 0;
+  const auto fetch = [&](Raw<T, RUN> (&r)[U], int64_t &pos) {
+    if (it.m >= p.d.M) return;
+    const int64_t h = (int64_t)it.run * HI + grp;
+    pos = load_position(p, it.m);
+    const T *x = sd.x + it.m * sd.ld + h * D;
 #pragma unroll
-    for (int u = 0; u < U; ++u) rx[u].load(x + u * G * D, l.c0, l.c1, l.on && h0 + u * G < sd.heads);
-    const Turn<RUN, NEAR> a(p, l, pos < 0 ? 0 : pos);
+    for (int u = 0; u < U; ++u) r[u].load(x + u * G * D, l.c0, l.c1, l.on && h + u * G < sd.heads);
+  };
+  fetch(nx, nat);
+  while (it.m < p.d.M) {
+    const int64_t m = it.m, h0 = (int64_t)it.run * HI + grp;
+    at = nat;
+#pragma unroll
+    for (int u = 0; u < U; ++u) rx[u] = nx[u];
+    it.next();
+    const int64_t pos = checked(p, at);  // one token to a warp
+    const Turn<RUN, NEAR, false> a(p, l, pos < 0 ? 0 : pos);
+    fetch(nx, nat);  // the next item's rows are on their way while this one is worked on
     T *y = sd.y + (m * sd.heads + h0) * D;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float v[2 * RUN], ss = 0.f;
+      f2 v[RUN], ss = f2_both(0.f);
       rx[u].get(v);
 #pragma unroll
-      for (int i = 0; i < 2 * RUN; ++i) ss = fmaf(v[i], v[i], ss);
-      const float rho = rsqrtf(row_sum<TPR>(ss) / (float)D + p.d.eps);
+      for (int i = 0; i < RUN; ++i) ss = f2_fma(v[i], v[i], ss);
+      const f2 rho = f2_both(rsqrtf(row_sum<TPR>(ss) / (float)D + p.d.eps));
       if (l.on && h0 + u * G < sd.heads) {
 #pragma unroll
-        for (int i = 0; i < 2 * RUN; ++i) v[i] = pos < 0 ? 0.f : v[i] * rho * w[i];
-        a.template apply<false>(v, l);
-        store_two<RUN>(y + u * G * D, l.c0, l.c1, v);
+        for (int i = 0; i < RUN; ++i) v[i] = pos < 0 ? f2_both(0.f) : f2_mul(f2_mul(v[i], rho), w[i]);
+        a.apply(v, l);
+        store_two(y + u * G * D, l.c0, l.c1, v);
       }
     }
   }
 }
 
 // The same with dy beside x; a thread sums dw of its channels over its items, a block's
-// warps and rows meet in shared memory, the blocks in a second launch.
+// warps and rows meet in shared memory, the blocks in a second launch.  x and dy of the next
+// item are copied into the thread's own part of shared memory meanwhile (in registers they spilled:
+// 16384 x 40 x 128 bf16 took 145 us, and 112-120 without any rows ahead; so it takes 99, 77 % of the copy
+// rate, and with one row to a thread 110).
+template <typename T, int RUN, int U>
+struct Ahead {
+  static constexpr int kBytes = RUN * sizeof(T);
+  struct __align__(16) Part {
+    unsigned char b[kThreads][kBytes];  // a run of every thread
+  };
+  Part part[2][U][2][2];  // buffer, row, x or dy, run
+};
+template <int TPR, int RUN>
+struct Sums {
+  float of[kThreads / TPR][2 * RUN * TPR + 1];
+};
+template <typename T, int RUN, int TPR, int U>
+constexpr size_t bwd_smem() {
+  return std::max(sizeof(Ahead<T, RUN, U>), sizeof(Sums<TPR, RUN>));
+}
 template <typename T, int RUN, int TPR, int U, bool NEAR>
 __global__ void __launch_bounds__(kThreads, 2) head_bwd_kernel(const __grid_constant__ HeadArgs p) {
   constexpr int G = 32 / TPR, HI = G * U, kWarps = kThreads / 32;
-  __shared__ float red[kWarps * G][2 * RUN * TPR + 1];
+  extern __shared__ __align__(16) unsigned char shared[];
+  const auto get_two = [](const unsigned char *a, const unsigned char *b, bool on, f2 (&v)[RUN]) {
+    Raw<T, RUN> r;
+    r.load(reinterpret_cast<const T *>(a), 0, (int)((b - a) / (int64_t)sizeof(T)), on);
+    r.get(v);
+  };
+  auto &ahead = *reinterpret_cast<Ahead<T, RUN, U> *>(shared);
+  auto &red = reinterpret_cast<Sums<TPR, RUN> *>(shared)->of;
   const bool query = blockIdx.x < p.bq;
   const Side<T> sd = side_of<T>(p, query);
   const int64_t block = query ? blockIdx.x : blockIdx.x - p.bq, blocks = query ? p.bq : gridDim.x - p.bq;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = (int)p.d.D, grp = lane / TPR;
   const Place<RUN, NEAR> l(p, lane % TPR);
-  float w[2 * RUN], sum[2 * RUN] = {};
-  load_weight<T>(p, sd.w, l, w);
-  const int64_t runs = (sd.heads + HI - 1) / HI, items = p.d.M * runs;
-  for (int64_t it = block * kWarps + warp; it < items; it += blocks * kWarps) {
-    const int64_t m = it / runs, h0 = (it - m * runs) * HI + grp;
-    const int64_t pos = position_of(p, m);
-    const T *x = sd.x + m * sd.ld + h0 * D, *dy = sd.dy + m * sd.ld_dy + h0 * D;
-    Raw<T, RUN> rx[U], rg[U];
+  f2 w[RUN], sum[RUN];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool on = l.on && h0 + u * G < sd.heads;
-      rx[u].load(x + u * G * D, l.c0, l.c1, on);
-      rg[u].load(dy + u * G * D, l.c0, l.c1, on);
+  for (int i = 0; i < RUN; ++i) sum[i] = f2_both(0.f);
+  load_weight<T>(p, sd.w, l, w);
+  Walk it(block * kWarps + warp, blocks * kWarps, sd.heads, HI);
+  int64_t at = 0, nat = 0;
+  int buf = 0;
+  const auto fetch = [&](int to) {
+    if (it.m < p.d.M) {
+      const int64_t h = (int64_t)it.run * HI + grp;
+      nat = load_position(p, it.m);
+      const T *x = sd.x + it.m * sd.ld + h * D, *dy = sd.dy + it.m * sd.ld_dy + h * D;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (l.on && h + u * G < sd.heads) {
+          auto &part = ahead.part[to][u];
+          copy_async<Ahead<T, RUN, U>::kBytes>(part[0][0].b[threadIdx.x], x + u * G * D + l.c0);
+          copy_async<Ahead<T, RUN, U>::kBytes>(part[0][1].b[threadIdx.x], x + u * G * D + l.c1);
+          copy_async<Ahead<T, RUN, U>::kBytes>(part[1][0].b[threadIdx.x], dy + u * G * D + l.c0);
+          copy_async<Ahead<T, RUN, U>::kBytes>(part[1][1].b[threadIdx.x], dy + u * G * D + l.c1);
+        }
+      }
     }
-    const Turn<RUN, NEAR> a(p, l, pos < 0 ? 0 : pos);
+    copy_commit();
+  };
+  fetch(0);
+  while (it.m < p.d.M) {
+    const int64_t m = it.m, h0 = (int64_t)it.run * HI + grp;
+    at = nat;
+    it.next();
+    fetch(buf ^ 1);
+    const int64_t pos = checked(p, at);  // one token to a warp
+    const Turn<RUN, NEAR, true> a(p, l, pos < 0 ? 0 : pos);
+    copy_wait<1>();  // this item is here, the next one on its way
     T *dx = sd.y + (m * sd.heads + h0) * D;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float v[2 * RUN], g[2 * RUN], ss = 0.f, px = 0.f;
-      rx[u].get(v);
-      rg[u].get(g);
-      a.template apply<true>(g, l);
+      f2 v[RUN], g[RUN], ss = f2_both(0.f), px = ss;
+      const bool on = l.on && h0 + u * G < sd.heads;
+      const auto &part = ahead.part[buf][u];
+      get_two(part[0][0].b[threadIdx.x], part[0][1].b[threadIdx.x], on, v);
+      get_two(part[1][0].b[threadIdx.x], part[1][1].b[threadIdx.x], on, g);
+      a.apply(g, l);
 #pragma unroll
-      for (int i = 0; i < 2 * RUN; ++i) {
-        ss = fmaf(v[i], v[i], ss);
-        px = fmaf(w[i] * g[i], v[i], px);
+      for (int i = 0; i < RUN; ++i) {
+        ss = f2_fma(v[i], v[i], ss);
+        px = f2_fma(f2_mul(w[i], g[i]), v[i], px);
       }
-      const float rho = rsqrtf(row_sum<TPR>(ss) / (float)D + p.d.eps);
-      const float mean = row_sum<TPR>(px) / (float)D * rho * rho;
-      if (l.on && h0 + u * G < sd.heads) {
-        float o[2 * RUN];
+      const float r = rsqrtf(row_sum<TPR>(ss) / (float)D + p.d.eps);
+      const f2 rho = f2_both(r), mean = f2_both(-(row_sum<TPR>(px) / (float)D * r * r));
+      if (on) {
+        f2 o[RUN];
 #pragma unroll
-        for (int i = 0; i < 2 * RUN; ++i) {
-          o[i] = pos < 0 ? 0.f : rho * (w[i] * g[i] - v[i] * mean);
-          sum[i] += pos < 0 ? 0.f : g[i] * (v[i] * rho);
+        for (int i = 0; i < RUN; ++i) {
+          o[i] = pos < 0 ? f2_both(0.f) : f2_mul(rho, f2_fma(v[i], mean, f2_mul(w[i], g[i])));
+          if (pos >= 0) sum[i] = f2_fma(g[i], f2_mul(v[i], rho), sum[i]);
         }
-        store_two<RUN>(dx + u * G * D, l.c0, l.c1, o);
+        store_two(dx + u * G * D, l.c0, l.c1, o);
       }
     }
+    buf ^= 1;
   }
+  copy_wait<0>();
+  __syncthreads();  // the copies' memory holds the sums from here on
   if (l.on) {
 #pragma unroll
-    for (int i = 0; i < RUN; ++i) {
-      red[warp * G + grp][l.c0 + i] = sum[i];
-      red[warp * G + grp][l.c1 + i] = sum[RUN + i];
+    for (int i = 0; i < RUN / 2; ++i) {
+      float *const to = red[warp * G + grp];
+      f2_split(sum[i], to[l.c0 + 2 * i], to[l.c0 + 2 * i + 1]);
+      f2_split(sum[RUN / 2 + i], to[l.c1 + 2 * i], to[l.c1 + 2 * i + 1]);
     }
   }
   __syncthreads();
@@ -320,7 +420,7 @@ __global__ void __launch_bounds__(kThreads) head_odd_kernel(const __grid_constan
     const int64_t m = row / sd.heads, h = row - m * sd.heads;
     const T *x = sd.x + m * sd.ld + h * D, *dy = sd.dy + (BWD ? m * sd.ld_dy + h * D : 0);
     T *y = sd.y + row * D;
-    const int64_t pos = position_of(p, m);
+    const int64_t pos = checked(p, load_position(p, m));
     float va[kMostUnits], vb[kMostUnits], ga[kMostUnits], gb[kMostUnits], ss = 0.f, px = 0.f;
 #pragma unroll
     for (int i = 0; i < kMostUnits; ++i) {
@@ -425,27 +525,27 @@ Blocks blocks_of(const gdr_qk_norm_desc &d, int heads_per_item, int64_t most) {
 template <typename T, int RUN, int TPR, int U>
 int launch_vec(const HeadArgs &a, bool bwd, int64_t blocks, cudaStream_t st) {
   const bool near = a.d.interleaved;
-  if constexpr (U < 4) if (bwd) {
+  if (bwd) {
     const auto kernel = near ? head_bwd_kernel<T, RUN, TPR, U, true> : head_bwd_kernel<T, RUN, TPR, U, false>;
-    kernel<<<(unsigned)blocks, kThreads, 0, st>>>(a);
+    constexpr size_t smem = bwd_smem<T, RUN, TPR, U>();
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return cuda_error(e, "cudaFuncSetAttribute(head_bwd_kernel)");
+    kernel<<<(unsigned)blocks, kThreads, smem, st>>>(a);
     return launched("head_bwd_kernel");
   }
-  if constexpr (U > 1) {
-    const auto kernel = near ? head_fwd_kernel<T, RUN, TPR, U, true> : head_fwd_kernel<T, RUN, TPR, U, false>;
-    kernel<<<(unsigned)blocks, kThreads, 0, st>>>(a);
-  }
+  const auto kernel = near ? head_fwd_kernel<T, RUN, TPR, U, true> : head_fwd_kernel<T, RUN, TPR, U, false>;
+  kernel<<<(unsigned)blocks, kThreads, 0, st>>>(a);
   return launched("head_fwd_kernel");
 }
 
-// Rows of a thread (U): four of x, or two of x and dy, are what the registers hold on their way; half
-// where the heads do not fill them.  16384 x 40 x 128 bf16: forward 79-84 us with four, 81-83 with two,
-// 116 with one; backward 112-120 with two, 142 with one.  16384 x 20 x 64: forward 36 with four, 24 with two.
+// Rows of a thread (U), while as many of the next item are on their way.
+constexpr int kRowsFwd = 2, kRowsBwd = 2;
 template <typename T, int RUN>
-int launch_runs(const HeadArgs &a, bool bwd, int tpr, bool half, int64_t blocks, cudaStream_t st) {
+int launch_runs(const HeadArgs &a, bool bwd, int tpr, int64_t blocks, cudaStream_t st) {
   const auto go = [&](auto t) {
     constexpr int TPR = decltype(t)::value;
-    if (bwd) return half ? launch_vec<T, RUN, TPR, 1>(a, bwd, blocks, st) : launch_vec<T, RUN, TPR, 2>(a, bwd, blocks, st);
-    return half ? launch_vec<T, RUN, TPR, 2>(a, bwd, blocks, st) : launch_vec<T, RUN, TPR, 4>(a, bwd, blocks, st);
+    return bwd ? launch_vec<T, RUN, TPR, kRowsBwd>(a, bwd, blocks, st)
+               : launch_vec<T, RUN, TPR, kRowsFwd>(a, bwd, blocks, st);
   };
   if (tpr == 4) return go(std::integral_constant<int, 4>{});
   if (tpr == 8) return go(std::integral_constant<int, 8>{});
@@ -461,11 +561,8 @@ int launch(HeadArgs a, bool bwd, float *dwq, float *dwk, cudaStream_t st) {
   const int run = runs_ok(a, kWide, bwd) ? kWide : runs_ok(a, 4, bwd) ? 4 : 1;
   int tpr = run > 1 ? 4 : 32;
   while (2 * run * tpr < d.D && run > 1) tpr *= 2;
-  // the backward's blocks stay and sum; more of them only leave more sums to add
-  const int64_t most = bwd || run == 1 ? 4 * kSMs : 0x7fffffff;
-  const int full = 32 / tpr * (bwd ? 2 : 4);  // heads of an item
-  const bool half = std::max(d.H, d.HK) <= full / 2;
-  const Blocks n = blocks_of(d, run > 1 ? full / (half ? 2 : 1) : 1, most);
+  // blocks stay, two to a multiprocessor (four of the warp-to-a-row form)
+  const Blocks n = blocks_of(d, run > 1 ? 32 / tpr * (bwd ? kRowsBwd : kRowsFwd) : 1, (run > 1 ? 2 : 4) * kSMs);
   if (n.all > 0x7fffffff) return set_error(GDR_ERR_SHAPE, "too many rows for one launch");
   a.bq = n.q;
   char *base = nullptr;
@@ -481,9 +578,9 @@ int launch(HeadArgs a, bool bwd, float *dwq, float *dwk, cudaStream_t st) {
       else head_odd_kernel<T, false><<<(unsigned)n.all, kThreads, 0, st>>>(a);
       rc = launched("head_odd_kernel");
     } else if (run == 8) {
-      if constexpr (sizeof(T) == 2) rc = launch_runs<T, 8>(a, bwd, tpr, half, n.all, st);
+      if constexpr (sizeof(T) == 2) rc = launch_runs<T, 8>(a, bwd, tpr, n.all, st);
     } else {
-      rc = launch_runs<T, 4>(a, bwd, tpr, half, n.all, st);
+      rc = launch_runs<T, 4>(a, bwd, tpr, n.all, st);
     }
   }
   if (!bwd) return rc;
