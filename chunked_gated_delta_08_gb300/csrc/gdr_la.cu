@@ -113,7 +113,6 @@ __global__ void __launch_bounds__(kThreads) la_any_kernel(const __grid_constant_
   const bool bw = q.backwards;
   const Segment s = segment_of(p, slot, bw, cut);
   if (!s.some) return;
-  if (p.mode == kStates && s.last) return;  // nobody reads the state behind the last segment
   const int D = (Da + 15) & ~15, LDA = D + 4, cols = min(kCols, Dc - col0);
   float *A = sm, *B = A + C * LDA, *Cm = B + C * LDA, *P = Cm + C * LDC, *S = P + C * LDP, *pw = S + D * LDC,
         *wt = pw + C + 4;
@@ -123,7 +122,7 @@ __global__ void __launch_bounds__(kThreads) la_any_kernel(const __grid_constant_
 
   for (int i = tid; i <= C; i += kThreads) pw[i] = decay_power(g, i);
   // the state the segment starts from
-  const float *from = entering(p, q, s, slot, hv, cut);
+  const float *from = entering(p, q, s, hv);
   for (int i = tid; i < D * kCols; i += kThreads) {
     const int r = i / kCols, c = i % kCols;
     S[r * LDC + c] = from && r < Da && c < cols ? from[r * q.si + (col0 + c) * q.sj] : 0.f;
@@ -191,9 +190,9 @@ __global__ void __launch_bounds__(kThreads) la_any_kernel(const __grid_constant_
         }
     }
   }
-  if (!q.s_out || (p.mode != kStates && !s.last)) return;
+  float *to = leaving(p, q, s, slot, hv);
+  if (!to) return;
   __syncthreads();
-  float *to = q.s_out + (p.mode == kStates ? slot * p.HV + hv : s.n * p.HV + hv) * p.KV;
   for (int i = tid; i < Da * kCols; i += kThreads) {
     const int r = i / kCols, c = i % kCols;
     if (c < cols) to[r * q.si + (col0 + c) * q.sj] = S[r * LDC + c];
@@ -201,40 +200,43 @@ __global__ void __launch_bounds__(kThreads) la_any_kernel(const __grid_constant_
 }
 
 // ------------------------------------------------------------------------------ carry, sums
-// The states that segments start from, in place of their own: over a sequence's
-// segments in the pass's order, S enters and leaves as r^len S + own.  A thread has
-// VEC elements of a head's state, and eight segments' of them on their way at once (74
-// segments one after the other took 50 us).
+// The states at the borders, in place of the segments' own: over a sequence's borders
+// in the pass's order, S = r^len S + own.  A thread has VEC elements of a head's state, and
+// eight borders' of them on their way at once (74 segments one after the other took 50 us).
+// Window j of L tokens, j >= 1: of the sequences that start in ((j - 1) L ..< j L) only the last can have
+// a border, and its first one has index j.
 template <int VEC>
 __global__ void __launch_bounds__(256) la_carry_kernel(const __grid_constant__ LaArgs p) {
   bool cut;
   if (!sequences_ok(p, cut) || !cut) return;
   const LaPass &q = p.pass[blockIdx.z];
-  const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * VEC;
-  const int64_t n = blockIdx.y / p.HV, hv = blockIdx.y % p.HV;
+  const int64_t e = ((int64_t)blockIdx.y * 256 + threadIdx.x) * VEC;
+  const int64_t j = blockIdx.x / p.HV + 1, hv = blockIdx.x % p.HV;
   if (e >= p.KV) return;
+  const int64_t n = seq_of_token(p.cu, p.N, p.T, j * p.L - 1);
   const SeqRange r = seq_range(p.cu, n, p.T);
-  const int64_t len = r.eos - r.bos, segs = segments_in(p, len, true);
+  const int64_t segs = segments_in(p, r.eos - r.bos);
+  if (r.bos < (j - 1) * p.L || segs < 2) return;
   const float g = p.g[hv];
   float S[VEC] = {};
   if (q.s_in) load_vec<VEC>(q.s_in + (n * p.HV + hv) * p.KV + e, S);
   const int64_t step = p.HV * p.KV * (q.backwards ? -1 : 1);
-  float *own = q.s_out + ((first_slot(p, n) + (q.backwards ? segs - 1 : 0)) * p.HV + hv) * p.KV + e;
-  const float full = decay_less1(g, p.L), tail = decay_less1(g, len - (segs - 1) * p.L);
+  float *own = q.s_out + ((j + (q.backwards ? segs - 2 : 0)) * p.HV + hv) * p.KV + e;
+  const float full = decay_less1(g, p.L), tail = decay_less1(g, r.eos - r.bos - (segs - 1) * p.L);
   constexpr int kAhead = 8;
-  for (int64_t u0 = 0; u0 < segs; u0 += kAhead, own += kAhead * step) {
-    float mine[kAhead][VEC] = {};
+  for (int64_t u0 = 0; u0 < segs - 1; u0 += kAhead, own += kAhead * step) {
+    float mine[kAhead][VEC];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
-      if (u0 + i + 1 < segs) load_vec<VEC>(own + i * step, mine[i]);  // of the last there is none
+      if (u0 + i < segs - 1) load_vec<VEC>(own + i * step, mine[i]);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      if (u0 + i < segs) {
-        store_vec<VEC>(own + i * step, S);
+      if (u0 + i < segs - 1) {
         // the ragged segment is a sequence's last: going back, the first of the pass
         const float less1 = q.backwards && u0 + i == 0 ? tail : full;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) S[j] = fmaf(S[j], less1, S[j]) + mine[i][j];
+        for (int k = 0; k < VEC; ++k) S[k] = fmaf(S[k], less1, S[k]) + mine[i][k];
+        store_vec<VEC>(own + i * step, S);
       }
     }
   }
@@ -288,7 +290,7 @@ void cut(LaArgs &p, int blocks_per_pair, int wave, int launches) {
   const int64_t alike = p.cu ? (p.N == 1 ? p.tokens : 0) : p.T, each = wave / (p.N * blocks);
   const int64_t chunks = alike && each ? cdiv(cdiv(alike, C), each) : cdiv(even, 2);
   p.L = C * std::max<int64_t>(4, chunks);
-  if (!p.cu && p.L >= p.T) p.L = 0;
+  if (p.L >= (alike ? alike : p.tokens)) p.L = 0;
 }
 
 template <typename T>
@@ -323,12 +325,14 @@ int run(LaArgs p, int passes, const LaPass *st_pass, int nstates, const int *fro
   else cut(p, passes * widest, 2 * kSMs, 3);
   if (!p.L) return launch(p, passes, dtype, tc, st);
   p.slots = slot_count(p.tokens, p.N, p.L);
-  const int64_t one = p.slots * p.HV * p.KV;
+  const int64_t borders = border_count(p.tokens, p.L) - 1, one = (borders + 1) * p.HV * p.KV;
+  if (borders * p.HV > 0x7fffffff) return set_error(GDR_ERR_SHAPE, "too many tokens and heads for one launch");
   char *base = nullptr;
   int rc = scratch_begin(sizeof(float) * (size_t)(one * nstates), st, "linear attention states", &base);
   if (rc != GDR_OK) return rc;
   LaArgs s = p;
   s.mode = kStates;
+  s.slots = borders;
   for (int i = 0; i < nstates; ++i) {
     s.pass[i] = st_pass[i];
     s.pass[i].s_out = (float *)base + i * one;
@@ -338,7 +342,7 @@ int run(LaArgs p, int passes, const LaPass *st_pass, int nstates, const int *fro
     bool vec = p.KV % 4 == 0;
     for (int i = 0; i < nstates; ++i) vec = vec && is_aligned16(s.pass[i].s_in);
     const auto kernel = vec ? la_carry_kernel<4> : la_carry_kernel<1>;
-    kernel<<<dim3((unsigned)cdiv(p.KV, vec ? 1024 : 256), (unsigned)(p.N * p.HV), nstates), 256, 0, st>>>(s);
+    kernel<<<dim3((unsigned)(borders * p.HV), (unsigned)cdiv(p.KV, vec ? 1024 : 256), nstates), 256, 0, st>>>(s);
     rc = launched("la_carry_kernel");
   }
   p.mode = kFromStates;

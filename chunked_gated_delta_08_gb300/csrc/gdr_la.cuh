@@ -47,8 +47,8 @@ struct LaPass {
   LaRows a, b, c;
   void *out;          // [tokens, HV, Dc] contiguous; fp32 where out_f32, else of the inputs' type
   const float *s_in;  // states that the sequences start from, null: zero
-  const float *carried;  // in kFromStates, where sequences are cut: those that the segments start from
-  float *s_out;       // state behind the sequence's last chunk (or the segment's own), null: not wanted
+  const float *carried;  // in kFromStates, where sequences are cut: the states at the segments' borders
+  float *s_out;       // state behind the sequence's last chunk, null: not wanted; in kStates: at the borders
   int64_t si, sj;     // element (i, j) of a Da x Dc state lies at i si + j sj
   float pscale, iscale, wscale;
   int backwards, out_f32;
@@ -66,7 +66,7 @@ struct LaArgs {
   int64_t KV;    // elements of a state
   int64_t L;     // tokens in a segment, a multiple of C (unused in kWhole)
   int64_t least; // sequences are cut where the longest has more tokens than this
-  int64_t slots; // segment slots over all sequences
+  int64_t slots; // segment slots over all sequences, in kStates borders
   int mode;
 };
 
@@ -76,6 +76,11 @@ struct LaArgs {
 __host__ __device__ __forceinline__ int64_t slot_count(int64_t tokens, int64_t N, int64_t L) {
   return tokens / L + N;
 }
+// The states at the borders between a sequence's segments.  The border at token b has
+// index b / L: borders of one sequence are L apart, and the first of the next
+// sequence is more than L behind the last of this one, so no two share an index,
+// and there are tokens / L + 1 of them however many sequences there are.
+__host__ __device__ __forceinline__ int64_t border_count(int64_t tokens, int64_t L) { return tokens / L + 1; }
 __device__ __forceinline__ int64_t first_slot(const LaArgs &p, int64_t n) {
   return (p.cu ? p.cu[n] : n * p.T) / p.L + n;
 }
@@ -102,12 +107,30 @@ struct Segment {
   int first, last;   // in the pass's order of time
   bool some;         // false: the slot is not in use
 };
-__device__ __forceinline__ int64_t segments_in(const LaArgs &p, int64_t len, bool cut) {
-  return cut && len > 0 ? (len + p.L - 1) / p.L : 1;
+__device__ __forceinline__ int64_t segments_in(const LaArgs &p, int64_t len) {
+  return len > 0 ? (len + p.L - 1) / p.L : 1;
 }
 // Every thread of the block calls it.  Uncut, the longest sequences come first, so that none of them starts last.
 __device__ __forceinline__ Segment segment_of(const LaArgs &p, int64_t slot, bool backwards, bool cut) {
   Segment s;
+  if (p.mode == kStates) {
+    // Border slot + 1: the segment before it covers token (slot + 1) L - 1.  Its state goes to the border behind it,
+    // going back that of the segment behind the border.
+    const int64_t t = (slot + 1) * p.L - 1;
+    s.some = cut && t < p.tokens;
+    if (!s.some) return s;
+    s.n = seq_of_token(p.cu, p.N, p.T, t);
+    const SeqRange r = seq_range(p.cu, s.n, p.T);
+    s.bos = t - (t - r.bos) % p.L;
+    s.eos = s.bos + p.L;
+    s.some = s.eos < r.eos;
+    if (backwards) {
+      s.bos = s.eos;
+      s.eos = r.eos - s.bos < p.L ? r.eos : s.bos + p.L;
+    }
+    s.first = s.last = 0;
+    return s;
+  }
   if (!cut) {
     s.some = slot < p.N;
     if (!s.some) return s;
@@ -125,8 +148,7 @@ __device__ __forceinline__ Segment segment_of(const LaArgs &p, int64_t slot, boo
     else hi = mid;
   }
   const SeqRange r = seq_range(p.cu, lo, p.T);
-  const int64_t len = r.eos - r.bos, i = slot - first_slot(p, lo);
-  const int64_t segs = segments_in(p, len, cut);
+  const int64_t len = r.eos - r.bos, i = slot - first_slot(p, lo), segs = segments_in(p, len);
   s.n = lo;
   s.bos = r.bos + i * p.L;
   s.eos = i == segs - 1 ? r.eos : s.bos + p.L;
@@ -137,11 +159,15 @@ __device__ __forceinline__ Segment segment_of(const LaArgs &p, int64_t slot, boo
 }
 
 // The state that a block starts from (null: zero).
-__device__ __forceinline__ const float *entering(const LaArgs &p, const LaPass &q, const Segment &s, int64_t slot,
-                                                 int64_t hv, bool cut) {
+__device__ __forceinline__ const float *entering(const LaArgs &p, const LaPass &q, const Segment &s, int64_t hv) {
   if (p.mode == kStates) return nullptr;
-  if (cut) return q.carried + (slot * p.HV + hv) * p.KV;
+  if (!s.first) return q.carried + ((s.bos / p.L + (q.backwards ? 1 : 0)) * p.HV + hv) * p.KV;
   return q.s_in ? q.s_in + (s.n * p.HV + hv) * p.KV : nullptr;
+}
+// Where the state that a block ends with goes (null: nowhere).
+__device__ __forceinline__ float *leaving(const LaArgs &p, const LaPass &q, const Segment &s, int64_t slot, int64_t hv) {
+  if (!q.s_out || !(p.mode == kStates || s.last)) return nullptr;
+  return q.s_out + ((p.mode == kStates ? slot + 1 : s.n) * p.HV + hv) * p.KV;
 }
 
 // r^n of a whole number n >= 0; r^0 is 1 for every g, -inf (each token forgets all before it) included.

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const bool bw = q.backwards, states = p.mode == kStates;
   const bool exact = q.s_out != nullptr;  // B' in two parts
   const Segment s = segment_of(p, slot, bw, cut);
-  if (!s.some || (states && s.last)) return;  // nobody reads the state behind the last segment
+  if (!s.some) return;
   const int Da = q.a.D, Dc = q.c.D, ka = Da > 64 ? 2 : 1, kc = Dc > 64 ? 2 : 1;
   const int64_t len = s.eos - s.bos;
   const int nch = (int)((len + C - 1) / C);
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t aS = lane_addr + TM_S + col0, aSb = lane_addr + TM_SB + col0 / 2;
     const bool mine = j < Dc;
     {
-      const float *from = mine ? entering(p, q, s, slot, hv, cut) : nullptr;
+      const float *from = mine ? entering(p, q, s, hv) : nullptr;
       if (from) from += j * q.sj;
 #pragma unroll 1
       for (int i0 = 0; i0 < cols; i0 += 16) {
@@ -238,8 +238,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     if (nch > 0) wait(S.b_state, (nch - 1) & 1);
     tc_fence_after();
-    if (q.s_out && (states || s.last)) {
-      float *to = q.s_out + ((states ? slot : s.n) * p.HV + hv) * p.KV + j * q.sj;
+    float *to = leaving(p, q, s, slot, hv);
+    if (to) {
+      to += j * q.sj;
 #pragma unroll 1
       for (int i0 = 0; i0 < cols; i0 += 16) {
         float r[16];

@@ -77,6 +77,46 @@ def test_sequences_cut_into_segments(gdr, dtype, K, V, lens):
 
 
 @both_types
+def test_many_short_sequences_and_a_long_one(gdr, dtype):
+    """5000 sequences of a token or none beside one that is worth cutting; few heads, no initial states."""
+    lens = [1, 0] * 1250 + [3000] + [1, 0] * 1250
+    p = put(ref.attention_inputs(lens, 1, 2, 16, 16, dtype, seed=11))
+    cu = cu_of(lens, "cuda")
+    args = (p["q"][None], p["k"][None], p["v"][None], p["g"])
+    o, ht = gdr.la_fwd(*args, h0=p["h0"], cu_seqlens=cu, scale=0.25)
+    d = {k: v.double() for k, v in p.items()}
+    want, s = ref.attention(*[d[k] for k in ("q", "k", "v", "g", "h0")], lens, 0.25)
+    ref.close(o[0], want, dtype, 3000, "o")
+    ref.close(ht, s, dtype, 3000, "ht")
+    got = gdr.la_bwd(*args, p["do"][None], h0=p["h0"], dht=p["dht"], cu_seqlens=cu, scale=0.25)
+    # the long sequence by itself, and the first of the short ones
+    for n, i, j in ((2500, 1250, 4250), (0, 0, 1)):
+        part = [p[k][None, i:j] for k in ("q", "k", "v")] + [p["g"], p["do"][None, i:j]]
+        alone = gdr.la_bwd(*part, h0=p["h0"][n:n + 1], dht=p["dht"][n:n + 1], scale=0.25)
+        for k, a, b in zip(("dq", "dk", "dv", "dh0"), got, alone):
+            ref.close(a[n:n + 1] if k == "dh0" else a[:, i:j], b.double(), dtype, 3000, k)
+    assert gdr.device_status() == 0
+
+
+@pytest.mark.parametrize("B,T,HV", [(1, 8192, 100), (1, 6400, 160), (2, 4096, 40), (1, 5000, 3)], ids=str)
+def test_how_sequences_are_cut_does_not_matter(gdr, B, T, HV):
+    """Heads and lengths on both sides of where sequences are cut: the same values as head by head."""
+    p = put(ref.attention_inputs([T] * B, HV, HV, 16, 16, BF16, seed=12))
+    lead = lambda t: t.view(B, T, *t.shape[1:])  # noqa: E731
+    o, ht = gdr.la_fwd(lead(p["q"]), lead(p["k"]), lead(p["v"]), p["g"], h0=p["h0"])
+    packed = gdr.la_fwd(p["q"][None], p["k"][None], p["v"][None], p["g"], h0=p["h0"], cu_seqlens=cu_of([T] * B, "cuda"))
+    for a, b in zip((o.flatten(0, 1)[None], ht), packed):
+        ref.close(a, b.double(), BF16, T)
+    for h in (0, HV - 1):
+        one = slice(h, h + 1)
+        a, s = gdr.la_fwd(lead(p["q"])[:, :, one], lead(p["k"])[:, :, one], lead(p["v"])[:, :, one],
+                          p["g"][one].clone(), h0=p["h0"][:, one].contiguous())
+        ref.close(o[:, :, one], a.double(), BF16, T, "o")
+        ref.close(ht[:, one], s.double(), BF16, T, "ht")
+    assert gdr.device_status() == 0
+
+
+@both_types
 @pytest.mark.parametrize("g", [0.0, -1e-5, -0.3, -5.0, -200.0, -math.inf, 0.01], ids=str)
 @pytest.mark.parametrize("K", [128, 24])
 def test_decays(gdr, dtype, g, K):
