@@ -374,8 +374,10 @@ typedef struct gdr_la_desc {
  * Tokens are taken in chunks of 64: what is not finite in a token may reach every
  * output of its own sequence from the start of its chunk on (in the gradients:
  * all of the sequence), but no other sequence and no other head's outputs.
- * With bf16 inputs, scores and states are rounded to bf16 where they are
- * multiplied for o; the states themselves are not (they take each product to 2^-17).
+ * bf16 inputs of K and V up to 128, both multiples of 8, in rows and bases of 16
+ * bytes take the tcgen05 form: scores and states are rounded to bf16 where they
+ * are multiplied for o; the states themselves are not (they take each product to
+ * 2^-17).  Everything else takes products of 2^-21.
  */
 int gdr_la_fwd(const gdr_la_desc *desc, const void *q, const void *k, const void *v, const float *g, const float *h0,
                const int64_t *cu_seqlens, void *o, float *ht, void *stream);
