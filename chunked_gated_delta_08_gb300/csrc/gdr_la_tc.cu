@@ -53,33 +53,43 @@ using fused::ld_sw128_chunk;
 using fused::st_sw128_chunk;
 using fused::sw128_chunk_off;
 
-constexpr int kStages = 3;
 constexpr int kTcThreads = 896;
 constexpr int kProducer = 24, kScoreMma = 25, kStateMma = 26;  // and one more for the outputs' MMAs
 constexpr int kBarOut = 1;  // named barrier of the output warps
 
-// shared memory, from a 1024-byte aligned base; tiles are two panels of 64 rows x 64 channels
-constexpr uint32_t SZ_TILE = 16384, SZ_PANEL = 8192;
-constexpr uint32_t SZ_STAGE = 3 * SZ_TILE;  // A | B | C
-constexpr uint32_t OFF_LO = kStages * SZ_STAGE;   // lower halves of B', two buffers
-constexpr uint32_t OFF_P = OFF_LO + 2 * SZ_TILE;  // P, two buffers
-constexpr uint32_t OFF_Y = OFF_P + 2 * SZ_PANEL;  // y on its way out: two buffers of bf16, one of fp32 (four panels of 32 channels)
-constexpr uint32_t OFF_SMALL = OFF_Y + 2 * SZ_TILE;
+// Shared memory, from a 1024-byte aligned base.  A tile is one panel of 64 rows x 64 channels where no row has more than
+// 64, else two; a stage waits in the ring from its load to its output, three periods and more, so the smaller ones
+// get six instead of three (4 x 4096 x 32 x 64: forward 82 -> 76 us, backward 228 -> 206 us).
+constexpr uint32_t SZ_PANEL = 8192;
+template <int PANELS>
+struct Layout {
+  static constexpr int kStages = 6 / PANELS;
+  static constexpr uint32_t SZ_TILE = PANELS * SZ_PANEL;
+  static constexpr uint32_t SZ_STAGE = 3 * SZ_TILE;            // A | B | C
+  static constexpr uint32_t OFF_LO = kStages * SZ_STAGE;       // lower parts of B', two buffers
+  static constexpr uint32_t OFF_P = OFF_LO + 2 * SZ_TILE;      // P, two buffers
+  static constexpr uint32_t OFF_Y = OFF_P + 2 * SZ_PANEL;      // y on its way out: two buffers of bf16, one of fp32
+  static constexpr uint32_t OFF_SMALL = OFF_Y + 2 * SZ_TILE;
+};
+constexpr int kMostStages = 6;
 
 // TMEM columns
 constexpr uint32_t TM_SC = 0 /* twice */, TM_O = 128 /* O1, O2 */, TM_S = 256, TM_SB = 384 /* twice */, TM_COLS = 512;
 
 struct Small {
   float pw[C + 4];  // r^0 .. r^64
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[kMostStages], empty[kMostStages];
   // (a stage is empty when its chunk's state and output MMAs are done, which frees P, B' and the bf16 state too)
   uint64_t b_sc[2], b_state, b_o, b_final[3];  // MMAs done
   uint64_t b_p[2], b_bs[2], b_s[2], b_ofree;   // arrivals of eight warps: P, B', state and its copy, O1 and O2 read
   uint32_t tmem_slot;
   int err;
 };
-constexpr uint32_t SMEM_BYTES = OFF_SMALL + sizeof(Small) + 1024;
-static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+template <int PANELS>
+constexpr uint32_t smem_bytes() {
+  return Layout<PANELS>::OFF_SMALL + sizeof(Small) + 1024;
+}
+static_assert(smem_bytes<1>() <= 232448 && smem_bytes<2>() <= 232448, "shared memory budget");
 
 __device__ __forceinline__ uint32_t pack_f2(f2 v) {
   float lo, hi;
@@ -123,14 +133,17 @@ struct Maps {
 };
 
 // PARTS: some of the passes write fp32 parts (grouped value heads); their code costs the others 8 %.
-template <bool PARTS>
+template <bool PARTS, int PANELS>
 __global__ void __launch_bounds__(kTcThreads, 1)
     la_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LaArgs p, int passes) {
+  using L = Layout<PANELS>;
+  constexpr int kStages = L::kStages;
+  constexpr uint32_t SZ_TILE = L::SZ_TILE, SZ_STAGE = L::SZ_STAGE, OFF_LO = L::OFF_LO, OFF_P = L::OFF_P, OFF_Y = L::OFF_Y;
   extern __shared__ uint8_t smem_raw[];
   bool cut;
   if (!sequences_ok(p, cut)) return;
   uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  Small &S = *reinterpret_cast<Small *>(sm + OFF_SMALL);
+  Small &S = *reinterpret_cast<Small *>(sm + L::OFF_SMALL);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the passes over one item run side by side: the rows that two of them read come from L2 the second time
   const int pi = (int)(blockIdx.x % passes);
@@ -140,7 +153,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const bool bw = q.backwards, states = p.mode == kStates;
   const Segment s = segment_of(p, slot, bw, cut);
   if (!s.some) return;
-  const int Da = q.a.D, Dc = q.c.D, ka = Da > 64 ? 2 : 1, kc = Dc > 64 ? 2 : 1;
+  const int Da = q.a.D, Dc = q.c.D, ka = PANELS == 2 && Da > 64 ? 2 : 1, kc = PANELS == 2 && Dc > 64 ? 2 : 1;
   const int64_t len = s.eos - s.bos;
   const int nch = (int)((len + C - 1) / C);
   const float g = p.g[hv];
@@ -579,10 +592,14 @@ int launch_tc(const LaArgs &p, int passes, cudaStream_t st) {
   if (items * passes > 0x7fffffff) return set_error(GDR_ERR_SHAPE, "too many sequences and heads for one launch");
   bool parts = false;
   for (int i = 0; i < passes; ++i) parts |= p.mode != kStates && p.pass[i].out_f32;
-  const auto kernel = parts ? la_tc_kernel<true> : la_tc_kernel<false>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+  bool wide = false;
+  for (int i = 0; i < passes; ++i) wide |= p.pass[i].a.D > 64 || p.pass[i].c.D > 64;
+  const auto kernel = wide ? parts ? la_tc_kernel<true, 2> : la_tc_kernel<false, 2>
+                           : parts ? la_tc_kernel<true, 1> : la_tc_kernel<false, 1>;
+  const int smem = (int)(wide ? smem_bytes<2>() : smem_bytes<1>());
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_error(e, "cudaFuncSetAttribute(la_tc_kernel)");
-  kernel<<<(unsigned)(items * passes), kTcThreads, SMEM_BYTES, st>>>(maps, p, passes);
+  kernel<<<(unsigned)(items * passes), kTcThreads, smem, st>>>(maps, p, passes);
   return launched("la_tc_kernel");
 }
 
