@@ -223,25 +223,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (c > 1) wait(S.empty[(c - 2) % kStages], ((c - 2) / kStages) & 1);  // O2 has read the copy of two chunks before
       tc_fence_after();
 #pragma unroll
-      for (int i0 = 0; i0 < 64; i0 += 32) {
+      for (int i0 = 0; i0 < 64; i0 += 16) {
         if (i0 < cols) {
-          float r[32];
-          tmem_ld32(aS + i0, r);
+          float r[16];
+          tmem_ld16(aS + i0, r);
           tmem_ld_wait();
-          uint32_t u[16];
+          uint32_t u[8];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) u[i] = gdr::pack_bf16(r[2 * i], r[2 * i + 1]);
-          if (!states) tmem_st16u(aSb + (c & 1) * 64 + i0 / 2, u);
-          uint32_t d[32];
+          for (int i = 0; i < 8; ++i) u[i] = gdr::pack_bf16(r[2 * i], r[2 * i + 1]);
+          if (!states) tmem_st8(aSb + (c & 1) * 64 + i0 / 2, u);
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
+          for (int i = 0; i < 16; i += 2) {
             const f2 x = f2_pack(r[i], r[i + 1]);
-            float lo, hi;
-            f2_split(f2_fma(x, f2_both(less1), x), lo, hi);
-            d[i] = __float_as_uint(lo);
-            d[i + 1] = __float_as_uint(hi);
+            f2_split(f2_fma(x, f2_both(less1), x), r[i], r[i + 1]);
           }
-          tmem_st32(aS + i0, d);
+          tmem_st16(aS + i0, r);
         }
       }
       tmem_st_wait();
