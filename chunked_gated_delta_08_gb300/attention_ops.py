@@ -216,7 +216,7 @@ def qk_norm_bwd(dyq, dyk, q, k, wq, wk, cos=None, sin=None, positions=None, eps=
         desc.ld_dyk = _rows(dyk, "dyk", dev, q.dtype, k.shape, 2)
         dk, dwk = _like(k), _new(q, desc.D, torch.float32)
     dq, dwq = _like(q), _new(q, desc.D, torch.float32)
-    _call(_lib.gdr_qk_norm_bwd, dev, desc, dyq.data_ptr(), _addr(dyk) if k is not None else None, q.data_ptr(), _addr(k),
-          wq.data_ptr(), _addr(wk), _addr(cos), _addr(sin), _addr(positions), dq.data_ptr(), _addr(dk), dwq.data_ptr(),
+    _call(_lib.gdr_qk_norm_bwd, dev, desc, dyq.data_ptr(), None if k is None else dyk.data_ptr(), q.data_ptr(),
+          _addr(k), wq.data_ptr(), _addr(wk), _addr(cos), _addr(sin), _addr(positions), dq.data_ptr(), _addr(dk), dwq.data_ptr(),
           _addr(dwk))
     return dq, dk, dwq, dwk

@@ -127,7 +127,8 @@ __device__ __forceinline__ float row_sum(f2 v) {
   return x;
 }
 
-// Both runs of a thread as they lie in memory (half the registers of bf16 until they are used); zeros where `on` is false.
+// Both runs of a thread as they lie in memory (half the registers of bf16 until they are used); zeros where `on` is
+// false.
 template <typename T, int RUN>
 struct Raw {
   static constexpr int kWords = RUN * sizeof(T) / 4;
@@ -607,7 +608,8 @@ int validate(const gdr_qk_norm_desc *d) {
   if (d->H < 1 || d->HK < 0 || d->H > 65535 || d->HK > 65535)
     return set_error(GDR_ERR_SHAPE, "H must be in [1, 65535] and HK in [0, 65535]");
   if (d->D < 1 || d->D > 256) return set_error(GDR_ERR_SHAPE, "D must be in [1, 256]");
-  if (d->R < 0 || 2 * d->R > d->D) return set_error(GDR_ERR_SHAPE, "the rotation must not be wider than a head: 2 R <= D");
+  if (d->R < 0 || 2 * d->R > d->D)
+    return set_error(GDR_ERR_SHAPE, "the rotation must not be wider than a head: 2 R <= D");
   if (d->P < 0 || d->P > kMost) return set_error(GDR_ERR_SHAPE, "P must be in [0, 2^31)");
   if (d->ld_q < d->H * d->D || d->ld_k < d->HK * d->D || d->ld_dyq < d->H * d->D || d->ld_dyk < d->HK * d->D)
     return set_error(GDR_ERR_SHAPE, "leading dimensions must be at least H * D, or HK * D");

@@ -32,8 +32,8 @@ inline size_t smem_bytes(int Da) {
 
 // rows x D elements of one head into dst [C][ld], zeros past `rows` and from D to Dp.
 template <typename T>
-__device__ __forceinline__ void load_tile(float *dst, int ld, const LaRows &r, int64_t row0, int head, int rows, int col0,
-                                          int cols, int Dp, bool vec) {
+__device__ __forceinline__ void load_tile(float *dst, int ld, const LaRows &r, int64_t row0, int head, int rows,
+                                          int col0, int cols, int Dp, bool vec) {
   const T *src = static_cast<const T *>(r.p) + row0 * r.ld + (int64_t)(head / r.group) * r.D + col0;
   if (vec) {
     const int per = Dp / 4;
@@ -51,8 +51,8 @@ __device__ __forceinline__ void load_tile(float *dst, int ld, const LaRows &r, i
   }
 }
 
-// x in tf32 parts: hi its first 11 bits, lo 11 of the 13 that are left (2^-22 of x is lost; cut off, not rounded: adding
-// to the bits would turn some NaN into numbers).  EXACT: x has no more than 8 bits.
+// x in tf32 parts: hi its first 11 bits, lo 11 of the 13 that are left (2^-22 of x is lost; cut off, not rounded:
+// adding to the bits would turn some NaN into numbers).  EXACT: x has no more than 8 bits.
 template <bool EXACT>
 struct Split {
   uint32_t hi, lo;
@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(256) la_carry_kernel(const __grid_constant__ L
 
 // out [M, H, D] = sums over groups of G value heads of part [M, H G, D], in order; VEC elements to a thread.
 template <typename T, int VEC>
-__global__ void __launch_bounds__(256) la_sum_kernel(const float *part0, const float *part1, T *out0, T *out1, int64_t n,
-                                                     int G, int D, SeqCheck check) {
+__global__ void __launch_bounds__(256) la_sum_kernel(const float *part0, const float *part1, T *out0, T *out1,
+                                                     int64_t n, int G, int D, SeqCheck check) {
   if (!seqlens_ok(check)) return;
   const float *part = blockIdx.y ? part1 : part0;
   T *out = blockIdx.y ? out1 : out0;
@@ -390,25 +390,27 @@ LaArgs base_args(const gdr_la_desc &d, const float *g, const int64_t *cu, int *s
 }
 
 // ------------------------------------------------------------------------------ single tokens
-// One block per (row, value head) walks the K x V state once: S = r S + k v^T is
-// written back and o = scale S^T q summed on the way.  Eight bytes of state a
-// multiply-add: HBM bound.  A thread keeps VEC columns; the block's row groups'
-// partial sums of o meet in shared memory.
+// One block per (row, value head, run of columns) walks its part of the K x V state once:
+// S = r S + k v^T is written back and o = scale S^T q summed on the way.  Eight bytes of
+// state a multiply-add: HBM bound.  A thread keeps VEC columns; the partial sums of o of
+// a block's row groups meet in shared memory, in order.  256 x 32 heads of 128 x 128 take 165 us, 97 % of the
+// copy rate (with one row on its way after the other 197).
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) la_step_kernel(gdr_la_desc d, const T *q, const T *k, const T *v, const float *g,
-                                                      const int32_t *slots, float *state, T *o, int *status) {
+                                                      const int32_t *slots, float *state, T *o, int *status, int run) {
   __shared__ float sq[256], sk[256];
   __shared__ __align__(16) float part[256 * VEC];
   const int K = (int)d.K, V = (int)d.V, tid = threadIdx.x;
   const int64_t row = blockIdx.x / d.HV, hv = blockIdx.x % d.HV, h = hv / (d.HV / d.H);
+  const int first = blockIdx.y * run, cols = min(run, V - first);
   int64_t slot = slots ? slots[row] : row;
   if (slot >= d.N) {
-    if (tid == 0 && hv == 0) raise_status(status, GDR_ERR_SLOTS);
+    if (tid == 0 && hv == 0 && first == 0) raise_status(status, GDR_ERR_SLOTS);
     slot = -1;
   }
-  T *to = o + (row * d.HV + hv) * V;
+  T *to = o + (row * d.HV + hv) * V + first;
   if (slot < 0) {
-    for (int c = tid; c < V; c += 256) to[c] = from_f32<T>(0.f);
+    for (int c = tid; c < cols; c += 256) to[c] = from_f32<T>(0.f);
     return;
   }
   if (tid < K) {
@@ -416,31 +418,39 @@ __global__ void __launch_bounds__(256) la_step_kernel(gdr_la_desc d, const T *q,
     sk[tid] = to_f32(k[row * d.ld_k + h * K + tid]);
   }
   __syncthreads();
-  const int across = (V + VEC - 1) / VEC, groups = 256 / across;  // V <= 256
+  const int across = (cols + VEC - 1) / VEC, groups = 256 / across;  // cols <= 256
   const int c = tid % across * VEC, r0 = tid / across;
   const float r = expf(g[hv]);
   float acc[VEC] = {};
   if (r0 < groups) {
     float vv[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) vv[i] = to_f32(v[row * d.ld_v + hv * V + c + i]);
-    float *S = state + (slot * d.HV + hv) * (int64_t)K * V + c;
-#pragma unroll 4
-    for (int i = r0; i < K; i += groups) {
-      float s[VEC];
-      load_vec<VEC>(S + (int64_t)i * V, s);
+    for (int i = 0; i < VEC; ++i) vv[i] = to_f32(v[row * d.ld_v + hv * V + first + c + i]);
+    float *S = state + (slot * d.HV + hv) * (int64_t)K * V + first + c;
+    constexpr int U = 4;  // rows on their way at once
+    for (int i0 = r0; i0 < K; i0 += U * groups) {
+      float s[U][VEC];
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        s[j] = fmaf(sk[i], vv[j], r * s[j]);
-        acc[j] = fmaf(sq[i], s[j], acc[j]);
+      for (int u = 0; u < U; ++u)
+        if (i0 + u * groups < K) load_vec<VEC>(S + (int64_t)(i0 + u * groups) * V, s[u]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * groups;
+        if (i < K) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) {
+            s[u][j] = fmaf(sk[i], vv[j], r * s[u][j]);
+            acc[j] = fmaf(sq[i], s[u][j], acc[j]);
+          }
+          store_vec<VEC>(S + (int64_t)i * V, s[u]);
+        }
       }
-      store_vec<VEC>(S + (int64_t)i * V, s);
     }
   }
 #pragma unroll
   for (int j = 0; j < VEC; ++j) part[tid * VEC + j] = acc[j];
   __syncthreads();
-  for (int i = tid; i < V; i += 256) {
+  for (int i = tid; i < cols; i += 256) {
     float s = 0.f;
     for (int gq = 0; gq < groups; ++gq) s += part[gq * across * VEC + i];
     to[i] = from_f32<T>(s);
@@ -453,8 +463,12 @@ int launch_step(const gdr_la_desc &d, const void *q, const void *k, const void *
   const int64_t blocks = d.B * d.HV;
   if (blocks > 0x7fffffff) return set_error(GDR_ERR_SHAPE, "too many rows and heads for one launch");
   const bool vec = d.V % 4 == 0 && is_aligned16(state);
+  // Few heads in all: runs of 32 columns, whole lines of the state, share a head out over four blocks
+  // (1 x 32 x 128 x 128 in a graph: 5.5 us in whole heads, 2.8 so).
+  const int run = blocks < 2 * kSMs ? 32 : 256;
   const auto kernel = vec ? la_step_kernel<T, 4> : la_step_kernel<T, 1>;
-  kernel<<<(unsigned)blocks, 256, 0, st>>>(d, (const T *)q, (const T *)k, (const T *)v, g, slots, state, (T *)o, status);
+  const dim3 grid((unsigned)blocks, (unsigned)cdiv(d.V, run));
+  kernel<<<grid, 256, 0, st>>>(d, (const T *)q, (const T *)k, (const T *)v, g, slots, state, (T *)o, status, run);
   return launched("la_step_kernel");
 }
 

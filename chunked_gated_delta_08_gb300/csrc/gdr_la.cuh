@@ -165,7 +165,8 @@ __device__ __forceinline__ const float *entering(const LaArgs &p, const LaPass &
   return q.s_in ? q.s_in + (s.n * p.HV + hv) * p.KV : nullptr;
 }
 // Where the state that a block ends with goes (null: nowhere).
-__device__ __forceinline__ float *leaving(const LaArgs &p, const LaPass &q, const Segment &s, int64_t slot, int64_t hv) {
+__device__ __forceinline__ float *leaving(const LaArgs &p, const LaPass &q, const Segment &s, int64_t slot,
+                                          int64_t hv) {
   if (!q.s_out || !(p.mode == kStates || s.last)) return nullptr;
   return q.s_out + ((p.mode == kStates ? slot + 1 : s.n) * p.HV + hv) * p.KV;
 }

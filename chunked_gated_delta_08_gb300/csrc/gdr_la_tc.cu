@@ -57,9 +57,9 @@ constexpr int kTcThreads = 896;
 constexpr int kProducer = 24, kScoreMma = 25, kStateMma = 26;  // and one more for the outputs' MMAs
 constexpr int kBarOut = 1;  // named barrier of the output warps
 
-// Shared memory, from a 1024-byte aligned base.  A tile is one panel of 64 rows x 64 channels where no row has more than
-// 64, else two; a stage waits in the ring from its load to its output, three periods and more, so the smaller ones
-// get six instead of three (4 x 4096 x 32 x 64: forward 82 -> 76 us, backward 228 -> 206 us).
+// Shared memory, from a 1024-byte aligned base.  A tile is one panel of 64 rows x 64 channels where no row has more
+// than 64, else two; a stage waits in the ring from its load to its output, three periods and more, so the smaller
+// ones get six instead of three (4 x 4096 x 32 x 64: forward 82 -> 76 us, backward 228 -> 206 us).
 constexpr uint32_t SZ_PANEL = 8192;
 template <int PANELS>
 struct Layout {
@@ -138,7 +138,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     la_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LaArgs p, int passes) {
   using L = Layout<PANELS>;
   constexpr int kStages = L::kStages;
-  constexpr uint32_t SZ_TILE = L::SZ_TILE, SZ_STAGE = L::SZ_STAGE, OFF_LO = L::OFF_LO, OFF_P = L::OFF_P, OFF_Y = L::OFF_Y;
+  constexpr uint32_t SZ_TILE = L::SZ_TILE, SZ_STAGE = L::SZ_STAGE;
+  constexpr uint32_t OFF_LO = L::OFF_LO, OFF_P = L::OFF_P, OFF_Y = L::OFF_Y;
   extern __shared__ uint8_t smem_raw[];
   bool cut;
   if (!sequences_ok(p, cut)) return;
@@ -158,7 +159,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int nch = (int)((len + C - 1) / C);
   const float g = p.g[hv];
   auto chunk_start = [&](int c) { return s.bos + (int64_t)(bw ? nch - 1 - c : c) * C; };
-  const int ragged = bw ? 0 : nch - 1, rest = (int)(len - (int64_t)(nch - 1) * C);  // the sequence's last chunk, its rows
+  // the segment's last chunk, which may be ragged, and its rows
+  const int ragged = bw ? 0 : nch - 1, rest = (int)(len - (int64_t)(nch - 1) * C);
   auto chunk_rows = [&](int c) { return c == ragged ? rest : C; };
 
   if (tid < C + 1) S.pw[tid] = decay_power(g, tid);
@@ -220,7 +222,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int n = chunk_rows(c);
       const float less1 = n == C ? whole1 : decay_less1(g, n);
       if (c > 0) wait(S.b_state, (c - 1) & 1);
-      if (c > 1) wait(S.empty[(c - 2) % kStages], ((c - 2) / kStages) & 1);  // O2 has read the copy of two chunks before
+      // O2 has read the copy of two chunks before
+      if (c > 1) wait(S.empty[(c - 2) % kStages], ((c - 2) / kStages) & 1);
       tc_fence_after();
 #pragma unroll
       for (int i0 = 0; i0 < 64; i0 += 16) {
@@ -284,8 +287,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       wait(S.full[st], (c / kStages) & 1);
       if (n < C) {  // rows past the end may hold the next sequence
         for (int i = gt; i < (C - n) * 8 * kc; i += 256)
-          st_sw128_chunk(tile + 2 * SZ_TILE + (kc == 2 && (i & 8) ? SZ_PANEL : 0), n + (kc == 2 ? i >> 4 : i >> 3), i & 7,
-                         make_uint4(0, 0, 0, 0));
+          st_sw128_chunk(tile + 2 * SZ_TILE + (kc == 2 && (i & 8) ? SZ_PANEL : 0), n + (kc == 2 ? i >> 4 : i >> 3),
+                         i & 7, make_uint4(0, 0, 0, 0));
       }
       if (c > 1) wait(S.empty[(c - 2) % kStages], ((c - 2) / kStages) & 1);  // the buffers' chunk before is done
       if (!states) {
@@ -329,7 +332,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int e = 0; e < 4; ++e) {
             const f2 x = f2_mul(f2_pack(v[2 * e], v[2 * e + 1]), f2_both(wt));
             h[e] = pack_f2(x);
-            l[e] = pack_f2(f2_fma(f2_pack(__uint_as_float(h[e] << 16), __uint_as_float(h[e] & 0xffff0000u)), f2_both(-1.f), x));
+            const f2 hf = f2_pack(__uint_as_float(h[e] << 16), __uint_as_float(h[e] & 0xffff0000u));
+            l[e] = pack_f2(f2_fma(hf, f2_both(-1.f), x));
           }
           st_sw128_chunk(hi, row, ch0 + i, make_uint4(h[0], h[1], h[2], h[3]));
           st_sw128_chunk(lo, row, ch0 + i, make_uint4(l[0], l[1], l[2], l[3]));
@@ -389,8 +393,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
             const float *fe = f[2 * i + (e >> 2)];
-            f2_split(f2_fma(f2_pack(y[i][e], y[i][e + 1]), f2_pack(fe[0], fe[1]), f2_pack(x[i][e], x[i][e + 1])), x[i][e],
-                     x[i][e + 1]);
+            const f2 xx = f2_pack(x[i][e], x[i][e + 1]), yy = f2_pack(y[i][e], y[i][e + 1]);
+            f2_split(f2_fma(yy, f2_pack(fe[0], fe[1]), xx), x[i][e], x[i][e + 1]);
           }
         if (w >= 2 * kc) continue;
         // channels of this thread: d0 and d0 + 8
@@ -401,7 +405,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const int tok = tok0 + 16 * i + 8 * (e >> 2) + (e & 1), d = d0 + ((e >> 1) & 1) * 8;
-              *reinterpret_cast<float *>(sY + w * SZ_PANEL + sw128_chunk_off(tok, (d >> 2) & 7) + (d & 3) * 4) = x[i][e];
+              uint8_t *at = sY + w * SZ_PANEL + sw128_chunk_off(tok, (d >> 2) & 7) + (d & 3) * 4;
+              *reinterpret_cast<float *>(at) = x[i][e];
             }
         } else if (stage) {
           const int chunk = (32 * w + 16 * h + 8 * (m & 1)) >> 3;
@@ -505,8 +510,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          mma_bf16(tbase + TM_O, at(dmn, off + 2 * SZ_TILE + ks * 2048), at(dk, OFF_P + buf * SZ_PANEL + ks * 32), id_o1,
-                   ks > 0);
+          mma_bf16(tbase + TM_O, at(dmn, off + 2 * SZ_TILE + ks * 2048), at(dk, OFF_P + buf * SZ_PANEL + ks * 32),
+                   id_o1, ks > 0);
         spin(S.b_s[buf], ph);
         if (*err) break;
         tc_fence_after();
@@ -552,7 +557,8 @@ int make_map(CUtensorMap *m, const LaRows &r, int64_t heads, int64_t tokens, boo
   const cuuint64_t dims[3] = {(cuuint64_t)r.D, (cuuint64_t)heads, (cuuint64_t)tokens};
   const cuuint64_t el = f32 ? 4 : 2, strides[2] = {(cuuint64_t)r.D * el, (cuuint64_t)r.ld * el};
   const cuuint32_t box[3] = {f32 ? 32u : 64u, 1, 64}, es[3] = {1, 1, 1};
-  const CUresult e = fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(r.p), dims, strides, box, es,
+  const CUtensorMapDataType type = f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUresult e = fn(m, type, 3, const_cast<void *>(r.p), dims, strides, box, es,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return e == CUDA_SUCCESS ? GDR_OK : set_error(GDR_ERR_CUDA, "cuTensorMapEncodeTiled failed");

@@ -5,7 +5,7 @@ automatic differentiation; and the tolerances of the tests.
 Tolerances are relative 2-norms, counted in roundings of half a step.
 
 fp32 (and the states, fp32 whatever the inputs): a product of the kernels is made
-of parts of its factors, three of tf32 (2^-21 of the product) or two of bf16
+of parts of its factors, two of tf32 (2^-21 of the product is lost) or two of bf16
 (2^-17, where the inputs are bf16).  An output is two products deep: a score and
 a value, or a state's entry and a query; so is a gradient.  Decay factors and the
 accumulation are fp32: eight roundings of 2^-24 a token, whose signs are independent,
