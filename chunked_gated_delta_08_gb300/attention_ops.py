@@ -170,7 +170,10 @@ def _qk_desc(q, k, wq, wk, cos, sin, positions, eps, interleaved):
         _whole(wk, "wk", dev, wq.dtype, (D,))
         HK, ld_k = k.shape[-2], _rows(k, "k", dev, q.dtype, None, 2)
     P = R = 0
-    if cos is not None:
+    if cos is None:
+        if sin is not None or positions is not None:
+            raise ValueError("a rotation needs cos, sin and positions")
+    else:
         if cos.dim() != 2:
             raise ValueError("cos and sin must be [P, R]")
         _whole(cos, "cos", dev, torch.float32, cos.shape)
@@ -217,6 +220,6 @@ def qk_norm_bwd(dyq, dyk, q, k, wq, wk, cos=None, sin=None, positions=None, eps=
         dk, dwk = _like(k), _new(q, desc.D, torch.float32)
     dq, dwq = _like(q), _new(q, desc.D, torch.float32)
     _call(_lib.gdr_qk_norm_bwd, dev, desc, dyq.data_ptr(), None if k is None else dyk.data_ptr(), q.data_ptr(),
-          _addr(k), wq.data_ptr(), _addr(wk), _addr(cos), _addr(sin), _addr(positions), dq.data_ptr(), _addr(dk), dwq.data_ptr(),
-          _addr(dwk))
+          _addr(k), wq.data_ptr(), _addr(wk), _addr(cos), _addr(sin), _addr(positions), dq.data_ptr(), _addr(dk),
+          dwq.data_ptr(), _addr(dwk))
     return dq, dk, dwq, dwk

@@ -186,6 +186,7 @@ def test_shapes_and_types_are_checked(gdr):
     bad = [(ValueError, lambda: f(q, k[:3], w, w)), (ValueError, lambda: f(q, z(4, 1, 8), w, w)),
            (ValueError, lambda: f(q, k, w[:8], w)), (gdr.GdrError, lambda: f(q, k.float(), w, w)),
            (gdr.GdrError, lambda: f(q, k, w, w.float())), (gdr.GdrError, lambda: f(q, k, w, None)),
+           (ValueError, lambda: f(q, k, w, w, None, cos, pos)), (ValueError, lambda: f(q, k, w, w, positions=pos)),
            (gdr.GdrError, lambda: f(q, k, w, w, cos)), (gdr.GdrError, lambda: f(q, k, w, w, cos, cos)),
            (ValueError, lambda: f(q, k, w, w, cos, cos[:7], pos)), (ValueError, lambda: f(q, k, w, w, cos, cos, pos[:3])),
            (gdr.GdrError, lambda: f(q, k, w, w, cos, cos, pos.int())),
