@@ -278,8 +278,8 @@ int launch_sum(const float *part0, const float *part1, void *out0, void *out1, i
 // blocks at a time (a tensor-core block takes 1.6 us a chunk, one of the other form 3.5).  Uncut, a
 // launch takes as long as its longest sequence, or its waves of whole sequences.  Cut, the work
 // spreads evenly, but forming the segments' states adds three fifths of it, and two more launches
-// the time of `launches` chunks.
-void cut(LaArgs &p, int blocks_per_pair, int wave, int launches) {
+// the time of `launches` chunks; a segment has at least `shortest` of them.
+void cut(LaArgs &p, int blocks_per_pair, int wave, int launches, int shortest) {
   const int64_t blocks = p.HV * blocks_per_pair;                // to a sequence
   const int64_t even = cdiv(cdiv(p.tokens, C) * blocks, wave);  // chunks of work to a block of a wave
   p.least = C * (launches + 8 * std::max<int64_t>(even, 4) / 5);
@@ -289,7 +289,7 @@ void cut(LaArgs &p, int blocks_per_pair, int wave, int launches) {
   // Where all sequences are alike, all segments in one wave; else half a wave's share, which packs better.
   const int64_t alike = p.cu ? (p.N == 1 ? p.tokens : 0) : p.T, each = wave / (p.N * blocks);
   const int64_t chunks = alike && each ? cdiv(cdiv(alike, C), each) : cdiv(even, 2);
-  p.L = C * std::max<int64_t>(4, chunks);
+  p.L = C * std::max<int64_t>(shortest, chunks);
   if (p.L >= (alike ? alike : p.tokens)) p.L = 0;
 }
 
@@ -321,8 +321,8 @@ int run(LaArgs p, int passes, const LaPass *st_pass, int nstates, const int *fro
   p.mode = kWhole;
   int widest = 1;
   for (int i = 0; i < passes; ++i) widest = std::max(widest, (int)cdiv(p.pass[i].c.D, kCols));
-  if (tc) cut(p, passes, kSMs, 10);
-  else cut(p, passes * widest, 2 * kSMs, 3);
+  if (tc) cut(p, passes, kSMs, 10, 4);
+  else cut(p, passes * widest, 2 * kSMs, 3, 2);
   if (!p.L) return launch(p, passes, dtype, tc, st);
   p.slots = slot_count(p.tokens, p.N, p.L);
   const int64_t borders = border_count(p.tokens, p.L) - 1, one = (borders + 1) * p.HV * p.KV;
