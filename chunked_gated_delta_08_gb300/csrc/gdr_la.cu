@@ -277,12 +277,13 @@ int launch_sum(const float *part0, const float *part1, void *out0, void *out1, i
 // How sequences are cut: p.L (0: not) and p.least.  A block walks a sequence chunk by chunk, `wave`
 // blocks at a time (a tensor-core block takes 1.6 us a chunk, one of the other form 3.5).  Uncut, a
 // launch takes as long as its longest sequence, or its waves of whole sequences.  Cut, the work
-// spreads evenly, but forming the segments' states adds three fifths of it, and two more launches
-// the time of `launches` chunks; a segment has at least `shortest` of them.
+// spreads evenly, but forming the segments' states and ragged waves make it 2.2 times as much (16384 x 32
+// heads in 7 sequences, 94 chunks the longest: 168 us uncut, 223 cut; 8192 x 16 heads 69 us cut), and
+// two more launches take the time of `launches` chunks; a segment has at least `shortest` of them.
 void cut(LaArgs &p, int blocks_per_pair, int wave, int launches, int shortest) {
   const int64_t blocks = p.HV * blocks_per_pair;                // to a sequence
   const int64_t even = cdiv(cdiv(p.tokens, C) * blocks, wave);  // chunks of work to a block of a wave
-  p.least = C * (launches + 8 * std::max<int64_t>(even, 4) / 5);
+  p.least = C * (launches + 11 * std::max<int64_t>(even, 4) / 5);
   p.L = 0;
   const int64_t longest = p.cu ? p.tokens : cdiv(p.N * blocks, wave) * p.T;
   if (p.N == 0 || longest <= p.least) return;
