@@ -20,7 +20,7 @@ import ctypes
 import torch
 
 from . import _lib
-from .layer_ops import _addr, _call, _device, _dtype_code, _like, _new, _param_code, _rows, _whole
+from .layer_ops import _addr, _call, _device, _dtype_code, _new, _param_code, _rows, _whole
 
 
 class GdrLaDesc(ctypes.Structure):
@@ -47,6 +47,11 @@ def _bind():
 
 
 _bind()
+
+
+def _like(t):
+    """An output of t's shape and dtype, contiguous (of a slice in one call, which q, k and v mostly are)."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 # ------------------------------------------------------------------------------------ linear attention
@@ -159,9 +164,7 @@ def _qk_desc(q, k, wq, wk, cos, sin, positions, eps, interleaved):
     dev = _device(q, "q")
     code, lead = _dtype_code(q, "q"), q.shape[:-2]
     H, D = q.shape[-2:]
-    M = 1
-    for n in lead:
-        M *= n
+    M = lead[0] if len(lead) == 1 else lead.numel()
     _whole(wq, "wq", dev, None, (D,))
     HK, ld_k = 0, 0
     if k is not None:

@@ -255,6 +255,33 @@ def test_earlier_chunks_and_heads_do_not_see_what_is_not_a_number(gdr, dtype, D)
 
 
 @both_types
+@pytest.mark.parametrize("D", [64, 20])
+def test_a_decay_that_is_not_a_number_spoils_its_head_alone(gdr, dtype, D):
+    lens = [1500, 70]
+    q = put(ref.attention_inputs(lens, 3, 3, D, D, dtype, seed=6))
+    clean = run(gdr, q, lens, 1.0)
+    got = run(gdr, dict(q, g=torch.stack([q["g"][0], q["g"][1] * math.nan, q["g"][2]])), lens, 1.0)
+    for k, v in got.items():
+        assert torch.equal(v[:, [0, 2]], clean[k][:, [0, 2]]) and v[:, 1].isnan().any(), k
+
+
+@both_types
+def test_cut_sequences_without_states(gdr, dtype):
+    lens = [2600]
+    p = ref.attention_inputs(lens, 1, 2, 32, 32, dtype, seed=13)
+    p["h0"].zero_()
+    p["dht"].zero_()
+    want, q = wanted(p, lens, 0.2), put(p)
+    args = (q["q"][None], q["k"][None], q["v"][None], q["g"])
+    before = gdr.launch_count()
+    o, _ = gdr.la_fwd(*args, scale=0.2, output_final_state=False)
+    assert gdr.launch_count() - before == 3
+    dq, dk, dv, dh0 = gdr.la_bwd(*args, q["do"][None], scale=0.2)
+    del want["ht"]
+    check(dict(o=o[0], dq=dq[0], dk=dk[0], dv=dv[0], dh0=dh0), want, dtype, lens)
+
+
+@both_types
 def test_results_repeat_bit_for_bit(gdr, dtype):
     lens = [1000, 77, 400]
     q = put(ref.attention_inputs(lens, 2, 4, 128, 128, dtype, seed=4))
