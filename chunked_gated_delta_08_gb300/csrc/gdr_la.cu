@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kThreads) la_any_kernel(const __grid_constant_
         }
     }
     // S = r^n S + (w B)^T C: a warp takes rows of S, 16 at a time
-    const float less1 = decay_less1(g, n);
+    const Decay decay = decay_of(g, n);
     for (int r0 = warp * 16; r0 < D; r0 += 8 * 16) {
       float acc[4][4] = {};
       tile_product<false, EX>(acc, C, [&](int i, int k) { return B[k * LDA + r0 + i] * wt[k]; },
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) la_any_kernel(const __grid_constant_
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float &at = S[(r0 + gr + (e >> 1) * 8) * LDC + 8 * j + 2 * tg + (e & 1)];
-          at = fmaf(at, less1, at) + acc[j][e];
+          at = decayed(at, decay) + acc[j][e];
         }
     }
   }
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(256) la_carry_kernel(const __grid_constant__ L
   if (q.s_in) load_vec<VEC>(q.s_in + (n * p.HV + hv) * p.KV + e, S);
   const int64_t step = p.HV * p.KV * (q.backwards ? -1 : 1);
   float *own = q.s_out + ((j + (q.backwards ? segs - 2 : 0)) * p.HV + hv) * p.KV + e;
-  const float full = decay_less1(g, p.L), tail = decay_less1(g, r.eos - r.bos - (segs - 1) * p.L);
+  const Decay full = decay_of(g, p.L), tail = decay_of(g, r.eos - r.bos - (segs - 1) * p.L);
   constexpr int kAhead = 8;
   for (int64_t u0 = 0; u0 < segs - 1; u0 += kAhead, own += kAhead * step) {
     float mine[kAhead][VEC];
@@ -233,9 +233,9 @@ __global__ void __launch_bounds__(256) la_carry_kernel(const __grid_constant__ L
     for (int i = 0; i < kAhead; ++i) {
       if (u0 + i < segs - 1) {
         // the ragged segment is a sequence's last: going back, the first of the pass
-        const float less1 = q.backwards && u0 + i == 0 ? tail : full;
+        const Decay decay = q.backwards && u0 + i == 0 ? tail : full;
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) S[k] = fmaf(S[k], less1, S[k]) + mine[i][k];
+        for (int k = 0; k < VEC; ++k) S[k] = decayed(S[k], decay) + mine[i][k];
         store_vec<VEC>(own + i * step, S);
       }
     }

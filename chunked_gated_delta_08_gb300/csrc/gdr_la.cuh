@@ -174,9 +174,19 @@ __device__ __forceinline__ float *leaving(const LaArgs &p, const LaPass &q, cons
 // r^n of a whole number n >= 0; r^0 is 1 for every g, -inf (each token forgets all before it) included.
 __device__ __forceinline__ float decay_power(float g, int n) { return n == 0 ? 1.f : expf(g * (float)n); }
 
-// r^n - 1: a state is decayed as S + S (r^n - 1), so that factors close to 1 are not rounded
-// over and over (r^64 of g = -1e-5, rounded to 24 bits, is off by 4e-5 after 512 chunks).
-__device__ __forceinline__ float decay_less1(float g, int64_t n) { return n == 0 ? 0.f : expm1f(g * (float)n); }
+// A state's decay over n tokens, S -> S a + S b.  Factors near 1 go by what they lack to it (a = r^n - 1, b = 1), so
+// that they are not rounded over and over (r^64 of g = -1e-5, rounded to 24 bits, is off by 4e-5 after 512 chunks);
+// those below a half as they are (a = r^n, b = 0), because r^n - 1 is rounded to 2^-25, whatever is left of r^n (at
+// g = -0.25, 6 % of r^64, and at -0.3 all of it).
+struct Decay {
+  float a, b;
+};
+__device__ __forceinline__ Decay decay_of(float g, int64_t n) {
+  if (n == 0) return {0.f, 1.f};
+  const float x = g * (float)n;
+  return x > -0.6931f ? Decay{expm1f(x), 1.f} : Decay{expf(x), 0.f};  // a NaN stays one
+}
+__device__ __forceinline__ float decayed(float s, Decay d) { return fmaf(s, d.a, s * d.b); }
 
 // The tensor-core form (gdr_la_tc.cu): whether it takes these passes, and its launch.
 bool tc_takes(const LaArgs &p, int passes, int dtype);
