@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(256) la_step_kernel(gdr_la_desc d, const T *q,
   __syncthreads();
   const int across = (cols + VEC - 1) / VEC, groups = 256 / across;  // cols <= 256
   const int c = tid % across * VEC, r0 = tid / across;
-  const float r = expf(g[hv]);
+  const Decay decay = decay_of(g[hv], 1);
   float acc[VEC] = {};
   if (r0 < groups) {
     float vv[VEC];
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(256) la_step_kernel(gdr_la_desc d, const T *q,
         if (i < K) {
 #pragma unroll
           for (int j = 0; j < VEC; ++j) {
-            s[u][j] = fmaf(sk[i], vv[j], r * s[u][j]);
+            s[u][j] = fmaf(sk[i], vv[j], decayed(s[u][j], decay));
             acc[j] = fmaf(sq[i], s[u][j], acc[j]);
           }
           store_vec<VEC>(S + (int64_t)i * V, s[u]);
