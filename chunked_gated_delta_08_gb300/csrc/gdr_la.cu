@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(256) la_carry_kernel(const __grid_constant__ L
   if (q.s_in) load_vec<VEC>(q.s_in + (n * p.HV + hv) * p.KV + e, S);
   const int64_t step = p.HV * p.KV * (q.backwards ? -1 : 1);
   float *own = q.s_out + ((j + (q.backwards ? segs - 2 : 0)) * p.HV + hv) * p.KV + e;
-  const Decay full = decay_of(g, p.L), tail = decay_of(g, r.eos - r.bos - (segs - 1) * p.L);
+  const LongDecay full = long_decay_of(g, p.L), tail = long_decay_of(g, r.eos - r.bos - (segs - 1) * p.L);
   constexpr int kAhead = 8;
   for (int64_t u0 = 0; u0 < segs - 1; u0 += kAhead, own += kAhead * step) {
     float mine[kAhead][VEC];
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(256) la_carry_kernel(const __grid_constant__ L
     for (int i = 0; i < kAhead; ++i) {
       if (u0 + i < segs - 1) {
         // the ragged segment is a sequence's last: going back, the first of the pass
-        const Decay decay = q.backwards && u0 + i == 0 ? tail : full;
+        const LongDecay decay = q.backwards && u0 + i == 0 ? tail : full;
 #pragma unroll
         for (int k = 0; k < VEC; ++k) S[k] = decayed(S[k], decay) + mine[i][k];
         store_vec<VEC>(own + i * step, S);

@@ -188,6 +188,21 @@ __device__ __forceinline__ Decay decay_of(float g, int64_t n) {
 }
 __device__ __forceinline__ float decayed(float s, Decay d) { return fmaf(s, d.a, s * d.b); }
 
+// The same over a segment, whose r^n may leave fp32's range where S r^n does not: in two halves, so that both factors
+// are in range wherever the product is, and no larger than the largest number, so that S = 0 stays 0.
+struct LongDecay {
+  Decay first, second;
+};
+__device__ __forceinline__ LongDecay long_decay_of(float g, int64_t n) {
+  if (!(fabsf(g * (float)n) > 64.f)) return {decay_of(g, n), {0.f, 1.f}};
+  LongDecay d{decay_of(g, n / 2), decay_of(g, n - n / 2)};
+  constexpr float kMost = 3.402823466e38f;
+  if (d.first.a > kMost) d.first.a = kMost;
+  if (d.second.a > kMost) d.second.a = kMost;
+  return d;
+}
+__device__ __forceinline__ float decayed(float s, LongDecay d) { return decayed(decayed(s, d.first), d.second); }
+
 // The tensor-core form (gdr_la_tc.cu): whether it takes these passes, and its launch.
 bool tc_takes(const LaArgs &p, int passes, int dtype);
 int launch_tc(const LaArgs &p, int passes, cudaStream_t st);
