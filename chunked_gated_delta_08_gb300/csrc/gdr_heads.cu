@@ -69,7 +69,8 @@ struct Place {
 // A thread's 2 RUN channels in packed pairs: those of the first run, then of the second.  (Single fp32 operations
 // and selects made 267 instructions of four rows of 128, and issue the bound: 51 %.)
 //
-// Cosines and sines of a thread's RUN pairs; BACK turns back.
+// Cosines and sines of a thread's RUN pairs; BACK turns back.  A padding token (pos < 0) has no place in the table:
+// nothing is loaded, and nothing may be applied.
 template <int RUN, bool NEAR, bool BACK>
 struct Turn {
   float c[RUN], s[RUN];
@@ -87,6 +88,7 @@ struct Turn {
     }
   }
   __device__ __forceinline__ Turn(const HeadArgs &p, const Place<RUN, NEAR> &l, int64_t pos) {
+    if (pos < 0) return;
     if constexpr (NEAR) {
       if (l.turned0) load_run(p, pos, l.c0 / 2, 0, RUN / 2);
       if (l.turned1) load_run(p, pos, l.c1 / 2, RUN / 2, RUN / 2);
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 2) head_fwd_kernel(const __grid_cons
     for (int u = 0; u < U; ++u) rx[u] = nx[u];
     it.next();
     const int64_t pos = checked(p, at);  // one token to a warp
-    const Turn<RUN, NEAR, false> a(p, l, pos < 0 ? 0 : pos);
+    const Turn<RUN, NEAR, false> a(p, l, pos);
     fetch(nx, nat);  // the next item's rows are on their way while this one is worked on
     T *y = sd.y + (m * sd.heads + h0) * D;
 #pragma unroll
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 2) head_fwd_kernel(const __grid_cons
       if (l.on && h0 + u * G < sd.heads) {
 #pragma unroll
         for (int i = 0; i < RUN; ++i) v[i] = pos < 0 ? f2_both(0.f) : f2_mul(f2_mul(v[i], rho), w[i]);
-        a.apply(v, l);
+        if (pos >= 0) a.apply(v, l);
         store_two(y + u * G * D, l.c0, l.c1, v);
       }
     }
@@ -349,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 2) head_bwd_kernel(const __grid_cons
     it.next();
     fetch(buf ^ 1);
     const int64_t pos = checked(p, at);  // one token to a warp
-    const Turn<RUN, NEAR, true> a(p, l, pos < 0 ? 0 : pos);
+    const Turn<RUN, NEAR, true> a(p, l, pos);
     copy_wait<1>();  // this item is here, the next one on its way
     T *dx = sd.y + (m * sd.heads + h0) * D;
 #pragma unroll
@@ -359,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 2) head_bwd_kernel(const __grid_cons
       const auto &part = ahead.part[buf][u];
       get_two(part[0][0].b[threadIdx.x], part[0][1].b[threadIdx.x], on, v);
       get_two(part[1][0].b[threadIdx.x], part[1][1].b[threadIdx.x], on, g);
-      a.apply(g, l);
+      if (pos >= 0) a.apply(g, l);
 #pragma unroll
       for (int i = 0; i < RUN; ++i) {
         ss = f2_fma(v[i], v[i], ss);
