@@ -637,6 +637,7 @@ int gdr_qk_norm_fwd(const gdr_qk_norm_desc *desc, const void *q, const void *k, 
     return set_error(GDR_ERR_NULLPTR, "q, k, wq, wk, yq and yk must be non-NULL");
   if (desc->R > 0 && (!cos || !sin || !positions))
     return set_error(GDR_ERR_NULLPTR, "a rotation needs cos, sin and positions");
+  if (desc->R > 0 && desc->P == 0) return set_error(GDR_ERR_SHAPE, "the rotation's table has no positions");
   HeadArgs a{};
   a.d = *desc;
   a.q = q; a.k = k; a.wq = wq; a.wk = wk; a.cos = cos; a.sin = sin; a.pos = positions; a.yq = yq; a.yk = yk;
@@ -657,6 +658,7 @@ int gdr_qk_norm_bwd(const gdr_qk_norm_desc *desc, const void *dyq, const void *d
     return set_error(GDR_ERR_NULLPTR, "dyq, dyk, q, k, dq and dk must be non-NULL");
   if (desc->M > 0 && desc->R > 0 && (!cos || !sin || !positions))
     return set_error(GDR_ERR_NULLPTR, "a rotation needs cos, sin and positions");
+  if (desc->M > 0 && desc->R > 0 && desc->P == 0) return set_error(GDR_ERR_SHAPE, "the rotation's table has no positions");
   HeadArgs a{};
   a.d = *desc;
   a.q = q; a.k = k; a.wq = wq; a.wk = wk; a.dyq = dyq; a.dyk = dyk; a.cos = cos; a.sin = sin; a.pos = positions;

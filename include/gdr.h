@@ -393,7 +393,8 @@ int gdr_la_step(const gdr_la_desc *desc, const void *q, const void *k, const voi
 
 typedef struct gdr_qk_norm_desc {
   int64_t M, H, HK, D;   /* tokens; heads of q and of k (HK 0: no k); channels of a head, 1 to 256 */
-  int64_t P, R;          /* the rotation's table: positions, and pairs turned (2 R <= D; 0: no rotation) */
+  int64_t P, R;          /* the rotation's table: positions (at least 1 where tokens are turned), and pairs turned
+                            (2 R <= D; 0: no rotation) */
   int64_t ld_q, ld_k, ld_dyq, ld_dyk; /* elements between tokens */
   float eps;
   int32_t dtype;         /* of q, k, yq, yk and their gradients */
