@@ -591,7 +591,7 @@ int launch(HeadArgs a, bool bwd, float *dwq, float *dwk, cudaStream_t st) {
     const auto sum = [&](int64_t first, int64_t rows, float *out) {
       return ColSum{a.part + first * d.D, rows, d.D, d.D, d.D, d.D, out, d.D, nullptr};
     };
-    head_sum_kernel<<<dim3((unsigned)cdiv(d.D, 32), d.HK ? 2 : 1), 1024, 0, st>>>(sum(0, n.q, dwq),
+    head_sum_kernel<<<dim3((unsigned)cdiv(d.D, 32), dwk ? 2 : 1), 1024, 0, st>>>(sum(0, n.q, dwq),
                                                                                 sum(n.q, n.all - n.q, dwk));
     rc = launched("head_sum_kernel");
   }

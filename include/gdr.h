@@ -415,7 +415,8 @@ typedef struct gdr_qk_norm_desc {
  */
 int gdr_qk_norm_fwd(const gdr_qk_norm_desc *desc, const void *q, const void *k, const void *wq, const void *wk,
                     const float *cos, const float *sin, const int64_t *positions, void *yq, void *yk, void *stream);
-/* Gradients of L = sum(yq * dyq) + sum(yk * dyk): dq, dk in dtype; dwq, dwk [D] fp32. */
+/* Gradients of L = sum(yq * dyq) + sum(yk * dyk): dq, dk in dtype; dwq, dwk [D] fp32 (without keys, HK 0, a dwk that
+ * is not NULL is zeroed). */
 int gdr_qk_norm_bwd(const gdr_qk_norm_desc *desc, const void *dyq, const void *dyk, const void *q, const void *k,
                     const void *wq, const void *wk, const float *cos, const float *sin, const int64_t *positions,
                     void *dq, void *dk, float *dwq, float *dwk, void *stream);
