@@ -11,24 +11,29 @@
 //                                                    leave 2^-9 in them; it saves 3 % where none leaves)
 //   O1^T = C^T P^T                                  M=128 N=64   K=64
 //   O2^T = S^T A^T, S^T as bf16 in tensor memory    M=128 N=64   K=Da
-//   S^T  = r^n S^T, then += C^T B'hi + C^T B'lo     M=128 N=Da K=64
+//   U^T  = C^T B'hi + C^T B'lo                      M=128 N=Da K=64
+//   S^T  = r^n S^T + U^T                            by the state's warps, in fp32
 //   y_i  = O1_i + iscale r^e(i) O2_i
 //
 // Every factor is a power of r with an exponent that the place in the chunk gives, so
 // the threads keep them in registers; only a ragged last chunk works them out anew.
 //
-// What follows one chunk after the other is the state alone: its decay and bf16 copy
-// (warps 0-7), then the update's MMAs.  An issuing thread stands still for some 200 cycles
-// at each burst of MMAs and each commit, so the three kinds have a thread each: one thread
-// for all of them was late for the update (1.8 us a chunk where three take 1.6).
+// The tensor cores cut off what they add to an accumulator: a state that all chunks are added to there loses
+// 1.6e-4 of itself over 32768 tokens of one sign and 7e-4 over 131072.  So U has a buffer of its own,
+// and the state loses 3e-7 and 6e-7 (4 x 4096 x 32 x 128: forward 110 -> 115 us, backward 318 -> 326).  That takes the columns of
+// the second scores and the second copy of the state; outputs' MMAs in the order O2, O1 took 4 % longer.
+//
+// What follows one chunk after the other is U's MMAs, then their reading by the state's warps (0-7), which make
+// the next bf16 copy meanwhile.  An issuing thread stands still for some 200 cycles at each burst of MMAs and each
+// commit, so the three kinds have a thread each (one for all took 1.8 us a chunk where three took 1.6).
 //
 // Warp roles (896 threads):
-//   warps 0-7    state: the decay of the fp32 state in tensor memory, its bf16 copy
+//   warps 0-7    state: S = r^n S + U in tensor memory, its bf16 copy
 //   warps 8-15   scores: P, B' (over B in place, its lower half beside), rows past a ragged end cleared
 //   warps 16-23  output: y through shared memory and a tensor store
 //   warp 24      producer: TMA loads into a ring of three stages
 //   warp 25      issues the scores' MMAs
-//   warp 26      issues the state's
+//   warp 26      issues U's
 //   warp 27      issues the outputs'
 // Hand-offs are mbarriers.  Every wait is bounded (about two seconds): where one runs out
 // the block's error flag makes all others return at once, the producer and the MMA thread
@@ -74,14 +79,15 @@ struct Layout {
 constexpr int kMostStages = 6;
 
 // TMEM columns
-constexpr uint32_t TM_SC = 0 /* twice */, TM_O = 128 /* O1, O2 */, TM_S = 256, TM_SB = 384 /* twice */, TM_COLS = 512;
+constexpr uint32_t TM_SC = 0, TM_O = 64 /* O1, O2 */, TM_S = 192, TM_U = 320, TM_SB = 448, TM_COLS = 512;
 
 struct Small {
   float pw[C + 4];  // r^0 .. r^64
   uint64_t full[kMostStages], empty[kMostStages];
-  // (a stage is empty when its chunk's state and output MMAs are done, which frees P, B' and the bf16 state too)
-  uint64_t b_sc[2], b_state, b_o, b_final[3];  // MMAs done
-  uint64_t b_p[2], b_bs[2], b_s[2], b_ofree;   // arrivals of eight warps: P, B', state and its copy, O1 and O2 read
+  // (a stage is empty when its chunk's state and output MMAs are done, which frees P and B' too)
+  uint64_t b_sc, b_u, b_o, b_final[3];  // MMAs done
+  // arrivals of eight warps: P, B', the state's copy; Sc, U, O1 and O2 read
+  uint64_t b_p[2], b_bs[2], b_sb, b_scfree, b_ufree, b_ofree;
   uint32_t tmem_slot;
   int err;
 };
@@ -170,7 +176,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(smem_u32(&S.full[i]), 1);
       mbar_init(smem_u32(&S.empty[i]), p.mode == kStates ? 1 : 2);
     }
-    for (uint64_t *b = S.b_sc; b <= &S.b_final[2]; ++b) mbar_init(smem_u32(b), 1);
+    for (uint64_t *b = &S.b_sc; b <= &S.b_final[2]; ++b) mbar_init(smem_u32(b), 1);
     for (uint64_t *b = S.b_p; b <= &S.b_ofree; ++b) mbar_init(smem_u32(b), 8);
     fence_mbar_init();
   }
@@ -202,8 +208,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ================================================================ state
     const int j = 32 * (warp & 3) + lane;                 // TMEM lane: channel of c
     const int cols = 32 * ka, col0 = (warp >> 2) * cols;  // this thread's channels of a
-    const uint32_t aS = lane_addr + TM_S + col0, aSb = lane_addr + TM_SB + col0 / 2;
+    const uint32_t aS = lane_addr + TM_S + col0, aU = lane_addr + TM_U + col0, aSb = lane_addr + TM_SB + col0 / 2;
     const bool mine = j < Dc;
+    auto copy = [&](int i0, const float (&r)[16]) {
+      uint32_t u[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] = gdr::pack_bf16(r[2 * i], r[2 * i + 1]);
+      tmem_st8(aSb + i0 / 2, u);
+    };
     {
       const float *from = mine ? entering(p, q, s, hv) : nullptr;
       if (from) from += j * q.sj;
@@ -213,43 +225,51 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int i = 0; i < 16; ++i) r[i] = from && col0 + i0 + i < Da ? from[(int64_t)(col0 + i0 + i) * q.si] : 0.f;
         tmem_st16(aS + i0, r);
+        copy(i0, r);
       }
     }
     tmem_st_wait();
+    tc_fence_before();
+    arrive(S.b_sb);
     const Decay whole = decay_of(g, C);
 #pragma unroll 1
     for (int c = 0; c < nch; ++c) {
       const int n = chunk_rows(c);
       const Decay decay = n == C ? whole : decay_of(g, n);
-      if (c > 0) wait(S.b_state, (c - 1) & 1);
-      // O2 has read the copy of two chunks before
-      if (c > 1) wait(S.empty[(c - 2) % kStages], ((c - 2) / kStages) & 1);
+      const bool more = !states && c + 1 < nch;  // chunks that read a copy
+      wait(S.b_u, c & 1);
       tc_fence_after();
 #pragma unroll
       for (int i0 = 0; i0 < 64; i0 += 16) {
         if (i0 < cols) {
-          float r[16];
+          float r[16], u[16];
+          tmem_ld16(aU + i0, u);
           tmem_ld16(aS + i0, r);
           tmem_ld_wait();
-          uint32_t u[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) u[i] = gdr::pack_bf16(r[2 * i], r[2 * i + 1]);
-          if (!states) tmem_st8(aSb + (c & 1) * 64 + i0 / 2, u);
+          if (i0 == 0 && more) {  // O2 has read the copy
+            wait(S.b_o, c & 1);
+            tc_fence_after();
+          }
+          if (i0 + 16 == cols) {
+            tc_fence_before();
+            arrive(S.b_ufree);
+          }
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            // (choosing between S + S a and S a instead took 15 % longer, masking the second S 5 %)
             const f2 x = f2_pack(r[i], r[i + 1]);
-            f2_split(f2_fma(x, f2_both(decay.a), f2_mul(x, f2_both(decay.b))), r[i], r[i + 1]);
+            const f2 y = f2_fma(x, f2_both(decay.a), f2_pack(u[i], u[i + 1]));
+            f2_split(f2_fma(x, f2_both(decay.b), y), r[i], r[i + 1]);
           }
+          if (more) copy(i0, r);
           tmem_st16(aS + i0, r);
         }
       }
       tmem_st_wait();
-      tc_fence_before();
-      arrive(S.b_s[c & 1]);
+      if (more) {
+        tc_fence_before();
+        arrive(S.b_sb);
+      }
     }
-    if (nch > 0) wait(S.b_state, (nch - 1) & 1);
-    tc_fence_after();
     float *to = leaving(p, q, s, slot, hv);
     if (to) {
       to += j * q.sj;
@@ -293,13 +313,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       if (c > 1) wait(S.empty[(c - 2) % kStages], ((c - 2) / kStages) & 1);  // the buffers' chunk before is done
       if (!states) {
-        wait(S.b_sc[buf], (c >> 1) & 1);
+        wait(S.b_sc, c & 1);
         tc_fence_after();
         float r[2][8];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) tmem_ld_16x256b_x2(lane_addr + TM_SC + 64 * buf + 32 * half + 16 * i, r[i]);
+        for (int i = 0; i < 2; ++i) tmem_ld_16x256b_x2(lane_addr + TM_SC + 32 * half + 16 * i, r[i]);
         tmem_ld_wait();
         tc_fence_before();
+        arrive(S.b_scfree);
         if (n < C) {  // columns past the end: what lies there is not multiplied
 #pragma unroll
           for (int k = 0; k < 16; ++k)
@@ -482,27 +503,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint32_t ph = (c >> 1) & 1, off = st * SZ_STAGE;
       spin(S.full[st], (c / kStages) & 1);
       if (warp == kScoreMma) {
-        if (c > 1) spin(S.b_p[buf], ((c >> 1) - 1) & 1);  // the scores of two chunks before have been read
+        if (c > 0) spin(S.b_scfree, (c - 1) & 1);
         if (*err) break;
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
           const uint32_t k = off + (ks >> 2) * SZ_PANEL + (ks & 3) * 32;
-          if (ks < 4 * ka) mma_bf16(tbase + TM_SC + 64 * buf, at(dk, k), at(dk, k + SZ_TILE), id_sc, ks > 0);
+          if (ks < 4 * ka) mma_bf16(tbase + TM_SC, at(dk, k), at(dk, k + SZ_TILE), id_sc, ks > 0);
         }
-        mma_commit(smem_u32(&S.b_sc[buf]));
+        mma_commit(smem_u32(&S.b_sc));
       } else if (warp == kStateMma) {
         spin(S.b_bs[buf], ph);
-        spin(S.b_s[buf], ph);
+        if (c > 0) spin(S.b_ufree, (c - 1) & 1);
         if (*err) break;
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
           const uint64_t a = at(dmn, off + 2 * SZ_TILE + ks * 2048);
-          mma_bf16(tbase + TM_S, a, at(dmn, off + SZ_TILE + ks * 2048), id_s, 1);
-          mma_bf16(tbase + TM_S, a, at(dmn, OFF_LO + buf * SZ_TILE + ks * 2048), id_s, 1);
+          mma_bf16(tbase + TM_U, a, at(dmn, off + SZ_TILE + ks * 2048), id_s, ks > 0);
+          mma_bf16(tbase + TM_U, a, at(dmn, OFF_LO + buf * SZ_TILE + ks * 2048), id_s, 1);
         }
-        mma_commit(smem_u32(&S.b_state));
+        mma_commit(smem_u32(&S.b_u));
         mma_commit(smem_u32(&S.empty[st]));
       } else {
         spin(S.b_p[buf], ph);
@@ -513,13 +534,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int ks = 0; ks < 4; ++ks)
           mma_bf16(tbase + TM_O, at(dmn, off + 2 * SZ_TILE + ks * 2048), at(dk, OFF_P + buf * SZ_PANEL + ks * 32),
                    id_o1, ks > 0);
-        spin(S.b_s[buf], ph);
+        spin(S.b_sb, c & 1);
         if (*err) break;
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
           if (ks < 4 * ka)
-            mma_bf16_ta(tbase + TM_O + 64, tbase + TM_SB + 64 * buf + 8 * ks,
+            mma_bf16_ta(tbase + TM_O + 64, tbase + TM_SB + 8 * ks,
                         at(dk, off + (ks >> 2) * SZ_PANEL + (ks & 3) * 32), id_o2, ks > 0);
         mma_commit(smem_u32(&S.b_o));
         mma_commit(smem_u32(&S.empty[st]));

@@ -376,8 +376,10 @@ typedef struct gdr_la_desc {
  * all of the sequence), but no other sequence and no other head's outputs.
  * bf16 inputs of K and V up to 128, both multiples of 8, in rows and bases of 16
  * bytes take the tcgen05 form: scores and states are rounded to bf16 where they
- * are multiplied for o; the states themselves are not (they take each product to
- * 2^-17).  Everything else takes products of 2^-21.
+ * are multiplied for o and the gradients (2.3e-3 of them, 1.7e-3 being their own
+ * rounding); the states themselves are not: they take each product to 2^-17 and
+ * add in fp32 (2.5e-6 of a state, whatever the length).  Everything else takes
+ * products of 2^-21 (6e-7).
  */
 int gdr_la_fwd(const gdr_la_desc *desc, const void *q, const void *k, const void *v, const float *g, const float *h0,
                const int64_t *cu_seqlens, void *o, float *ht, void *stream);
