@@ -231,7 +231,7 @@ struct Walk {
 // TPR threads to a row (a power of two, at least D / (2 RUN)), so 32 / TPR rows to a warp at once; U such
 // sets of one token's heads to a warp.  A block belongs to q or to k: its weights stay in registers.
 // Warps go through the items (token, run of heads) of their tensor, the next one's rows on their way:
-// 16384 x 40 x 128 bf16 in 66 us, 78 % of the copy rate (79 us with one item to a warp, 3 blocks at 80
+// 16384 x 40 x 128 bf16 in 64 us, 80 % of the copy rate (79 us with one item to a warp, 3 blocks at 80
 // registers 82).
 template <typename T, int RUN, int TPR, int U, bool NEAR>
 __global__ void __launch_bounds__(kThreads, 2) head_fwd_kernel(const __grid_constant__ HeadArgs p) {
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 2) head_fwd_kernel(const __grid_cons
 // The same with dy beside x; a thread sums dw of its channels over its items, a block's
 // warps and rows meet in shared memory, the blocks in a second launch.  x and dy of the next
 // item are copied into the thread's own part of shared memory meanwhile (in registers they spilled:
-// 16384 x 40 x 128 bf16 took 145 us, and 112-120 without any rows ahead; so it takes 99, 77 % of the copy
+// 16384 x 40 x 128 bf16 took 145 us, and 112-120 without any rows ahead; so it takes 95, 80 % of the copy
 // rate, and with one row to a thread 110).
 template <typename T, int RUN, int U>
 struct Ahead {

@@ -18,7 +18,7 @@ namespace {
 // summed by itself: 4e-7 of a state after 16384 tokens, where one accumulator for
 // all left 5e-6.  Rows past the segment's end and channels past the width are zeros in
 // shared memory.  Two blocks a multiprocessor are bound by issue (40 %) and the
-// tensor pipe (37 %): 2 x 2048 x 8 x 64 fp32 take 79 us in three launches.
+// tensor pipe (37 %): 2 x 2048 x 8 x 64 fp32 take 82 us in three launches.
 constexpr int kThreads = 256;
 constexpr int kCols = 32;       // columns of c in a block
 constexpr int LDC = kCols + 4;  // row strides in shared memory, chosen off multiples of 32 banks
@@ -275,10 +275,13 @@ int launch_sum(const float *part0, const float *part1, void *out0, void *out1, i
 
 // -------------------------------------------------------------------------------- host side
 // How sequences are cut: p.L (0: not) and p.least.  A block walks a sequence chunk by chunk, `wave`
-// blocks at a time (a tensor-core block takes 1.6 us a chunk, one of the other form 3.5).  Uncut, a
-// launch takes as long as its longest sequence, or its waves of whole sequences.  Cut, the work
+// blocks at a time (a tensor-core block takes 1.7 us a chunk, one of the other form some 9 at 64 fp32 channels).  Rows of
+// more than 128 channels leave room for one block of the other form on a multiprocessor, not two; these constants
+// were measured with two, and with one in their place as many calls became slower as faster (bf16: 4 x 4096 x 4 heads x
+// 256 x 256 1734 -> 1408 us, but 32768 x 4 3730 -> 4103, its backward 8103 -> 9833, and that of 16384 x 2 heads x 128 x
+// 256 1333 -> 1861).  Uncut, a launch takes as long as its longest sequence, or its waves of whole sequences.  Cut, the work
 // spreads evenly, but forming the segments' states and ragged waves make it 2.2 times as much (16384 x 32
-// heads in 7 sequences, 94 chunks the longest: 168 us uncut, 223 cut; 8192 x 16 heads 69 us cut), and
+// heads in 7 sequences, 94 chunks the longest: 168 us uncut, 223 cut, when measured for this; 8192 x 16 heads 69 us cut), and
 // two more launches take the time of `launches` chunks; a segment has at least `shortest` of them.
 void cut(LaArgs &p, int blocks_per_pair, int wave, int launches, int shortest) {
   const int64_t blocks = p.HV * blocks_per_pair;                // to a sequence
@@ -394,7 +397,7 @@ LaArgs base_args(const gdr_la_desc &d, const float *g, const int64_t *cu, int *s
 // One block per (row, value head, run of columns) walks its part of the K x V state once:
 // S = r S + k v^T is written back and o = scale S^T q summed on the way.  Eight bytes of
 // state a multiply-add: HBM bound.  A thread keeps VEC columns; the partial sums of o of
-// a block's row groups meet in shared memory, in order.  256 x 32 heads of 128 x 128 take 165 us, 97 % of the
+// a block's row groups meet in shared memory, in order.  256 x 32 heads of 128 x 128 take 168 us, 97 % of the
 // copy rate (with one row on its way after the other 197).
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) la_step_kernel(gdr_la_desc d, const T *q, const T *k, const T *v, const float *g,

@@ -110,7 +110,8 @@ struct Segment {
 __device__ __forceinline__ int64_t segments_in(const LaArgs &p, int64_t len) {
   return len > 0 ? (len + p.L - 1) / p.L : 1;
 }
-// Every thread of the block calls it.  Uncut, the longest sequences come first, so that none of them starts last.
+// Every thread of the block calls it.  Uncut, the longest of up to 256 sequences come first, so that none of them starts
+// last; more take their own order.
 __device__ __forceinline__ Segment segment_of(const LaArgs &p, int64_t slot, bool backwards, bool cut) {
   Segment s;
   if (p.mode == kStates) {

@@ -31,12 +31,12 @@
 //   warps 0-7    state: S = r^n S + U in tensor memory, its bf16 copy
 //   warps 8-15   scores: P, B' (over B in place, its lower half beside), rows past a ragged end cleared
 //   warps 16-23  output: y through shared memory and a tensor store
-//   warp 24      producer: TMA loads into a ring of three stages
+//   warp 24      producer: TMA loads into a ring of three stages, six where rows have up to 64 channels
 //   warp 25      issues the scores' MMAs
 //   warp 26      issues U's
 //   warp 27      issues the outputs'
 // Hand-offs are mbarriers.  Every wait is bounded (about two seconds): where one runs out
-// the block's error flag makes all others return at once, the producer and the MMA thread
+// the block's error flag makes all others return at once, the producer and the MMA threads
 // stop, the rest run to their end on what is there (in bounds), the block lets its copies
 // and MMAs finish, frees its tensor memory and reports GDR_ERR_TIMEOUT.
 #include <cuda.h>

@@ -414,6 +414,7 @@ typedef struct gdr_qk_norm_desc {
  * [M] int64.  Channels from 2 R on are normed only.  A negative position is a
  * padding token: its rows are zero, its gradients too.  One past the table is
  * treated so and reported by gdr_device_status as GDR_ERR_POSITION.
+ * The squares are summed in fp32: a head of values about 1e19 passes its range.
  */
 int gdr_qk_norm_fwd(const gdr_qk_norm_desc *desc, const void *q, const void *k, const void *wq, const void *wk,
                     const float *cos, const float *sin, const int64_t *positions, void *yq, void *yk, void *stream);
